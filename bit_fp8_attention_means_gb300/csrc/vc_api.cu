@@ -228,6 +228,132 @@ vc_status vc_attn_fwd_hybrid(const uint8_t* Q8, const float* sq, const uint8_t* 
                        reinterpret_cast<cudaStream_t>(stream), nullptr);
 }
 
+// ------------------------------------------------------------ paged cache
+
+static bool row_strides_ok(int64_t s_n, int64_t s_h) { return s_n > 0 && s_h > 0 && s_n % 8 == 0 && s_h % 8 == 0; }
+
+static vc_status check_cache_shape(const vc_cache_shape& c) {
+    if (c.pages < 1 || c.page_size < 1 || c.H < 1 || c.d < 1) return VC_ERR_INVALID_ARG;
+    if (c.s_page <= 0 || c.s_head <= 0 || c.s_tok <= 0 || c.s_page % 16 || c.s_head % 16 || c.s_tok % 16)
+        return VC_ERR_INVALID_ARG;
+    if (c.t_page <= 0 || c.t_head <= 0 || c.t_page % 4 || c.t_head % 4) return VC_ERR_INVALID_ARG;
+    if (c.d != 64 && c.d != 128) return VC_ERR_UNSUPPORTED;
+    if (c.page_size < 16 || c.page_size > 4096 || (c.page_size & (c.page_size - 1))) return VC_ERR_UNSUPPORTED;
+    return VC_OK;
+}
+
+// Checks what the three cache entry points share and fills the kernels' view.
+// Called for T > 0 only: without rows the pointers may be null.
+static vc_status cache_view(const vc_cache_shape& c, const uint8_t* K8, const float* sk, const uint8_t* V8,
+                            const float* sv, const vc_batch& b, int32_t* dev_status, CacheView* out) {
+    if (!K8 || !sk || !V8 || !sv || !b.cu || !b.kv_len || !b.table) return VC_ERR_INVALID_ARG;
+    if (!aligned16(K8) || !aligned16(V8) || !aligned16(sk) || !aligned16(sv)) return VC_ERR_INVALID_ARG;
+    if (b.s_table < b.cols) return VC_ERR_INVALID_ARG;
+    if ((int64_t)b.cols * c.page_size >= (int64_t(1) << 31) || (int64_t)b.T * c.H >= (int64_t(1) << 31))
+        return VC_ERR_UNSUPPORTED;
+    out->K8 = const_cast<uint8_t*>(K8);
+    out->sk = const_cast<float*>(sk);
+    out->V8 = const_cast<uint8_t*>(V8);
+    out->sv = const_cast<float*>(sv);
+    out->s_page = c.s_page;
+    out->s_head = c.s_head;
+    out->s_tok = c.s_tok;
+    out->t_page = c.t_page;
+    out->t_head = c.t_head;
+    out->cu = b.cu;
+    out->kv_len = b.kv_len;
+    out->table = b.table;
+    out->s_table = b.s_table;
+    out->pages = c.pages;
+    out->page_log2 = __builtin_ctz((unsigned)c.page_size);
+    out->H = c.H;
+    out->B = b.B;
+    out->T = b.T;
+    out->cols = b.cols;
+    out->dev_status = dev_status;
+    return VC_OK;
+}
+
+static vc_status check_batch_sizes(const vc_batch& b) {
+    return (b.B < 1 || b.T < 0 || b.cols < 1) ? VC_ERR_INVALID_ARG : VC_OK;
+}
+
+vc_status vc_cache_append(const void* K, const void* V, int64_t s_n, int64_t s_h, vc_cache_shape cache, uint8_t* K8,
+                          float* sk, uint8_t* V8, float* sv, vc_batch batch, int32_t* dev_status,
+                          vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    if ((st = check_batch_sizes(batch)) != VC_OK) return st;
+    if (!row_strides_ok(s_n, s_h)) return VC_ERR_INVALID_ARG;
+    if (batch.T == 0) return VC_OK;
+    if (!K || !V || !aligned16(K) || !aligned16(V)) return VC_ERR_INVALID_ARG;
+    CacheView v;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    return launch_cache_append(static_cast<const uint16_t*>(K), static_cast<const uint16_t*>(V), s_n, s_h, cache.d, v,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                        vc_batch batch, void* K, void* V, int64_t s_n, int64_t s_h, int32_t* dev_status,
+                        vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    if ((st = check_batch_sizes(batch)) != VC_OK) return st;
+    if (!row_strides_ok(s_n, s_h)) return VC_ERR_INVALID_ARG;
+    if (batch.T == 0) return VC_OK;
+    if (!K || !V || !aligned16(K) || !aligned16(V)) return VC_ERR_INVALID_ARG;
+    CacheView v;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    return launch_cache_read(v, cache.d, static_cast<uint16_t*>(K), static_cast<uint16_t*>(V), s_n, s_h,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+static vc_status check_paged_heads(const vc_cache_shape& c, int Hq, int T, int max_q) {
+    if (Hq < 1 || Hq % c.H || max_q < 0) return VC_ERR_INVALID_ARG;
+    if ((int64_t)T * Hq >= (int64_t(1) << 31)) return VC_ERR_UNSUPPORTED;
+    return VC_OK;
+}
+
+size_t vc_attn_paged_workspace(vc_cache_shape cache, int Hq, int B, int T, int max_q) {
+    if (check_cache_shape(cache) != VC_OK || B < 1 || T < 1 || check_paged_heads(cache, Hq, T, max_q) != VC_OK)
+        return 0;
+    return attn_paged_workspace(cache, Hq, B, T, max_q);
+}
+
+vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache, const uint8_t* K8,
+                        const float* sk, const uint8_t* V8, const float* sv, vc_batch batch, float softmax_scale,
+                        int causal, int window, int max_q, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    if ((st = check_batch_sizes(batch)) != VC_OK) return st;
+    if ((st = check_paged_heads(cache, Hq, batch.T, max_q)) != VC_OK) return st;
+    if ((causal != 0 && causal != 1) || window < 0 || !__builtin_isfinite(softmax_scale)) return VC_ERR_INVALID_ARG;
+    if (!row_strides_ok(q_sn, q_sh) || !row_strides_ok(o_sn, o_sh)) return VC_ERR_INVALID_ARG;
+    if (batch.T == 0) return VC_OK;
+    if (!Q || !O || !aligned16(Q) || !aligned16(O) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return VC_ERR_INVALID_ARG;
+    CacheView v;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    const size_t need = attn_paged_workspace(cache, Hq, batch.B, batch.T, max_q);
+    if (need && !workspace_ok(workspace, workspace_bytes, need)) return VC_ERR_WORKSPACE;
+    PagedAttn a;
+    a.Q = static_cast<const uint16_t*>(Q);
+    a.q_sn = q_sn;
+    a.q_sh = q_sh;
+    a.O = static_cast<uint16_t*>(O);
+    a.o_sn = o_sn;
+    a.o_sh = o_sh;
+    a.lse = lse;
+    a.G = Hq / cache.H;
+    const double sc = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / __builtin_sqrt((double)cache.d);
+    a.scale_log2 = (float)(sc * 1.4426950408889634);
+    a.causal = causal;
+    a.window = window;
+    a.max_q = max_q;
+    return launch_attn_paged(a, v, cache.d, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
 vc_status vc_attn_fwd_debug(const uint8_t* Q8, const float* sq, const uint8_t* K8, const float* sk,
                             const uint8_t* V8T, const float* sv, const void* mu, vc_shape shape, float softmax_scale,
                             int expcast, int vsmooth, void* O, int32_t* dev_status, vc_stream_t stream, int dbg_bh,

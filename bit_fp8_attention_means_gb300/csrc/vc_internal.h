@@ -70,4 +70,35 @@ vc_status launch_attn(const uint8_t* Q8, const float* sq, const uint8_t* K8, con
                       float exact_margin, int vsmooth, uint16_t* O, int32_t* dev_status, cudaStream_t st,
                       const AttnDebug* dbg);
 
+// paged cache (vc_cache.cu) and the attention over it (vc_attn_paged.cu)
+struct CacheView {                 // what a kernel needs of vc_cache_shape and vc_batch
+    uint8_t* K8;
+    float* sk;
+    uint8_t* V8;
+    float* sv;
+    int64_t s_page, s_head, s_tok, t_page, t_head;
+    const int32_t* cu;
+    const int32_t* kv_len;
+    const int32_t* table;
+    int64_t s_table;
+    int pages, page_log2, H, B, T, cols;
+    int32_t* dev_status;
+};
+struct PagedAttn {
+    const uint16_t* Q;
+    int64_t q_sn, q_sh;
+    uint16_t* O;
+    int64_t o_sn, o_sh;
+    float* lse;
+    int G;             // query heads of a key/value head
+    float scale_log2;  // softmax_scale * log2 e
+    int causal, window, max_q;
+};
+vc_status launch_cache_append(const uint16_t* K, const uint16_t* V, int64_t s_n, int64_t s_h, int d,
+                              const CacheView& c, cudaStream_t st);
+vc_status launch_cache_read(const CacheView& c, int d, uint16_t* K, uint16_t* V, int64_t s_n, int64_t s_h,
+                            cudaStream_t st);
+size_t attn_paged_workspace(const vc_cache_shape& c, int Hq, int B, int T, int max_q);
+vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void* ws, cudaStream_t st);
+
 }  // namespace vc

@@ -28,6 +28,17 @@ class VcShape(ctypes.Structure):
                 ("s_b", ctypes.c_int64), ("s_n", ctypes.c_int64), ("s_h", ctypes.c_int64)]
 
 
+class VcCacheShape(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("H", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("s_page", ctypes.c_int64), ("s_head", ctypes.c_int64), ("s_tok", ctypes.c_int64),
+                ("t_page", ctypes.c_int64), ("t_head", ctypes.c_int64)]
+
+
+class VcBatch(ctypes.Structure):
+    _fields_ = [("cu", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("cols", ctypes.c_int32), ("s_table", ctypes.c_int64)]
+
+
 _lib = None
 _vp = ctypes.c_void_p
 
@@ -74,6 +85,18 @@ def lib():
         L.vc_attn_fwd_debug.restype = ctypes.c_int
         L.vc_attn_fwd_debug.argtypes = L.vc_attn_fwd.argtypes + [ctypes.c_int, ctypes.c_int, _vp, _vp,
                                                                  ctypes.c_float]
+        L.vc_cache_append.restype = ctypes.c_int
+        L.vc_cache_append.argtypes = [_vp, _vp, ctypes.c_int64, ctypes.c_int64, VcCacheShape, _vp, _vp, _vp, _vp,
+                                      VcBatch, _vp, _vp]
+        L.vc_cache_read.restype = ctypes.c_int
+        L.vc_cache_read.argtypes = [VcCacheShape, _vp, _vp, _vp, _vp, VcBatch, _vp, _vp, ctypes.c_int64,
+                                    ctypes.c_int64, _vp, _vp]
+        L.vc_attn_paged_workspace.restype = ctypes.c_size_t
+        L.vc_attn_paged_workspace.argtypes = [VcCacheShape, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+        L.vc_attn_paged.restype = ctypes.c_int
+        L.vc_attn_paged.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp, _vp, _vp,
+                                    _vp, VcBatch, ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp,
+                                    ctypes.c_int64, ctypes.c_int64, _vp, _vp, ctypes.c_size_t, _vp, _vp]
         L.vc_debug_e4m3_encode.restype = ctypes.c_int
         L.vc_debug_e4m3_encode.argtypes = [_vp, ctypes.c_int64, _vp, _vp]
         L.vc_debug_wait_timeout.restype = ctypes.c_int
@@ -282,6 +305,196 @@ def vc_attn_fwd(qz, shape: VcShape, softmax_scale=0.0, expcast=1, vsmooth=1, O=N
     _check(lib().vc_attn_fwd_debug(*ops, int(expcast), int(vsmooth), *tail, int(debug[0]), int(debug[1]), _ptr(S),
                                    _ptr(P), float(exact_margin or 0.0)), "vc_attn_fwd_debug")
     return O, S, P
+
+
+# ------------------------------------------------------------ paged cache
+
+def alloc_cache(pages, page_size, H, d, device):
+    """A page pool for vc_cache_append, vc_cache_read and vc_attn_paged: dict of K8, V8 (E4M3 bytes
+    [pages, H, page_size, d]) and their scales sk, sv (fp32 [pages, H, page_size]), zeroed.
+
+    Any tensors of these shapes and types do, in any order of the first three
+    dimensions of K8 and V8 (as views, e.g. one half of a joint pool): the
+    channels and the scales' tokens have to be contiguous, the strides of K8
+    and V8 equal, and those of sk and sv too."""
+    c = {}
+    for code, scale in (("K8", "sk"), ("V8", "sv")):
+        c[code] = _empty((pages, H, page_size, d), torch.uint8, device, 0)
+        c[scale] = _empty((pages, H, page_size), torch.float32, device, 0)
+    return c
+
+
+def _stride(t, dim, unit):
+    """Stride of a dimension; one of a single element may have any, so it gets a legal one."""
+    return t.stride(dim) if t.shape[dim] > 1 else unit
+
+
+def cache_shape_of(cache) -> VcCacheShape:
+    """The vc_cache_shape of a dict of K8, sk, V8, sv (see alloc_cache)."""
+    K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
+    if K8.dim() != 4 or K8.dtype != torch.uint8 or V8.dtype != torch.uint8 or V8.shape != K8.shape:
+        raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
+    if sk.dtype != torch.float32 or sv.dtype != torch.float32 or sk.shape != K8.shape[:3] or sv.shape != sk.shape:
+        raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
+    pages, H, page, d = K8.shape
+    s = tuple(_stride(K8, i, d) for i in range(3))
+    t = tuple(_stride(sk, i, page) for i in range(2))
+    if tuple(_stride(V8, i, d) for i in range(3)) != s or tuple(_stride(sv, i, page) for i in range(2)) != t:
+        raise ValueError("K8 and V8, and sk and sv, must share strides")
+    if min(K8.shape) and (_stride(K8, 3, 1), _stride(V8, 3, 1), _stride(sk, 2, 1), _stride(sv, 2, 1)) != (1,) * 4:
+        raise ValueError("channels and the scales' tokens must be contiguous")
+    return VcCacheShape(pages, page, H, d, s[0], s[1], s[2], t[0], t[1])
+
+
+def _batch_of(cu, kv_len, table, T, dev) -> VcBatch:
+    for name, t, dim in (("cu", cu, 1), ("kv_len", kv_len, 1), ("table", table, 2)):
+        if t.dtype != torch.int32 or t.dim() != dim:
+            raise ValueError("%s must be an int32 tensor of %d dimension(s)" % (name, dim))
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError("%s must be contiguous in its last dimension" % name)
+        _on(dev, name, t)
+    B, cols = table.shape
+    if cu.shape[0] != B + 1 or kv_len.shape[0] != B:
+        raise ValueError("cu, kv_len and table disagree on the number of sequences")
+    return VcBatch(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), B, T, cols, _stride(table, 0, max(cols, 1)))
+
+
+def _on(dev, name, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, dev))
+
+
+def _rows(name, t, H, d):
+    """Checks a bf16 [T, H, d] tensor with contiguous channels; its row and head strides."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+        raise ValueError("%s must be bf16 [T, %d, %d]" % (name, H, d))
+    if t.stride(2) != 1:
+        raise ValueError("%s must have contiguous channels" % name)
+    return _stride(t, 0, H * d), _stride(t, 1, d)
+
+
+def _status_word(dev_status, dev):
+    if dev_status is not None and dev_status.dtype != torch.int32:
+        raise ValueError("dev_status must be int32")
+    _on(dev, "dev_status", dev_status)
+
+
+class _Launch:
+    """The device and stream of a call: the cache's device is made current, and tensors made here are
+    kept for `stream` where that is not the one they were made on."""
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("the cache must be on a CUDA device")
+        self._guard = torch.cuda.device(dev)
+        self._dev, self._given = dev, stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        self.current = torch.cuda.current_stream(self._dev)
+        self.stream = self._given if self._given is not None else self.current
+        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
+        return self
+
+    def __exit__(self, *e):
+        return self._guard.__exit__(*e)
+
+    def new(self, *tensors):
+        if self.stream.cuda_stream != self.current.cuda_stream:
+            for t in tensors:
+                t.record_stream(self.stream)
+
+
+def vc_cache_append(K, V, cache, cu, kv_len, table, dev_status=None, stream=None):
+    """Quantizes new keys and values (bf16 [T, H, d]) into the pages of `cache` (see alloc_cache).
+
+    cu int32 [B+1], kv_len int32 [B], table int32 [B, cols]: sequence b has
+    rows cu[b] .. cu[b+1]-1 of the call and kv_len[b] tokens in the cache with
+    these included; position p lies in page table[b, p // page_size]."""
+    L = lib()
+    s = cache_shape_of(cache)
+    strides = _rows("K", K, s.H, s.d)
+    if V.shape != K.shape or _rows("V", V, s.H, s.d) != strides:
+        raise ValueError("K and V must share shape and strides")
+    dev = cache["K8"].device
+    _on(dev, "K, V, or a tensor of the cache", K, V, cache["V8"], cache["sk"], cache["sv"])
+    _status_word(dev_status, dev)
+    batch = _batch_of(cu, kv_len, table, K.shape[0], dev)
+    with _Launch(dev, stream) as at:
+        _check(L.vc_cache_append(_ptr(K), _ptr(V), *strides, s, _ptr(cache["K8"]), _ptr(cache["sk"]),
+                                 _ptr(cache["V8"]), _ptr(cache["sv"]), batch, _ptr(dev_status), at.handle),
+               "vc_cache_append")
+    return cache
+
+
+def vc_cache_read(cache, cu, kv_len, table, T, K=None, V=None, dev_status=None, stream=None):
+    """Reads cached tokens back as bf16 [T, H, d] (K, V): the rows that vc_cache_append would write.
+    Rows of no sequence stay as they are in K and V given, and hold anything in new ones."""
+    L = lib()
+    s = cache_shape_of(cache)
+    dev = cache["K8"].device
+    _status_word(dev_status, dev)
+    batch = _batch_of(cu, kv_len, table, T, dev)
+    with _Launch(dev, stream) as at:
+        if K is None:
+            K = _empty((T, s.H, s.d), torch.bfloat16, dev)
+            at.new(K)
+        if V is None:
+            V = torch.empty_strided(K.shape, K.stride(), dtype=torch.bfloat16, device=dev)
+            at.new(V)
+        _on(dev, "K, V, or a tensor of the cache", K, V, cache["V8"], cache["sk"], cache["sv"])
+        strides = _rows("K", K, s.H, s.d)
+        if K.shape[0] != T or V.shape != K.shape or _rows("V", V, s.H, s.d) != strides:
+            raise ValueError("K and V must have T rows and share strides")
+        _check(L.vc_cache_read(s, _ptr(cache["K8"]), _ptr(cache["sk"]), _ptr(cache["V8"]), _ptr(cache["sv"]), batch,
+                               _ptr(K), _ptr(V), *strides, _ptr(dev_status), at.handle), "vc_cache_read")
+    return K, V
+
+
+def attn_paged_workspace_bytes(cache, Hq, B, T, max_q=0) -> int:
+    return lib().vc_attn_paged_workspace(cache_shape_of(cache), Hq, B, T, max_q)
+
+
+def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, window=0, max_q=0, O=None, lse=None,
+                  workspace=None, dev_status=None, stream=None):
+    """Attention of the call's queries (bf16 [T, Hq, d]) over the paged cache, their own keys included:
+    append them first.  Returns (O bf16 [T, Hq, d], lse fp32 [T, Hq]).
+
+    cu, kv_len, table as in vc_cache_append.  causal=0: a row sees all of its
+    sequence's keys; window > 0: only the last `window` of those it would see.
+    max_q: the longest chunk among the sequences, if known (it chooses the
+    kernel, nothing else).  Rows of no sequence stay as they are in O and lse."""
+    L = lib()
+    s = cache_shape_of(cache)
+    dev = cache["K8"].device
+    if Q.dim() != 3:
+        raise ValueError("Q must be bf16 [T, Hq, %d]" % s.d)
+    T, Hq, _ = Q.shape
+    q_strides = _rows("Q", Q, Hq, s.d)
+    _on(dev, "Q, or a tensor of the cache", Q, cache["V8"], cache["sk"], cache["sv"])
+    _status_word(dev_status, dev)
+    batch = _batch_of(cu, kv_len, table, T, dev)
+    with _Launch(dev, stream) as at:
+        if O is None:
+            O = _empty((T, Hq, s.d), torch.bfloat16, dev)
+            at.new(O)
+        if lse is None:
+            lse = _empty((T, Hq), torch.float32, dev)
+            at.new(lse)
+        o_strides = _rows("O", O, Hq, s.d)
+        if O.shape != Q.shape or lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
+            raise ValueError("O must have Q's shape and lse be contiguous fp32 [T, Hq]")
+        _on(dev, "O, lse or workspace", O, lse, workspace)
+        if workspace is None:
+            workspace = _workspace(L.vc_attn_paged_workspace(s, Hq, batch.B, T, max_q), dev)
+            at.new(workspace)
+        _check(L.vc_attn_paged(_ptr(Q), *q_strides, Hq, s, _ptr(cache["K8"]), _ptr(cache["sk"]), _ptr(cache["V8"]),
+                               _ptr(cache["sv"]), batch, float(softmax_scale), int(causal), int(window), int(max_q),
+                               _ptr(O), *o_strides, _ptr(lse), _ptr(workspace),
+                               workspace.numel() * workspace.element_size(), _ptr(dev_status), at.handle),
+               "vc_attn_paged")
+    return O, lse
 
 
 def vc_debug_e4m3_encode(x: torch.Tensor, out=None, stream=None):

@@ -351,6 +351,137 @@ vc_status vc_attn_fwd_hybrid(const uint8_t* Q8, const float* sq, const uint8_t* 
                              float softmax_scale, float exact_margin, int vsmooth,
                              void* O, int32_t* dev_status, vc_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A paged FP8 key/value cache and the attention that reads it.
+ *
+ * vc_quantize and vc_attn_fwd take a whole sequence at once.  These entry
+ * points serve generation in chunks (a latent frame, a prompt's part, one
+ * token): the keys and values of finished tokens stay in E4M3 in the pages of
+ * a cache, new tokens are quantized as they are written, and a chunk of
+ * queries attends to everything cached, its own keys included.  The paper's
+ * pages have no counterpart; the number format is the one of vc_quantize with
+ * a scale for each token and head, because a token's neighbours in its block
+ * are not known when it is written.
+ *
+ * The cache.  K8, V8: E4M3 codes, page x head x token x channel, in any order
+ * of the first three (byte strides below, channel stride 1; the two share
+ * strides).  sk, sv: fp32 scales [page, head, token], token stride 1.  The
+ * value of a code is code * scale.  K8 and V8 may be two halves of one
+ * allocation.
+ */
+typedef struct {
+    int32_t pages;     /* pages in the pool, >= 1 */
+    int32_t page_size; /* tokens of a page: a power of two, 16 .. 4096 */
+    int32_t H, d;      /* key/value heads; channels of a head, 64 or 128 */
+    int64_t s_page, s_head, s_tok; /* strides of K8 and V8 in bytes, positive multiples of 16 */
+    int64_t t_page, t_head;        /* strides of sk and sv in floats, positive multiples of 4 */
+} vc_cache_shape;
+
+/*
+ * The batch of a call: B sequences, whose tokens of this call lie packed in
+ * the T rows of its tensors.  All arrays are device memory, read when the
+ * kernel runs (a captured graph may be replayed on new contents).
+ *   cu      int32 [B+1], non-decreasing, 0 <= cu[0], cu[B] <= T: sequence b
+ *           has the n_b = cu[b+1] - cu[b] rows from cu[b] on (n_b = 0 is
+ *           fine); rows from cu[B] on belong to no sequence.
+ *   kv_len  int32 [B]: tokens of sequence b in the cache with the n_b tokens
+ *           of this call included, 0 <= kv_len[b] <= cols * page_size.  Row
+ *           cu[b] + i is the token at position kv_len[b] - n_b + i.
+ *   table   int32 [B, cols], row stride s_table (elements, >= cols): position
+ *           p of sequence b lies in page table[b][p / page_size].  Entries
+ *           past the sequence's last page are not read as pages.  Sequences
+ *           may share pages that are only read.
+ * What breaks these rules on the device cannot be refused by the host.  It
+ * never leads outside the caller's buffers: cu is clamped to 0 .. T and
+ * kv_len to 0 .. cols * page_size, a page number outside 0 .. pages - 1
+ * stands for a page that is not there, and VC_ERR_INVALID_ARG is written to
+ * *dev_status (nullable, as for the other entry points).
+ */
+typedef struct {
+    const int32_t* cu;
+    const int32_t* kv_len;
+    const int32_t* table;
+    int32_t B, T, cols;
+    int64_t s_table;
+} vc_batch;
+
+/*
+ * Quantizes the call's keys and values into the cache.
+ *   K, V     bf16 [T, H, d], element strides s_n, s_h shared by the two
+ *            (positive multiples of 8, channel stride 1), 16-byte aligned.
+ *   For each row (token, head) x of K and of V: amax = max |x_c|,
+ *   scale = fl(amax / 448), code_c = E4M3_RNE_sat(fl(x_c * fl(448 / amax))).
+ *   A row with amax < 2^-100 is written as zeros with scale 0.  A row that
+ *   holds a NaN or an infinity is written as zeros with a NaN scale: every
+ *   query that sees the token then gets NaN, and no other does.
+ * Positions below 0 (kv_len[b] < n_b) and pages that are not there are not
+ * written and reported through *dev_status.  Cache slots of other tokens stay as
+ * they are.  Two rows of one call that name the same slot (sequences sharing
+ * the page that is written) race: out of contract.  Deterministic, no
+ * workspace.  T = 0 does nothing.
+ * Errors, before any launch: VC_ERR_INVALID_ARG (a null pointer, a misaligned
+ * K, V, K8, V8, sk or sv (16 bytes), a stride or size out of the ranges above,
+ * B < 1, T < 0, cols < 1), VC_ERR_UNSUPPORTED (d not 64 or 128, a page_size
+ * outside the list, T * H >= 2^31, cols * page_size >= 2^31); VC_ERR_CUDA if
+ * a launch fails.
+ */
+vc_status vc_cache_append(const void* K, const void* V, int64_t s_n, int64_t s_h, vc_cache_shape cache,
+                          uint8_t* K8, float* sk, uint8_t* V8, float* sv, vc_batch batch,
+                          int32_t* dev_status, vc_stream_t stream);
+
+/*
+ * Reads cached tokens back: the same rows that vc_cache_append would write
+ * (n_b = kv_len[b] reads whole sequences), K, V bf16 [T, H, d] with element
+ * strides s_n, s_h as above, each value bf16_RNE(fl(code * scale)).  A
+ * position below 0 or a page that is not there reads as zeros and is reported
+ * through *dev_status; rows of no sequence stay as they were.  Errors as
+ * vc_cache_append.
+ */
+vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk, const uint8_t* V8,
+                        const float* sv, vc_batch batch, void* K, void* V, int64_t s_n, int64_t s_h,
+                        int32_t* dev_status, vc_stream_t stream);
+
+/*
+ * Attention of the call's queries over the cache.
+ *   Q        bf16 [T, Hq, d], element strides q_sn, q_sh (positive multiples
+ *            of 8, channel stride 1), 16-byte aligned.  Hq is a multiple of
+ *            cache.H; query head h reads key/value head h / (Hq / H).
+ *   causal   1: the token at position p sees keys up to p; 0: it sees all
+ *            kv_len[b] keys (a chunk whose tokens see each other).
+ *   window   0: no lower limit; w > 0: only the last w of those keys.
+ *   With k_t = sk K8, v_t = sv V8 (values, not rounded), over the keys t that
+ *   row (i, h) sees:
+ *     s_t = softmax_scale q . k_t,  O = sum_t e^(s_t) v_t / sum_t e^(s_t),
+ *     lse = ln sum_t e^(s_t).
+ *   Sums, maxima and the scores' scaling are fp32; the probabilities enter the
+ *   product with the value codes as fp16 (relative error <= 2^-11 above 2^-14
+ *   of the row's largest), after the tokens' value scales are folded into
+ *   their exponents.  A row that sees no key gets O = 0 and lse = -inf.
+ *   Tokens of pages that are not there count as unseen (*dev_status).
+ *   max_q    the largest n_b, as far as the caller knows it (0: unknown).  It
+ *            chooses among kernels and sizes the workspace's share of each; a
+ *            wrong value costs time, never correctness.
+ *   O        bf16 [T, Hq, d], element strides o_sn, o_sh as Q's, 16-byte
+ *            aligned, not overlapping any input.  Rows of no sequence stay as
+ *            they were, in O and lse.
+ *   lse      fp32 [T, Hq] contiguous, or NULL.
+ *   workspace  >= vc_attn_paged_workspace(cache, Hq, B, T, max_q) bytes,
+ *            256-byte aligned, contents on entry ignored.  Calls that may
+ *            overlap (other streams, two captured graphs) need one each.
+ * The order of every sum is fixed by the shapes and lengths: same call, same
+ * bits.  softmax_scale <= 0 stands for 1/sqrt(d).  T = 0 does nothing.
+ * Errors as vc_cache_append, plus VC_ERR_INVALID_ARG for Hq not a positive
+ * multiple of cache.H, causal not in {0, 1}, window < 0, max_q < 0, a
+ * softmax_scale that is not finite; VC_ERR_UNSUPPORTED for T * Hq >= 2^31;
+ * VC_ERR_WORKSPACE.
+ */
+size_t vc_attn_paged_workspace(vc_cache_shape cache, int Hq, int B, int T, int max_q);
+vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
+                        const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv, vc_batch batch,
+                        float softmax_scale, int causal, int window, int max_q, void* O, int64_t o_sn,
+                        int64_t o_sh, float* lse, void* workspace, size_t workspace_bytes,
+                        int32_t* dev_status, vc_stream_t stream);
+
 /*
  * Test hook for the ExpCast byte check: runs vc_attn_fwd and additionally,
  * for the single query tile `dbg_qtile` of head-slot `dbg_bh` (= b*H + h),
