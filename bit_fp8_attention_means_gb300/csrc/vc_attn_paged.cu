@@ -1,12 +1,21 @@
 // vc_attn_paged.cu -- attention of a chunk of new tokens over the paged FP8
-// cache (vc_attn_paged).
+// cache (vc_attn_paged): the kernel for few rows, the kernel that joins partial
+// results, and the choice among kernels.
 //
-// One warp per (row, query head): each lane holds d/32 channels of q and of
-// the accumulator, and walks the keys the row sees with the running maximum
-// and sum of the softmax.  Reads the whole visible cache once per row.
+// Row (token, query head) sees keys t with scores s_t = scale q . k_t; with the
+// cached codes k8, v8 and the tokens' scales sk, sv,
+//   x_t = (q . k8_t) sk_t scale log2 e + log2 sv_t,   P_t = 2^(x_t - M),
+//   A = sum_t P_t v8_t,   l = sum_t P_t / sv_t,   O = A / l,
+//   lse = ln 2 (M + log2 l).
+// Folding sv into the exponent lets P, at most 2^8 above the running maximum M
+// of x, enter the product with the value codes as fp16 whatever the scales are;
+// E4M3 codes are fp16 numbers exactly.  A token whose values are all zero
+// (sv = 0) has log2 sv = -60 instead: it counts in l and neither in A nor,
+// beside other tokens, in M.  M moves only when the maximum has risen by more
+// than 8 (P then stays below 2^8, far inside fp16), which saves most of the
+// rescaling of A.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "vc_device.cuh"
 #include "vc_internal.h"
@@ -15,78 +24,609 @@
 namespace vc {
 namespace {
 
-constexpr int kWarps = 8;
+// ------------------------------------------------------------ few rows
+//
+// attn_few_kernel: tiles of 16 RG rows.  What bounds it is reading the cache
+// once (2d + 8 bytes per key and head), so everything else is arranged around a
+// full memory pipe: one persistent CTA on each SM, a producer warp that keeps
+// NS stages of 128 keys in flight by TMA, and eight consumer warps that share
+// nothing until an item ends.  A consumer warp owns 16 rows and every 8/RG-th
+// slice of a stage's keys, with its own M, l and A in registers; its products
+// are m16n8k16 fp16 (the tcgen05 tile of 128 rows would be mostly padding here,
+// and the tensor work of 16 rows is a third of the memory time).  Codes become
+// fp16 on the way from shared memory to registers; the channels of q . k and
+// the keys and channels of P V are permuted so that each thread reads 16
+// consecutive bytes, in an order that has no bank conflicts under the TMA
+// swizzle.
+
+constexpr int kConsumers = 8;
+constexpr int kFewThreads = (kConsumers + 1) * 32;
+constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
+constexpr float kZeroLog2 = -60.f;     // log2 sv of a token whose values are all zero
+constexpr uint64_t kTimeoutNs = 4000000000ull;
+
+struct StageInfo {
+    int flags;  // bits below
+    int key0;   // position of the stage's first key
+    int q0, n, L, h, r0, rows;
+    int box_ok;  // bit i: the stage's i-th run of min(128, page_size) keys has its page
+    int pad[7];
+};
+static_assert(sizeof(StageInfo) == 64, "one line");
+enum : int { kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8, kHead = 16, kTail = 32 };
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const PagedAttn a, const CacheView c) {
-    constexpr int E = D / 32;  // channels of a lane
+struct FewCfg {
+    static constexpr int NS = D == 128 ? 4 : 8;
+    static constexpr int TILE = kUnit * D;                       // codes of K or V in a stage
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = OFF_K + NS * TILE;
+    static constexpr int OFF_SCR = OFF_V + NS * TILE;            // [warp][16][D] accumulators at an item's end
+    static constexpr int OFF_SC = OFF_SCR + kConsumers * 16 * D * 4;  // [stage][sk | sv][128]
+    static constexpr int OFF_ML = OFF_SC + NS * 2 * kUnit * 4;   // [m | l][warp][16]
+    static constexpr int OFF_INFO = OFF_ML + 2 * kConsumers * 16 * 4;
+    static constexpr int OFF_BAR = OFF_INFO + NS * 64;           // full[NS], empty[NS], written, read
+    static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 2) * 8;
+    static constexpr int SMEM = OFF_MISC + 16 + 1024;
+    static_assert(SMEM <= 232448, "shared memory budget");
+    // Key (of 8) that column n of a score tile stands for, so that the eight
+    // lanes of a 16-byte shared-memory phase fall on different banks.
+    __device__ static int key_of(int n) {
+        if (D == 128) return (n >> 1) + 4 * (n & 1);
+        const int i = n >> 1;
+        return (n & 1) ? 2 * i + 1 - (i & 1) : 2 * i + (i & 1);
+    }
+    // Byte offset of 16-byte chunk ch of key row r under the TMA swizzle.
+    __device__ static int chunk(int r, int ch) {
+        return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+    }
+    // First of the D/8 consecutive channels that column n of every output tile stands for.
+    __device__ static int channel_of(int n) { return D == 128 ? ((n >> 1) + 4 * (n & 1)) * 16 : n * 8; }
+};
+
+// Four E4M3 codes -> four fp16.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Power of two that brings a row whose largest magnitude has the bf16 bits
+// `top` into [128, 256); 1 for rows of zeros and for rows that are not finite.
+__device__ __forceinline__ float row_factor(uint32_t top) {
+    if (top == 0u || top >= 0x7F80u) return 1.f;
+    const int e = max((int)(top >> 7), 14) - 127;
+    return __int_as_float((134 - e) << 23);
+}
+
+// Channels ch .. ch + N - 1 of row r (a (token, head) pair of its sequence), acc * inv as bf16.
+template <int N>
+__device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int r, int ch, const float (&acc)[N],
+                                          float inv) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint16_t* dst = a.O + (int64_t)(q0 + r / a.G) * a.o_sn + (int64_t)(h * a.G + r % a.G) * a.o_sh + ch;
+    if (N == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2 % (N / 2)], w[3 % (N / 2)]);
+    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c, int q0, int h, int r, float m,
+                                          float l) {
+    if (a.lse) a.lse[(int64_t)(q0 + r / a.G) * (c.H * a.G) + h * a.G + r % a.G] = lse_of(m, l);
+}
+
+template <int D, int RG>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const PagedAttn a, const CacheView c, void* ws) {
+    using C = FewCfg<D>;
+    constexpr int NS = C::NS, RT = 16 * RG;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t full = sbase + C::OFF_BAR, empty = full + 8 * NS, written = empty + 8 * NS, read = written + 8;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Partials part = partials_at(ws, RT, D);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full + 8 * s, 33);  // the stage's info and TMA bytes, and each producer lane's scales
+            mbar_init(empty + 8 * s, kConsumers);
+        }
+        mbar_init(written, kConsumers);
+        mbar_init(read, kConsumers);
+        *abort_flag = 0;
+        fence_barrier_init();
+        part.head[2 * blockIdx.x].valid = 0;
+        part.head[2 * blockIdx.x + 1].valid = 0;
+    }
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < c.B; b += kWarps * 32)
+        for (int b = threadIdx.x; b < c.B; b += kFewThreads)
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
-    const int lane = threadIdx.x & 31;
-    const int Hq = c.H * a.G;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)c.T * Hq) return;
-    const int tok = (int)(row / Hq), hq = (int)(row % Hq), h = hq / a.G;
-    int b = 0;
-    while (b + 1 < c.B && __ldg(c.cu + b + 1) <= tok) ++b;
-    const SeqInfo s = seq_info(c, b);
-    if (tok < s.q0 || tok >= s.q0 + s.n) return;
-    const int last = a.causal ? s.L - s.n + (tok - s.q0) : s.L - 1;
-    const int first = a.window ? max(0, last - a.window + 1) : 0;
-    float q[E], acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf16_bits_to_f32(a.Q[(int64_t)tok * a.q_sn + (int64_t)hq * a.q_sh + lane * E + e]);
-        acc[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int p = first; p <= last; ++p) {
-        const int pg = page_of(c, b, p);
-        if (pg < 0) {
-            if (lane == 0) flag_invalid(c.dev_status);
-            continue;
+    const Part p = plan_part<kFewThreads>(c, a, RT, blockIdx.x, gridDim.x);
+    __syncthreads();
+    if (p.g0 == p.g1) return;
+
+    if (warp == kConsumers) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            prefetch_tensormap(&tmK);
+            prefetch_tensormap(&tmV);
         }
-        const int in = p & ((1 << c.page_log2) - 1);
-        const int64_t at = (int64_t)pg * c.s_page + (int64_t)h * c.s_head + (int64_t)in * c.s_tok + lane * E;
-        const int64_t st = (int64_t)pg * c.t_page + (int64_t)h * c.t_head + in;
-        const float sk = c.sk[st], sv = c.sv[st];
-        float dot = 0.f, v[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const __half_raw kr = __nv_cvt_fp8_to_halfraw(c.K8[at + e], __NV_E4M3);
-            const __half_raw vr = __nv_cvt_fp8_to_halfraw(c.V8[at + e], __NV_E4M3);
-            dot = fmaf(q[e], __half2float(__half(kr)), dot);
-            v[e] = __half2float(__half(vr)) * sv;
+        const int box_log2 = min(c.page_log2, 7), boxes = kUnit >> box_log2;  // runs of keys in one page
+        ItemWalk w;
+        w.start(c, a, RT, p);
+        int it = 0;
+        bool more = true, ok = true;
+        while (more && ok) {
+            const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
+            for (int u = w.unit; u < w.end; ++u, ++it) {
+                const int st = it % NS, key0 = u * kUnit;
+                // page of run `lane` of the unit, -1 where no row sees it or it is not there
+                int pg = -1;
+                if (lane < boxes) {
+                    const int k = key0 + (lane << box_log2);
+                    if (k <= w.r.hi && k + (1 << box_log2) > w.r.lo) {
+                        pg = page_of(c, w.b, k);
+                        if (pg < 0) flag_invalid(c.dev_status);
+                    }
+                }
+                const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
+                if (it >= NS && !mbar_wait_warp(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    StageInfo* f = reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64);
+                    const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all &&
+                                          box_ok == (1 << boxes) - 1;
+                    f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) | (all_seen ? 0 : kMasked) |
+                               (w.head ? kHead : 0) | (w.tail ? kTail : 0);
+                    f->key0 = key0;
+                    f->q0 = w.s.q0;
+                    f->n = w.s.n;
+                    f->L = w.s.L;
+                    f->h = w.h;
+                    f->r0 = r0;
+                    f->rows = rows;
+                    f->box_ok = box_ok;
+                    mbar_arrive_expect_tx(full + 8 * st, 2 * C::TILE);
+                }
+                __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t at = (uint32_t)(lane << box_log2) * D;
+                    const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
+                    tma_load_4d(sbase + C::OFF_K + st * C::TILE + at, &tmK, 0, in, w.h, pg, full + 8 * st);
+                    tma_load_4d(sbase + C::OFF_V + st * C::TILE + at, &tmV, 0, in, w.h, pg, full + 8 * st);
+                }
+                {
+                    // four keys' scales a lane
+                    const int spg = __shfl_sync(0xffffffffu, pg, (4 * lane) >> box_log2);
+                    const int in = (key0 + 4 * lane) & ((1 << c.page_log2) - 1);
+                    const int64_t off = spg < 0 ? 0 : (int64_t)spg * c.t_page + (int64_t)w.h * c.t_head + in;
+                    const uint32_t dst = sbase + C::OFF_SC + st * (2 * kUnit * 4) + lane * 16;
+                    cp_async16(dst, c.sk + off, spg < 0 ? 0 : 16);
+                    cp_async16(dst + kUnit * 4, c.sv + off, spg < 0 ? 0 : 16);
+                    cp_async_arrive(full + 8 * st);
+                }
+            }
+            if (ok) more = w.next(c, a, RT);
         }
+        if (ok) {
+            // the stage that ends the consumers' loop
+            const int st = it % NS;
+            if (it < NS || mbar_wait_warp(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                if (lane == 0) {
+                    reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
+                }
+                __syncwarp();
+                mbar_arrive(full + 8 * st);
+                if (lane == 0) mbar_arrive(full + 8 * st);
+                ++it;
+            }
+        }
+        // this CTA's own copies land before it can exit
+        for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait(full + 8 * (j % NS), (j / NS) & 1, kTimeoutNs);
+    } else {
+        // ------------------------------------------------------------ consumers
+        constexpr int SLICES = kConsumers / RG, SLICE = kUnit / SLICES;
+        constexpr int KSTEPS = D / 16, NT = D / 8;
+        const int g = lane >> 2, tig = lane & 3;
+        const int rg = warp % RG, slice = warp / RG;
+        float* scr = reinterpret_cast<float*>(smem + C::OFF_SCR);
+        float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+        const int kr0 = C::key_of(2 * tig), kr1 = C::key_of(2 * tig + 1), krg = C::key_of(g);
+        uint32_t q[KSTEPS][4];
+        float o[NT][4], M[2], l[2], qs[2];
+        int last[2], first[2];
+        int it = 0, items = 0;
+        while (true) {
+            const int st = it % NS;
+            if (!mbar_wait_warp(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            const StageInfo* info = reinterpret_cast<const StageInfo*>(smem + C::OFF_INFO + st * 64);
+            const int flags = info->flags;
+            if (flags & kEnd) break;
+            const int key0 = info->key0, L = info->L, box_ok = info->box_ok;
+            const int q0 = info->q0, h = info->h, r0 = info->r0, rows = info->rows;
+            if (flags & kFirst) {
+                // this thread's channels of rows g and g + 8 of its 16, as the A operand:
+                // step s of 16 channels holds, per thread, 4 consecutive ones
 #pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float x = dot * sk * a.scale_log2;
-        const float m_new = fmaxf(m, x);
-        const float alpha = exp2f(m - m_new), w = exp2f(x - m_new);
-        m = m_new;
-        l = fmaf(l, alpha, w);
+                for (int e = 0; e < 2; ++e) {
+                    const int row = rg * 16 + g + 8 * e;
+                    const bool there = row < rows;
+                    const int r = r0 + (there ? row : 0), tok = r / a.G, j = r % a.G;
+                    const uint16_t* src = a.Q + (int64_t)(q0 + tok) * a.q_sn + (int64_t)(h * a.G + j) * a.q_sh + tig * 16;
+                    uint4 x[D / 32];
+                    uint32_t top = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], alpha, w * v[e]);
+                    for (int i = 0; i < D / 32; ++i) {
+                        x[i] = there ? __ldg(reinterpret_cast<const uint4*>(src + (i / 2) * 64) + (i & 1)) : make_uint4(0, 0, 0, 0);
+                        const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max(wd[k] & 0x7FFFu, (wd[k] >> 16) & 0x7FFFu));
+                    }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float f = row_factor(top);
+                    qs[e] = a.scale_log2 / f;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float lo = bf16_bits_to_f32(wd[k] & 0xFFFFu) * f;
+                            const float hi = __uint_as_float(wd[k] & 0xFFFF0000u) * f;
+                            q[2 * i + k / 2][e + 2 * (k & 1)] = pack_f16(lo, hi);
+                        }
+                    }
+                    const SeqInfo s{q0, info->n, L};
+                    last[e] = row_last(a, s, tok);
+                    first[e] = row_first(a, last[e]);
+                    M[e] = -INFINITY;
+                    l[e] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+            }
+            const uint8_t* ks = smem + C::OFF_K + st * C::TILE;
+            const uint8_t* vs = smem + C::OFF_V + st * C::TILE;
+            const float* sks = reinterpret_cast<const float*>(smem + C::OFF_SC + st * (2 * kUnit * 4));
+            const float* svs = sks + kUnit;
+#pragma unroll
+            for (int blk = 0; blk < SLICE / 16; ++blk) {
+                const int kb = slice * SLICE + blk * 16;  // 16 keys
+                float x[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[t][i] = 0.f;
+                    const int r = kb + 8 * t + krg;
+#pragma unroll
+                    for (int hf = 0; hf < D / 64; ++hf) {
+                        const uint4 kw = *reinterpret_cast<const uint4*>(ks + C::chunk(r, hf * 4 + tig));
+                        const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t b0, b1;
+                            e4m3x4_to_f16(wd[k], b0, b1);
+                            mma_f16(x[t], q[hf * 4 + k], b0, b1);
+                        }
+                    }
+                }
+                // x = (q . k8) sk scale log2 e + log2 sv
+                float isv[2][2];
+                bool keep[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = kb + 8 * t + (e ? kr1 : kr0);
+                        const float sk = sks[k], sv = svs[k];
+                        const float lv = sv == 0.f ? kZeroLog2 : lg2_approx(sv);
+                        // a NaN scale makes x NaN where it is seen; elsewhere 0 * isv has to stay 0
+                        isv[t][e] = sv == 0.f ? 0x1p60f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
+                        x[t][e] = fmaf(x[t][e] * sk, qs[0], lv);
+                        x[t][2 + e] = fmaf(x[t][2 + e] * sk, qs[1], lv);
+                        keep[t][e] = true;
+                        if (flags & kMasked) {
+                            const int pos = key0 + k;
+                            keep[t][e] = pos < L && ((box_ok >> (k >> min(c.page_log2, 7))) & 1);
+                            if (!keep[t][e] || pos > last[0] || pos < first[0]) x[t][e] = -INFINITY;
+                            if (!keep[t][e] || pos > last[1] || pos < first[1]) x[t][2 + e] = -INFINITY;
+                            if (!keep[t][e]) isv[t][e] = 0.f;  // whatever lies behind the last token
+                        }
+                    }
+                // the running maximum of each row over the 16 keys
+                float mx[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[e] = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+                }
+                const bool rise0 = mx[0] > M[0] + kStale || (M[0] == -INFINITY && mx[0] > -INFINITY);
+                const bool rise1 = mx[1] > M[1] + kStale || (M[1] == -INFINITY && mx[1] > -INFINITY);
+                if (__any_sync(0xffffffffu, rise0 || rise1)) {
+                    const float n0 = rise0 ? mx[0] : M[0], n1 = rise1 ? mx[1] : M[1];
+                    const float a0 = rise0 ? part_weight(M[0], n0) : 1.f, a1 = rise1 ? part_weight(M[1], n1) : 1.f;
+                    M[0] = n0;
+                    M[1] = n1;
+                    l[0] *= a0;
+                    l[1] *= a1;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][0] *= a0;
+                        o[j][1] *= a0;
+                        o[j][2] *= a1;
+                        o[j][3] *= a1;
+                    }
+                }
+                const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[t][e] = ex2_approx(x[t][e] - m0);
+                        x[t][2 + e] = ex2_approx(x[t][2 + e] - m1);
+                        l[0] = fmaf(x[t][e], isv[t][e], l[0]);
+                        l[1] = fmaf(x[t][2 + e], isv[t][e], l[1]);
+                    }
+                const uint32_t pa[4] = {pack_f16(x[0][0], x[0][1]), pack_f16(x[0][2], x[0][3]),
+                                        pack_f16(x[1][0], x[1][1]), pack_f16(x[1][2], x[1][3])};
+                // P V: the four keys of this thread, D/8 channels of each
+                uint32_t v[4][D / 32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = kb + 8 * (k >> 1) + ((k & 1) ? kr1 : kr0);
+                    if (D == 128) {
+                        const uint4 t4 = *reinterpret_cast<const uint4*>(vs + C::chunk(r, (g >> 1) + 4 * (g & 1)));
+                        v[k][0] = t4.x;
+                        v[k][1] = t4.y;
+                        v[k][2 % (D / 32)] = t4.z;
+                        v[k][3 % (D / 32)] = t4.w;
+                    } else {
+                        const uint2 t2 = *reinterpret_cast<const uint2*>(vs + C::chunk(r, g >> 1) + (g & 1) * 8);
+                        v[k][0] = t2.x;
+                        v[k][1] = t2.y;
+                    }
+                    // what lies behind the last token may be any bits: not a factor
+                    if ((flags & kMasked) && !keep[k >> 1][k & 1]) {
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) v[k][i] = 0u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t b0[4], b1[4];
+                    e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x5140u), b0[0], b0[1]);
+                    e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x7362u), b0[2], b0[3]);
+                    e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x5140u), b1[0], b1[1]);
+                    e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x7362u), b1[2], b1[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_f16(o[4 * i + k], pa, b0[k], b1[k]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * st);
+            ++it;
+            if (!(flags & kLast)) continue;
+
+            // ------------------------------------------------------------ the item's end
+            // the accumulators are free to overwrite once the last item's were read
+            if (items > 0 && !mbar_wait_warp(read, (items - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                float* dst = scr + ((size_t)warp * 16 + g + 8 * e) * D;
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+                    for (int j = 0; j < NT; j += 4)
+                        *reinterpret_cast<float4*>(dst + C::channel_of(2 * tig + cc) + j) =
+                            make_float4(o[j][2 * e + cc], o[j + 1][2 * e + cc], o[j + 2][2 * e + cc], o[j + 3][2 * e + cc]);
+                if (tig == 0) {
+                    ml[warp * 16 + g + 8 * e] = M[e];
+                    ml[kConsumers * 16 + warp * 16 + g + 8 * e] = l[e];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(written);
+            if (!mbar_wait_warp(written, items & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            const bool split = flags & (kHead | kTail);
+            const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
+            for (int i = threadIdx.x; i < RT * (D / 8); i += kConsumers * 32) {
+                const int row = i / (D / 8), ch = (i % (D / 8)) * 8;
+                if (row >= rows) break;
+                float m = -INFINITY, lsum = 0.f, acc[8];
+#pragma unroll
+                for (int s = 0; s < SLICES; ++s) m = fmaxf(m, ml[(s * RG + row / 16) * 16 + row % 16]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll
+                for (int s = 0; s < SLICES; ++s) {
+                    const int at = (s * RG + row / 16) * 16 + row % 16;
+                    const float w = part_weight(ml[at], m);
+                    lsum = fmaf(w, ml[kConsumers * 16 + at], lsum);
+                    const float4 u0 = *reinterpret_cast<const float4*>(scr + (size_t)at * D + ch);
+                    const float4 u1 = *reinterpret_cast<const float4*>(scr + (size_t)at * D + ch + 4);
+                    const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, u[k], acc[k]);
+                }
+                if (split) {
+                    float* dst = part.o + ((size_t)slot * RT + row) * D + ch;
+                    *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                    if (ch == 0) {
+                        part.m[(size_t)slot * RT + row] = m;
+                        part.l[(size_t)slot * RT + row] = lsum;
+                    }
+                } else {
+                    store_row<8>(a, q0, h, r0 + row, ch, acc, inverse_sum(lsum));
+                    if (ch == 0) store_lse(a, c, q0, h, r0 + row, m, lsum);
+                }
+            }
+            if (split && threadIdx.x == 0)
+                part.head[slot] = PartHeader{1, (flags & kTail) ? 0 : 1, q0, h, r0, rows};
+            __syncwarp();
+            if (lane == 0) mbar_arrive(read);
+            ++items;
+        }
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        a.O[(int64_t)tok * a.o_sn + (int64_t)hq * a.o_sh + lane * E + e] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(acc[e] * inv));
-    if (a.lse && lane == 0)
-        a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
+}
+
+// ------------------------------------------------------------ joining
+//
+// join_kernel: block i takes the item that begins in CTA i's part and goes on
+// in the next ones, and adds their parts in key order; the blocks also share
+// out the rows whose tiles see no key at all, which no CTA had.  A part of 16
+// rows is 8 KB, so this is a launch and a few L2 round trips.
+constexpr int kJoinThreads = 256;
+
+template <int D, int RT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn a, const CacheView c, void* ws, int parts) {
+    const Partials part = partials_at(ws, RT, D);
+    const int i0 = 2 * blockIdx.x + 1;
+    const PartHeader hd = part.head[i0];
+    if (hd.valid) {
+        // parts of CTAs blockIdx.x .. end - 1; with fewer units than CTAs some of them are empty
+        int end = blockIdx.x + 1;
+        while (end < parts) {
+            const PartHeader next = part.head[2 * end];
+            ++end;
+            if (next.valid && next.last) break;
+        }
+        for (int i = threadIdx.x; i < hd.rows * (D / 4); i += kJoinThreads) {
+            const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+            float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = blockIdx.x; k < end; ++k) {
+                const int slot = k == (int)blockIdx.x ? i0 : 2 * k;
+                if (part.head[slot].valid) m = fmaxf(m, part.m[(size_t)slot * RT + row]);
+            }
+            for (int k = blockIdx.x; k < end; ++k) {
+                const int slot = k == (int)blockIdx.x ? i0 : 2 * k;
+                if (!part.head[slot].valid) continue;
+                const size_t at = (size_t)slot * RT + row;
+                const float w = part_weight(part.m[at], m);
+                l = fmaf(w, part.l[at], l);
+                const float4 u = *reinterpret_cast<const float4*>(part.o + at * D + ch);
+                acc[0] = fmaf(w, u.x, acc[0]);
+                acc[1] = fmaf(w, u.y, acc[1]);
+                acc[2] = fmaf(w, u.z, acc[2]);
+                acc[3] = fmaf(w, u.w, acc[3]);
+            }
+            store_row<4>(a, hd.q0, hd.h, hd.r0 + row, ch, acc, inverse_sum(l));
+            if (ch == 0) store_lse(a, c, hd.q0, hd.h, hd.r0 + row, m, l);
+        }
+    }
+    const float none[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+        const SeqInfo s = seq_info(c, b);
+        const int nt = seq_tiles(a, s, RT);
+        for (int t = 0; t < nt; ++t) {
+            if (item_range(a, s, t, RT).units()) continue;
+            const int r0 = t * RT, rows = min(RT, s.n * a.G - r0);
+            for (int i = threadIdx.x; i < c.H * rows * (D / 4); i += kJoinThreads) {
+                const int h = i / (rows * (D / 4)), row = i / (D / 4) % rows, ch = (i % (D / 4)) * 4;
+                store_row<4>(a, s.q0, h, r0 + row, ch, none, 0.f);
+                if (ch == 0) store_lse(a, c, s.q0, h, r0 + row, 0.f, 0.f);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ host side
+
+// K8 or V8 as a tensor [page][head][token][channel] of bytes, in boxes of up to 128 tokens.
+bool make_cache_map(CUtensorMap* map, const uint8_t* base, int d, const CacheView& c) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled_fn();
+    if (!enc) return false;
+    const int page = 1 << c.page_log2;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)c.H, (cuuint64_t)c.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.s_tok, (cuuint64_t)c.s_head, (cuuint64_t)c.s_page};
+    const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)(page < kUnit ? page : kUnit), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a tile, by the rows of the longest chunk as far as the caller told.
+int tile_rows(int G, int B, int T, int max_q) {
+    const int64_t q = max_q > 0 ? max_q : ((int64_t)T + B - 1) / B;
+    const int64_t rows = q * G;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+template <int D, int RG>
+vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
+                     cudaStream_t st) {
+    auto kern = attn_few_kernel<D, RG>;
+    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
+    if (s != VC_OK) return s;
+    kern<<<kMaxCtas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
+    if ((s = cuda_status(cudaGetLastError())) != VC_OK) return s;
+    join_kernel<D, 16 * RG><<<kMaxCtas, kJoinThreads, 0, st>>>(a, c, ws, kMaxCtas);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+vc_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
+                   cudaStream_t st) {
+    switch (tile_rows(a.G, c.B, c.T, a.max_q)) {
+        case 16: return launch_few<D, 1>(mk, mv, a, c, ws, st);
+        case 32: return launch_few<D, 2>(mk, mv, a, c, ws, st);
+        default: return launch_few<D, 4>(mk, mv, a, c, ws, st);
+    }
 }
 
 }  // namespace
 
-size_t attn_paged_workspace(const vc_cache_shape&, int, int, int, int) { return 0; }
+size_t attn_paged_workspace(const vc_cache_shape& c, int Hq, int B, int T, int max_q) {
+    return partials_bytes(tile_rows(Hq / c.H, B, T, max_q), c.d);
+}
 
-vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void*, cudaStream_t st) {
-    const unsigned grid = (unsigned)(((int64_t)c.T * c.H * a.G + kWarps - 1) / kWarps);
-    if (d == 128) attn_rows_kernel<128><<<grid, kWarps * 32, 0, st>>>(a, c);
-    else attn_rows_kernel<64><<<grid, kWarps * 32, 0, st>>>(a, c);
-    return cuda_status(cudaGetLastError());
+vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void* ws, cudaStream_t st) {
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, c.K8, d, c) || !make_cache_map(&mv, c.V8, d, c)) return VC_ERR_CUDA;
+    return d == 128 ? launch_d<128>(mk, mv, a, c, ws, st) : launch_d<64>(mk, mv, a, c, ws, st);
 }
 
 }  // namespace vc
