@@ -30,8 +30,11 @@ namespace {
 // once (2d + 8 bytes per key and head), so everything else is arranged around a
 // full memory pipe: one persistent CTA on each SM, a producer warp that keeps
 // NS stages of 128 keys in flight by TMA, and eight consumer warps that share
-// nothing until an item ends.  A consumer warp owns 16 rows and every 8/RG-th
-// slice of a stage's keys, with its own M, l and A in registers; its products
+// nothing until an item ends.  A consumer warp owns 16 rows and 32 keys of a
+// stage (RG = 1: of every other stage; RG = 4: two such blocks), with its own
+// M, l and A in registers; 32 keys give four independent chains of products to
+// hide their latency (16 keys, in twice as many warps a stage: 260 us against
+// XX us for one token of 96 sequences).  The products
 // are m16n8k16 fp16 (the tcgen05 tile of 128 rows would be mostly padding here,
 // and the tensor work of 16 rows is a third of the memory time).  Codes become
 // fp16 on the way from shared memory to registers; the channels of q . k and
@@ -40,7 +43,9 @@ namespace {
 // swizzle.
 
 constexpr int kConsumers = 8;
-constexpr int kFewThreads = (kConsumers + 1) * 32;
+constexpr int kFewThreads = (kConsumers + 4) * 32;  // the producer's warpgroup has three idle warps
+// 384 threads start with 168 registers each; 2 x 128 x 216 + 128 x 64 = 63,488 fit into those 64,512
+constexpr int kFewRegsUp = 216, kFewRegsDown = 64;
 constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
 constexpr float kZeroLog2 = -60.f;     // log2 sv of a token whose values are all zero
 constexpr uint64_t kTimeoutNs = 4000000000ull;
@@ -177,9 +182,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
     const Part p = plan_part<kFewThreads>(c, a, RT, blockIdx.x, gridDim.x);
     __syncthreads();
+    launch_dependents();
     if (p.g0 == p.g1) return;
 
-    if (warp == kConsumers) {
+    if (warp > kConsumers) {
+        regs_down<kFewRegsDown>();
+    } else if (warp == kConsumers) {
+        regs_down<kFewRegsDown>();
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             prefetch_tensormap(&tmK);
@@ -261,12 +270,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait(full + 8 * (j % NS), (j / NS) & 1, kTimeoutNs);
     } else {
         // ------------------------------------------------------------ consumers
-        constexpr int SLICES = kConsumers / RG, SLICE = kUnit / SLICES;
+        regs_up<kFewRegsUp>();
+        constexpr int SLICES = RG == 4 ? 2 : 4, SLICE = kUnit / SLICES;  // of a stage's keys
+        constexpr int SETS = kConsumers / (RG * SLICES);                 // sets of warps that take turns
         constexpr int KSTEPS = D / 16, NT = D / 8;
         const int g = lane >> 2, tig = lane & 3;
-        const int rg = warp % RG, slice = warp / RG;
+        const int rg = warp % RG, slice = warp / RG % SLICES, set = warp / (RG * SLICES);
         float* scr = reinterpret_cast<float*>(smem + C::OFF_SCR);
         float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+        const int box_log2 = min(c.page_log2, 7);
         const int kr0 = C::key_of(2 * tig), kr1 = C::key_of(2 * tig + 1), krg = C::key_of(g);
         uint32_t q[KSTEPS][4];
         float o[NT][4], M[2], l[2], qs[2];
@@ -327,32 +339,40 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const uint8_t* vs = smem + C::OFF_V + st * C::TILE;
             const float* sks = reinterpret_cast<const float*>(smem + C::OFF_SC + st * (2 * kUnit * 4));
             const float* svs = sks + kUnit;
+            if (SETS == 1 || it % SETS == set)
+#pragma unroll 1
+            for (int blk = 0; blk < SLICE / 32; ++blk) {
+                const int kb = slice * SLICE + blk * 32;  // 32 keys
+                float x[4][4];
 #pragma unroll
-            for (int blk = 0; blk < SLICE / 16; ++blk) {
-                const int kb = slice * SLICE + blk * 16;  // 16 keys
-                float x[2][4];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[t][i] = 0.f;
-                    const int r = kb + 8 * t + krg;
 #pragma unroll
-                    for (int hf = 0; hf < D / 64; ++hf) {
-                        const uint4 kw = *reinterpret_cast<const uint4*>(ks + C::chunk(r, hf * 4 + tig));
-                        const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    uint32_t kw[4][4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                    for (int t = 0; t < 4; ++t) {
+                        const uint4 w4 = *reinterpret_cast<const uint4*>(ks + C::chunk(kb + 8 * t + krg, hf * 4 + tig));
+                        kw[t][0] = w4.x;
+                        kw[t][1] = w4.y;
+                        kw[t][2] = w4.z;
+                        kw[t][3] = w4.w;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
                             uint32_t b0, b1;
-                            e4m3x4_to_f16(wd[k], b0, b1);
+                            e4m3x4_to_f16(kw[t][k], b0, b1);
                             mma_f16(x[t], q[hf * 4 + k], b0, b1);
                         }
-                    }
                 }
                 // x = (q . k8) sk scale log2 e + log2 sv
-                float isv[2][2];
-                bool keep[2][2];
+                float isv[4][2];
+                uint32_t keep = 0xFFu;  // bit 2t + e: the key exists
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int k = kb + 8 * t + (e ? kr1 : kr0);
@@ -362,25 +382,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         isv[t][e] = sv == 0.f ? 0x1p60f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
                         x[t][e] = fmaf(x[t][e] * sk, qs[0], lv);
                         x[t][2 + e] = fmaf(x[t][2 + e] * sk, qs[1], lv);
-                        keep[t][e] = true;
-                        if (flags & kMasked) {
-                            const int pos = key0 + k;
-                            keep[t][e] = pos < L && ((box_ok >> (k >> min(c.page_log2, 7))) & 1);
-                            if (!keep[t][e] || pos > last[0] || pos < first[0]) x[t][e] = -INFINITY;
-                            if (!keep[t][e] || pos > last[1] || pos < first[1]) x[t][2 + e] = -INFINITY;
-                            if (!keep[t][e]) isv[t][e] = 0.f;  // whatever lies behind the last token
-                        }
                     }
-                // the running maximum of each row over the 16 keys
+                if (flags & kMasked) {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int k = kb + 8 * t + (e ? kr1 : kr0), pos = key0 + k;
+                            const bool there = pos < L && ((box_ok >> (k >> box_log2)) & 1);
+                            if (!there || pos > last[0] || pos < first[0]) x[t][e] = -INFINITY;
+                            if (!there || pos > last[1] || pos < first[1]) x[t][2 + e] = -INFINITY;
+                            if (!there) {  // whatever lies behind the last token
+                                isv[t][e] = 0.f;
+                                keep &= ~(1u << (2 * t + e));
+                            }
+                        }
+                }
+                // the running maximum of each row over the 32 keys
                 float mx[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+                    mx[e] = fmaxf(max3(x[0][2 * e], x[0][2 * e + 1], x[1][2 * e]),
+                                  max3(x[1][2 * e + 1], x[2][2 * e], x[2][2 * e + 1]));
+                    mx[e] = max3(mx[e], x[3][2 * e], x[3][2 * e + 1]);
                     mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
                     mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
                 }
-                const bool rise0 = mx[0] > M[0] + kStale || (M[0] == -INFINITY && mx[0] > -INFINITY);
-                const bool rise1 = mx[1] > M[1] + kStale || (M[1] == -INFINITY && mx[1] > -INFINITY);
+                const bool rise0 = mx[0] > M[0] + kStale, rise1 = mx[1] > M[1] + kStale;
                 if (__any_sync(0xffffffffu, rise0 || rise1)) {
                     const float n0 = rise0 ? mx[0] : M[0], n1 = rise1 ? mx[1] : M[1];
                     const float a0 = rise0 ? part_weight(M[0], n0) : 1.f, a1 = rise1 ? part_weight(M[1], n1) : 1.f;
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
                 const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         x[t][e] = ex2_approx(x[t][e] - m0);
@@ -406,39 +434,45 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         l[0] = fmaf(x[t][e], isv[t][e], l[0]);
                         l[1] = fmaf(x[t][2 + e], isv[t][e], l[1]);
                     }
-                const uint32_t pa[4] = {pack_f16(x[0][0], x[0][1]), pack_f16(x[0][2], x[0][3]),
-                                        pack_f16(x[1][0], x[1][1]), pack_f16(x[1][2], x[1][3])};
-                // P V: the four keys of this thread, D/8 channels of each
-                uint32_t v[4][D / 32];
+                // P V, 16 keys at a time: the four keys of this thread, D/8 channels of each
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = kb + 8 * (k >> 1) + ((k & 1) ? kr1 : kr0);
-                    if (D == 128) {
-                        const uint4 t4 = *reinterpret_cast<const uint4*>(vs + C::chunk(r, (g >> 1) + 4 * (g & 1)));
-                        v[k][0] = t4.x;
-                        v[k][1] = t4.y;
-                        v[k][2 % (D / 32)] = t4.z;
-                        v[k][3 % (D / 32)] = t4.w;
-                    } else {
-                        const uint2 t2 = *reinterpret_cast<const uint2*>(vs + C::chunk(r, g >> 1) + (g & 1) * 8);
-                        v[k][0] = t2.x;
-                        v[k][1] = t2.y;
+                for (int hb = 0; hb < 2; ++hb) {
+                    const float(&y0)[4] = x[2 * hb];
+                    const float(&y1)[4] = x[2 * hb + 1];
+                    const uint32_t pa[4] = {pack_f16(y0[0], y0[1]), pack_f16(y0[2], y0[3]), pack_f16(y1[0], y1[1]),
+                                            pack_f16(y1[2], y1[3])};
+                    uint32_t v[4][D / 32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = kb + 16 * hb + 8 * (k >> 1) + ((k & 1) ? kr1 : kr0);
+                        if (D == 128) {
+                            const uint4 t4 = *reinterpret_cast<const uint4*>(vs + C::chunk(r, (g >> 1) + 4 * (g & 1)));
+                            v[k][0] = t4.x;
+                            v[k][1] = t4.y;
+                            v[k][2 % (D / 32)] = t4.z;
+                            v[k][3 % (D / 32)] = t4.w;
+                        } else {
+                            const uint2 t2 = *reinterpret_cast<const uint2*>(vs + C::chunk(r, g >> 1) + (g & 1) * 8);
+                            v[k][0] = t2.x;
+                            v[k][1] = t2.y;
+                        }
+                        // what lies behind the last token may be any bits: not a factor
+                        if (flags & kMasked) {
+                            const uint32_t on = (keep >> (4 * hb + k)) & 1u ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) v[k][i] &= on;
+                        }
                     }
-                    // what lies behind the last token may be any bits: not a factor
-                    if ((flags & kMasked) && !keep[k >> 1][k & 1]) {
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) v[k][i] = 0u;
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t b0[4], b1[4];
+                        e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x5140u), b0[0], b0[1]);
+                        e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x7362u), b0[2], b0[3]);
+                        e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x5140u), b1[0], b1[1]);
+                        e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x7362u), b1[2], b1[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_f16(o[4 * i + k], pa, b0[k], b1[k]);
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t b0[4], b1[4];
-                    e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x5140u), b0[0], b0[1]);
-                    e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x7362u), b0[2], b0[3]);
-                    e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x5140u), b1[0], b1[1]);
-                    e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x7362u), b1[2], b1[3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_f16(o[4 * i + k], pa, b0[k], b1[k]);
                 }
             }
             __syncwarp();
@@ -475,11 +509,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if (row >= rows) break;
                 float m = -INFINITY, lsum = 0.f, acc[8];
 #pragma unroll
-                for (int s = 0; s < SLICES; ++s) m = fmaxf(m, ml[(s * RG + row / 16) * 16 + row % 16]);
+                for (int s = 0; s < kConsumers / RG; ++s) m = fmaxf(m, ml[(s * RG + row / 16) * 16 + row % 16]);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) acc[k] = 0.f;
 #pragma unroll
-                for (int s = 0; s < SLICES; ++s) {
+                for (int s = 0; s < kConsumers / RG; ++s) {
                     const int at = (s * RG + row / 16) * 16 + row % 16;
                     const float w = part_weight(ml[at], m);
                     lsum = fmaf(w, ml[kConsumers * 16 + at], lsum);
@@ -522,28 +556,30 @@ constexpr int kJoinThreads = 256;
 
 template <int D, int RT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn a, const CacheView c, void* ws, int parts) {
+    __shared__ int s_end;
     const Partials part = partials_at(ws, RT, D);
-    const int i0 = 2 * blockIdx.x + 1;
+    const int mine = blockIdx.x, i0 = 2 * mine + 1;
+    if (threadIdx.x == 0) s_end = parts;
+    __syncthreads();
+    wait_for_primary();
     const PartHeader hd = part.head[i0];
     if (hd.valid) {
-        // parts of CTAs blockIdx.x .. end - 1; with fewer units than CTAs some of them are empty
-        int end = blockIdx.x + 1;
-        while (end < parts) {
-            const PartHeader next = part.head[2 * end];
-            ++end;
-            if (next.valid && next.last) break;
+        // the parts of CTAs mine .. end - 1: the first later one that has the item's end
+        for (int k = mine + 1 + threadIdx.x; k < parts; k += kJoinThreads) {
+            const PartHeader next = part.head[2 * k];
+            if (next.valid && next.last) atomicMin(&s_end, k + 1);
         }
+        __syncthreads();
+        const int end = s_end;
         for (int i = threadIdx.x; i < hd.rows * (D / 4); i += kJoinThreads) {
             const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
-            float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int k = blockIdx.x; k < end; ++k) {
-                const int slot = k == (int)blockIdx.x ? i0 : 2 * k;
-                if (part.head[slot].valid) m = fmaxf(m, part.m[(size_t)slot * RT + row]);
-            }
-            for (int k = blockIdx.x; k < end; ++k) {
-                const int slot = k == (int)blockIdx.x ? i0 : 2 * k;
-                if (!part.head[slot].valid) continue;
-                const size_t at = (size_t)slot * RT + row;
+            const float* pm = part.m + row;
+            float m = pm[(size_t)i0 * RT], l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int k = mine + 1; k < end; ++k) m = fmaxf(m, pm[(size_t)(2 * k) * RT]);
+#pragma unroll 4
+            for (int k = mine; k < end; ++k) {
+                const size_t at = (size_t)(k == mine ? i0 : 2 * k) * RT + row;
                 const float w = part_weight(part.m[at], m);
                 l = fmaf(w, part.l[at], l);
                 const float4 u = *reinterpret_cast<const float4*>(part.o + at * D + ch);
@@ -595,16 +631,38 @@ int tile_rows(int G, int B, int T, int max_q) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
+// CTAs of a call: as many as there can be units, one on each SM at most.
+int part_count(const PagedAttn& a, const CacheView& c, int RT) {
+    const int64_t tiles = (int64_t)c.T * a.G / RT + c.B;
+    const int64_t units = (((int64_t)c.cols << c.page_log2) + kUnit - 1) / kUnit;
+    if (tiles * c.H >= kMaxCtas || units >= kMaxCtas) return kMaxCtas;
+    return (int)(tiles * c.H * units < kMaxCtas ? tiles * c.H * units : kMaxCtas);
+}
+
+template <int D, int RT>
+vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int parts, cudaStream_t st) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(parts);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D, RT>, a, c, ws, parts));
+}
+
 template <int D, int RG>
 vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
                      cudaStream_t st) {
     auto kern = attn_few_kernel<D, RG>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
     if (s != VC_OK) return s;
-    kern<<<kMaxCtas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
+    const int ctas = part_count(a, c, 16 * RG);
+    kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
     if ((s = cuda_status(cudaGetLastError())) != VC_OK) return s;
-    join_kernel<D, 16 * RG><<<kMaxCtas, kJoinThreads, 0, st>>>(a, c, ws, kMaxCtas);
-    return cuda_status(cudaGetLastError());
+    return launch_join<D, 16 * RG>(a, c, ws, ctas, st);
 }
 
 template <int D>

@@ -46,8 +46,8 @@ __device__ __forceinline__ int page_of(const CacheView& c, int b, int p) {
 // head) pairs, token by token; an item is a tile of RT of them, and its work is
 // the units of 128 keys that at least one of its rows sees.  All units of a
 // call stand in one order (sequence, head, tile, key) and CTA i of C takes the
-// i-th of C equal parts, so lengths that differ, few rows and long caches keep
-// all SMs equally busy.  An item cut by the border of two CTAs leaves partial
+// i-th of C equal parts (with fewer units than CTAs, one unit each), so lengths
+// that differ, few rows and long caches keep all SMs equally busy.  An item cut by the border of two CTAs leaves partial
 // results (running maximum, sum, accumulator) in the workspace, which a second
 // kernel joins in key order.
 
@@ -118,11 +118,15 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     int64_t total = 0;
     for (int w = 0; w < NT / 32; ++w) total += warp_sum[w];
     Part p;
-    p.g0 = total * part / parts;
-    p.g1 = total * (part + 1) / parts;
+    if (total < parts) parts = (int)total;  // no empty part between two others
     p.b = 0;
     p.off = 0;
-    if (p.g0 == p.g1) return p;
+    if (part >= parts) {
+        p.g0 = p.g1 = 0;
+        return p;
+    }
+    p.g0 = total * part / parts;
+    p.g1 = total * (part + 1) / parts;
     int64_t before = 0;  // units of the sequences of earlier rounds
     for (int b0 = 0; b0 < c.B; b0 += NT) {
         const int b = b0 + threadIdx.x;

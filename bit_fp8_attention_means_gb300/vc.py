@@ -324,86 +324,97 @@ def alloc_cache(pages, page_size, H, d, device):
     return c
 
 
-def _stride(t, dim, unit):
-    """Stride of a dimension; one of a single element may have any, so it gets a legal one."""
-    return t.stride(dim) if t.shape[dim] > 1 else unit
+def _cache_parts(cache):
+    """Checks a dict of K8, sk, V8, sv (see alloc_cache): its vc_cache_shape, the four pointers, the device's index."""
+    K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
+    shape, k, t = tuple(K8.shape), K8.stride(), sk.stride()
+    if len(shape) != 4 or K8.dtype != torch.uint8 or V8.dtype != torch.uint8 or tuple(V8.shape) != shape:
+        raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
+    if sk.dtype != torch.float32 or sv.dtype != torch.float32 or tuple(sk.shape) != shape[:3] or \
+            tuple(sv.shape) != shape[:3]:
+        raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
+    v, u = V8.stride(), sv.stride()
+    pages, H, page, d = shape
+    if pages < 2 or H < 2:  # a dimension of one element may have any stride: it gets a legal one
+        k, v = _plain_strides(shape, k, d), _plain_strides(shape, v, d)
+        t, u = _plain_strides(shape[:3], t, page), _plain_strides(shape[:3], u, page)
+    if v != k or u != t:
+        raise ValueError("K8 and V8, and sk and sv, must share strides")
+    if (k[3] != 1 or t[2] != 1) and min(shape) > 0:
+        raise ValueError("channels and the scales' tokens must be contiguous")
+    dev = K8.get_device()
+    if V8.get_device() != dev or sk.get_device() != dev or sv.get_device() != dev:
+        raise ValueError("the cache's tensors are on different devices")
+    return (VcCacheShape(pages, page, H, d, k[0], k[1], k[2], t[0], t[1]),
+            (K8.data_ptr(), sk.data_ptr(), V8.data_ptr(), sv.data_ptr()), dev)
+
+
+def _plain_strides(shape, strides, unit):
+    """`strides`, with `unit` in the place of an outer dimension's of one element."""
+    return tuple(s if n > 1 or i >= 2 else unit for i, (n, s) in enumerate(zip(shape, strides)))
 
 
 def cache_shape_of(cache) -> VcCacheShape:
     """The vc_cache_shape of a dict of K8, sk, V8, sv (see alloc_cache)."""
-    K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
-    if K8.dim() != 4 or K8.dtype != torch.uint8 or V8.dtype != torch.uint8 or V8.shape != K8.shape:
-        raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
-    if sk.dtype != torch.float32 or sv.dtype != torch.float32 or sk.shape != K8.shape[:3] or sv.shape != sk.shape:
-        raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
-    pages, H, page, d = K8.shape
-    s = tuple(_stride(K8, i, d) for i in range(3))
-    t = tuple(_stride(sk, i, page) for i in range(2))
-    if tuple(_stride(V8, i, d) for i in range(3)) != s or tuple(_stride(sv, i, page) for i in range(2)) != t:
-        raise ValueError("K8 and V8, and sk and sv, must share strides")
-    if min(K8.shape) and (_stride(K8, 3, 1), _stride(V8, 3, 1), _stride(sk, 2, 1), _stride(sv, 2, 1)) != (1,) * 4:
-        raise ValueError("channels and the scales' tokens must be contiguous")
-    return VcCacheShape(pages, page, H, d, s[0], s[1], s[2], t[0], t[1])
+    return _cache_parts(cache)[0]
 
 
 def _batch_of(cu, kv_len, table, T, dev) -> VcBatch:
-    for name, t, dim in (("cu", cu, 1), ("kv_len", kv_len, 1), ("table", table, 2)):
-        if t.dtype != torch.int32 or t.dim() != dim:
-            raise ValueError("%s must be an int32 tensor of %d dimension(s)" % (name, dim))
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError("%s must be contiguous in its last dimension" % name)
-        _on(dev, name, t)
-    B, cols = table.shape
-    if cu.shape[0] != B + 1 or kv_len.shape[0] != B:
+    i32 = torch.int32
+    n, B, c = tuple(cu.shape), tuple(kv_len.shape), tuple(table.shape)
+    if cu.dtype != i32 or kv_len.dtype != i32 or table.dtype != i32 or len(n) != 1 or len(B) != 1 or len(c) != 2:
+        raise ValueError("cu [B+1], kv_len [B] and table [B, cols] must be int32")
+    if n[0] != c[0] + 1 or B[0] != c[0]:
         raise ValueError("cu, kv_len and table disagree on the number of sequences")
-    return VcBatch(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), B, T, cols, _stride(table, 0, max(cols, 1)))
+    s, cols = table.stride(), c[1]
+    if cu.stride()[0] != 1 or (kv_len.stride()[0] != 1 and c[0] > 1) or (s[1] != 1 and cols > 1):
+        raise ValueError("cu, kv_len and the rows of table must be contiguous")
+    if cu.get_device() != dev or kv_len.get_device() != dev or table.get_device() != dev:
+        raise ValueError("cu, kv_len or table is not on the cache's device")
+    return VcBatch(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), c[0], T, cols, s[0] if c[0] > 1 else max(cols, 1))
 
 
-def _on(dev, name, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, the cache on %s" % (name, t.device, dev))
-
-
-def _rows(name, t, H, d):
-    """Checks a bf16 [T, H, d] tensor with contiguous channels; its row and head strides."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+def _rows(name, t, H, d, dev):
+    """Checks a bf16 [T, H, d] tensor with contiguous channels: its row and head strides."""
+    shape, s = tuple(t.shape), t.stride()
+    if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != H or shape[2] != d:
         raise ValueError("%s must be bf16 [T, %d, %d]" % (name, H, d))
-    if t.stride(2) != 1:
+    if s[2] != 1:
         raise ValueError("%s must have contiguous channels" % name)
-    return _stride(t, 0, H * d), _stride(t, 1, d)
+    if t.get_device() != dev:
+        raise ValueError("%s is not on the cache's device" % name)
+    return s[0] if shape[0] > 1 else H * d, s[1] if H > 1 else d
 
 
-def _status_word(dev_status, dev):
-    if dev_status is not None and dev_status.dtype != torch.int32:
-        raise ValueError("dev_status must be int32")
-    _on(dev, "dev_status", dev_status)
+def _status_ptr(dev_status, dev):
+    if dev_status is None:
+        return None
+    if dev_status.dtype != torch.int32 or dev_status.numel() < 1 or dev_status.get_device() != dev:
+        raise ValueError("dev_status must be int32 on the cache's device")
+    return dev_status.data_ptr()
 
 
-class _Launch:
-    """The device and stream of a call: the cache's device is made current, and tensors made here are
-    kept for `stream` where that is not the one they were made on."""
+def _on_device(dev, stream, fn, args, where, made):
+    """Calls fn(*args, stream) with device `dev` current, and keeps the tensors in `made` (made here, on
+    the current stream) for a stream that is not the current one."""
+    here = torch.cuda.current_device()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    try:
+        current = torch._C._cuda_getCurrentRawStream(dev)
+        handle = current if stream is None else stream.cuda_stream
+        _check(fn(*args, handle), where)
+    finally:
+        if here != dev:
+            torch.cuda.set_device(here)
+    if handle != current:
+        for t in made:
+            t.record_stream(stream)
 
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError("the cache must be on a CUDA device")
-        self._guard = torch.cuda.device(dev)
-        self._dev, self._given = dev, stream
 
-    def __enter__(self):
-        self._guard.__enter__()
-        self.current = torch.cuda.current_stream(self._dev)
-        self.stream = self._given if self._given is not None else self.current
-        self.handle = ctypes.c_void_p(self.stream.cuda_stream)
-        return self
-
-    def __exit__(self, *e):
-        return self._guard.__exit__(*e)
-
-    def new(self, *tensors):
-        if self.stream.cuda_stream != self.current.cuda_stream:
-            for t in tensors:
-                t.record_stream(self.stream)
+def _need_cuda(dev):
+    if dev < 0:
+        raise ValueError("the cache must be on a CUDA device")
 
 
 def vc_cache_append(K, V, cache, cu, kv_len, table, dev_status=None, stream=None):
@@ -413,18 +424,15 @@ def vc_cache_append(K, V, cache, cu, kv_len, table, dev_status=None, stream=None
     rows cu[b] .. cu[b+1]-1 of the call and kv_len[b] tokens in the cache with
     these included; position p lies in page table[b, p // page_size]."""
     L = lib()
-    s = cache_shape_of(cache)
-    strides = _rows("K", K, s.H, s.d)
-    if V.shape != K.shape or _rows("V", V, s.H, s.d) != strides:
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    strides = _rows("K", K, s.H, s.d, dev)
+    if V.shape != K.shape or _rows("V", V, s.H, s.d, dev) != strides:
         raise ValueError("K and V must share shape and strides")
-    dev = cache["K8"].device
-    _on(dev, "K, V, or a tensor of the cache", K, V, cache["V8"], cache["sk"], cache["sv"])
-    _status_word(dev_status, dev)
     batch = _batch_of(cu, kv_len, table, K.shape[0], dev)
-    with _Launch(dev, stream) as at:
-        _check(L.vc_cache_append(_ptr(K), _ptr(V), *strides, s, _ptr(cache["K8"]), _ptr(cache["sk"]),
-                                 _ptr(cache["V8"]), _ptr(cache["sv"]), batch, _ptr(dev_status), at.handle),
-               "vc_cache_append")
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _on_device(dev, stream, L.vc_cache_append, (K.data_ptr(), V.data_ptr(), *strides, s, K8, sk, V8, sv, batch, status),
+               "vc_cache_append", ())
     return cache
 
 
@@ -432,23 +440,22 @@ def vc_cache_read(cache, cu, kv_len, table, T, K=None, V=None, dev_status=None, 
     """Reads cached tokens back as bf16 [T, H, d] (K, V): the rows that vc_cache_append would write.
     Rows of no sequence stay as they are in K and V given, and hold anything in new ones."""
     L = lib()
-    s = cache_shape_of(cache)
-    dev = cache["K8"].device
-    _status_word(dev_status, dev)
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
     batch = _batch_of(cu, kv_len, table, T, dev)
-    with _Launch(dev, stream) as at:
-        if K is None:
-            K = _empty((T, s.H, s.d), torch.bfloat16, dev)
-            at.new(K)
-        if V is None:
-            V = torch.empty_strided(K.shape, K.stride(), dtype=torch.bfloat16, device=dev)
-            at.new(V)
-        _on(dev, "K, V, or a tensor of the cache", K, V, cache["V8"], cache["sk"], cache["sv"])
-        strides = _rows("K", K, s.H, s.d)
-        if K.shape[0] != T or V.shape != K.shape or _rows("V", V, s.H, s.d) != strides:
-            raise ValueError("K and V must have T rows and share strides")
-        _check(L.vc_cache_read(s, _ptr(cache["K8"]), _ptr(cache["sk"]), _ptr(cache["V8"]), _ptr(cache["sv"]), batch,
-                               _ptr(K), _ptr(V), *strides, _ptr(dev_status), at.handle), "vc_cache_read")
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    made = []
+    if K is None:
+        K = torch.empty((T, s.H, s.d), dtype=torch.bfloat16, device=cache["K8"].device)
+        made.append(K)
+    if V is None:
+        V = torch.empty_strided(K.shape, K.stride(), dtype=torch.bfloat16, device=K.device)
+        made.append(V)
+    strides = _rows("K", K, s.H, s.d, dev)
+    if K.shape[0] != T or V.shape != K.shape or _rows("V", V, s.H, s.d, dev) != strides:
+        raise ValueError("K and V must have T rows and share strides")
+    _on_device(dev, stream, L.vc_cache_read, (s, K8, sk, V8, sv, batch, K.data_ptr(), V.data_ptr(), *strides, status),
+               "vc_cache_read", made)
     return K, V
 
 
@@ -466,34 +473,40 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
     max_q: the longest chunk among the sequences, if known (it chooses the
     kernel, nothing else).  Rows of no sequence stay as they are in O and lse."""
     L = lib()
-    s = cache_shape_of(cache)
-    dev = cache["K8"].device
-    if Q.dim() != 3:
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    shape = tuple(Q.shape)
+    if len(shape) != 3:
         raise ValueError("Q must be bf16 [T, Hq, %d]" % s.d)
-    T, Hq, _ = Q.shape
-    q_strides = _rows("Q", Q, Hq, s.d)
-    _on(dev, "Q, or a tensor of the cache", Q, cache["V8"], cache["sk"], cache["sv"])
-    _status_word(dev_status, dev)
+    T, Hq, d = shape
+    q_strides = _rows("Q", Q, Hq, s.d, dev)
     batch = _batch_of(cu, kv_len, table, T, dev)
-    with _Launch(dev, stream) as at:
-        if O is None:
-            O = _empty((T, Hq, s.d), torch.bfloat16, dev)
-            at.new(O)
-        if lse is None:
-            lse = _empty((T, Hq), torch.float32, dev)
-            at.new(lse)
-        o_strides = _rows("O", O, Hq, s.d)
-        if O.shape != Q.shape or lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
-            raise ValueError("O must have Q's shape and lse be contiguous fp32 [T, Hq]")
-        _on(dev, "O, lse or workspace", O, lse, workspace)
-        if workspace is None:
-            workspace = _workspace(L.vc_attn_paged_workspace(s, Hq, batch.B, T, max_q), dev)
-            at.new(workspace)
-        _check(L.vc_attn_paged(_ptr(Q), *q_strides, Hq, s, _ptr(cache["K8"]), _ptr(cache["sk"]), _ptr(cache["V8"]),
-                               _ptr(cache["sv"]), batch, float(softmax_scale), int(causal), int(window), int(max_q),
-                               _ptr(O), *o_strides, _ptr(lse), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), _ptr(dev_status), at.handle),
-               "vc_attn_paged")
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    made = []
+    if O is None:
+        O = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
+        o_strides = (Hq * d, d)
+        made.append(O)
+    else:
+        o_strides = _rows("O", O, Hq, d, dev)
+        if tuple(O.shape) != shape:
+            raise ValueError("O must have Q's shape")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
+        made.append(lse)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or \
+            lse.get_device() != dev:
+        raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
+    if workspace is None:
+        workspace = torch.empty(max(L.vc_attn_paged_workspace(s, Hq, batch.B, T, max_q), 256), dtype=torch.uint8,
+                                device=Q.device)
+        made.append(workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    _on_device(dev, stream, L.vc_attn_paged,
+               (Q.data_ptr(), *q_strides, Hq, s, K8, sk, V8, sv, batch, softmax_scale, causal, window, max_q,
+                O.data_ptr(), *o_strides, lse.data_ptr(), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), status), "vc_attn_paged", made)
     return O, lse
 
 
