@@ -26,26 +26,25 @@ namespace {
 
 // ------------------------------------------------------------ few rows
 //
-// attn_few_kernel: tiles of 16 RG rows.  What bounds it is reading the cache
+// attn_few_kernel: tiles of 8 RG rows.  What bounds it is reading the cache
 // once (2d + 8 bytes per key and head), so everything else is arranged around a
-// full memory pipe: one persistent CTA on each SM, a producer warp that keeps
-// NS stages of 128 keys in flight by TMA, and eight consumer warps that share
-// nothing until an item ends.  A consumer warp owns 16 rows and 32 keys of a
-// stage (RG = 1: of every other stage; RG = 4: two such blocks), with its own
-// M, l and A in registers; 32 keys give four independent chains of products to
-// hide their latency (16 keys, in twice as many warps a stage: 260 us against
-// XX us for one token of 96 sequences).  The products
-// are m16n8k16 fp16 (the tcgen05 tile of 128 rows would be mostly padding here,
-// and the tensor work of 16 rows is a third of the memory time).  Codes become
-// fp16 on the way from shared memory to registers; the channels of q . k and
-// the keys and channels of P V are permuted so that each thread reads 16
-// consecutive bytes, in an order that has no bank conflicts under the TMA
-// swizzle.
+// full memory pipe: one persistent CTA on each SM, three producer warps (keys,
+// values, scales) that keep NS stages of 128 keys in flight, and sixteen
+// consumer warps that share nothing until an item ends.  A consumer warp owns 8
+// rows and blocks of 16 keys, with its own M, l and A in registers.  Keys and
+// channels are the wide side of the products (K q^T, V^T P^T as m16n8k16 fp16),
+// so 8 rows fill them; a tcgen05 tile of 128 rows would be mostly padding here.
+// Codes become fp16 on the way from shared memory to registers; the channels of
+// q . k and the keys and channels of P V are permuted so that each thread reads
+// 16 consecutive bytes, in an order without bank conflicts under the TMA
+// swizzle.  Rows as the wide side, 8 warps and one producer took 251 us where
+// this takes XX us (one token of 96 sequences, 747 MB).
 
-constexpr int kConsumers = 8;
-constexpr int kFewThreads = (kConsumers + 4) * 32;  // the producer's warpgroup has three idle warps
-// 384 threads start with 168 registers each; 2 x 128 x 216 + 128 x 64 = 63,488 fit into those 64,512
-constexpr int kFewRegsUp = 216, kFewRegsDown = 64;
+constexpr int kConsumers = 16;
+constexpr int kFewThreads = (kConsumers + 4) * 32;  // the producers' warpgroup has an idle warp
+constexpr int kKeyWarp = kConsumers, kValueWarp = kConsumers + 1, kScaleWarp = kConsumers + 2;
+// 640 threads start with 96 registers each; 4 x 128 x 104 + 128 x 56 = 60,416 fit into those 61,440
+constexpr int kFewRegsUp = 104, kFewRegsDown = 56;
 constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
 constexpr float kZeroLog2 = -60.f;     // log2 sv of a token whose values are all zero
 constexpr uint64_t kTimeoutNs = 4000000000ull;
@@ -66,15 +65,15 @@ struct FewCfg {
     static constexpr int TILE = kUnit * D;                       // codes of K or V in a stage
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = OFF_K + NS * TILE;
-    static constexpr int OFF_SCR = OFF_V + NS * TILE;            // [warp][16][D] accumulators at an item's end
-    static constexpr int OFF_SC = OFF_SCR + kConsumers * 16 * D * 4;  // [stage][sk | sv][128]
-    static constexpr int OFF_ML = OFF_SC + NS * 2 * kUnit * 4;   // [m | l][warp][16]
-    static constexpr int OFF_INFO = OFF_ML + 2 * kConsumers * 16 * 4;
+    static constexpr int OFF_SCR = OFF_V + NS * TILE;            // [warp][8][D] accumulators at an item's end
+    static constexpr int OFF_SC = OFF_SCR + kConsumers * 8 * D * 4;  // [stage][sk | sv][128]
+    static constexpr int OFF_ML = OFF_SC + NS * 2 * kUnit * 4;   // [m | l][warp][8]
+    static constexpr int OFF_INFO = OFF_ML + 2 * kConsumers * 8 * 4;
     static constexpr int OFF_BAR = OFF_INFO + NS * 64;           // full[NS], empty[NS], written, read
     static constexpr int OFF_MISC = OFF_BAR + (2 * NS + 2) * 8;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;
     static_assert(SMEM <= 232448, "shared memory budget");
-    // Key (of 8) that column n of a score tile stands for, so that the eight
+    // Key (of 8) that row n of a score tile stands for, so that the eight
     // lanes of a 16-byte shared-memory phase fall on different banks.
     __device__ static int key_of(int n) {
         if (D == 128) return (n >> 1) + 4 * (n & 1);
@@ -85,7 +84,7 @@ struct FewCfg {
     __device__ static int chunk(int r, int ch) {
         return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
     }
-    // First of the D/8 consecutive channels that column n of every output tile stands for.
+    // First of the D/8 consecutive channels that rows n and n + 8 of the output tiles stand for.
     __device__ static int channel_of(int n) { return D == 128 ? ((n >> 1) + 4 * (n & 1)) * 16 : n * 8; }
 };
 
@@ -104,17 +103,17 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit elements held across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -135,15 +134,11 @@ __device__ __forceinline__ float row_factor(uint32_t top) {
 template <int N>
 __device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int r, int ch, const float (&acc)[N],
                                           float inv) {
-    uint32_t w[N / 2];
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
-        w[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    uint16_t* dst = a.O + (int64_t)(q0 + r / a.G) * a.o_sn + (int64_t)(h * a.G + r % a.G) * a.o_sh + ch;
-    if (N == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2 % (N / 2)], w[3 % (N / 2)]);
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    static_assert(N == 4, "8 bytes");
+    const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+    const __nv_bfloat162 v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2*>(a.O + (int64_t)(q0 + r / a.G) * a.o_sn + (int64_t)(h * a.G + r % a.G) * a.o_sh + ch) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
 }
 
 __device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c, int q0, int h, int r, float m,
@@ -156,18 +151,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedAttn a, const CacheView c, void* ws) {
     using C = FewCfg<D>;
-    constexpr int NS = C::NS, RT = 16 * RG;
+    constexpr int NS = C::NS, RT = 8 * RG;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full = sbase + C::OFF_BAR, empty = full + 8 * NS, written = empty + 8 * NS, read = written + 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const Partials part = partials_at(ws, RT, D);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(full + 8 * s, 33);  // the stage's info and TMA bytes, and each producer lane's scales
+            mbar_init(full + 8 * s, 3);  // keys and info, values, scales
             mbar_init(empty + 8 * s, kConsumers);
         }
         mbar_init(written, kConsumers);
@@ -185,155 +180,162 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     launch_dependents();
     if (p.g0 == p.g1) return;
 
-    if (warp > kConsumers) {
+    const int box_log2 = min(c.page_log2, 7);  // runs of keys in one page
+    if (warp >= kConsumers) {
         regs_down<kFewRegsDown>();
-    } else if (warp == kConsumers) {
-        regs_down<kFewRegsDown>();
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            prefetch_tensormap(&tmK);
-            prefetch_tensormap(&tmV);
-        }
-        const int box_log2 = min(c.page_log2, 7), boxes = kUnit >> box_log2;  // runs of keys in one page
-        ItemWalk w;
-        w.start(c, a, RT, p);
-        int it = 0;
-        bool more = true, ok = true;
-        while (more && ok) {
-            const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
-            for (int u = w.unit; u < w.end; ++u, ++it) {
-                const int st = it % NS, key0 = u * kUnit;
-                // page of run `lane` of the unit, -1 where no row sees it or it is not there
-                int pg = -1;
-                if (lane < boxes) {
-                    const int k = key0 + (lane << box_log2);
-                    if (k <= w.r.hi && k + (1 << box_log2) > w.r.lo) {
-                        pg = page_of(c, w.b, k);
-                        if (pg < 0) flag_invalid(c.dev_status);
+        if (warp <= kScaleWarp) {
+            // ------------------------------------------------------------ producers
+            if (lane == 0 && warp != kScaleWarp) prefetch_tensormap(warp == kKeyWarp ? &tmK : &tmV);
+            const int boxes = kUnit >> box_log2;
+            ItemWalk w;
+            w.start(c, a, RT, p);
+            int it = 0;
+            bool more = true, ok = true;
+            while (more && ok) {
+                const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
+                // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
+                auto entry = [&](int u) -> int {
+                    const int k = u * kUnit + (lane << box_log2);
+                    if (lane >= boxes || u >= w.end || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
+                    const int pg = __ldg(c.table + (int64_t)w.b * c.s_table + (k >> c.page_log2));
+                    return pg < 0 ? -2 : pg;
+                };
+                int ahead = entry(w.unit);
+                for (int u = w.unit; u < w.end; ++u, ++it) {
+                    const int st = it % NS, key0 = u * kUnit;
+                    int pg = ahead;
+                    ahead = entry(u + 1);
+                    if (pg == -2 || pg >= c.pages) {
+                        flag_invalid(c.dev_status);
+                        pg = -1;
+                    }
+                    const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
+                    if (it >= NS &&
+                        !mbar_wait_short(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                        ok = false;
+                        break;
+                    }
+                    if (warp == kScaleWarp) {
+                        // scales of the runs that are there; the others are masked
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(full + 8 * st, (uint32_t)__popc(box_ok) << (box_log2 + 3));
+                        __syncwarp();
+                        if (pg >= 0) {
+                            const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
+                            const int64_t off = (int64_t)pg * c.t_page + (int64_t)w.h * c.t_head + in;
+                            const uint32_t dst = sbase + C::OFF_SC + st * (2 * kUnit * 4) + (lane << (box_log2 + 2));
+                            bulk_load(dst, c.sk + off, 4u << box_log2, full + 8 * st);
+                            bulk_load(dst + kUnit * 4, c.sv + off, 4u << box_log2, full + 8 * st);
+                        }
+                        continue;
+                    }
+                    if (lane == 0) {
+                        if (warp == kKeyWarp) {
+                            StageInfo* f = reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64);
+                            const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all &&
+                                                  box_ok == (1 << boxes) - 1;
+                            f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) |
+                                       (all_seen ? 0 : kMasked) | (w.head ? kHead : 0) | (w.tail ? kTail : 0);
+                            f->key0 = key0;
+                            f->q0 = w.s.q0;
+                            f->n = w.s.n;
+                            f->L = w.s.L;
+                            f->h = w.h;
+                            f->r0 = r0;
+                            f->rows = rows;
+                            f->box_ok = box_ok;
+                        }
+                        mbar_arrive_expect_tx(full + 8 * st, C::TILE);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const uint32_t at = sbase + (warp == kKeyWarp ? C::OFF_K : C::OFF_V) + st * C::TILE +
+                                            (uint32_t)(lane << box_log2) * D;
+                        const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
+                        tma_load_4d(at, warp == kKeyWarp ? &tmK : &tmV, 0, in, w.h, pg, full + 8 * st);
                     }
                 }
-                const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
-                if (it >= NS && !mbar_wait_warp(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    StageInfo* f = reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64);
-                    const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all &&
-                                          box_ok == (1 << boxes) - 1;
-                    f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) | (all_seen ? 0 : kMasked) |
-                               (w.head ? kHead : 0) | (w.tail ? kTail : 0);
-                    f->key0 = key0;
-                    f->q0 = w.s.q0;
-                    f->n = w.s.n;
-                    f->L = w.s.L;
-                    f->h = w.h;
-                    f->r0 = r0;
-                    f->rows = rows;
-                    f->box_ok = box_ok;
-                    mbar_arrive_expect_tx(full + 8 * st, 2 * C::TILE);
-                }
-                __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t at = (uint32_t)(lane << box_log2) * D;
-                    const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
-                    tma_load_4d(sbase + C::OFF_K + st * C::TILE + at, &tmK, 0, in, w.h, pg, full + 8 * st);
-                    tma_load_4d(sbase + C::OFF_V + st * C::TILE + at, &tmV, 0, in, w.h, pg, full + 8 * st);
-                }
-                {
-                    // four keys' scales a lane
-                    const int spg = __shfl_sync(0xffffffffu, pg, (4 * lane) >> box_log2);
-                    const int in = (key0 + 4 * lane) & ((1 << c.page_log2) - 1);
-                    const int64_t off = spg < 0 ? 0 : (int64_t)spg * c.t_page + (int64_t)w.h * c.t_head + in;
-                    const uint32_t dst = sbase + C::OFF_SC + st * (2 * kUnit * 4) + lane * 16;
-                    cp_async16(dst, c.sk + off, spg < 0 ? 0 : 16);
-                    cp_async16(dst + kUnit * 4, c.sv + off, spg < 0 ? 0 : 16);
-                    cp_async_arrive(full + 8 * st);
+                if (ok) more = w.next(c, a, RT);
+            }
+            if (ok) {
+                // the stage that ends the consumers' loop
+                const int st = it % NS;
+                if (it < NS ||
+                    mbar_wait_short(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                    if (lane == 0 && warp == kKeyWarp)
+                        reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
+                    if (lane == 0) mbar_arrive(full + 8 * st);
+                    ++it;
                 }
             }
-            if (ok) more = w.next(c, a, RT);
+            // this CTA's own copies land before it can exit
+            for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait(full + 8 * (j % NS), (j / NS) & 1, kTimeoutNs);
         }
-        if (ok) {
-            // the stage that ends the consumers' loop
-            const int st = it % NS;
-            if (it < NS || mbar_wait_warp(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
-                if (lane == 0) {
-                    reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
-                }
-                __syncwarp();
-                mbar_arrive(full + 8 * st);
-                if (lane == 0) mbar_arrive(full + 8 * st);
-                ++it;
-            }
-        }
-        // this CTA's own copies land before it can exit
-        for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait(full + 8 * (j % NS), (j / NS) & 1, kTimeoutNs);
     } else {
         // ------------------------------------------------------------ consumers
         regs_up<kFewRegsUp>();
-        constexpr int SLICES = RG == 4 ? 2 : 4, SLICE = kUnit / SLICES;  // of a stage's keys
-        constexpr int SETS = kConsumers / (RG * SLICES);                 // sets of warps that take turns
-        constexpr int KSTEPS = D / 16, NT = D / 8;
+        constexpr int SLICES = RG <= 2 ? 8 : kConsumers / RG, SLICE = kUnit / SLICES;  // of a stage's keys
+        constexpr int SETS = kConsumers / (RG * SLICES);  // sets of warps that take turns at the stages
+        constexpr int KSTEPS = D / 16, MT = D / 16;
         const int g = lane >> 2, tig = lane & 3;
         const int rg = warp % RG, slice = warp / RG % SLICES, set = warp / (RG * SLICES);
         float* scr = reinterpret_cast<float*>(smem + C::OFF_SCR);
         float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
-        const int box_log2 = min(c.page_log2, 7);
         const int kr0 = C::key_of(2 * tig), kr1 = C::key_of(2 * tig + 1), krg = C::key_of(g);
-        uint32_t q[KSTEPS][4];
-        float o[NT][4], M[2], l[2], qs[2];
+        uint32_t q[KSTEPS][2];
+        float o[MT][4], M[2], l[2], qs[2];  // rows 2 tig and 2 tig + 1 of the warp's 8
         int last[2], first[2];
         int it = 0, items = 0;
         while (true) {
             const int st = it % NS;
-            if (!mbar_wait_warp(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (!mbar_wait_short(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
             const StageInfo* info = reinterpret_cast<const StageInfo*>(smem + C::OFF_INFO + st * 64);
             const int flags = info->flags;
             if (flags & kEnd) break;
-            const int key0 = info->key0, L = info->L, box_ok = info->box_ok;
-            const int q0 = info->q0, h = info->h, r0 = info->r0, rows = info->rows;
             if (flags & kFirst) {
-                // this thread's channels of rows g and g + 8 of its 16, as the A operand:
-                // step s of 16 channels holds, per thread, 4 consecutive ones
+                const int q0 = info->q0, h = info->h, r0 = info->r0, rows = info->rows;
+                // this thread's channels of row g, as the narrow operand: step s of 16
+                // channels holds, per thread, 4 consecutive ones
+                const int row = rg * 8 + g;
+                const int r = r0 + (row < rows ? row : 0), tok = r / a.G, j = r - tok * a.G;
+                const uint16_t* src = a.Q + (int64_t)(q0 + tok) * a.q_sn + (int64_t)(h * a.G + j) * a.q_sh + tig * 16;
+                uint32_t wd[D / 32][4], top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 x = row < rows ? __ldg(reinterpret_cast<const uint4*>(src + (i / 2) * 64) + (i & 1))
+                                               : make_uint4(0, 0, 0, 0);
+                    wd[i][0] = x.x;
+                    wd[i][1] = x.y;
+                    wd[i][2] = x.z;
+                    wd[i][3] = x.w;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = max(top, max(wd[i][k] & 0x7FFFu, (wd[i][k] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float f = row_factor(top), qg = a.scale_log2 / f;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        q[2 * i + k / 2][k & 1] = pack_f16(bf16_bits_to_f32(wd[i][k] & 0xFFFFu) * f,
+                                                           __uint_as_float(wd[i][k] & 0xFFFF0000u) * f);
+                const SeqInfo s{q0, info->n, info->L};
+                const int lg = row_last(a, s, tok);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int row = rg * 16 + g + 8 * e;
-                    const bool there = row < rows;
-                    const int r = r0 + (there ? row : 0), tok = r / a.G, j = r % a.G;
-                    const uint16_t* src = a.Q + (int64_t)(q0 + tok) * a.q_sn + (int64_t)(h * a.G + j) * a.q_sh + tig * 16;
-                    uint4 x[D / 32];
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        x[i] = there ? __ldg(reinterpret_cast<const uint4*>(src + (i / 2) * 64) + (i & 1)) : make_uint4(0, 0, 0, 0);
-                        const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(wd[k] & 0x7FFFu, (wd[k] >> 16) & 0x7FFFu));
-                    }
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float f = row_factor(top);
-                    qs[e] = a.scale_log2 / f;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const uint32_t wd[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float lo = bf16_bits_to_f32(wd[k] & 0xFFFFu) * f;
-                            const float hi = __uint_as_float(wd[k] & 0xFFFF0000u) * f;
-                            q[2 * i + k / 2][e + 2 * (k & 1)] = pack_f16(lo, hi);
-                        }
-                    }
-                    const SeqInfo s{q0, info->n, L};
-                    last[e] = row_last(a, s, tok);
+                    qs[e] = __shfl_sync(0xffffffffu, qg, (2 * tig + e) * 4);
+                    last[e] = __shfl_sync(0xffffffffu, lg, (2 * tig + e) * 4);
                     first[e] = row_first(a, last[e]);
                     M[e] = -INFINITY;
                     l[e] = 0.f;
                 }
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) o[j][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) o[m][i] = 0.f;
             }
             const uint8_t* ks = smem + C::OFF_K + st * C::TILE;
             const uint8_t* vs = smem + C::OFF_V + st * C::TILE;
@@ -341,110 +343,82 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const float* svs = sks + kUnit;
             if (SETS == 1 || it % SETS == set)
 #pragma unroll 1
-            for (int blk = 0; blk < SLICE / 32; ++blk) {
-                const int kb = slice * SLICE + blk * 32;  // 32 keys
-                float x[4][4];
+                for (int blk = 0; blk < SLICE / 16; ++blk) {
+                    const int kb = slice * SLICE + blk * 16;  // 16 keys
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};  // keys g (x[0], x[1]) and g + 8, rows 2 tig and 2 tig + 1
+                    float z[4] = {0.f, 0.f, 0.f, 0.f};  // the same of the other half of the channels' steps
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                    for (int hf = 0; hf < D / 64; ++hf) {
+                        const uint4 u0 = *reinterpret_cast<const uint4*>(ks + C::chunk(kb + krg, hf * 4 + tig));
+                        const uint4 u1 = *reinterpret_cast<const uint4*>(ks + C::chunk(kb + 8 + krg, hf * 4 + tig));
+                        const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[t][i] = 0.f;
-#pragma unroll
-                for (int hf = 0; hf < D / 64; ++hf) {
-                    uint32_t kw[4][4];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint4 w4 = *reinterpret_cast<const uint4*>(ks + C::chunk(kb + 8 * t + krg, hf * 4 + tig));
-                        kw[t][0] = w4.x;
-                        kw[t][1] = w4.y;
-                        kw[t][2] = w4.z;
-                        kw[t][3] = w4.w;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            uint32_t b0, b1;
-                            e4m3x4_to_f16(kw[t][k], b0, b1);
-                            mma_f16(x[t], q[hf * 4 + k], b0, b1);
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t ka[4];
+                            e4m3x4_to_f16(w0[k], ka[0], ka[2]);
+                            e4m3x4_to_f16(w1[k], ka[1], ka[3]);
+                            mma_f16((k & 1) ? z : x, ka, q[hf * 4 + k][0], q[hf * 4 + k][1]);
                         }
-                }
-                // x = (q . k8) sk scale log2 e + log2 sv
-                float isv[4][2];
-                uint32_t keep = 0xFFu;  // bit 2t + e: the key exists
+                    }
+                    // x = (q . k8) sk scale log2 e + log2 sv
+                    float isv[2];
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int k = kb + 8 * t + (e ? kr1 : kr0);
+                    for (int t = 0; t < 2; ++t) {
+                        const int k = kb + 8 * t + krg;
                         const float sk = sks[k], sv = svs[k];
                         const float lv = sv == 0.f ? kZeroLog2 : lg2_approx(sv);
                         // a NaN scale makes x NaN where it is seen; elsewhere 0 * isv has to stay 0
-                        isv[t][e] = sv == 0.f ? 0x1p60f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
-                        x[t][e] = fmaf(x[t][e] * sk, qs[0], lv);
-                        x[t][2 + e] = fmaf(x[t][2 + e] * sk, qs[1], lv);
+                        isv[t] = sv == 0.f ? 0x1p60f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
+                        x[2 * t] = fmaf((x[2 * t] + z[2 * t]) * sk, qs[0], lv);
+                        x[2 * t + 1] = fmaf((x[2 * t + 1] + z[2 * t + 1]) * sk, qs[1], lv);
                     }
-                if (flags & kMasked) {
+                    if (flags & kMasked) {
+                        const int key0 = info->key0, L = info->L, box_ok = info->box_ok;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int k = kb + 8 * t + (e ? kr1 : kr0), pos = key0 + k;
+                        for (int t = 0; t < 2; ++t) {
+                            const int k = kb + 8 * t + krg, pos = key0 + k;
                             const bool there = pos < L && ((box_ok >> (k >> box_log2)) & 1);
-                            if (!there || pos > last[0] || pos < first[0]) x[t][e] = -INFINITY;
-                            if (!there || pos > last[1] || pos < first[1]) x[t][2 + e] = -INFINITY;
-                            if (!there) {  // whatever lies behind the last token
-                                isv[t][e] = 0.f;
-                                keep &= ~(1u << (2 * t + e));
-                            }
+                            if (!there || pos > last[0] || pos < first[0]) x[2 * t] = -INFINITY;
+                            if (!there || pos > last[1] || pos < first[1]) x[2 * t + 1] = -INFINITY;
+                            if (!there) isv[t] = 0.f;  // whatever lies behind the last token
                         }
-                }
-                // the running maximum of each row over the 32 keys
-                float mx[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(max3(x[0][2 * e], x[0][2 * e + 1], x[1][2 * e]),
-                                  max3(x[1][2 * e + 1], x[2][2 * e], x[2][2 * e + 1]));
-                    mx[e] = max3(mx[e], x[3][2 * e], x[3][2 * e + 1]);
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-                    mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-                }
-                const bool rise0 = mx[0] > M[0] + kStale, rise1 = mx[1] > M[1] + kStale;
-                if (__any_sync(0xffffffffu, rise0 || rise1)) {
-                    const float n0 = rise0 ? mx[0] : M[0], n1 = rise1 ? mx[1] : M[1];
-                    const float a0 = rise0 ? part_weight(M[0], n0) : 1.f, a1 = rise1 ? part_weight(M[1], n1) : 1.f;
-                    M[0] = n0;
-                    M[1] = n1;
-                    l[0] *= a0;
-                    l[1] *= a1;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        o[j][0] *= a0;
-                        o[j][1] *= a0;
-                        o[j][2] *= a1;
-                        o[j][3] *= a1;
                     }
-                }
-                const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
+                    float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+                    if (__any_sync(0xffffffffu, mx0 > M[0] + kStale || mx1 > M[1] + kStale)) {
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                        for (int i = 4; i < 32; i <<= 1) {
+                            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, i));
+                            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, i));
+                        }
+                        const float n0 = fmaxf(M[0], mx0), n1 = fmaxf(M[1], mx1);
+                        const float a0 = part_weight(M[0], n0), a1 = part_weight(M[1], n1);
+                        M[0] = n0;
+                        M[1] = n1;
+                        l[0] *= a0;
+                        l[1] *= a1;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[t][e] = ex2_approx(x[t][e] - m0);
-                        x[t][2 + e] = ex2_approx(x[t][2 + e] - m1);
-                        l[0] = fmaf(x[t][e], isv[t][e], l[0]);
-                        l[1] = fmaf(x[t][2 + e], isv[t][e], l[1]);
+                        for (int m = 0; m < MT; ++m) {
+                            o[m][0] *= a0;
+                            o[m][1] *= a1;
+                            o[m][2] *= a0;
+                            o[m][3] *= a1;
+                        }
                     }
-                // P V, 16 keys at a time: the four keys of this thread, D/8 channels of each
+                    const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
 #pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    const float(&y0)[4] = x[2 * hb];
-                    const float(&y1)[4] = x[2 * hb + 1];
-                    const uint32_t pa[4] = {pack_f16(y0[0], y0[1]), pack_f16(y0[2], y0[3]), pack_f16(y1[0], y1[1]),
-                                            pack_f16(y1[2], y1[3])};
+                    for (int t = 0; t < 2; ++t) {
+                        x[2 * t] = ex2_approx(x[2 * t] - m0);
+                        x[2 * t + 1] = ex2_approx(x[2 * t + 1] - m1);
+                        l[0] = fmaf(x[2 * t], isv[t], l[0]);
+                        l[1] = fmaf(x[2 * t + 1], isv[t], l[1]);
+                    }
+                    // P^T: keys as the products' inner index, this thread's row g
+                    const uint32_t p0 = transpose8(pack_f16(x[0], x[1])), p1 = transpose8(pack_f16(x[2], x[3]));
+                    // V^T P^T: the four keys of this thread, D/8 channels of each
                     uint32_t v[4][D / 32];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int r = kb + 16 * hb + 8 * (k >> 1) + ((k & 1) ? kr1 : kr0);
+                        const int r = kb + 8 * (k >> 1) + ((k & 1) ? kr1 : kr0);
                         if (D == 128) {
                             const uint4 t4 = *reinterpret_cast<const uint4*>(vs + C::chunk(r, (g >> 1) + 4 * (g & 1)));
                             v[k][0] = t4.x;
@@ -456,83 +430,85 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             v[k][0] = t2.x;
                             v[k][1] = t2.y;
                         }
+                    }
+                    if (flags & kMasked) {
                         // what lies behind the last token may be any bits: not a factor
-                        if (flags & kMasked) {
-                            const uint32_t on = (keep >> (4 * hb + k)) & 1u ? 0xFFFFFFFFu : 0u;
+                        const int key0 = info->key0, L = info->L, box_ok = info->box_ok;
 #pragma unroll
-                            for (int i = 0; i < D / 32; ++i) v[k][i] &= on;
+                        for (int k = 0; k < 4; ++k) {
+                            const int r = kb + 8 * (k >> 1) + ((k & 1) ? kr1 : kr0);
+                            const bool there = key0 + r < L && ((box_ok >> (r >> box_log2)) & 1);
+#pragma unroll
+                            for (int i = 0; i < D / 32; ++i) v[k][i] = there ? v[k][i] : 0u;
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
-                        uint32_t b0[4], b1[4];
-                        e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x5140u), b0[0], b0[1]);
-                        e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x7362u), b0[2], b0[3]);
-                        e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x5140u), b1[0], b1[1]);
-                        e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x7362u), b1[2], b1[3]);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma_f16(o[4 * i + k], pa, b0[k], b1[k]);
+                        // channels 4 i .. 4 i + 3 of this thread: rows g and g + 8 of two tiles
+                        uint32_t va[4], vb[4];
+                        e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x5140u), va[0], va[1]);
+                        e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x5140u), va[2], va[3]);
+                        e4m3x4_to_f16(prmt(v[0][i], v[1][i], 0x7362u), vb[0], vb[1]);
+                        e4m3x4_to_f16(prmt(v[2][i], v[3][i], 0x7362u), vb[2], vb[3]);
+                        mma_f16(o[2 * i], va, p0, p1);
+                        mma_f16(o[2 * i + 1], vb, p0, p1);
                     }
                 }
-            }
+            const int key_end = flags & kLast;
+            const int q0 = info->q0, h = info->h, r0 = info->r0, rows = info->rows;
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * st);
             ++it;
-            if (!(flags & kLast)) continue;
+            if (!key_end) continue;
 
             // ------------------------------------------------------------ the item's end
             // the accumulators are free to overwrite once the last item's were read
-            if (items > 0 && !mbar_wait_warp(read, (items - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (items > 0 && !mbar_wait_short(read, (items - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-                float* dst = scr + ((size_t)warp * 16 + g + 8 * e) * D;
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc)
+                for (int i = 4; i < 32; i <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], i);
+                float* dst = scr + ((size_t)warp * 8 + 2 * tig + e) * D + C::channel_of(g);
 #pragma unroll
-                    for (int j = 0; j < NT; j += 4)
-                        *reinterpret_cast<float4*>(dst + C::channel_of(2 * tig + cc) + j) =
-                            make_float4(o[j][2 * e + cc], o[j + 1][2 * e + cc], o[j + 2][2 * e + cc], o[j + 3][2 * e + cc]);
-                if (tig == 0) {
-                    ml[warp * 16 + g + 8 * e] = M[e];
-                    ml[kConsumers * 16 + warp * 16 + g + 8 * e] = l[e];
+                for (int i = 0; i < D / 32; ++i)
+                    *reinterpret_cast<float4*>(dst + 4 * i) =
+                        make_float4(o[2 * i][e], o[2 * i][2 + e], o[2 * i + 1][e], o[2 * i + 1][2 + e]);
+                if (g == 0) {
+                    ml[warp * 8 + 2 * tig + e] = M[e];
+                    ml[kConsumers * 8 + warp * 8 + 2 * tig + e] = l[e];
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(written);
-            if (!mbar_wait_warp(written, items & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (!mbar_wait_short(written, items & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
             const bool split = flags & (kHead | kTail);
             const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
-            for (int i = threadIdx.x; i < RT * (D / 8); i += kConsumers * 32) {
-                const int row = i / (D / 8), ch = (i % (D / 8)) * 8;
-                if (row >= rows) break;
-                float m = -INFINITY, lsum = 0.f, acc[8];
+            for (int i = threadIdx.x; i < rows * (D / 4); i += kConsumers * 32) {
+                const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+                const int at0 = (row / 8) * 8 + row % 8;  // warp rg of the first slice
+                float m = -INFINITY, lsum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int s = 0; s < kConsumers / RG; ++s) m = fmaxf(m, ml[(s * RG + row / 16) * 16 + row % 16]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+                for (int s = 0; s < kConsumers / RG; ++s) m = fmaxf(m, ml[at0 + s * RG * 8]);
 #pragma unroll
                 for (int s = 0; s < kConsumers / RG; ++s) {
-                    const int at = (s * RG + row / 16) * 16 + row % 16;
+                    const int at = at0 + s * RG * 8;
                     const float w = part_weight(ml[at], m);
-                    lsum = fmaf(w, ml[kConsumers * 16 + at], lsum);
-                    const float4 u0 = *reinterpret_cast<const float4*>(scr + (size_t)at * D + ch);
-                    const float4 u1 = *reinterpret_cast<const float4*>(scr + (size_t)at * D + ch + 4);
-                    const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, u[k], acc[k]);
+                    lsum = fmaf(w, ml[kConsumers * 8 + at], lsum);
+                    const float4 u = *reinterpret_cast<const float4*>(scr + (size_t)at * D + ch);
+                    acc[0] = fmaf(w, u.x, acc[0]);
+                    acc[1] = fmaf(w, u.y, acc[1]);
+                    acc[2] = fmaf(w, u.z, acc[2]);
+                    acc[3] = fmaf(w, u.w, acc[3]);
                 }
                 if (split) {
-                    float* dst = part.o + ((size_t)slot * RT + row) * D + ch;
-                    *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+                    *reinterpret_cast<float4*>(part.o + ((size_t)slot * RT + row) * D + ch) =
+                        make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (ch == 0) {
                         part.m[(size_t)slot * RT + row] = m;
                         part.l[(size_t)slot * RT + row] = lsum;
                     }
                 } else {
-                    store_row<8>(a, q0, h, r0 + row, ch, acc, inverse_sum(lsum));
+                    store_row<4>(a, q0, h, r0 + row, ch, acc, inverse_sum(lsum));
                     if (ch == 0) store_lse(a, c, q0, h, r0 + row, m, lsum);
                 }
             }
@@ -628,7 +604,7 @@ bool make_cache_map(CUtensorMap* map, const uint8_t* base, int d, const CacheVie
 int tile_rows(int G, int B, int T, int max_q) {
     const int64_t q = max_q > 0 ? max_q : ((int64_t)T + B - 1) / B;
     const int64_t rows = q * G;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 // CTAs of a call: as many as there can be units, one on each SM at most.
@@ -659,19 +635,20 @@ vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAt
     auto kern = attn_few_kernel<D, RG>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
     if (s != VC_OK) return s;
-    const int ctas = part_count(a, c, 16 * RG);
+    const int ctas = part_count(a, c, 8 * RG);
     kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
     if ((s = cuda_status(cudaGetLastError())) != VC_OK) return s;
-    return launch_join<D, 16 * RG>(a, c, ws, ctas, st);
+    return launch_join<D, 8 * RG>(a, c, ws, ctas, st);
 }
 
 template <int D>
 vc_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
                    cudaStream_t st) {
     switch (tile_rows(a.G, c.B, c.T, a.max_q)) {
-        case 16: return launch_few<D, 1>(mk, mv, a, c, ws, st);
-        case 32: return launch_few<D, 2>(mk, mv, a, c, ws, st);
-        default: return launch_few<D, 4>(mk, mv, a, c, ws, st);
+        case 8: return launch_few<D, 1>(mk, mv, a, c, ws, st);
+        case 16: return launch_few<D, 2>(mk, mv, a, c, ws, st);
+        case 32: return launch_few<D, 4>(mk, mv, a, c, ws, st);
+        default: return launch_few<D, 8>(mk, mv, a, c, ws, st);
     }
 }
 

@@ -97,6 +97,17 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status, timeout_ns));
 }
 
+// mbar_wait_warp for waits that are short as a rule: the timer (a slow read) is
+// looked at only after 64 attempts, each of which may suspend the thread for a
+// while, so the bound is timeout_ns past that.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                int32_t* dev_status, uint64_t timeout_ns) {
+    bool ok = mbar_test_wait(bar, parity);
+    for (int i = 0; !ok && i < 64; ++i) ok = mbar_try_wait(bar, parity);
+    if (!ok) ok = mbar_wait(bar, parity, abort_flag, dev_status, timeout_ns);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // ------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
@@ -114,6 +125,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
         "[%6];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// Untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) into this CTA's shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
 
