@@ -1,0 +1,663 @@
+// vc_attn_chunk.cu -- vc_attn_paged for chunks of many rows, on tcgen05.
+//
+// The mathematics is that of vc_attn_paged.cu.  One persistent CTA on each SM
+// takes tiles of 256 rows as two pipelines A and B of 128 rows, which share the
+// keys and values and the tensor core, so that the softmax of one overlaps the
+// products of the other; a tile of up to 128 rows is given to both, which then
+// take its units of 128 keys in turn and are added up at its end.
+//
+// Per unit and pipeline, 128 rows x 128 keys:
+//   S = q K8^T in kind::f8f6f4, straight from the cached codes: the query row,
+//       scaled by a power of two, is the sum of two E4M3 numbers (4 + 4 bits of
+//       the 8 that bf16 has: exact down to 2^-9 of its largest channel, within
+//       2^-17 of it below), so two FP8 products of depth d give the score.
+//       They cost what one bf16 product would and need no conversion of keys.
+//   P V8 in kind::f16: P as fp16 in tensor memory, in the place of S; V8 as fp16,
+//       which a warpgroup converts once a unit for both pipelines.  (P as two
+//       E4M3 numbers would spare that, but lose everything below 2^-17 of the
+//       row's largest: a few thousand keys there are a visible part of a sum.)
+// What bounds it is the tensor core: 4 x 512 clocks a unit for both pipelines;
+// the softmax needs about 700 issue slots a warp and unit, two such warps and a
+// converting one on each scheduler.
+//
+// 16 warps:
+//   0-3, 4-7  softmax of A and B: a thread owns a row (its TMEM lane).
+//   8-11      converter: a thread owns a key for the scales (log2 sv, 1 / sv),
+//             and 16-byte pieces of the values.
+//   12, 13    MMA issuers of A and B (12 owns the tensor memory).
+//   14        loader: K8, V8 and scales by TMA and bulk copies, and what the
+//             others need to know of a unit.  15 is idle.
+// Tensor memory of pipeline X at X (d + 128): O [0, d), S [d, d + 128), P in the
+// first 64 columns of S.
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "vc_device.cuh"
+#include "vc_internal.h"
+#include "vc_paged.cuh"
+
+namespace vc {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kLoadWarp = 14;
+// 512 x 128 registers at launch; 2 x 128 x 168 + 128 x 96 + 128 x 72 = 64,512 fit into those 65,536
+constexpr int kRegsSoftmax = 168, kRegsConv = 96, kRegsOther = 72;
+
+template <int D>
+struct ManyCfg {
+    static constexpr int NK = 3, NV = 2, NW = 2, NC = 3, NI = 4;  // stages: K8, V8, fp16 V, scales, infos
+    static constexpr int QB = 128 * D;                    // one E4M3 part of a pipeline's queries
+    static constexpr int TILE = kUnit * D;                // codes of K or V in a unit
+    static constexpr int WB = kUnit * D * 2;              // fp16 values of a unit
+    static constexpr int OFF_Q = 0;                       // [X][hi, lo]
+    static constexpr int OFF_K = OFF_Q + 4 * QB;
+    static constexpr int OFF_V = OFF_K + NK * TILE;
+    static constexpr int OFF_W = OFF_V + NV * TILE;
+    static constexpr int OFF_RAW = OFF_W + NW * WB;       // [NV][sk | sv][128]
+    static constexpr int OFF_SC = OFF_RAW + NV * 2 * kUnit * 4;  // [NC][sk | log2 sv | 1 / sv][128]
+    static constexpr int OFF_ML = OFF_SC + NC * 3 * kUnit * 4;   // [m | l][128] of B, for A
+    static constexpr int OFF_INFO = OFF_ML + 2 * 128 * 4;
+    static constexpr int OFF_BAR = OFF_INFO + NI * 64;
+    static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
+    static constexpr int USED = OFF_MISC + 32;
+    // at least 116 KB, so that one CTA (and one owner of the tensor memory) sits on an SM
+    static constexpr int SMEM = (USED > 118784 ? USED : 118784) + 1024;
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static_assert(QB % 1024 == 0 && TILE % 1024 == 0 && WB % 1024 == 0, "swizzle alignment");
+    // barriers
+    static constexpr int IF = 0, IE = IF + NI, KF = IE + NI, KE = KF + NK, VF = KE + NK, VE = VF + NV, WF = VE + NV,
+                         WE = WF + NW, CF = WE + NW, CE = CF + NC, QF = CE + NC, SF = QF + 2, PF = SF + 2,
+                         OD = PF + 2, OE = OD + 2, MB = OE + 2, TD = MB + 1, NBAR = TD + 2;
+    static_assert(NBAR <= 48, "barrier area");
+    static constexpr uint32_t SWZ = D == 128 ? kSwizzle128B : kSwizzle64B;
+    __host__ __device__ static constexpr uint32_t base(int X) { return (uint32_t)X * (D + 128); }
+    // Byte offset of 16-byte piece ch of code row r under the swizzle.
+    __device__ static int chunk(int r, int ch) {
+        return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+    }
+};
+
+// Instruction descriptor, kind::f16: A and B fp16, D fp32, B with its N index contiguous.
+__host__ __device__ constexpr uint32_t idesc_f16_bn(uint32_t M, uint32_t N) {
+    return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const PagedAttn a, const CacheView c, int RT, void* ws) {
+    using C = ManyCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);
+    const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const Partials part = partials_at(ws, RT, D);
+    auto wait = [&](int i, int phase) -> bool {
+        return mbar_wait_short(bar(i), phase & 1, abort_flag, c.dev_status, kTimeoutNs);
+    };
+
+    if (threadIdx.x == 0) {
+        auto init = [&](int first, int n, int count) {
+            for (int i = 0; i < n; ++i) mbar_init(bar(first + i), count);
+        };
+        init(C::IF, C::NI, 1);
+        init(C::IE, C::NI, 8 + 4 + 2);  // softmax and converter warps, MMA warps
+        init(C::KF, C::NK, 1);
+        init(C::KE, C::NK, 2);
+        init(C::VF, C::NV, 1);
+        init(C::VE, C::NV, 4);
+        init(C::WF, C::NW, 4);
+        init(C::WE, C::NW, 2);
+        init(C::CF, C::NC, 4);
+        init(C::CE, C::NC, 8);
+        init(C::QF, 2, 4);
+        init(C::SF, 2, 1);
+        init(C::PF, 2, 4);
+        init(C::OD, 2, 1);
+        init(C::OE, 2, 4);
+        init(C::MB, 1, 4);
+        init(C::TD, 2, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        part.head[2 * blockIdx.x].valid = 0;
+        part.head[2 * blockIdx.x + 1].valid = 0;
+    }
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < c.B; b += kThreads)
+            if (!seq_valid(c, b)) flag_invalid(c.dev_status);
+    const Part p = plan_part<kThreads>(c, a, RT, blockIdx.x, gridDim.x);
+    __syncthreads();
+    launch_dependents();
+    if (p.g0 == p.g1) return;
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+    const int box_log2 = min(c.page_log2, 7);  // runs of keys in one page
+    auto info_at = [&](int it) -> const StageInfo* {
+        return reinterpret_cast<const StageInfo*>(smem + C::OFF_INFO + (it % C::NI) * 64);
+    };
+
+    if (warp >= kMmaWarp) {
+        regs_down<kRegsOther>();
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ loader
+            if (lane == 0) {
+                prefetch_tensormap(&tmK);
+                prefetch_tensormap(&tmV);
+            }
+            const int boxes = kUnit >> box_log2;
+            ItemWalk w;
+            w.start(c, a, RT, p);
+            int it = 0, loaded_k = 0, loaded_v = 0;
+            bool more = true, ok = true;
+            while (more && ok) {
+                const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
+                // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
+                auto entry = [&](int u) -> int {
+                    const int k = u * kUnit + (lane << box_log2);
+                    if (lane >= boxes || u >= w.end || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
+                    const int pg = __ldg(c.table + (int64_t)w.b * c.s_table + (k >> c.page_log2));
+                    return pg < 0 ? -2 : pg;
+                };
+                int ahead = entry(w.unit);
+                for (int u = w.unit; u < w.end; ++u, ++it) {
+                    const int key0 = u * kUnit;
+                    int pg = ahead;
+                    ahead = entry(u + 1);
+                    if (pg == -2 || pg >= c.pages) {
+                        flag_invalid(c.dev_status);
+                        pg = -1;
+                    }
+                    const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
+                    ok = it < C::NI || wait(C::IE + it % C::NI, it / C::NI - 1);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        StageInfo* f = const_cast<StageInfo*>(info_at(it));
+                        const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all;
+                        f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) |
+                                   (all_seen ? 0 : kMasked) | (w.head ? kHead : 0) | (w.tail ? kTail : 0);
+                        f->key0 = key0;
+                        f->q0 = w.s.q0;
+                        f->n = w.s.n;
+                        f->L = w.s.L;
+                        f->h = w.h;
+                        f->r0 = r0;
+                        f->rows = rows;
+                        f->box_ok = box_ok;
+                        f->pad[0] = u - w.unit;
+                        mbar_arrive(bar(C::IF + it % C::NI));
+                    }
+                    __syncwarp();
+                    const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
+                    const uint32_t at = (uint32_t)(lane << box_log2) * D;
+                    const int sk = it % C::NK, sv = it % C::NV;
+                    ok = it < C::NK || wait(C::KE + sk, it / C::NK - 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(C::KF + sk), C::TILE);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_4d(sbase + C::OFF_K + sk * C::TILE + at, &tmK, 0, in, w.h, pg, bar(C::KF + sk));
+                    loaded_k = it + 1;
+                    ok = it < C::NV || wait(C::VE + sv, it / C::NV - 1);
+                    if (!ok) break;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(bar(C::VF + sv),
+                                              C::TILE + ((uint32_t)__popc(box_ok) << (box_log2 + 3)));
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_4d(sbase + C::OFF_V + sv * C::TILE + at, &tmV, 0, in, w.h, pg, bar(C::VF + sv));
+                    if (pg >= 0) {
+                        const int64_t off = (int64_t)pg * c.t_page + (int64_t)w.h * c.t_head + in;
+                        const uint32_t dst = sbase + C::OFF_RAW + sv * (2 * kUnit * 4) + (lane << (box_log2 + 2));
+                        bulk_load(dst, c.sk + off, 4u << box_log2, bar(C::VF + sv));
+                        bulk_load(dst + kUnit * 4, c.sv + off, 4u << box_log2, bar(C::VF + sv));
+                    }
+                    loaded_v = it + 1;
+                }
+                if (ok) more = w.next(c, a, RT);
+            }
+            if (ok && (it < C::NI || wait(C::IE + it % C::NI, it / C::NI - 1))) {
+                if (lane == 0) {
+                    const_cast<StageInfo*>(info_at(it))->flags = kEnd;
+                    mbar_arrive(bar(C::IF + it % C::NI));
+                }
+                __syncwarp();
+            }
+            // this CTA's own copies land before it can exit
+            for (int j = max(loaded_k - C::NK, 0); j < loaded_k; ++j)
+                drain_wait(bar(C::KF + j % C::NK), (j / C::NK) & 1, kTimeoutNs);
+            for (int j = max(loaded_v - C::NV, 0); j < loaded_v; ++j)
+                drain_wait(bar(C::VF + j % C::NV), (j / C::NV) & 1, kTimeoutNs);
+        } else if (warp < kLoadWarp) {
+            // ------------------------------------------------------------ MMA issuer of pipeline X
+            const int X = warp - kMmaWarp;
+            const uint32_t tb = tmem + C::base(X);
+            constexpr uint32_t IDESC_QK = idesc_f8_e4m3(128, 128), IDESC_PV = idesc_f16_bn(128, D);
+            int items = 0, own = 0;  // items begun, own units
+            bool fresh = true;       // no product of this item in O yet
+            for (int it = 0;; ++it) {
+                if (!wait(C::IF + it % C::NI, it / C::NI)) break;
+                const StageInfo* f = info_at(it);
+                const int flags = f->flags, place = f->pad[0];
+                const bool both = f->rows > 128;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
+                if (flags & kEnd) break;
+                const int sk = it % C::NK, sw = it % C::NW;
+                const bool mine = both || (place & 1) == X;
+                if (flags & kFirst) {
+                    fresh = true;
+                    if (!wait(C::QF + X, items)) break;
+                }
+                if (!wait(C::KF + sk, it / C::NK)) break;
+                if (mine) {
+                    // S is free: the product that reads the last P from its place was issued before
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 2 * (D / 32); ++i) {
+                        const uint32_t qa = sbase + C::OFF_Q + (2 * X + i / (D / 32)) * C::QB + (i % (D / 32)) * 32;
+                        const uint32_t kb = sbase + C::OFF_K + sk * C::TILE + (i % (D / 32)) * 32;
+                        mma_f8_ss_w(tb + D, smem_desc(qa, 8 * D, C::SWZ), smem_desc(kb, 8 * D, C::SWZ), IDESC_QK,
+                                    i > 0 ? 1u : 0u);
+                    }
+                    mma_commit_w(bar(C::SF + X));
+                    mma_commit_w(bar(C::KE + sk));
+                } else if (lane == 0) {
+                    mbar_arrive(bar(C::KE + sk));
+                }
+                // O is free: the rows of the item before have been read
+                if ((flags & kFirst) && items > 0 && !wait(C::OE + X, items - 1)) break;
+                if (!wait(C::WF + sw, it / C::NW)) break;
+                if (mine) {
+                    if (!wait(C::PF + X, own)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < kUnit / 16; ++i) {
+                        const uint64_t bd =
+                            smem_desc_lbo(sbase + C::OFF_W + sw * C::WB + i * 2048, 128 * 128, 1024, kSwizzle128B);
+                        mma_bf16_ts_w(tb, tb + D + i * 8, bd, IDESC_PV, (fresh && i == 0) ? 0u : 1u);
+                    }
+                    mma_commit_w(bar(C::WE + sw));
+                    fresh = false;
+                    ++own;
+                } else if (lane == 0) {
+                    mbar_arrive(bar(C::WE + sw));
+                }
+                if (flags & kLast) {
+                    mma_commit_w(bar(C::OD + X));
+                    ++items;
+                }
+            }
+            // every MMA this warp issued has completed once this phase flips
+            mma_commit_w(bar(C::TD + X));
+            drain_wait(bar(C::TD + X), 0, kTimeoutNs);
+            __syncwarp();
+        }
+    } else if (warp >= kConvWarp) {
+        // ------------------------------------------------------------ converter
+        regs_down<kRegsConv>();
+        const int t = threadIdx.x - kConvWarp * 32;
+        for (int it = 0;; ++it) {
+            if (!wait(C::IF + it % C::NI, it / C::NI)) break;
+            const StageInfo* f = info_at(it);
+            const int flags = f->flags, key0 = f->key0, L = f->L, box_ok = f->box_ok;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
+            if (flags & kEnd) break;
+            const int sv = it % C::NV, sw = it % C::NW, sc = it % C::NC;
+            if (!wait(C::VF + sv, it / C::NV)) break;
+            if (it >= C::NC && !wait(C::CE + sc, it / C::NC - 1)) break;
+            {
+                const float* raw = reinterpret_cast<const float*>(smem + C::OFF_RAW + sv * (2 * kUnit * 4));
+                float* out = reinterpret_cast<float*>(smem + C::OFF_SC + sc * (3 * kUnit * 4));
+                const bool there = key0 + t < L && ((box_ok >> (t >> box_log2)) & 1);
+                const float k = raw[t], v = raw[kUnit + t];
+                out[t] = there ? k : 0.f;
+                out[kUnit + t] = !there ? -INFINITY : v == 0.f ? kZeroLog2 : lg2_approx(v);
+                // a NaN scale makes the score NaN where it is seen; elsewhere 0 / sv has to stay 0
+                out[2 * kUnit + t] = !there ? 0.f : v == 0.f ? 0x1p60f : v > 0.f ? __fdividef(1.f, v) : 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::CF + sc));
+            }
+            if (it >= C::NW && !wait(C::WE + sw, it / C::NW - 1)) break;
+            const uint8_t* vs = smem + C::OFF_V + sv * C::TILE;
+            uint8_t* wd = smem + C::OFF_W + sw * C::WB;
+            constexpr int PIECES = D / 16;  // 16 codes each
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int r = (i * 128 + t) / PIECES, ch = t % PIECES;
+                uint4 x = *reinterpret_cast<const uint4*>(vs + C::chunk(r, ch));
+                if ((flags & kMasked) && key0 + r >= L) x = make_uint4(0, 0, 0, 0);  // any bits behind the last token
+                uint4 lo, hi;
+                e4m3x4_to_f16(x.x, lo.x, lo.y);
+                e4m3x4_to_f16(x.y, lo.z, lo.w);
+                e4m3x4_to_f16(x.z, hi.x, hi.y);
+                e4m3x4_to_f16(x.w, hi.z, hi.w);
+                // 64 channels a half, 128 bytes a token, 128-byte swizzle; the halves' threads
+                // write their two pieces in opposite order, which keeps them on different banks
+                uint8_t* row = wd + (ch / 4) * (kUnit * 128) + r * 128;
+                const int c0 = ((ch & 3) * 2) ^ (r & 7), c1 = ((ch & 3) * 2 + 1) ^ (r & 7);
+                const bool swap = ch >= 4;
+                *reinterpret_cast<uint4*>(row + ((swap ? c1 : c0) << 4)) = swap ? hi : lo;
+                *reinterpret_cast<uint4*>(row + ((swap ? c0 : c1) << 4)) = swap ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::WF + sw));
+                mbar_arrive(bar(C::VE + sv));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax of pipeline X
+        regs_up<kRegsSoftmax>();
+        const int X = warp >> 2, q = warp & 3, row = q * 32 + lane;
+        const uint32_t la = tmem + ((uint32_t)(q * 32) << 16) + C::base(X);
+        float M = -INFINITY, l = 0.f, qs = 0.f;
+        int last = -1, first = 0, items = 0, own = 0, shared = 0;
+        bool fresh = true;
+        for (int it = 0;; ++it) {
+            if (!wait(C::IF + it % C::NI, it / C::NI)) break;
+            const StageInfo* f = info_at(it);
+            const int flags = f->flags, key0 = f->key0, place = f->pad[0];
+            const int q0 = f->q0, n = f->n, L = f->L, h = f->h, r0 = f->r0, rows = f->rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
+            if (flags & kEnd) break;
+            const bool both = rows > 128, mine = both || (place & 1) == X;
+            const int tr = both ? X * 128 + row : row;  // this thread's row of the tile
+            if (flags & kFirst) {
+                // the row's two E4M3 parts; the products that read the last item's have completed
+                const bool there = tr < rows;
+                const int r = r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
+                const uint4* src = reinterpret_cast<const uint4*>(a.Q + (int64_t)(q0 + tok) * a.q_sn +
+                                                                  (int64_t)(h * a.G + j) * a.q_sh);
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 x = there ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = max(top, max(w4[k] & 0x7FFFu, (w4[k] >> 16) & 0x7FFFu));
+                }
+                const float fac = row_factor(top);
+                qs = a.scale_log2 / fac;
+                uint8_t* qh = smem + C::OFF_Q + 2 * X * C::QB;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    uint32_t hw[4], lw[4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint4 x = there ? __ldg(src + 2 * i + u) : make_uint4(0, 0, 0, 0);
+                        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float y[4];
+                            y[0] = bf16_bits_to_f32(w4[2 * k] & 0xFFFFu) * fac;
+                            y[1] = __uint_as_float(w4[2 * k] & 0xFFFF0000u) * fac;
+                            y[2] = bf16_bits_to_f32(w4[2 * k + 1] & 0xFFFFu) * fac;
+                            y[3] = __uint_as_float(w4[2 * k + 1] & 0xFFFF0000u) * fac;
+                            const uint32_t hi = cvt_e4m3x2(y[0], y[1]) | (cvt_e4m3x2(y[2], y[3]) << 16);
+                            uint32_t f01, f23;
+                            e4m3x4_to_f16(hi, f01, f23);
+                            const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
+                            const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
+                            hw[2 * u + k] = hi;
+                            lw[2 * u + k] = cvt_e4m3x2(y[0] - g01.x, y[1] - g01.y) |
+                                            (cvt_e4m3x2(y[2] - g23.x, y[3] - g23.y) << 16);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(qh + C::chunk(row, i)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+                    *reinterpret_cast<uint4*>(qh + C::QB + C::chunk(row, i)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::QF + X));
+                const SeqInfo s{q0, n, L};
+                last = row_last(a, s, tok);
+                first = row_first(a, last);
+                M = -INFINITY;
+                l = 0.f;
+                fresh = true;
+            }
+            const int sc = it % C::NC;
+            if (!wait(C::CF + sc, it / C::NC)) break;
+            if (mine) {
+                if (!wait(C::SF + X, own)) break;
+                ++own;
+                tc_fence_after();
+                const float4* scl = reinterpret_cast<const float4*>(smem + C::OFF_SC + sc * (3 * kUnit * 4));
+                const int lo = first - key0, hi = last - key0;  // the unit's keys that this row sees
+                uint32_t pw[kUnit / 2];
+                float lsum;
+                // Scores, probabilities against M and the row's maximum, in one pass; again
+                // with the new M where the maximum has risen too far.
+                auto pass = [&](auto masked_tag) -> float {
+                    constexpr bool MASKED = decltype(masked_tag)::value;
+                    const float m = M == -INFINITY ? 0.f : M;
+                    const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(-m, -m);
+                    float2 l2 = make_float2(0.f, 0.f);
+                    float mx = -INFINITY;
+                    uint32_t s0[32], s1[32];
+                    auto part32 = [&](const uint32_t(&s)[32], int cc) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const int at = (cc * 32 + i) / 4;
+                            const float4 sk = scl[at], lv = scl[kUnit / 4 + at], iv = scl[kUnit / 2 + at];
+                            float2 y0 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                                              make_float2(sk.x, sk.y)),
+                                                   qs2, make_float2(lv.x, lv.y));
+                            float2 y1 = __ffma2_rn(
+                                __fmul2_rn(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])),
+                                           make_float2(sk.z, sk.w)),
+                                qs2, make_float2(lv.z, lv.w));
+                            if (MASKED) {
+                                const int k = cc * 32 + i;
+                                if (k < lo || k > hi) y0.x = -INFINITY;
+                                if (k + 1 < lo || k + 1 > hi) y0.y = -INFINITY;
+                                if (k + 2 < lo || k + 2 > hi) y1.x = -INFINITY;
+                                if (k + 3 < lo || k + 3 > hi) y1.y = -INFINITY;
+                            }
+                            mx = max3(max3(mx, y0.x, y0.y), y1.x, y1.y);
+                            y0 = __fadd2_rn(y0, nm2);
+                            y1 = __fadd2_rn(y1, nm2);
+                            y0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
+                            y1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
+                            l2 = __ffma2_rn(y0, make_float2(iv.x, iv.y), l2);
+                            l2 = __ffma2_rn(y1, make_float2(iv.z, iv.w), l2);
+                            pw[cc * 16 + i / 2] = pack_f16(y0.x, y0.y);
+                            pw[cc * 16 + i / 2 + 1] = pack_f16(y1.x, y1.y);
+                        }
+                    };
+                    tmem_ld32(la + D, s0);
+                    tmem_wait_ld();
+                    tmem_ld32(la + D + 32, s1);
+                    part32(s0, 0);
+                    tmem_wait_ld();
+                    tmem_ld32(la + D + 64, s0);
+                    part32(s1, 1);
+                    tmem_wait_ld();
+                    tmem_ld32(la + D + 96, s1);
+                    part32(s0, 2);
+                    tmem_wait_ld();
+                    part32(s1, 3);
+                    lsum = l2.x + l2.y;
+                    return mx;
+                };
+                auto run = [&]() -> float {
+                    return (flags & kMasked) ? pass(std::true_type{}) : pass(std::false_type{});
+                };
+                float alpha = 1.f;
+#pragma unroll 1
+                for (int rep = 0; rep < 2; ++rep) {
+                    const float mx = (flags & kMasked) ? pass(std::true_type{}) : pass(std::false_type{});
+                    const bool rise = mx > M + kStale;
+                    if (rep || !__any_sync(0xffffffffu, rise)) break;
+                    if (rise) {
+                        alpha = part_weight(M, mx);
+                        M = mx;
+                        l *= alpha;
+                    }
+                }
+                l += lsum;
+                if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // O holds every product up to the pipeline's last unit: the scores' completion
+                    // covers what was issued before them
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(la + c0, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                                        make_float2(alpha, alpha));
+                            o[i] = __float_as_uint(v.x);
+                            o[i + 1] = __float_as_uint(v.y);
+                        }
+                        tmem_st32(la + c0, o);
+                    }
+                }
+                fresh = false;
+                {
+                    uint32_t w0[32], w1[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        w0[i] = pw[i];
+                        w1[i] = pw[32 + i];
+                    }
+                    tmem_st32(la + D, w0);
+                    tmem_st32(la + D + 32, w1);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::PF + X));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::CE + sc));
+            if (!(flags & kLast)) continue;
+
+            // ------------------------------------------------------------ the item's end
+            float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+            if (!wait(C::OD + X, items)) break;
+            if (!both && X == 1) {
+                // A adds the two halves of the keys up; it reads this row's O in tensor memory
+                // itself and gets M and l here, once it has read the last ones
+                if (items > 0 && !wait(C::OE + 1, items - 1)) break;
+                ml[row] = M;
+                ml[128 + row] = l;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(C::MB));
+                ++items;
+                continue;
+            }
+            const bool add = !both && place > 0;  // B had units of this item
+            float wa = 1.f, wb = 0.f;
+            if (!both) {
+                if (!wait(C::OD + 1, items) || !wait(C::MB, shared)) break;
+                ++shared;
+                if (add) {
+                    const float mb = ml[row], lb = ml[128 + row], m = fmaxf(M, mb);
+                    wa = part_weight(M, m);
+                    wb = part_weight(mb, m);
+                    l = wa * l + wb * lb;
+                    M = m;
+                }
+            }
+            tc_fence_after();
+            const bool split = flags & (kHead | kTail), there = tr < rows;
+            const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
+            const int r = r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
+            const float inv = split ? 1.f : inverse_sum(l);
+            wa *= inv;
+            wb *= inv;
+            float* po = part.o + ((size_t)slot * RT + (there ? tr : 0)) * D;
+            uint16_t* dst = a.O + (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t oa[32];
+                float v[32];
+                tmem_ld32(la + c0, oa);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(oa[i]) * wa;
+                if (add) {
+                    tmem_ld32(la + C::base(1) + c0, oa);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(oa[i]), wb, v[i]);
+                }
+                if (there && split) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(po + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                } else if (there) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
+                            w4[k] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(C::OE + X));
+                if (!both) mbar_arrive(bar(C::OE + 1));
+            }
+            if (there && split) {
+                part.m[(size_t)slot * RT + tr] = M;
+                part.l[(size_t)slot * RT + tr] = l;
+            } else if (there) {
+                store_lse(a, c, q0, h, r, M, l);
+            }
+            if (split && threadIdx.x == 0)
+                part.head[slot] = PartHeader{1, (flags & kTail) ? 0 : 1, q0, h, r0, rows};
+            ++items;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
+                      int ctas, void* ws, cudaStream_t st) {
+    auto kern = attn_many_kernel<D>;
+    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
+    if (s != VC_OK) return s;
+    kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
+    return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
+                           int d, int RT, int ctas, void* ws, cudaStream_t st) {
+    return d == 128 ? launch_many<128>(mk, mv, a, c, RT, ctas, ws, st)
+                    : launch_many<64>(mk, mv, a, c, RT, ctas, ws, st);
+}
+
+}  // namespace vc

@@ -45,19 +45,6 @@ constexpr int kFewThreads = (kConsumers + 4) * 32;  // the producers' warpgroup 
 constexpr int kKeyWarp = kConsumers, kValueWarp = kConsumers + 1, kScaleWarp = kConsumers + 2;
 // 640 threads start with 96 registers each; 4 x 128 x 104 + 128 x 56 = 60,416 fit into those 61,440
 constexpr int kFewRegsUp = 104, kFewRegsDown = 56;
-constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
-constexpr float kZeroLog2 = -60.f;     // log2 sv of a token whose values are all zero
-constexpr uint64_t kTimeoutNs = 4000000000ull;
-
-struct StageInfo {
-    int flags;  // bits below
-    int key0;   // position of the stage's first key
-    int q0, n, L, h, r0, rows;
-    int box_ok;  // bit i: the stage's i-th run of min(128, page_size) keys has its page
-    int pad[7];
-};
-static_assert(sizeof(StageInfo) == 64, "one line");
-enum : int { kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8, kHead = 16, kTail = 32 };
 
 template <int D>
 struct FewCfg {
@@ -88,14 +75,6 @@ struct FewCfg {
     __device__ static int channel_of(int n) { return D == 128 ? ((n >> 1) + 4 * (n & 1)) * 16 : n * 8; }
 };
 
-// Four E4M3 codes -> four fp16.
-__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-        : "=r"(a), "=r"(b)
-        : "r"(w));
-}
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -108,42 +87,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float lg2_approx(float x) {
-    float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// Power of two that brings a row whose largest magnitude has the bf16 bits
-// `top` into [128, 256); 1 for rows of zeros and for rows that are not finite.
-__device__ __forceinline__ float row_factor(uint32_t top) {
-    if (top == 0u || top >= 0x7F80u) return 1.f;
-    const int e = max((int)(top >> 7), 14) - 127;
-    return __int_as_float((134 - e) << 23);
-}
-
-// Channels ch .. ch + N - 1 of row r (a (token, head) pair of its sequence), acc * inv as bf16.
-template <int N>
-__device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int r, int ch, const float (&acc)[N],
-                                          float inv) {
-    static_assert(N == 4, "8 bytes");
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-    const __nv_bfloat162 v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(a.O + (int64_t)(q0 + r / a.G) * a.o_sn + (int64_t)(h * a.G + r % a.G) * a.o_sh + ch) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
-}
-
-__device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c, int q0, int h, int r, float m,
-                                          float l) {
-    if (a.lse) a.lse[(int64_t)(q0 + r / a.G) * (c.H * a.G) + h * a.G + r % a.G] = lse_of(m, l);
 }
 
 template <int D, int RG>
@@ -508,7 +451,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         part.l[(size_t)slot * RT + row] = lsum;
                     }
                 } else {
-                    store_row<4>(a, q0, h, r0 + row, ch, acc, inverse_sum(lsum));
+                    store_row(a, q0, h, r0 + row, ch, acc, inverse_sum(lsum));
                     if (ch == 0) store_lse(a, c, q0, h, r0 + row, m, lsum);
                 }
             }
@@ -530,8 +473,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // rows is 8 KB, so this is a launch and a few L2 round trips.
 constexpr int kJoinThreads = 256;
 
-template <int D, int RT>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn a, const CacheView c, void* ws, int parts) {
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_kernel(const PagedAttn a, const CacheView c, void* ws, int RT, int parts) {
     __shared__ int s_end;
     const Partials part = partials_at(ws, RT, D);
     const int mine = blockIdx.x, i0 = 2 * mine + 1;
@@ -564,7 +508,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn a, c
                 acc[2] = fmaf(w, u.z, acc[2]);
                 acc[3] = fmaf(w, u.w, acc[3]);
             }
-            store_row<4>(a, hd.q0, hd.h, hd.r0 + row, ch, acc, inverse_sum(l));
+            store_row(a, hd.q0, hd.h, hd.r0 + row, ch, acc, inverse_sum(l));
             if (ch == 0) store_lse(a, c, hd.q0, hd.h, hd.r0 + row, m, l);
         }
     }
@@ -577,7 +521,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const PagedAttn a, c
             const int r0 = t * RT, rows = min(RT, s.n * a.G - r0);
             for (int i = threadIdx.x; i < c.H * rows * (D / 4); i += kJoinThreads) {
                 const int h = i / (rows * (D / 4)), row = i / (D / 4) % rows, ch = (i % (D / 4)) * 4;
-                store_row<4>(a, s.q0, h, r0 + row, ch, none, 0.f);
+                store_row(a, s.q0, h, r0 + row, ch, none, 0.f);
                 if (ch == 0) store_lse(a, c, s.q0, h, r0 + row, 0.f, 0.f);
             }
         }
@@ -600,11 +544,36 @@ bool make_cache_map(CUtensorMap* map, const uint8_t* base, int d, const CacheVie
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tile, by the rows of the longest chunk as far as the caller told.
+// Rows of a tile, by the rows of the longest chunk as far as the caller told: up
+// to 32 go to the kernel for few rows, more to the one for many.
 int tile_rows(int G, int B, int T, int max_q) {
     const int64_t q = max_q > 0 ? max_q : ((int64_t)T + B - 1) / B;
     const int64_t rows = q * G;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+}
+
+template <int D>
+vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, int parts, cudaStream_t st) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(parts);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D>, a, c, ws, RT, parts));
+}
+
+template <int D, int RG>
+vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
+                     int ctas, cudaStream_t st) {
+    auto kern = attn_few_kernel<D, RG>;
+    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
+    if (s != VC_OK) return s;
+    kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
+    return cuda_status(cudaGetLastError());
 }
 
 // CTAs of a call: as many as there can be units, one on each SM at most.
@@ -615,41 +584,18 @@ int part_count(const PagedAttn& a, const CacheView& c, int RT) {
     return (int)(tiles * c.H * units < kMaxCtas ? tiles * c.H * units : kMaxCtas);
 }
 
-template <int D, int RT>
-vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int parts, cudaStream_t st) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(parts);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D, RT>, a, c, ws, parts));
-}
-
-template <int D, int RG>
-vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
-                     cudaStream_t st) {
-    auto kern = attn_few_kernel<D, RG>;
-    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
-    if (s != VC_OK) return s;
-    const int ctas = part_count(a, c, 8 * RG);
-    kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
-    if ((s = cuda_status(cudaGetLastError())) != VC_OK) return s;
-    return launch_join<D, 8 * RG>(a, c, ws, ctas, st);
-}
-
 template <int D>
 vc_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
                    cudaStream_t st) {
-    switch (tile_rows(a.G, c.B, c.T, a.max_q)) {
-        case 8: return launch_few<D, 1>(mk, mv, a, c, ws, st);
-        case 16: return launch_few<D, 2>(mk, mv, a, c, ws, st);
-        case 32: return launch_few<D, 4>(mk, mv, a, c, ws, st);
-        default: return launch_few<D, 8>(mk, mv, a, c, ws, st);
+    const int RT = tile_rows(a.G, c.B, c.T, a.max_q), ctas = part_count(a, c, RT);
+    vc_status s;
+    switch (RT) {
+        case 8: s = launch_few<D, 1>(mk, mv, a, c, ws, ctas, st); break;
+        case 16: s = launch_few<D, 2>(mk, mv, a, c, ws, ctas, st); break;
+        case 32: s = launch_few<D, 4>(mk, mv, a, c, ws, ctas, st); break;
+        default: s = launch_attn_many(mk, mv, a, c, D, RT, ctas, ws, st);
     }
+    return s == VC_OK ? launch_join<D>(a, c, ws, RT, ctas, st) : s;
 }
 
 }  // namespace

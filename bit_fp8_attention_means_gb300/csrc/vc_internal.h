@@ -100,5 +100,8 @@ vc_status launch_cache_read(const CacheView& c, int d, uint16_t* K, uint16_t* V,
                             cudaStream_t st);
 size_t attn_paged_workspace(const vc_cache_shape& c, int Hq, int B, int T, int max_q);
 vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void* ws, cudaStream_t st);
+// its kernel for many rows, in tiles of RT = 128 or 256 (vc_attn_chunk.cu)
+vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
+                           int d, int RT, int ctas, void* ws, cudaStream_t st);
 
 }  // namespace vc

@@ -5,6 +5,8 @@
 #pragma once
 #include <cstdint>
 
+#include <cuda_bf16.h>
+
 #include "vc_device.cuh"
 #include "vc_internal.h"
 
@@ -260,6 +262,65 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // Weight of a part with maximum m_part in a whole with maximum m.
 __device__ __forceinline__ float part_weight(float m_part, float m) {
     return m_part == -INFINITY ? 0.f : ex2_approx(m_part - m);
+}
+
+// ------------------------------------------------------------ shared by the attention kernels
+
+constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
+constexpr float kZeroLog2 = -60.f;     // log2 sv of a token whose values are all zero
+constexpr uint64_t kTimeoutNs = 4000000000ull;  // bound of every wait
+
+// What a producer tells the other warps of a CTA about a unit.
+struct StageInfo {
+    int flags;  // bits below
+    int key0;   // position of the stage's first key
+    int q0, n, L, h, r0, rows;
+    int box_ok;  // bit i: the stage's i-th run of min(128, page_size) keys has its page
+    int pad[7];
+};
+static_assert(sizeof(StageInfo) == 64, "one line");
+enum : int { kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8, kHead = 16, kTail = 32 };
+
+// Four E4M3 codes -> four fp16.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(a), "=r"(b)
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Power of two that brings a row whose largest magnitude has the bf16 bits
+// `top` into [128, 256); 1 for rows of zeros and for rows that are not finite.
+__device__ __forceinline__ float row_factor(uint32_t top) {
+    if (top == 0u || top >= 0x7F80u) return 1.f;
+    const int e = max((int)(top >> 7), 14) - 127;
+    return __int_as_float((134 - e) << 23);
+}
+
+// Channels ch .. ch + 3 of row r (a (token, head) pair of its sequence), acc * inv as bf16.
+__device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int r, int ch, const float (&acc)[4],
+                                          float inv) {
+    const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+    const __nv_bfloat162 v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2*>(a.O + (int64_t)(q0 + r / a.G) * a.o_sn + (int64_t)(h * a.G + r % a.G) * a.o_sh + ch) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+}
+
+__device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c, int q0, int h, int r, float m,
+                                          float l) {
+    if (a.lse) a.lse[(int64_t)(q0 + r / a.G) * (c.H * a.G) + h * a.G + r % a.G] = lse_of(m, l);
 }
 
 }  // namespace vc
