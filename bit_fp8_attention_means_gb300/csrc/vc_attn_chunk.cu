@@ -43,8 +43,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kLoadWarp = 14;
-// 512 x 128 registers at launch; 2 x 128 x 168 + 128 x 96 + 128 x 72 = 64,512 fit into those 65,536
-constexpr int kRegsSoftmax = 168, kRegsConv = 96, kRegsOther = 72;
+// 512 x 128 registers at launch: 2 x 128 x 184 + 2 x 128 x 72 = 65,536
+constexpr int kRegsSoftmax = 184, kRegsConv = 72, kRegsOther = 72;
 
 template <int D>
 struct ManyCfg {
@@ -85,21 +85,27 @@ __host__ __device__ constexpr uint32_t idesc_f16_bn(uint32_t M, uint32_t N) {
     return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+__device__ __forceinline__ uint64_t no_hoist(uint64_t x) {
+    asm volatile("" : "+l"(x));
+    return x;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedAttn a, const CacheView c, int RT, void* ws) {
     using C = ManyCfg<D>;
+    // offsets from the array itself: through an integer the compiler would lose sight of
+    // the address space, and generic loads take the slow road to shared memory
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) -> uint32_t { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const Partials part = partials_at(ws, RT, D);
     auto wait = [&](int i, int phase) -> bool {
-        return mbar_wait_short(bar(i), phase & 1, abort_flag, c.dev_status, kTimeoutNs);
+        return mbar_wait_suspended(bar(i), phase & 1, abort_flag, c.dev_status, kTimeoutNs);
     };
 
     if (threadIdx.x == 0) {
@@ -125,6 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         init(C::TD, 2, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        const Partials part = partials_at(ws, RT, D);
         part.head[2 * blockIdx.x].valid = 0;
         part.head[2 * blockIdx.x + 1].valid = 0;
     }
@@ -264,13 +271,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine) {
                     // S is free: the product that reads the last P from its place was issued before
                     tc_fence_after();
+                    // steps of 32 bytes (2 in a descriptor's units); no_hoist keeps the
+                    // descriptors from being held in registers across units
+                    const uint64_t kd = no_hoist(smem_desc(sbase + C::OFF_K + sk * C::TILE, 8 * D, C::SWZ));
+                    const uint64_t qd = no_hoist(smem_desc(sbase + C::OFF_Q + 2 * X * C::QB, 8 * D, C::SWZ));
 #pragma unroll
-                    for (int i = 0; i < 2 * (D / 32); ++i) {
-                        const uint32_t qa = sbase + C::OFF_Q + (2 * X + i / (D / 32)) * C::QB + (i % (D / 32)) * 32;
-                        const uint32_t kb = sbase + C::OFF_K + sk * C::TILE + (i % (D / 32)) * 32;
-                        mma_f8_ss_w(tb + D, smem_desc(qa, 8 * D, C::SWZ), smem_desc(kb, 8 * D, C::SWZ), IDESC_QK,
-                                    i > 0 ? 1u : 0u);
-                    }
+                    for (int i = 0; i < 2 * (D / 32); ++i)
+                        mma_f8_ss_w(tb + D, qd + (i / (D / 32)) * (C::QB / 16) + (i % (D / 32)) * 2,
+                                    kd + (i % (D / 32)) * 2, IDESC_QK, i > 0 ? 1u : 0u);
                     mma_commit_w(bar(C::SF + X));
                     mma_commit_w(bar(C::KE + sk));
                 } else if (lane == 0) {
@@ -282,12 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mine) {
                     if (!wait(C::PF + X, own)) break;
                     tc_fence_after();
+                    const uint64_t wd =
+                        no_hoist(smem_desc_lbo(sbase + C::OFF_W + sw * C::WB, 128 * 128, 1024, kSwizzle128B));
 #pragma unroll
-                    for (int i = 0; i < kUnit / 16; ++i) {
-                        const uint64_t bd =
-                            smem_desc_lbo(sbase + C::OFF_W + sw * C::WB + i * 2048, 128 * 128, 1024, kSwizzle128B);
-                        mma_bf16_ts_w(tb, tb + D + i * 8, bd, IDESC_PV, (fresh && i == 0) ? 0u : 1u);
-                    }
+                    for (int i = 0; i < kUnit / 16; ++i)
+                        mma_bf16_ts_w(tb, tb + D + i * 8, wd + i * 128, IDESC_PV, (fresh && i == 0) ? 0u : 1u);
                     mma_commit_w(bar(C::WE + sw));
                     fresh = false;
                     ++own;
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* vs = smem + C::OFF_V + sv * C::TILE;
             uint8_t* wd = smem + C::OFF_W + sw * C::WB;
             constexpr int PIECES = D / 16;  // 16 codes each
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < PIECES; ++i) {
                 const int r = (i * 128 + t) / PIECES, ch = t % PIECES;
                 uint4 x = *reinterpret_cast<const uint4*>(vs + C::chunk(r, ch));
@@ -371,18 +378,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(C::IF + it % C::NI, it / C::NI)) break;
             const StageInfo* f = info_at(it);
             const int flags = f->flags, key0 = f->key0, place = f->pad[0];
-            const int q0 = f->q0, n = f->n, L = f->L, h = f->h, r0 = f->r0, rows = f->rows;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
             if (flags & kEnd) break;
-            const bool both = rows > 128, mine = both || (place & 1) == X;
+            const bool both = f->rows > 128, mine = both || (place & 1) == X;
             const int tr = both ? X * 128 + row : row;  // this thread's row of the tile
             if (flags & kFirst) {
                 // the row's two E4M3 parts; the products that read the last item's have completed
-                const bool there = tr < rows;
-                const int r = r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
-                const uint4* src = reinterpret_cast<const uint4*>(a.Q + (int64_t)(q0 + tok) * a.q_sn +
-                                                                  (int64_t)(h * a.G + j) * a.q_sh);
+                const bool there = tr < f->rows;
+                const int r = f->r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
+                const uint4* src = reinterpret_cast<const uint4*>(a.Q + (int64_t)(f->q0 + tok) * a.q_sn +
+                                                                  (int64_t)(f->h * a.G + j) * a.q_sh);
                 uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::QF + X));
-                const SeqInfo s{q0, n, L};
+                const SeqInfo s{f->q0, f->n, f->L};
                 last = row_last(a, s, tok);
                 first = row_first(a, last);
                 M = -INFINITY;
@@ -449,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(-m, -m);
                     float2 l2 = make_float2(0.f, 0.f);
                     float mx = -INFINITY;
-                    uint32_t s0[32], s1[32];
-                    auto part32 = [&](const uint32_t(&s)[32], int cc) {
+                    uint32_t s0[16], s1[16];
+                    auto part16 = [&](const uint32_t(&s)[16], int cc) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const int at = (cc * 32 + i) / 4;
+                        for (int i = 0; i < 16; i += 4) {
+                            const int at = (cc * 16 + i) / 4;
                             const float4 sk = scl[at], lv = scl[kUnit / 4 + at], iv = scl[kUnit / 2 + at];
                             float2 y0 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
                                                               make_float2(sk.x, sk.y)),
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            make_float2(sk.z, sk.w)),
                                 qs2, make_float2(lv.z, lv.w));
                             if (MASKED) {
-                                const int k = cc * 32 + i;
+                                const int k = cc * 16 + i;
                                 if (k < lo || k > hi) y0.x = -INFINITY;
                                 if (k + 1 < lo || k + 1 > hi) y0.y = -INFINITY;
                                 if (k + 2 < lo || k + 2 > hi) y1.x = -INFINITY;
@@ -476,22 +480,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                             y1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
                             l2 = __ffma2_rn(y0, make_float2(iv.x, iv.y), l2);
                             l2 = __ffma2_rn(y1, make_float2(iv.z, iv.w), l2);
-                            pw[cc * 16 + i / 2] = pack_f16(y0.x, y0.y);
-                            pw[cc * 16 + i / 2 + 1] = pack_f16(y1.x, y1.y);
+                            pw[cc * 8 + i / 2] = pack_f16(y0.x, y0.y);
+                            pw[cc * 8 + i / 2 + 1] = pack_f16(y1.x, y1.y);
                         }
                     };
-                    tmem_ld32(la + D, s0);
+                    // 16 scores at a time, the next ones on their way
+                    tmem_ld16(la + D, s0);
                     tmem_wait_ld();
-                    tmem_ld32(la + D + 32, s1);
-                    part32(s0, 0);
-                    tmem_wait_ld();
-                    tmem_ld32(la + D + 64, s0);
-                    part32(s1, 1);
-                    tmem_wait_ld();
-                    tmem_ld32(la + D + 96, s1);
-                    part32(s0, 2);
-                    tmem_wait_ld();
-                    part32(s1, 3);
+#pragma unroll
+                    for (int cc = 0; cc < kUnit / 16; cc += 2) {
+                        tmem_ld16(la + D + (cc + 1) * 16, s1);
+                        part16(s0, cc);
+                        tmem_wait_ld();
+                        if (cc + 2 < kUnit / 16) tmem_ld16(la + D + (cc + 2) * 16, s0);
+                        part16(s1, cc + 1);
+                        tmem_wait_ld();
+                    }
                     lsum = l2.x + l2.y;
                     return mx;
                 };
@@ -547,6 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::CE + sc));
+            const int q0 = f->q0, h = f->h, r0 = f->r0, rows = f->rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
             if (!(flags & kLast)) continue;
 
             // ------------------------------------------------------------ the item's end
@@ -583,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = split ? 1.f : inverse_sum(l);
             wa *= inv;
             wb *= inv;
+            const Partials part = partials_at(ws, RT, D);
             float* po = part.o + ((size_t)slot * RT + (there ? tr : 0)) * D;
             uint16_t* dst = a.O + (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
 #pragma unroll 1

@@ -95,8 +95,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     const PagedAttn a, const CacheView c, void* ws) {
     using C = FewCfg<D>;
     constexpr int NS = C::NS, RT = 8 * RG;
+    // offsets from the array itself: through an integer the compiler would lose sight of
+    // the address space, and generic loads take the slow road to shared memory
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full = sbase + C::OFF_BAR, empty = full + 8 * NS, written = empty + 8 * NS, read = written + 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                     const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
                     if (it >= NS &&
-                        !mbar_wait_short(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                        !mbar_wait_suspended(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
                         ok = false;
                         break;
                     }
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 // the stage that ends the consumers' loop
                 const int st = it % NS;
                 if (it < NS ||
-                    mbar_wait_short(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                    mbar_wait_suspended(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
                     if (lane == 0 && warp == kKeyWarp)
                         reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
                     if (lane == 0) mbar_arrive(full + 8 * st);
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         int it = 0, items = 0;
         while (true) {
             const int st = it % NS;
-            if (!mbar_wait_short(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (!mbar_wait_suspended(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
             const StageInfo* info = reinterpret_cast<const StageInfo*>(smem + C::OFF_INFO + st * 64);
             const int flags = info->flags;
             if (flags & kEnd) break;
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
             // ------------------------------------------------------------ the item's end
             // the accumulators are free to overwrite once the last item's were read
-            if (items > 0 && !mbar_wait_short(read, (items - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (items > 0 && !mbar_wait_suspended(read, (items - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(written);
-            if (!mbar_wait_short(written, items & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (!mbar_wait_suspended(written, items & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
             const bool split = flags & (kHead | kTail);
             const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
             for (int i = threadIdx.x; i < rows * (D / 4); i += kConsumers * 32) {

@@ -97,14 +97,32 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status, timeout_ns));
 }
 
-// mbar_wait_warp for waits that are short as a rule: the timer (a slow read) is
-// looked at only after 64 attempts, each of which may suspend the thread for a
-// while, so the bound is timeout_ns past that.
-__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                int32_t* dev_status, uint64_t timeout_ns) {
+// mbar_wait_warp that leaves the issue slots to the other warps: an attempt may
+// suspend the thread for up to 20 us, and the timer (a slow read) is looked at
+// only after a failed one.  With attempts that return at once, five waiting
+// warps spent half of a CTA's instructions.
+__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                    int32_t* dev_status, uint64_t timeout_ns) {
     bool ok = mbar_test_wait(bar, parity);
-    for (int i = 0; !ok && i < 64; ++i) ok = mbar_try_wait(bar, parity);
-    if (!ok) ok = mbar_wait(bar, parity, abort_flag, dev_status, timeout_ns);
+    for (uint64_t t0 = 0; !ok;) {
+        uint32_t got;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(got)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        ok = got != 0;
+        if (ok || *abort_flag) break;
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > timeout_ns) {
+            *abort_flag = 1;
+            if (dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
+            break;
+        }
+    }
     return __all_sync(0xffffffffu, ok);
 }
 
