@@ -85,8 +85,13 @@ __host__ __device__ constexpr uint32_t idesc_f16_bn(uint32_t M, uint32_t N) {
     return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// The same value, as far as the compiler may know another one each time.
 __device__ __forceinline__ uint64_t no_hoist(uint64_t x) {
     asm volatile("" : "+l"(x));
+    return x;
+}
+__device__ __forceinline__ int no_hoist(int x) {
+    asm volatile("" : "+r"(x));
     return x;
 }
 
@@ -441,8 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(C::SF + X, own)) break;
                 ++own;
                 tc_fence_after();
-                const float4* scl = reinterpret_cast<const float4*>(smem + C::OFF_SC + sc * (3 * kUnit * 4));
-                const int lo = first - key0, hi = last - key0;  // the unit's keys that this row sees
+                const uint32_t scl = sbase + C::OFF_SC + sc * (3 * kUnit * 4);
                 uint32_t pw[kUnit / 2];
                 float lsum;
                 // Scores, probabilities against M and the row's maximum, in one pass; again
@@ -451,52 +455,72 @@ __global__ void __launch_bounds__(kThreads, 1)
                     constexpr bool MASKED = decltype(masked_tag)::value;
                     const float m = M == -INFINITY ? 0.f : M;
                     const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(-m, -m);
-                    float2 l2 = make_float2(0.f, 0.f);
+                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
                     float mx = -INFINITY;
-                    uint32_t s0[16], s1[16];
-                    auto part16 = [&](const uint32_t(&s)[16], int cc) {
+                    uint32_t s0[32], s1[32];
+                    // Step by step over 32 scores, so that 16 independent operations stand
+                    // behind one another instead of 4.
+                    auto part32 = [&](const uint32_t(&s)[32], int cc) {
+                        float2 y[16];
+                        int lo, hi;  // the unit's keys that this row sees
+                        if (MASKED) {
+                            // computed here: 128 comparisons taken out of the repetition would
+                            // be made for every unit
+                            lo = no_hoist(first - key0);
+                            hi = no_hoist(last - key0);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const int at = (cc * 16 + i) / 4;
-                            const float4 sk = scl[at], lv = scl[kUnit / 4 + at], iv = scl[kUnit / 2 + at];
-                            float2 y0 = __ffma2_rn(__fmul2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
-                                                              make_float2(sk.x, sk.y)),
-                                                   qs2, make_float2(lv.x, lv.y));
-                            float2 y1 = __ffma2_rn(
-                                __fmul2_rn(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])),
+                        for (int i = 0; i < 16; i += 2) {
+                            const uint32_t at = scl + (cc * 32 + 2 * i) * 4;
+                            const float4 sk = ld_shared4(at), lv = ld_shared4(at + kUnit * 4);
+                            y[i] = __ffma2_rn(
+                                __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                           make_float2(sk.x, sk.y)),
+                                qs2, make_float2(lv.x, lv.y));
+                            y[i + 1] = __ffma2_rn(
+                                __fmul2_rn(make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])),
                                            make_float2(sk.z, sk.w)),
                                 qs2, make_float2(lv.z, lv.w));
-                            if (MASKED) {
-                                const int k = cc * 16 + i;
-                                if (k < lo || k > hi) y0.x = -INFINITY;
-                                if (k + 1 < lo || k + 1 > hi) y0.y = -INFINITY;
-                                if (k + 2 < lo || k + 2 > hi) y1.x = -INFINITY;
-                                if (k + 3 < lo || k + 3 > hi) y1.y = -INFINITY;
+                        }
+                        if (MASKED) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = cc * 32 + 2 * i;
+                                if (k < lo || k > hi) y[i].x = -INFINITY;
+                                if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
                             }
-                            mx = max3(max3(mx, y0.x, y0.y), y1.x, y1.y);
-                            y0 = __fadd2_rn(y0, nm2);
-                            y1 = __fadd2_rn(y1, nm2);
-                            y0 = make_float2(ex2_approx(y0.x), ex2_approx(y0.y));
-                            y1 = make_float2(ex2_approx(y1.x), ex2_approx(y1.y));
-                            l2 = __ffma2_rn(y0, make_float2(iv.x, iv.y), l2);
-                            l2 = __ffma2_rn(y1, make_float2(iv.z, iv.w), l2);
-                            pw[cc * 8 + i / 2] = pack_f16(y0.x, y0.y);
-                            pw[cc * 8 + i / 2 + 1] = pack_f16(y1.x, y1.y);
+                        }
+                        float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) m4[i & 3] = max3(m4[i & 3], y[i].x, y[i].y);
+                        mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = __fadd2_rn(y[i], nm2);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 iv = ld_shared4(scl + 2 * kUnit * 4 + (cc * 32 + 2 * i) * 4);
+                            l2 = __ffma2_rn(y[i], make_float2(iv.x, iv.y), l2);
+                            l3 = __ffma2_rn(y[i + 1], make_float2(iv.z, iv.w), l3);
+                            pw[cc * 16 + i] = pack_f16(y[i].x, y[i].y);
+                            pw[cc * 16 + i + 1] = pack_f16(y[i + 1].x, y[i + 1].y);
                         }
                     };
-                    // 16 scores at a time, the next ones on their way
-                    tmem_ld16(la + D, s0);
+                    // 32 scores at a time, the next ones on their way
+                    tmem_ld32(la + D, s0);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int cc = 0; cc < kUnit / 16; cc += 2) {
-                        tmem_ld16(la + D + (cc + 1) * 16, s1);
-                        part16(s0, cc);
-                        tmem_wait_ld();
-                        if (cc + 2 < kUnit / 16) tmem_ld16(la + D + (cc + 2) * 16, s0);
-                        part16(s1, cc + 1);
-                        tmem_wait_ld();
-                    }
-                    lsum = l2.x + l2.y;
+                    tmem_ld32(la + D + 32, s1);
+                    part32(s0, 0);
+                    tmem_wait_ld();
+                    tmem_ld32(la + D + 64, s0);
+                    part32(s1, 1);
+                    tmem_wait_ld();
+                    tmem_ld32(la + D + 96, s1);
+                    part32(s0, 2);
+                    tmem_wait_ld();
+                    part32(s1, 3);
+                    lsum = (l2.x + l2.y) + (l3.x + l3.y);
                     return mx;
                 };
                 auto run = [&]() -> float {
