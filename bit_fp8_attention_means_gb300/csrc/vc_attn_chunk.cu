@@ -1,6 +1,14 @@
 // vc_attn_chunk.cu -- vc_attn_paged for chunks of many rows, on tcgen05.
 //
-// The mathematics is that of vc_attn_paged.cu.  One persistent CTA on each SM
+// Per row, over its keys t, with the cached codes k8, v8 and scales sk, sv:
+//   s_t = (q . k8_t) sk_t scale log2 e,   P_t = 2^(s_t - M),   l = sum_t P_t,
+//   A = sum_t (P_t sv_t) v8_t,            O = A / l,
+// M being the running maximum of s_t + log2 sv_t: P sv, which goes to the product
+// as fp16, is then at most 1 whatever the scales are.  M follows only where P sv
+// would pass 2^8 (far inside fp16), which the units themselves show; where it
+// does, a pass of its own over the unit finds the new M.
+//
+// One persistent CTA on each SM
 // takes tiles of 256 rows as two pipelines A and B of 128 rows, which share the
 // keys and values and the tensor core, so that the softmax of one overlaps the
 // products of the other; a tile of up to 128 rows is given to both, which then
@@ -22,8 +30,8 @@
 //
 // 16 warps:
 //   0-3, 4-7  softmax of A and B: a thread owns a row (its TMEM lane).
-//   8-11      converter: a thread owns a key for the scales (log2 sv, 1 / sv),
-//             and 16-byte pieces of the values.
+//   8-11      converter: a thread owns a key for the scales and 16-byte pieces of
+//             the values.
 //   12, 13    MMA issuers of A and B (12 owns the tensor memory).
 //   14        loader: K8, V8 and scales by TMA and bulk copies, and what the
 //             others need to know of a unit.  15 is idle.
@@ -57,8 +65,8 @@ struct ManyCfg {
     static constexpr int OFF_V = OFF_K + NK * TILE;
     static constexpr int OFF_W = OFF_V + NV * TILE;
     static constexpr int OFF_RAW = OFF_W + NW * WB;       // [NV][sk | sv][128]
-    static constexpr int OFF_SC = OFF_RAW + NV * 2 * kUnit * 4;  // [NC][sk | log2 sv | 1 / sv][128]
-    static constexpr int OFF_ML = OFF_SC + NC * 3 * kUnit * 4;   // [m | l][128] of B, for A
+    static constexpr int OFF_SC = OFF_RAW + NV * 2 * kUnit * 4;  // [NC][sk | sv][128], 0 where there is no token
+    static constexpr int OFF_ML = OFF_SC + NC * 2 * kUnit * 4;   // [m | l][128] of B, for A
     static constexpr int OFF_INFO = OFF_ML + 2 * 128 * 4;
     static constexpr int OFF_BAR = OFF_INFO + NI * 64;
     static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
@@ -187,10 +195,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int key0 = u * kUnit;
                     int pg = ahead;
                     ahead = entry(u + 1);
-                    if (pg == -2 || pg >= c.pages) {
+                    const bool missing = pg == -2 || pg >= c.pages;
+                    if (missing) {
                         flag_invalid(c.dev_status);
                         pg = -1;
                     }
+                    const bool holes = __any_sync(0xffffffffu, missing);
                     const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
                     ok = it < C::NI || wait(C::IE + it % C::NI, it / C::NI - 1);
                     if (!ok) break;
@@ -198,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         StageInfo* f = const_cast<StageInfo*>(info_at(it));
                         const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all;
                         f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) |
-                                   (all_seen ? 0 : kMasked) | (w.head ? kHead : 0) | (w.tail ? kTail : 0);
+                                   (all_seen && !holes ? 0 : kMasked) | (holes ? kHoles : 0) | (w.head ? kHead : 0) |
+                                   (w.tail ? kTail : 0);
                         f->key0 = key0;
                         f->q0 = w.s.q0;
                         f->n = w.s.n;
@@ -326,19 +337,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int flags = f->flags, key0 = f->key0, L = f->L, box_ok = f->box_ok;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
-            if (flags & kEnd) break;
             const int sv = it % C::NV, sw = it % C::NW, sc = it % C::NC;
-            if (!wait(C::VF + sv, it / C::NV)) break;
             if (it >= C::NC && !wait(C::CE + sc, it / C::NC - 1)) break;
+            if (flags & kEnd) {
+                if (lane == 0) mbar_arrive(bar(C::CF + sc));
+                break;
+            }
+            if (!wait(C::VF + sv, it / C::NV)) break;
             {
                 const float* raw = reinterpret_cast<const float*>(smem + C::OFF_RAW + sv * (2 * kUnit * 4));
-                float* out = reinterpret_cast<float*>(smem + C::OFF_SC + sc * (3 * kUnit * 4));
+                float* out = reinterpret_cast<float*>(smem + C::OFF_SC + sc * (2 * kUnit * 4));
                 const bool there = key0 + t < L && ((box_ok >> (t >> box_log2)) & 1);
                 const float k = raw[t], v = raw[kUnit + t];
-                out[t] = there ? k : 0.f;
-                out[kUnit + t] = !there ? -INFINITY : v == 0.f ? kZeroLog2 : lg2_approx(v);
-                // a NaN scale makes the score NaN where it is seen; elsewhere 0 / sv has to stay 0
-                out[2 * kUnit + t] = !there ? 0.f : v == 0.f ? 0x1p60f : v > 0.f ? __fdividef(1.f, v) : 0.f;
+                const bool number = v < INFINITY;
+                // a token whose values are not numbers gets a score that is none: it spoils the
+                // rows that see it and no other, for which 0 * 0 stays 0
+                out[t] = !there ? 0.f : number ? k : __int_as_float(0x7FFFFFFF);
+                out[kUnit + t] = there && number ? v : 0.f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::CF + sc));
             }
@@ -380,7 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int last = -1, first = 0, items = 0, own = 0, shared = 0;
         bool fresh = true;
         for (int it = 0;; ++it) {
-            if (!wait(C::IF + it % C::NI, it / C::NI)) break;
+            const int sc = it % C::NC;
+            // the converter has seen the unit's info and passes it on with the scales
+            if (!wait(C::CF + sc, it / C::NC)) break;
             const StageInfo* f = info_at(it);
             const int flags = f->flags, key0 = f->key0, place = f->pad[0];
             if (flags & kEnd) break;
@@ -440,72 +457,111 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = 0.f;
                 fresh = true;
             }
-            const int sc = it % C::NC;
-            if (!wait(C::CF + sc, it / C::NC)) break;
             if (mine) {
                 if (!wait(C::SF + X, own)) break;
                 ++own;
                 tc_fence_after();
-                const uint32_t scl = sbase + C::OFF_SC + sc * (3 * kUnit * 4);
+                const uint32_t scl = sbase + C::OFF_SC + sc * (2 * kUnit * 4);
                 uint32_t pw[kUnit / 2];
-                float lsum;
-                // Scores, probabilities against M and the row's maximum, in one pass; again
-                // with the new M where the maximum has risen too far.
-                auto pass = [&](auto masked_tag) -> float {
-                    constexpr bool MASKED = decltype(masked_tag)::value;
-                    const float m = M == -INFINITY ? 0.f : M;
-                    const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(-m, -m);
-                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
-                    float mx = -INFINITY;
-                    uint32_t s0[32], s1[32];
-                    // Step by step over 32 scores, so that 16 independent operations stand
-                    // behind one another instead of 4.
-                    auto part32 = [&](const uint32_t(&s)[32], int cc) {
+                const float2 qs2 = make_float2(qs, qs);
+                // y: the scaled scores s of keys 32 cc .. 32 cc + 31, -inf where the row does not see
+                // the key.  Step by step over 32, so that 16 independent operations stand behind
+                // one another.
+                auto hide = [&](float2(&y)[16], int cc) {
+                    // computed here: comparisons taken out of a loop would be made for every unit
+                    const int lo = no_hoist(first - key0), hi = no_hoist(last - key0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int k = cc * 32 + 2 * i;
+                        if (k < lo || k > hi) y[i].x = -INFINITY;
+                        if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
+                    }
+                    if (flags & kHoles) {
+                        const int box_ok = f->box_ok;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)  // runs are even
+                            if (!((box_ok >> ((cc * 32 + 2 * i) >> box_log2)) & 1))
+                                y[i] = make_float2(-INFINITY, -INFINITY);
+                    }
+                };
+                // The unit's part of M: the maximum of s + log2 sv, and of s - 100, which keeps P
+                // finite where a row sees little but tokens whose values are all zero.
+                auto find_m = [&]() -> float {
+                    float mj = -INFINITY, ms = -INFINITY;
+#pragma unroll 1
+                    for (int cc = 0; cc < 4; ++cc) {
+                        uint32_t s[32];
                         float2 y[16];
-                        int lo, hi;  // the unit's keys that this row sees
-                        if (MASKED) {
-                            // computed here: 128 comparisons taken out of the repetition would
-                            // be made for every unit
-                            lo = no_hoist(first - key0);
-                            hi = no_hoist(last - key0);
+                        tmem_ld32(la + D + cc * 32, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 sk = ld_shared4(scl + (cc * 32 + 2 * i) * 4);
+                            y[i] = __fmul2_rn(y[i], make_float2(sk.x, sk.y));
+                            y[i + 1] = __fmul2_rn(y[i + 1], make_float2(sk.z, sk.w));
+                        }
+                        if (flags & kMasked) {
+                            const int lo = first - key0 - cc * 32, hi = last - key0 - cc * 32;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const bool hole =
+                                    (flags & kHoles) && !((f->box_ok >> ((cc * 32 + 2 * i) >> box_log2)) & 1);
+                                if (2 * i < lo || 2 * i > hi || hole) y[i].x = -INFINITY;
+                                if (2 * i + 1 < lo || 2 * i + 1 > hi || hole) y[i].y = -INFINITY;
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const uint32_t at = scl + (cc * 32 + 2 * i) * 4;
-                            const float4 sk = ld_shared4(at), lv = ld_shared4(at + kUnit * 4);
-                            y[i] = __ffma2_rn(
-                                __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                                           make_float2(sk.x, sk.y)),
-                                qs2, make_float2(lv.x, lv.y));
-                            y[i + 1] = __ffma2_rn(
-                                __fmul2_rn(make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])),
-                                           make_float2(sk.z, sk.w)),
-                                qs2, make_float2(lv.z, lv.w));
+                            const float4 sv = ld_shared4(scl + kUnit * 4 + (cc * 32 + 2 * i) * 4);
+                            ms = max3(ms, fmaxf(y[i].x, y[i].y), fmaxf(y[i + 1].x, y[i + 1].y));
+                            mj = max3(mj, fmaf(y[i].x, qs, lg2_approx(sv.x)), fmaf(y[i].y, qs, lg2_approx(sv.y)));
+                            mj = max3(mj, fmaf(y[i + 1].x, qs, lg2_approx(sv.z)), fmaf(y[i + 1].y, qs, lg2_approx(sv.w)));
                         }
-                        if (MASKED) {
+                    }
+                    return fmaxf(mj, ms * qs - 100.f);
+                };
+                // P sv of the unit against M, as fp16 in pw; the sum of P; the largest P sv.
+                float lsum;
+                auto find_p = [&](auto masked_tag) -> float {
+                    constexpr bool MASKED = decltype(masked_tag)::value;
+                    const float m = M == -INFINITY ? 0.f : M;
+                    const float2 nm2 = make_float2(-m, -m);
+                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+                    float mx = 0.f;
+                    uint32_t s0[32], s1[32];
+                    auto part32 = [&](const uint32_t(&s)[32], int cc) {
+                        float2 y[16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int k = cc * 32 + 2 * i;
-                                if (k < lo || k > hi) y[i].x = -INFINITY;
-                                if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
-                            }
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 sk = ld_shared4(scl + (cc * 32 + 2 * i) * 4);
+                            y[i] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                              make_float2(sk.x, sk.y));
+                            y[i + 1] = __fmul2_rn(
+                                make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])),
+                                make_float2(sk.z, sk.w));
                         }
-                        float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) m4[i & 3] = max3(m4[i & 3], y[i].x, y[i].y);
-                        mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __fadd2_rn(y[i], nm2);
+                        for (int i = 0; i < 16; ++i) y[i] = __ffma2_rn(y[i], qs2, nm2);
+                        if (MASKED) hide(y, cc);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const float4 iv = ld_shared4(scl + 2 * kUnit * 4 + (cc * 32 + 2 * i) * 4);
-                            l2 = __ffma2_rn(y[i], make_float2(iv.x, iv.y), l2);
-                            l3 = __ffma2_rn(y[i + 1], make_float2(iv.z, iv.w), l3);
-                            pw[cc * 16 + i] = pack_f16(y[i].x, y[i].y);
-                            pw[cc * 16 + i + 1] = pack_f16(y[i + 1].x, y[i + 1].y);
+                            const float4 sv = ld_shared4(scl + kUnit * 4 + (cc * 32 + 2 * i) * 4);
+                            l2 = __fadd2_rn(l2, y[i]);
+                            l3 = __fadd2_rn(l3, y[i + 1]);
+                            y[i] = __fmul2_rn(y[i], make_float2(sv.x, sv.y));
+                            y[i + 1] = __fmul2_rn(y[i + 1], make_float2(sv.z, sv.w));
                         }
+                        float m4[4] = {mx, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            m4[i & 3] = max3(m4[i & 3], y[i].x, y[i].y);
+                            pw[cc * 16 + i] = pack_f16(y[i].x, y[i].y);
+                        }
+                        mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
                     };
                     // 32 scores at a time, the next ones on their way
                     tmem_ld32(la + D, s0);
@@ -523,20 +579,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     lsum = (l2.x + l2.y) + (l3.x + l3.y);
                     return mx;
                 };
-                auto run = [&]() -> float {
-                    return (flags & kMasked) ? pass(std::true_type{}) : pass(std::false_type{});
-                };
                 float alpha = 1.f;
+                bool raise = M == -INFINITY;
 #pragma unroll 1
                 for (int rep = 0; rep < 2; ++rep) {
-                    const float mx = (flags & kMasked) ? pass(std::true_type{}) : pass(std::false_type{});
-                    const bool rise = mx > M + kStale;
-                    if (rep || !__any_sync(0xffffffffu, rise)) break;
-                    if (rise) {
-                        alpha = part_weight(M, mx);
-                        M = mx;
-                        l *= alpha;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float mu = find_m();
+                        if (raise && mu > M) {
+                            const float w = part_weight(M, mu);
+                            M = mu;
+                            l *= w;
+                            alpha *= w;
+                        }
                     }
+                    const float mx = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
+                    // a sum that is infinite: a token whose values are all zero far above M
+                    raise = mx > 256.f || lsum == INFINITY;
+                    if (!__any_sync(0xffffffffu, raise)) break;
                 }
                 l += lsum;
                 if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {

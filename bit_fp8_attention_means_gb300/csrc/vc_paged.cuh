@@ -279,7 +279,7 @@ struct StageInfo {
     int pad[7];
 };
 static_assert(sizeof(StageInfo) == 64, "one line");
-enum : int { kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8, kHead = 16, kTail = 32 };
+enum : int { kFirst = 1, kLast = 2, kMasked = 4, kEnd = 8, kHead = 16, kTail = 32, kHoles = 64 };
 
 // Four E4M3 codes -> four fp16.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
