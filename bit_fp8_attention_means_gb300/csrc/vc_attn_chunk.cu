@@ -4,9 +4,10 @@
 //   s_t = (q . k8_t) sk_t scale log2 e,   P_t = 2^(s_t - M),   l = sum_t P_t,
 //   A = sum_t (P_t sv_t) v8_t,            O = A / l,
 // M being the running maximum of s_t + log2 sv_t: P sv, which goes to the product
-// as fp16, is then at most 1 whatever the scales are.  M follows only where P sv
-// would pass 2^8 (far inside fp16), which the units themselves show; where it
-// does, a pass of its own over the unit finds the new M.
+// as fp16, is then at most 1 whatever the scales are.  M follows only where the
+// unit's sum of P times its largest sv passes 2^15, so that P sv stays finite in
+// fp16 (whose precision is the same up to there) without a maximum being taken;
+// then a pass of its own over the unit finds the new M.
 //
 // One persistent CTA on each SM
 // takes tiles of 256 rows as two pipelines A and B of 128 rows, which share the
@@ -54,6 +55,9 @@ constexpr int kConvWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 // 512 x 128 registers at launch: 2 x 128 x 184 + 2 x 128 x 72 = 65,536
 constexpr int kRegsSoftmax = 184, kRegsConv = 72, kRegsOther = 72;
 
+// A unit's scales: sk[128], sv[128] (0 where there is no token), the largest sv of each 32.
+constexpr int kScaleBytes = (2 * kUnit + 4) * 4;
+
 template <int D>
 struct ManyCfg {
     static constexpr int NK = 3, NV = 2, NW = 2, NC = 3, NI = 4;  // stages: K8, V8, fp16 V, scales, infos
@@ -65,8 +69,8 @@ struct ManyCfg {
     static constexpr int OFF_V = OFF_K + NK * TILE;
     static constexpr int OFF_W = OFF_V + NV * TILE;
     static constexpr int OFF_RAW = OFF_W + NW * WB;       // [NV][sk | sv][128]
-    static constexpr int OFF_SC = OFF_RAW + NV * 2 * kUnit * 4;  // [NC][sk | sv][128], 0 where there is no token
-    static constexpr int OFF_ML = OFF_SC + NC * 2 * kUnit * 4;   // [m | l][128] of B, for A
+    static constexpr int OFF_SC = OFF_RAW + NV * 2 * kUnit * 4;  // [NC]
+    static constexpr int OFF_ML = OFF_SC + NC * kScaleBytes;   // [m | l][128] of B, for A
     static constexpr int OFF_INFO = OFF_ML + 2 * 128 * 4;
     static constexpr int OFF_BAR = OFF_INFO + NI * 64;
     static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(C::VF + sv, it / C::NV)) break;
             {
                 const float* raw = reinterpret_cast<const float*>(smem + C::OFF_RAW + sv * (2 * kUnit * 4));
-                float* out = reinterpret_cast<float*>(smem + C::OFF_SC + sc * (2 * kUnit * 4));
+                float* out = reinterpret_cast<float*>(smem + C::OFF_SC + sc * kScaleBytes);
                 const bool there = key0 + t < L && ((box_ok >> (t >> box_log2)) & 1);
                 const float k = raw[t], v = raw[kUnit + t];
                 const bool number = v < INFINITY;
@@ -362,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rows that see it and no other, for which 0 * 0 stays 0
                 out[t] = !there ? 0.f : number ? k : __int_as_float(0x7FFFFFFF);
                 out[kUnit + t] = there && number ? v : 0.f;
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(there && number ? v : 0.f));
+                if (lane == 0) out[2 * kUnit + (t >> 5)] = __uint_as_float(top);  // the largest of these 32
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::CF + sc));
             }
@@ -469,27 +475,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(C::SF + X, own)) break;
                 ++own;
                 tc_fence_after();
-                const uint32_t scl = sbase + C::OFF_SC + sc * (2 * kUnit * 4);
+                const uint32_t scl = sbase + C::OFF_SC + sc * kScaleBytes;
                 uint32_t pw[kUnit / 2];
                 const float2 qs2 = make_float2(qs, qs);
-                // y: the scaled scores s of keys 32 cc .. 32 cc + 31, -inf where the row does not see
-                // the key.  Step by step over 32, so that 16 independent operations stand behind
-                // one another.
-                auto hide = [&](float2(&y)[16], int cc) {
+                // -inf for those of keys 16 g .. 16 g + 15 that the row does not see.
+                auto hide = [&](float2(&y)[8], int g) {
                     // computed here: comparisons taken out of a loop would be made for every unit
                     const int lo = no_hoist(first - key0), hi = no_hoist(last - key0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int k = cc * 32 + 2 * i;
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = g * 16 + 2 * i;
                         if (k < lo || k > hi) y[i].x = -INFINITY;
                         if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
                     }
-                    if (flags & kHoles) {
-                        const int box_ok = f->box_ok;
+                    if ((flags & kHoles) && !((f->box_ok >> ((g * 16) >> box_log2)) & 1)) {  // a run has 16 keys or more
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)  // runs are even
-                            if (!((box_ok >> ((cc * 32 + 2 * i) >> box_log2)) & 1))
-                                y[i] = make_float2(-INFINITY, -INFINITY);
+                        for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
                     }
                 };
                 // The unit's part of M: the maximum of s + log2 sv, and of s - 100, which keeps P
@@ -530,64 +531,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return fmaxf(mj, ms * qs - 100.f);
                 };
-                // P sv of the unit against M, as fp16 in pw; the sum of P; the largest P sv.
-                float lsum;
+                // P sv of the unit against M, as fp16 in pw; returns the sum of P.  16 keys at a time,
+                // the next scores and key scales on their way, eight independent operations behind
+                // one another.
                 auto find_p = [&](auto masked_tag) -> float {
                     constexpr bool MASKED = decltype(masked_tag)::value;
                     const float m = M == -INFINITY ? 0.f : M;
                     const float2 nm2 = make_float2(-m, -m);
                     float2 l2 = make_float2(0.f, 0.f), l3 = l2;
-                    float mx = 0.f;
-                    uint32_t s0[32], s1[32];
-                    auto part32 = [&](const uint32_t(&s)[32], int cc) {
-                        float2 y[16];
+                    uint32_t s[2][16];
+                    float4 sk[4], sv[4];
+                    tmem_ld16(la + D, s[0]);
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 sk = ld_shared4(scl + (cc * 32 + 2 * i) * 4);
-                            y[i] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
-                                              make_float2(sk.x, sk.y));
-                            y[i + 1] = __fmul2_rn(
-                                make_float2(__uint_as_float(s[2 * i + 2]), __uint_as_float(s[2 * i + 3])),
-                                make_float2(sk.z, sk.w));
+                    for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scl + i * 16);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < kUnit / 16; ++g) {
+                        if (g + 1 < kUnit / 16) tmem_ld16(la + D + (g + 1) * 16, s[(g + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sv[i] = ld_shared4(scl + kUnit * 4 + g * 64 + i * 16);
+                        const uint32_t(&x)[16] = s[g & 1];
+                        float2 y[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                              (i & 1) ? make_float2(sk[i / 2].z, sk[i / 2].w)
+                                                      : make_float2(sk[i / 2].x, sk[i / 2].y));
+                        if (g + 1 < kUnit / 16) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scl + (g + 1) * 64 + i * 16);
                         }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __ffma2_rn(y[i], qs2, nm2);
-                        if (MASKED) hide(y, cc);
+                        for (int i = 0; i < 8; ++i) y[i] = __ffma2_rn(y[i], qs2, nm2);
+                        if (MASKED) hide(y, g);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+                        for (int i = 0; i < 8; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 sv = ld_shared4(scl + kUnit * 4 + (cc * 32 + 2 * i) * 4);
+                        for (int i = 0; i < 8; i += 2) {
                             l2 = __fadd2_rn(l2, y[i]);
                             l3 = __fadd2_rn(l3, y[i + 1]);
-                            y[i] = __fmul2_rn(y[i], make_float2(sv.x, sv.y));
-                            y[i + 1] = __fmul2_rn(y[i + 1], make_float2(sv.z, sv.w));
                         }
-                        float m4[4] = {mx, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            m4[i & 3] = max3(m4[i & 3], y[i].x, y[i].y);
-                            pw[cc * 16 + i] = pack_f16(y[i].x, y[i].y);
+                        for (int i = 0; i < 8; ++i) {
+                            y[i] = __fmul2_rn(y[i], (i & 1) ? make_float2(sv[i / 2].z, sv[i / 2].w)
+                                                            : make_float2(sv[i / 2].x, sv[i / 2].y));
+                            pw[g * 8 + i] = pack_f16(y[i].x, y[i].y);
                         }
-                        mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                    };
-                    // 32 scores at a time, the next ones on their way
-                    tmem_ld32(la + D, s0);
-                    tmem_wait_ld();
-                    tmem_ld32(la + D + 32, s1);
-                    part32(s0, 0);
-                    tmem_wait_ld();
-                    tmem_ld32(la + D + 64, s0);
-                    part32(s1, 1);
-                    tmem_wait_ld();
-                    tmem_ld32(la + D + 96, s1);
-                    part32(s0, 2);
-                    tmem_wait_ld();
-                    part32(s1, 3);
-                    lsum = (l2.x + l2.y) + (l3.x + l3.y);
-                    return mx;
+                        if (g + 1 < kUnit / 16) tmem_wait_ld();
+                    }
+                    return (l2.x + l2.y) + (l3.x + l3.y);
                 };
                 float alpha = 1.f;
+                float lsum = 0.f;
+                const float4 tops = ld_shared4(scl + 2 * kUnit * 4);
+                const float sv_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
                 bool raise = M == -INFINITY;
 #pragma unroll 1
                 for (int rep = 0; rep < 2; ++rep) {
@@ -600,9 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             alpha *= w;
                         }
                     }
-                    const float mx = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
-                    // a sum that is infinite: a token whose values are all zero far above M
-                    raise = mx > 256.f || lsum == INFINITY;
+                    lsum = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
+                    // (an infinite sum: a token whose values are all zero far above M)
+                    raise = lsum * sv_top > 32768.f || lsum == INFINITY;
                     if (!__any_sync(0xffffffffu, raise)) break;
                 }
                 l += lsum;
