@@ -55,6 +55,7 @@ constexpr int kConvWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 // 512 x 128 registers at launch: 2 x 128 x 184 + 2 x 128 x 72 = 65,536
 constexpr int kRegsSoftmax = 184, kRegsConv = 72, kRegsOther = 72;
 
+constexpr int kChunk = 64;  // keys that the softmax takes at a time
 // A unit's scales: sk[128], sv[128] (0 where there is no token), the largest sv of each 32.
 constexpr int kScaleBytes = (2 * kUnit + 4) * 4;
 
@@ -476,133 +477,158 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++own;
                 tc_fence_after();
                 const uint32_t scl = sbase + C::OFF_SC + sc * kScaleBytes;
-                uint32_t pw[kUnit / 2];
                 const float2 qs2 = make_float2(qs, qs);
-                // -inf for those of keys 16 g .. 16 g + 15 that the row does not see.
-                auto hide = [&](float2(&y)[8], int g) {
-                    // computed here: comparisons taken out of a loop would be made for every unit
-                    const int lo = no_hoist(first - key0), hi = no_hoist(last - key0);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int k = g * 16 + 2 * i;
-                        if (k < lo || k > hi) y[i].x = -INFINITY;
-                        if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
-                    }
-                    if ((flags & kHoles) && !((f->box_ok >> ((g * 16) >> box_log2)) & 1)) {  // a run has 16 keys or more
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
-                    }
-                };
-                // The unit's part of M: the maximum of s + log2 sv, and of s - 100, which keeps P
-                // finite where a row sees little but tokens whose values are all zero.
-                auto find_m = [&]() -> float {
-                    float mj = -INFINITY, ms = -INFINITY;
-#pragma unroll 1
-                    for (int cc = 0; cc < 4; ++cc) {
-                        uint32_t s[32];
-                        float2 y[16];
-                        tmem_ld32(la + D + cc * 32, s);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 sk = ld_shared4(scl + (cc * 32 + 2 * i) * 4);
-                            y[i] = __fmul2_rn(y[i], make_float2(sk.x, sk.y));
-                            y[i + 1] = __fmul2_rn(y[i + 1], make_float2(sk.z, sk.w));
-                        }
-                        if (flags & kMasked) {
-                            const int lo = first - key0 - cc * 32, hi = last - key0 - cc * 32;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const bool hole =
-                                    (flags & kHoles) && !((f->box_ok >> ((cc * 32 + 2 * i) >> box_log2)) & 1);
-                                if (2 * i < lo || 2 * i > hi || hole) y[i].x = -INFINITY;
-                                if (2 * i + 1 < lo || 2 * i + 1 > hi || hole) y[i].y = -INFINITY;
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float4 sv = ld_shared4(scl + kUnit * 4 + (cc * 32 + 2 * i) * 4);
-                            ms = max3(ms, fmaxf(y[i].x, y[i].y), fmaxf(y[i + 1].x, y[i + 1].y));
-                            mj = max3(mj, fmaf(y[i].x, qs, lg2_approx(sv.x)), fmaf(y[i].y, qs, lg2_approx(sv.y)));
-                            mj = max3(mj, fmaf(y[i + 1].x, qs, lg2_approx(sv.z)), fmaf(y[i + 1].y, qs, lg2_approx(sv.w)));
-                        }
-                    }
-                    return fmaxf(mj, ms * qs - 100.f);
-                };
-                // P sv of the unit against M, as fp16 in pw; returns the sum of P.  16 keys at a time,
-                // the next scores and key scales on their way, eight independent operations behind
-                // one another.
-                auto find_p = [&](auto masked_tag) -> float {
-                    constexpr bool MASKED = decltype(masked_tag)::value;
-                    const float m = M == -INFINITY ? 0.f : M;
-                    const float2 nm2 = make_float2(-m, -m);
-                    float2 l2 = make_float2(0.f, 0.f), l3 = l2;
-                    uint32_t s[2][16];
-                    float4 sk[4], sv[4];
-                    tmem_ld16(la + D, s[0]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scl + i * 16);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int g = 0; g < kUnit / 16; ++g) {
-                        if (g + 1 < kUnit / 16) tmem_ld16(la + D + (g + 1) * 16, s[(g + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sv[i] = ld_shared4(scl + kUnit * 4 + g * 64 + i * 16);
-                        const uint32_t(&x)[16] = s[g & 1];
-                        float2 y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            y[i] = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                                              (i & 1) ? make_float2(sk[i / 2].z, sk[i / 2].w)
-                                                      : make_float2(sk[i / 2].x, sk[i / 2].y));
-                        if (g + 1 < kUnit / 16) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scl + (g + 1) * 64 + i * 16);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = __ffma2_rn(y[i], qs2, nm2);
-                        if (MASKED) hide(y, g);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
-#pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            l2 = __fadd2_rn(l2, y[i]);
-                            l3 = __fadd2_rn(l3, y[i + 1]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            y[i] = __fmul2_rn(y[i], (i & 1) ? make_float2(sv[i / 2].z, sv[i / 2].w)
-                                                            : make_float2(sv[i / 2].x, sv[i / 2].y));
-                            pw[g * 8 + i] = pack_f16(y[i].x, y[i].y);
-                        }
-                        if (g + 1 < kUnit / 16) tmem_wait_ld();
-                    }
-                    return (l2.x + l2.y) + (l3.x + l3.y);
-                };
-                float alpha = 1.f;
-                float lsum = 0.f;
                 const float4 tops = ld_shared4(scl + 2 * kUnit * 4);
                 const float sv_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
-                bool raise = M == -INFINITY;
+                float alpha = 1.f;
+                // kChunk keys at a time, in a loop: straight-line code for all 128 keys, run by the two
+                // pipelines' warps at different times, spent a third of their time waiting for
+                // instructions.  P of a chunk takes the place of scores that have been read.
 #pragma unroll 1
-                for (int rep = 0; rep < 2; ++rep) {
-                    if (__any_sync(0xffffffffu, raise)) {
-                        const float mu = find_m();
-                        if (raise && mu > M) {
-                            const float w = part_weight(M, mu);
-                            M = mu;
+                for (int ck = 0; ck < kUnit / kChunk; ++ck) {
+                    const uint32_t scores = la + D + ck * kChunk, scales = scl + ck * kChunk * 4;
+                    const int at = key0 + ck * kChunk;  // position of the chunk's first key
+                    // -inf for those of the chunk's keys 16 g .. 16 g + 15 that the row does not see
+                    auto hide = [&](float2(&y)[8], int g) {
+                        // computed here: comparisons taken out of a loop would be made for every unit
+                        const int lo = no_hoist(first - at), hi = no_hoist(last - at);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int k = g * 16 + 2 * i;
+                            if (k < lo || k > hi) y[i].x = -INFINITY;
+                            if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
+                        }
+                        // a run has 16 keys or more
+                        if ((flags & kHoles) && !((f->box_ok >> ((ck * kChunk + g * 16) >> box_log2)) & 1)) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+                        }
+                    };
+                    // The chunk's part of M: the maximum of s + log2 sv, and of s - 100, which keeps P
+                    // finite where a row sees little but tokens whose values are all zero.
+                    auto find_m = [&]() -> float {
+                        float mj = -INFINITY, ms = -INFINITY;
+#pragma unroll
+                        for (int g = 0; g < kChunk / 16; ++g) {
+                            uint32_t s[16];
+                            float2 y[8];
+                            tmem_ld16(scores + g * 16, s);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float4 sk = ld_shared4(scales + g * 64 + i * 8);
+                                y[i] = make_float2(__uint_as_float(s[2 * i]) * sk.x, __uint_as_float(s[2 * i + 1]) * sk.y);
+                                y[i + 1] =
+                                    make_float2(__uint_as_float(s[2 * i + 2]) * sk.z, __uint_as_float(s[2 * i + 3]) * sk.w);
+                            }
+                            if (flags & kMasked) hide(y, g);
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const float4 sv = ld_shared4(scales + kUnit * 4 + g * 64 + i * 8);
+                                ms = max3(ms, fmaxf(y[i].x, y[i].y), fmaxf(y[i + 1].x, y[i + 1].y));
+                                mj = max3(mj, fmaf(y[i].x, qs, lg2_approx(sv.x)), fmaf(y[i].y, qs, lg2_approx(sv.y)));
+                                mj = max3(mj, fmaf(y[i + 1].x, qs, lg2_approx(sv.z)),
+                                          fmaf(y[i + 1].y, qs, lg2_approx(sv.w)));
+                            }
+                        }
+                        return fmaxf(mj, ms * qs - 100.f);
+                    };
+                    // P sv of the chunk against M, as fp16 in pw; returns the sum of P.  16 keys at a time,
+                    // the next scores and key scales on their way, eight independent operations behind
+                    // one another.
+                    uint32_t pw[kChunk / 2];
+                    auto find_p = [&](auto masked_tag) -> float {
+                        constexpr bool MASKED = decltype(masked_tag)::value;
+                        const float m = M == -INFINITY ? 0.f : M;
+                        const float2 nm2 = make_float2(-m, -m);
+                        float2 l2 = make_float2(0.f, 0.f), l3 = l2;
+                        uint32_t s[2][16];
+                        float4 sk[4], sv[4];
+                        tmem_ld16(scores, s[0]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scales + i * 16);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int g = 0; g < kChunk / 16; ++g) {
+                            if (g + 1 < kChunk / 16) tmem_ld16(scores + (g + 1) * 16, s[(g + 1) & 1]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sv[i] = ld_shared4(scales + kUnit * 4 + g * 64 + i * 16);
+                            const uint32_t(&x)[16] = s[g & 1];
+                            float2 y[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                y[i] = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                                  (i & 1) ? make_float2(sk[i / 2].z, sk[i / 2].w)
+                                                          : make_float2(sk[i / 2].x, sk[i / 2].y));
+                            if (g + 1 < kChunk / 16) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scales + (g + 1) * 64 + i * 16);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = __ffma2_rn(y[i], qs2, nm2);
+                            if (MASKED) hide(y, g);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                l2 = __fadd2_rn(l2, y[i]);
+                                l3 = __fadd2_rn(l3, y[i + 1]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                y[i] = __fmul2_rn(y[i], (i & 1) ? make_float2(sv[i / 2].z, sv[i / 2].w)
+                                                                : make_float2(sv[i / 2].x, sv[i / 2].y));
+                                pw[g * 8 + i] = pack_f16(y[i].x, y[i].y);
+                            }
+                            if (g + 1 < kChunk / 16) tmem_wait_ld();
+                        }
+                        return (l2.x + l2.y) + (l3.x + l3.y);
+                    };
+                    bool raise = M == -INFINITY;
+                    float sum = 0.f;
+#pragma unroll 1
+                    for (int rep = 0; rep < 2; ++rep) {
+                        if (__any_sync(0xffffffffu, raise)) {
+                            const float mu = find_m();
+                            float w = 1.f;
+                            if (raise && mu > M) {
+                                w = part_weight(M, mu);
+                                M = mu;
+                            }
                             l *= w;
                             alpha *= w;
+                            if (ck > 0) {
+                                // the unit's P so far
+                                const __half2 w2 = __half2half2(__float2half_rn(w));
+                                tmem_wait_st();
+#pragma unroll 1
+                                for (int c0 = 0; c0 < ck * kChunk / 2; c0 += 16) {
+                                    uint32_t x[16];
+                                    tmem_ld16(la + D + c0, x);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x[i]), w2);
+                                        x[i] = *reinterpret_cast<const uint32_t*>(&v);
+                                    }
+                                    tmem_st16(la + D + c0, x);
+                                }
+                            }
                         }
+                        sum = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
+                        // (an infinite sum: a token whose values are all zero far above M)
+                        raise = sum * sv_top > 32768.f || sum == INFINITY;
+                        if (!__any_sync(0xffffffffu, raise)) break;
                     }
-                    lsum = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
-                    // (an infinite sum: a token whose values are all zero far above M)
-                    raise = lsum * sv_top > 32768.f || lsum == INFINITY;
-                    if (!__any_sync(0xffffffffu, raise)) break;
+                    l += sum;
+#pragma unroll
+                    for (int c0 = 0; c0 < kChunk / 2; c0 += 16) {
+                        uint32_t x[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = pw[c0 + i];
+                        tmem_st16(la + D + ck * kChunk / 2 + c0, x);
+                    }
                 }
-                l += lsum;
                 if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
                     // O holds every product up to the pipeline's last unit: the scores' completion
                     // covers what was issued before them
@@ -622,16 +648,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fresh = false;
-                {
-                    uint32_t w0[32], w1[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        w0[i] = pw[i];
-                        w1[i] = pw[32 + i];
-                    }
-                    tmem_st32(la + D, w0);
-                    tmem_st32(la + D + 32, w1);
-                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
