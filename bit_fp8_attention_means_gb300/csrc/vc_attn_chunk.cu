@@ -179,9 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int boxes = kUnit >> box_log2;
             ItemWalk w;
-            w.start(c, a, RT, p);
+            bool more = w.start(c, a, RT, p), ok = true;
             int it = 0, loaded_k = 0, loaded_v = 0;
-            bool more = true, ok = true;
             while (more && ok) {
                 const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
                 // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
@@ -419,29 +418,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool both = f->rows > 128, mine = both || (place & 1) == X;
             const int tr = both ? X * 128 + row : row;  // this thread's row of the tile
             if (flags & kFirst) {
-                // the row's two E4M3 parts; the products that read the last item's have completed
-                const bool there = tr < f->rows;
-                const int r = f->r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
-                const uint4* src = reinterpret_cast<const uint4*>(a.Q + (int64_t)(f->q0 + tok) * a.q_sn +
-                                                                  (int64_t)(f->h * a.G + j) * a.q_sh);
-                uint32_t top = 0;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = there ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top = max(top, max(w4[k] & 0x7FFFu, (w4[k] >> 16) & 0x7FFFu));
-                }
-                const float fac = row_factor(top);
-                qs = a.scale_log2 / fac;
+                // The warp's 32 rows as two E4M3 parts each; the products that read the last item's
+                // have completed.  LR lanes of 16 bytes take a row, so that a load is whole lines:
+                // one thread a row took 7 us an item where this takes 2.
+                constexpr int LR = D / 8, NR = 32 / LR;
+                const int q0 = f->q0, r0 = f->r0, rows = f->rows, hq = f->h * a.G;
+                const int sub = lane % LR, tile_row = (both ? X * 128 : 0) + q * 32;
                 uint8_t* qh = smem + C::OFF_Q + 2 * X * C::QB;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += 8 * NR) {
+                    uint4 x[8];
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    uint32_t hw[4], lw[4];
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i0 + i * NR + lane / LR;  // of the warp's rows
+                        const bool there = tile_row + rr < rows;
+                        const int r = r0 + (there ? tile_row + rr : 0), tok = r / a.G, j = r - tok * a.G;
+                        x[i] = there ? __ldg(reinterpret_cast<const uint4*>(a.Q + (int64_t)(q0 + tok) * a.q_sn +
+                                                                            (int64_t)(hq + j) * a.q_sh) + sub)
+                                     : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint4 x = there ? __ldg(src + 2 * i + u) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i0 + i * NR + lane / LR, wrow = q * 32 + rr;
+                        const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max(w4[k] & 0x7FFFu, (w4[k] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int o = LR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float fac = row_factor(top);
+                        uint32_t hw[2], lw[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             float y[4];
@@ -449,19 +455,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                             y[1] = __uint_as_float(w4[2 * k] & 0xFFFF0000u) * fac;
                             y[2] = bf16_bits_to_f32(w4[2 * k + 1] & 0xFFFFu) * fac;
                             y[3] = __uint_as_float(w4[2 * k + 1] & 0xFFFF0000u) * fac;
-                            const uint32_t hi = cvt_e4m3x2(y[0], y[1]) | (cvt_e4m3x2(y[2], y[3]) << 16);
+                            hw[k] = cvt_e4m3x2(y[0], y[1]) | (cvt_e4m3x2(y[2], y[3]) << 16);
                             uint32_t f01, f23;
-                            e4m3x4_to_f16(hi, f01, f23);
+                            e4m3x4_to_f16(hw[k], f01, f23);
                             const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
                             const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-                            hw[2 * u + k] = hi;
-                            lw[2 * u + k] = cvt_e4m3x2(y[0] - g01.x, y[1] - g01.y) |
-                                            (cvt_e4m3x2(y[2] - g23.x, y[3] - g23.y) << 16);
+                            lw[k] = cvt_e4m3x2(y[0] - g01.x, y[1] - g01.y) |
+                                    (cvt_e4m3x2(y[2] - g23.x, y[3] - g23.y) << 16);
+                        }
+                        const int at = C::chunk(wrow, sub / 2) + (sub & 1) * 8;
+                        *reinterpret_cast<uint2*>(qh + at) = make_uint2(hw[0], hw[1]);
+                        *reinterpret_cast<uint2*>(qh + C::QB + at) = make_uint2(lw[0], lw[1]);
+                        // to the row's own thread
+#pragma unroll
+                        for (int e = 0; e < NR; ++e) {
+                            const float g = __shfl_sync(0xffffffffu, fac, e * LR);
+                            if (lane == i0 + i * NR + e) qs = a.scale_log2 / g;
                         }
                     }
-                    *reinterpret_cast<uint4*>(qh + C::chunk(row, i)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-                    *reinterpret_cast<uint4*>(qh + C::QB + C::chunk(row, i)) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
                 }
+                const int r = r0 + (tr < rows ? tr : 0), tok = r / a.G;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::QF + X));

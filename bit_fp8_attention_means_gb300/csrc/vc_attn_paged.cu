@@ -133,9 +133,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (lane == 0 && warp != kScaleWarp) prefetch_tensormap(warp == kKeyWarp ? &tmK : &tmV);
             const int boxes = kUnit >> box_log2;
             ItemWalk w;
-            w.start(c, a, RT, p);
+            bool more = w.start(c, a, RT, p), ok = true;
             int it = 0;
-            bool more = true, ok = true;
             while (more && ok) {
                 const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
                 // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
@@ -581,7 +580,7 @@ vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAt
 // CTAs of a call: as many as there can be units, one on each SM at most.
 int part_count(const PagedAttn& a, const CacheView& c, int RT) {
     const int64_t tiles = (int64_t)c.T * a.G / RT + c.B;
-    const int64_t units = (((int64_t)c.cols << c.page_log2) + kUnit - 1) / kUnit;
+    const int64_t units = (((int64_t)c.cols << c.page_log2) + kUnit - 1) / kUnit + kItemCost;
     if (tiles * c.H >= kMaxCtas || units >= kMaxCtas) return kMaxCtas;
     return (int)(tiles * c.H * units < kMaxCtas ? tiles * c.H * units : kMaxCtas);
 }

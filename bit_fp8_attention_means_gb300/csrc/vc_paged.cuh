@@ -46,15 +46,18 @@ __device__ __forceinline__ int page_of(const CacheView& c, int b, int p) {
 //
 // The rows of a sequence for one key/value head are its n * G (token, query
 // head) pairs, token by token; an item is a tile of RT of them, and its work is
-// the units of 128 keys that at least one of its rows sees.  All units of a
-// call stand in one order (sequence, head, tile, key) and CTA i of C takes the
-// i-th of C equal parts (with fewer units than CTAs, one unit each), so lengths
-// that differ, few rows and long caches keep all SMs equally busy.  An item cut by the border of two CTAs leaves partial
-// results (running maximum, sum, accumulator) in the workspace, which a second
-// kernel joins in key order.
+// the units of 128 keys that at least one of its rows sees.  All items of a
+// call stand in one order (sequence, head, tile), each as long as its units and
+// what beginning and ending an item costs, kItemCost units more; CTA i of C takes
+// the i-th of C equal parts of this line, so lengths that differ, few rows and
+// long caches keep all SMs equally busy.  (Without the items' own cost, CTAs with
+// many short items took three times as long as those with one long one.)  An
+// item cut by the border of two CTAs leaves partial results (running maximum,
+// sum, accumulator) in the workspace, which a second kernel joins in key order.
 
 constexpr int kUnit = 128;       // keys of a unit
 constexpr int kMaxCtas = 152;    // one CTA on each SM
+constexpr int kItemCost = 3;     // of an item besides its units, in units
 
 struct ItemRange {
     int lo, hi;     // first and last key that some row sees (hi < lo: none)
@@ -86,33 +89,62 @@ __device__ __forceinline__ int seq_tiles(const PagedAttn& a, const SeqInfo& s, i
     return (int)(((int64_t)s.n * a.G + RT - 1) / RT);
 }
 
-__device__ __forceinline__ int64_t seq_units(const CacheView& c, const PagedAttn& a, int b, int RT) {
+__device__ __forceinline__ int item_cost(const PagedAttn& a, const SeqInfo& s, int tile, int RT) {
+    const int u = item_range(a, s, tile, RT).units();
+    return u ? u + kItemCost : 0;
+}
+
+// Cost of one head's tiles of a sequence: by one thread, or by a warp.
+__device__ __forceinline__ int64_t seq_cost(const CacheView& c, const PagedAttn& a, int b, int RT) {
     const SeqInfo s = seq_info(c, b);
     const int nt = seq_tiles(a, s, RT);
     int64_t u = 0;
-    for (int t = 0; t < nt; ++t) u += item_range(a, s, t, RT).units();
+    for (int t = 0; t < nt; ++t) u += item_cost(a, s, t, RT);
+    return u;
+}
+__device__ __forceinline__ int64_t seq_cost_warp(const PagedAttn& a, const SeqInfo& s, int RT) {
+    const int nt = seq_tiles(a, s, RT);
+    int64_t u = 0;
+    for (int t = threadIdx.x & 31; t < nt; t += 32) u += item_cost(a, s, t, RT);
+    for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
 }
 
-// The part of a CTA: global units [g0, g1), and where g0 lies.
+// The part of a CTA: [g0, g1) of the line, and where g0 lies.
 struct Part {
     int64_t g0, g1;
-    int b;        // sequence of unit g0
-    int64_t off;  // unit g0's place in its sequence (all heads)
+    int b;        // sequence of g0
+    int64_t off;  // g0's place in its sequence (all heads)
 };
 
 // Called by all NT threads of a block; the result is the same in all of them.
-// Two passes over the sequences: the total, then the one that holds g0.
+// Two passes over the sequences, NT at a time: the total, then the one that
+// holds g0.  Sequences of many tiles are added up by a warp each.
 template <int NT>
 __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a, int RT, int part, int parts) {
-    __shared__ int64_t warp_sum[NT / 32 + 1];
+    __shared__ int64_t warp_sum[NT / 32];
+    __shared__ int64_t cost[NT];
     __shared__ Part found;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t mine = 0, first_u = 0;
-    for (int b = threadIdx.x; b < c.B; b += NT) {
-        const int64_t u = seq_units(c, a, b, RT) * c.H;
-        if (b == (int)threadIdx.x) first_u = u;
-        mine += u;
+    const bool by_warp = (int64_t)c.T * a.G > (int64_t)c.B * RT * 4;
+    // cost of sequence b0 + threadIdx.x
+    auto costs = [&](int b0) -> int64_t {
+        if (by_warp) {
+            for (int i = warp; i < NT && b0 + i < c.B; i += NT / 32) {
+                const int64_t u = seq_cost_warp(a, seq_info(c, b0 + i), RT);
+                if (lane == 0) cost[i] = u * c.H;
+            }
+            __syncthreads();
+            return b0 + (int)threadIdx.x < c.B ? cost[threadIdx.x] : 0;
+        }
+        return b0 + (int)threadIdx.x < c.B ? seq_cost(c, a, b0 + threadIdx.x, RT) * c.H : 0;
+    };
+    if (threadIdx.x == 0) found = Part{0, 0, 0, 0};
+    const int64_t first_u = costs(0);
+    int64_t mine = first_u;
+    for (int b0 = NT; b0 < c.B; b0 += NT) {
+        __syncthreads();
+        mine += costs(b0);
     }
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
     if (lane == 0) warp_sum[warp] = mine;
@@ -129,16 +161,15 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     }
     p.g0 = total * part / parts;
     p.g1 = total * (part + 1) / parts;
-    int64_t before = 0;  // units of the sequences of earlier rounds
+    int64_t before = 0;  // cost of the sequences of earlier rounds
     for (int b0 = 0; b0 < c.B; b0 += NT) {
-        const int b = b0 + threadIdx.x;
-        const int64_t u = b >= c.B ? 0 : b0 ? seq_units(c, a, b, RT) * c.H : first_u;
+        __syncthreads();
+        const int64_t u = b0 ? costs(b0) : first_u;
         int64_t scan = u;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
             if (lane >= o) scan += v;
         }
-        __syncthreads();
         if (lane == 31) warp_sum[warp] = scan;
         __syncthreads();
         int64_t base = before, all = before;
@@ -148,7 +179,7 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
         }
         const int64_t end = base + scan, begin = end - u;
         if (begin <= p.g0 && p.g0 < end) {
-            found.b = b;
+            found.b = b0 + threadIdx.x;
             found.off = p.g0 - begin;
         }
         before = all;
@@ -160,10 +191,10 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     return p;
 }
 
-// Walks the items of a CTA's part, in order.  All members are uniform over the
-// threads that walk together.
+// Walks the items of a CTA's part that have units in it, in order.  For whole
+// warps; all members are uniform over the warp.
 struct ItemWalk {
-    int64_t left;    // units still to take
+    int64_t left;    // of the part's length
     int b, h, tile;  // the item
     SeqInfo s;
     ItemRange r;
@@ -171,55 +202,65 @@ struct ItemWalk {
     bool head;       // an earlier CTA has the item's first units
     bool tail;       // a later CTA has its last units
 
-    __device__ void start(const CacheView& c, const PagedAttn& a, int RT, const Part& p) {
+    // To the first item; false where the part holds no unit at all.
+    __device__ bool start(const CacheView& c, const PagedAttn& a, int RT, const Part& p) {
         left = p.g1 - p.g0;
         b = p.b;
         s = seq_info(c, b);
-        const int nt = seq_tiles(a, s, RT);
-        int64_t per_head = 0;
-        for (int t = 0; t < nt; ++t) per_head += item_range(a, s, t, RT).units();
+        const int64_t per_head = seq_cost_warp(a, s, RT);
         h = (int)(p.off / per_head);
         int64_t off = p.off % per_head;
-        tile = 0;
-        while (true) {
-            r = item_range(a, s, tile, RT);
-            if (off < r.units()) break;
-            off -= r.units();
-            ++tile;
+        const int nt = seq_tiles(a, s, RT), lane = threadIdx.x & 31;
+        for (int t0 = 0;; t0 += 32) {
+            int64_t scan = t0 + lane < nt ? item_cost(a, s, t0 + lane, RT) : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
+                if (lane >= o) scan += v;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, scan > off);
+            if (past || t0 + 32 >= nt) {
+                const int k = past ? __ffs(past) - 1 : 0;
+                const int64_t before = __shfl_sync(0xffffffffu, scan, k ? k - 1 : 0);
+                tile = t0 + k;
+                if (k) off -= before;
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, scan, 31);
         }
-        head = off > 0;
-        set((int)off);
+        r = item_range(a, s, tile, RT);
+        return take((int)off) || next(c, a, RT);
     }
-    __device__ void set(int off) {
-        unit = r.first() + off;
-        const int u = r.units() - off;
-        tail = u > left;
-        end = unit + (tail ? (int)left : u);
-        left -= end - unit;
+    // The item from place `off` of its length on; false where that holds none of its units.
+    __device__ bool take(int off) {
+        const int u = r.units(), all = u + kItemCost;
+        const int to = left < all - off ? off + (int)left : all;
+        left -= to - off;
+        const int u0 = max(off - kItemCost, 0), u1 = to - kItemCost;
+        head = u0 > 0;
+        tail = u1 < u;
+        unit = r.first() + u0;
+        end = r.first() + u1;
+        return u1 > u0;
     }
-    // To the next item; false at the part's end.
+    // To the next item with units in the part; false at its end.
     __device__ bool next(const CacheView& c, const PagedAttn& a, int RT) {
-        if (left == 0) return false;
-        head = false;
-        do {
+        while (left > 0) {
             if (++tile >= seq_tiles(a, s, RT)) {
                 tile = 0;
-                if (++h == c.H) {
+                if (++h >= c.H) {
                     h = 0;
                     if (++b >= c.B) return false;
                     s = seq_info(c, b);
                 }
                 if (seq_tiles(a, s, RT) == 0) {  // a sequence without rows has no heads to walk
-                    h = c.H - 1;
-                    r.lo = 0;
-                    r.hi = -1;
+                    h = c.H;
                     continue;
                 }
             }
             r = item_range(a, s, tile, RT);
-        } while (r.units() == 0);
-        set(0);
-        return true;
+            if (r.units() && take(0)) return true;
+        }
+        return false;
     }
 };
 
