@@ -55,6 +55,9 @@ constexpr int kConvWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
 // 512 x 128 registers at launch: 2 x 128 x 184 + 2 x 128 x 72 = 65,536
 constexpr int kRegsSoftmax = 184, kRegsConv = 72, kRegsOther = 72;
 
+// What an item costs besides its units, in units: its queries (5 us), the first scores and the
+// last rows, with both pipelines empty, against 2 us a unit.
+constexpr int kItemCost = 7;
 constexpr int kChunk = 64;  // keys that the softmax takes at a time
 // A unit's scales: sk[128], sv[128] (0 where there is no token), the largest sv of each 32.
 constexpr int kScaleBytes = (2 * kUnit + 4) * 4;
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < c.B; b += kThreads)
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
-    const Part p = plan_part<kThreads>(c, a, RT, blockIdx.x, gridDim.x);
+    const Part p = plan_part<kThreads>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
     __syncthreads();
     launch_dependents();
     if (p.g0 == p.g1) return;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 prefetch_tensormap(&tmV);
             }
             const int boxes = kUnit >> box_log2;
-            ItemWalk w;
+            ItemWalk<kItemCost> w;
             bool more = w.start(c, a, RT, p), ok = true;
             int it = 0, loaded_k = 0, loaded_v = 0;
             while (more && ok) {
@@ -350,12 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
             const int sv = it % C::NV, sw = it % C::NW, sc = it % C::NC;
-            if (it >= C::NC && !wait(C::CE + sc, it / C::NC - 1)) break;
-            if (flags & kEnd) {
-                if (lane == 0) mbar_arrive(bar(C::CF + sc));
-                break;
-            }
+            if (flags & kEnd) break;
             if (!wait(C::VF + sv, it / C::NV)) break;
+            if (it >= C::NC && !wait(C::CE + sc, it / C::NC - 1)) break;
             {
                 const float* raw = reinterpret_cast<const float*>(smem + C::OFF_RAW + sv * (2 * kUnit * 4));
                 float* out = reinterpret_cast<float*>(smem + C::OFF_SC + sc * kScaleBytes);
@@ -407,11 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t la = tmem + ((uint32_t)(q * 32) << 16) + C::base(X);
         float M = -INFINITY, l = 0.f, qs = 0.f;
         int last = -1, first = 0, items = 0, own = 0, shared = 0;
-        bool fresh = true;
+        bool fresh = true, begin = true;
         for (int it = 0;; ++it) {
             const int sc = it % C::NC;
-            // the converter has seen the unit's info and passes it on with the scales
-            if (!wait(C::CF + sc, it / C::NC)) break;
+            // inside an item the scales' arrival says that the info, which the converter reads
+            // before, is there too
+            if (begin ? !wait(C::IF + it % C::NI, it / C::NI) : !wait(C::CF + sc, it / C::NC)) break;
             const StageInfo* f = info_at(it);
             const int flags = f->flags, key0 = f->key0, place = f->pad[0];
             if (flags & kEnd) break;
@@ -419,59 +420,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tr = both ? X * 128 + row : row;  // this thread's row of the tile
             if (flags & kFirst) {
                 // The warp's 32 rows as two E4M3 parts each; the products that read the last item's
-                // have completed.  LR lanes of 16 bytes take a row, so that a load is whole lines:
-                // one thread a row took 7 us an item where this takes 2.
-                constexpr int LR = D / 8, NR = 32 / LR;
-                const int q0 = f->q0, r0 = f->r0, rows = f->rows, hq = f->h * a.G;
-                const int sub = lane % LR, tile_row = (both ? X * 128 : 0) + q * 32;
+                // have completed.  LR lanes of 16 bytes take a row, so that a load is whole lines,
+                // four loads ahead of their use.  A scaled channel's parts are its first 4
+                // significant bits and the rest: x & ~15 on the bf16 bits, and the difference.
+                constexpr int LR = D / 8, NR = 32 / LR, BATCH = 4;
+                const int q0 = f->q0, r0 = f->r0, rows = f->rows;
+                const int sub = lane % LR, my = (both ? X * 128 : 0) + q * 32 + lane;  // tile row `lane` of the warp
+                const int mr = r0 + (my < rows ? my : 0), mtok = mr / a.G;
+                const int64_t my_off = (int64_t)(q0 + mtok) * a.q_sn + (int64_t)(f->h * a.G + mr - mtok * a.G) * a.q_sh;
+                const unsigned there = __ballot_sync(0xffffffffu, my < rows);
                 uint8_t* qh = smem + C::OFF_Q + 2 * X * C::QB;
-#pragma unroll 1
-                for (int i0 = 0; i0 < 32; i0 += 8 * NR) {
-                    uint4 x[8];
+                auto load = [&](int i) -> uint4 {
+                    const int rr = i * NR + lane / LR;
+                    const int64_t off = __shfl_sync(0xffffffffu, my_off, rr & 31);
+                    return rr < 32 && (there >> rr & 1u) ? __ldg(reinterpret_cast<const uint4*>(a.Q + off) + sub)
+                                                         : make_uint4(0, 0, 0, 0);
+                };
+                uint4 nx[BATCH];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i0 + i * NR + lane / LR;  // of the warp's rows
-                        const bool there = tile_row + rr < rows;
-                        const int r = r0 + (there ? tile_row + rr : 0), tok = r / a.G, j = r - tok * a.G;
-                        x[i] = there ? __ldg(reinterpret_cast<const uint4*>(a.Q + (int64_t)(q0 + tok) * a.q_sn +
-                                                                            (int64_t)(hq + j) * a.q_sh) + sub)
-                                     : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < BATCH; ++i) nx[i] = load(i);
+#pragma unroll 1
+                for (int i0 = 0; i0 < LR; i0 += BATCH) {
+                    uint4 x[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        x[i] = nx[i];
+                        nx[i] = load(i0 + BATCH + i);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i0 + i * NR + lane / LR, wrow = q * 32 + rr;
+                    for (int i = 0; i < BATCH; ++i) {
                         const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                         uint32_t top = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(w4[k] & 0x7FFFu, (w4[k] >> 16) & 0x7FFFu));
+                        for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w4[k] & 0x7FFF7FFFu);
+                        top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
                         for (int o = LR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
                         const float fac = row_factor(top);
+                        const __nv_bfloat162 f2 = __float2bfloat162_rn(fac);  // a power of two
                         uint32_t hw[2], lw[2];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float y[4];
-                            y[0] = bf16_bits_to_f32(w4[2 * k] & 0xFFFFu) * fac;
-                            y[1] = __uint_as_float(w4[2 * k] & 0xFFFF0000u) * fac;
-                            y[2] = bf16_bits_to_f32(w4[2 * k + 1] & 0xFFFFu) * fac;
-                            y[3] = __uint_as_float(w4[2 * k + 1] & 0xFFFF0000u) * fac;
-                            hw[k] = cvt_e4m3x2(y[0], y[1]) | (cvt_e4m3x2(y[2], y[3]) << 16);
-                            uint32_t f01, f23;
-                            e4m3x4_to_f16(hw[k], f01, f23);
-                            const float2 g01 = __half22float2(*reinterpret_cast<const __half2*>(&f01));
-                            const float2 g23 = __half22float2(*reinterpret_cast<const __half2*>(&f23));
-                            lw[k] = cvt_e4m3x2(y[0] - g01.x, y[1] - g01.y) |
-                                    (cvt_e4m3x2(y[2] - g23.x, y[3] - g23.y) << 16);
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w4[k]), f2);
+                            const uint32_t hb = *reinterpret_cast<const uint32_t*>(&y) & 0xFFF0FFF0u;
+                            const __nv_bfloat162 ly = __hsub2(y, *reinterpret_cast<const __nv_bfloat162*>(&hb));
+                            const uint32_t lb = *reinterpret_cast<const uint32_t*>(&ly);
+                            const uint32_t hc = cvt_e4m3x2(bf16_bits_to_f32(hb & 0xFFFFu), __uint_as_float(hb & 0xFFFF0000u));
+                            const uint32_t lc = cvt_e4m3x2(bf16_bits_to_f32(lb & 0xFFFFu), __uint_as_float(lb & 0xFFFF0000u));
+                            hw[k / 2] = (k & 1) ? hw[k / 2] | (hc << 16) : hc;
+                            lw[k / 2] = (k & 1) ? lw[k / 2] | (lc << 16) : lc;
                         }
-                        const int at = C::chunk(wrow, sub / 2) + (sub & 1) * 8;
+                        const int rr = (i0 + i) * NR + lane / LR;
+                        const int at = C::chunk(q * 32 + rr, sub / 2) + (sub & 1) * 8;
                         *reinterpret_cast<uint2*>(qh + at) = make_uint2(hw[0], hw[1]);
                         *reinterpret_cast<uint2*>(qh + C::QB + at) = make_uint2(lw[0], lw[1]);
                         // to the row's own thread
-#pragma unroll
-                        for (int e = 0; e < NR; ++e) {
-                            const float g = __shfl_sync(0xffffffffu, fac, e * LR);
-                            if (lane == i0 + i * NR + e) qs = a.scale_log2 / g;
-                        }
+                        const float g = __shfl_sync(0xffffffffu, fac, (lane % NR) * LR);
+                        if (lane / NR == i0 + i) qs = a.scale_log2 / g;
                     }
                 }
                 const int r = r0 + (tr < rows ? tr : 0), tok = r / a.G;
@@ -485,6 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = 0.f;
                 fresh = true;
             }
+            if (begin && !wait(C::CF + sc, it / C::NC)) break;
+            begin = flags & kLast;
             if (mine) {
                 if (!wait(C::SF + X, own)) break;
                 ++own;

@@ -40,6 +40,8 @@ namespace {
 // swizzle.  Rows as the wide side, 8 warps and one producer took 251 us where
 // this takes XX us (one token of 96 sequences, 747 MB).
 
+// What an item costs besides its units, in units: the queries, and adding up the warps' parts.
+constexpr int kItemCost = 3;
 constexpr int kConsumers = 16;
 constexpr int kFewThreads = (kConsumers + 4) * 32;  // the producers' warpgroup has an idle warp
 constexpr int kKeyWarp = kConsumers, kValueWarp = kConsumers + 1, kScaleWarp = kConsumers + 2;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < c.B; b += kFewThreads)
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
-    const Part p = plan_part<kFewThreads>(c, a, RT, blockIdx.x, gridDim.x);
+    const Part p = plan_part<kFewThreads>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
     __syncthreads();
     launch_dependents();
     if (p.g0 == p.g1) return;
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             // ------------------------------------------------------------ producers
             if (lane == 0 && warp != kScaleWarp) prefetch_tensormap(warp == kKeyWarp ? &tmK : &tmV);
             const int boxes = kUnit >> box_log2;
-            ItemWalk w;
+            ItemWalk<kItemCost> w;
             bool more = w.start(c, a, RT, p), ok = true;
             int it = 0;
             while (more && ok) {
@@ -468,11 +470,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
 // ------------------------------------------------------------ joining
 //
-// join_kernel: block i takes the item that begins in CTA i's part and goes on
-// in the next ones, and adds their parts in key order; the blocks also share
-// out the rows whose tiles see no key at all, which no CTA had.  A part of 16
-// rows is 8 KB, so this is a launch and a few L2 round trips.
-constexpr int kJoinThreads = 256;
+// join_kernel: blocks (i, .) take the item that begins in CTA i's part and goes
+// on in the next ones, kJoinRows rows each, and add their parts in key order;
+// the blocks also share out the rows whose tiles see no key at all, which no CTA
+// had.  A launch and a few L2 round trips (one block an item took 45 us for
+// tiles of 256 rows).
+constexpr int kJoinThreads = 256, kJoinRows = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads)
@@ -492,8 +495,9 @@ __global__ void __launch_bounds__(kJoinThreads)
         }
         __syncthreads();
         const int end = s_end;
-        for (int i = threadIdx.x; i < hd.rows * (D / 4); i += kJoinThreads) {
-            const int row = i / (D / 4), ch = (i % (D / 4)) * 4;
+        const int first_row = blockIdx.y * kJoinRows, some = min(hd.rows - first_row, kJoinRows);
+        for (int i = threadIdx.x; i < some * (D / 4); i += kJoinThreads) {
+            const int row = first_row + i / (D / 4), ch = (i % (D / 4)) * 4;
             const float* pm = part.m + row;
             float m = pm[(size_t)i0 * RT], l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         }
     }
     const float none[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int b = blockIdx.x; b < c.B; b += gridDim.x) {
+    for (int b = blockIdx.y * gridDim.x + blockIdx.x; b < c.B; b += gridDim.x * gridDim.y) {
         const SeqInfo s = seq_info(c, b);
         const int nt = seq_tiles(a, s, RT);
         for (int t = 0; t < nt; ++t) {
@@ -559,7 +563,7 @@ vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(parts);
+    cfg.gridDim = dim3(parts, (RT + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cfg.attrs = &attr;
@@ -577,10 +581,10 @@ vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAt
     return cuda_status(cudaGetLastError());
 }
 
-// CTAs of a call: as many as there can be units, one on each SM at most.
+// CTAs of a call: one on each SM, fewer where there cannot be that much work.
 int part_count(const PagedAttn& a, const CacheView& c, int RT) {
     const int64_t tiles = (int64_t)c.T * a.G / RT + c.B;
-    const int64_t units = (((int64_t)c.cols << c.page_log2) + kUnit - 1) / kUnit + kItemCost;
+    const int64_t units = (((int64_t)c.cols << c.page_log2) + kUnit - 1) / kUnit + 1;
     if (tiles * c.H >= kMaxCtas || units >= kMaxCtas) return kMaxCtas;
     return (int)(tiles * c.H * units < kMaxCtas ? tiles * c.H * units : kMaxCtas);
 }

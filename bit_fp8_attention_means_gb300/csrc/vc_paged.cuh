@@ -48,7 +48,7 @@ __device__ __forceinline__ int page_of(const CacheView& c, int b, int p) {
 // head) pairs, token by token; an item is a tile of RT of them, and its work is
 // the units of 128 keys that at least one of its rows sees.  All items of a
 // call stand in one order (sequence, head, tile), each as long as its units and
-// what beginning and ending an item costs, kItemCost units more; CTA i of C takes
+// what beginning and ending an item costs, IC units more; CTA i of C takes
 // the i-th of C equal parts of this line, so lengths that differ, few rows and
 // long caches keep all SMs equally busy.  (Without the items' own cost, CTAs with
 // many short items took three times as long as those with one long one.)  An
@@ -57,7 +57,6 @@ __device__ __forceinline__ int page_of(const CacheView& c, int b, int p) {
 
 constexpr int kUnit = 128;       // keys of a unit
 constexpr int kMaxCtas = 152;    // one CTA on each SM
-constexpr int kItemCost = 3;     // of an item besides its units, in units
 
 struct ItemRange {
     int lo, hi;     // first and last key that some row sees (hi < lo: none)
@@ -89,23 +88,23 @@ __device__ __forceinline__ int seq_tiles(const PagedAttn& a, const SeqInfo& s, i
     return (int)(((int64_t)s.n * a.G + RT - 1) / RT);
 }
 
-__device__ __forceinline__ int item_cost(const PagedAttn& a, const SeqInfo& s, int tile, int RT) {
+__device__ __forceinline__ int item_cost(const PagedAttn& a, const SeqInfo& s, int tile, int RT, int IC) {
     const int u = item_range(a, s, tile, RT).units();
-    return u ? u + kItemCost : 0;
+    return u ? u + IC : 0;
 }
 
 // Cost of one head's tiles of a sequence: by one thread, or by a warp.
-__device__ __forceinline__ int64_t seq_cost(const CacheView& c, const PagedAttn& a, int b, int RT) {
+__device__ __forceinline__ int64_t seq_cost(const CacheView& c, const PagedAttn& a, int b, int RT, int IC) {
     const SeqInfo s = seq_info(c, b);
     const int nt = seq_tiles(a, s, RT);
     int64_t u = 0;
-    for (int t = 0; t < nt; ++t) u += item_cost(a, s, t, RT);
+    for (int t = 0; t < nt; ++t) u += item_cost(a, s, t, RT, IC);
     return u;
 }
-__device__ __forceinline__ int64_t seq_cost_warp(const PagedAttn& a, const SeqInfo& s, int RT) {
+__device__ __forceinline__ int64_t seq_cost_warp(const PagedAttn& a, const SeqInfo& s, int RT, int IC) {
     const int nt = seq_tiles(a, s, RT);
     int64_t u = 0;
-    for (int t = threadIdx.x & 31; t < nt; t += 32) u += item_cost(a, s, t, RT);
+    for (int t = threadIdx.x & 31; t < nt; t += 32) u += item_cost(a, s, t, RT, IC);
     for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
 }
@@ -121,7 +120,7 @@ struct Part {
 // Two passes over the sequences, NT at a time: the total, then the one that
 // holds g0.  Sequences of many tiles are added up by a warp each.
 template <int NT>
-__device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a, int RT, int part, int parts) {
+__device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a, int RT, int IC, int part, int parts) {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ int64_t cost[NT];
     __shared__ Part found;
@@ -131,13 +130,13 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     auto costs = [&](int b0) -> int64_t {
         if (by_warp) {
             for (int i = warp; i < NT && b0 + i < c.B; i += NT / 32) {
-                const int64_t u = seq_cost_warp(a, seq_info(c, b0 + i), RT);
+                const int64_t u = seq_cost_warp(a, seq_info(c, b0 + i), RT, IC);
                 if (lane == 0) cost[i] = u * c.H;
             }
             __syncthreads();
             return b0 + (int)threadIdx.x < c.B ? cost[threadIdx.x] : 0;
         }
-        return b0 + (int)threadIdx.x < c.B ? seq_cost(c, a, b0 + threadIdx.x, RT) * c.H : 0;
+        return b0 + (int)threadIdx.x < c.B ? seq_cost(c, a, b0 + threadIdx.x, RT, IC) * c.H : 0;
     };
     if (threadIdx.x == 0) found = Part{0, 0, 0, 0};
     const int64_t first_u = costs(0);
@@ -193,6 +192,7 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
 
 // Walks the items of a CTA's part that have units in it, in order.  For whole
 // warps; all members are uniform over the warp.
+template <int IC>
 struct ItemWalk {
     int64_t left;    // of the part's length
     int b, h, tile;  // the item
@@ -207,12 +207,12 @@ struct ItemWalk {
         left = p.g1 - p.g0;
         b = p.b;
         s = seq_info(c, b);
-        const int64_t per_head = seq_cost_warp(a, s, RT);
+        const int64_t per_head = seq_cost_warp(a, s, RT, IC);
         h = (int)(p.off / per_head);
         int64_t off = p.off % per_head;
         const int nt = seq_tiles(a, s, RT), lane = threadIdx.x & 31;
         for (int t0 = 0;; t0 += 32) {
-            int64_t scan = t0 + lane < nt ? item_cost(a, s, t0 + lane, RT) : 0;
+            int64_t scan = t0 + lane < nt ? item_cost(a, s, t0 + lane, RT, IC) : 0;
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
                 if (lane >= o) scan += v;
@@ -232,10 +232,10 @@ struct ItemWalk {
     }
     // The item from place `off` of its length on; false where that holds none of its units.
     __device__ bool take(int off) {
-        const int u = r.units(), all = u + kItemCost;
+        const int u = r.units(), all = u + IC;
         const int to = left < all - off ? off + (int)left : all;
         left -= to - off;
-        const int u0 = max(off - kItemCost, 0), u1 = to - kItemCost;
+        const int u0 = max(off - IC, 0), u1 = to - IC;
         head = u0 > 0;
         tail = u1 < u;
         unit = r.first() + u0;
