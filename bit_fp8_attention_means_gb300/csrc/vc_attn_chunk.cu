@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     auto wait = [&](int i, int phase) -> bool {
-        return mbar_wait_suspended(bar(i), phase & 1, abort_flag, c.dev_status, kTimeoutNs);
+        return mbar_wait_counted(bar(i), phase & 1, abort_flag, c.dev_status);
     };
 
     if (threadIdx.x == 0) {
@@ -194,6 +194,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return pg < 0 ? -2 : pg;
                 };
                 int ahead = entry(w.unit);
+                // the item's queries on their way to L2 while the last item's units are under way
+                for (int i = lane; i < rows; i += 32) {
+                    const int r = r0 + i, tok = r / a.G;
+                    const uint16_t* src =
+                        a.Q + (int64_t)(w.s.q0 + tok) * a.q_sn + (int64_t)(w.h * a.G + r - tok * a.G) * a.q_sh;
+                    prefetch_l2(src);
+                    if (D == 128) prefetch_l2(src + 64);
+                }
                 for (int u = w.unit; u < w.end; ++u, ++it) {
                     const int key0 = u * kUnit;
                     int pg = ahead;
@@ -262,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // this CTA's own copies land before it can exit
             for (int j = max(loaded_k - C::NK, 0); j < loaded_k; ++j)
-                drain_wait(bar(C::KF + j % C::NK), (j / C::NK) & 1, kTimeoutNs);
+                drain_wait_counted(bar(C::KF + j % C::NK), (j / C::NK) & 1);
             for (int j = max(loaded_v - C::NV, 0); j < loaded_v; ++j)
-                drain_wait(bar(C::VF + j % C::NV), (j / C::NV) & 1, kTimeoutNs);
+                drain_wait_counted(bar(C::VF + j % C::NV), (j / C::NV) & 1);
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ MMA issuer
             // One warp issues for both pipelines, in turn: the product P V of a pipeline's last
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every MMA this warp issued has completed once this phase flips
             mma_commit_w(bar(C::TD));
-            drain_wait(bar(C::TD), 0, kTimeoutNs);
+            drain_wait_counted(bar(C::TD), 0);
             __syncwarp();
         }
     } else if (warp >= kConvWarp) {
@@ -508,27 +516,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int ck = 0; ck < kUnit / kChunk; ++ck) {
                     const uint32_t scores = la + D + ck * kChunk, scales = scl + ck * kChunk * 4;
                     const int at = key0 + ck * kChunk;  // position of the chunk's first key
-                    // -inf for those of the chunk's keys 16 g .. 16 g + 15 that the row does not see
+                    // -inf for those of the chunk's keys 16 g .. 16 g + 15 that the row does not see.  Most
+                    // groups of a masked unit are seen by all of the warp's rows or by none.
                     auto hide = [&](float2(&y)[8], int g) {
                         // computed here: comparisons taken out of a loop would be made for every unit
-                        const int lo = no_hoist(first - at), hi = no_hoist(last - at);
+                        const int lo = no_hoist(first - at) - g * 16, hi = no_hoist(last - at) - g * 16;
+                        // a run has 16 keys or more
+                        const bool hole = (flags & kHoles) && !((f->box_ok >> ((ck * kChunk + g * 16) >> box_log2)) & 1);
+                        if (__all_sync(0xffffffffu, lo <= 0 && hi >= 15) && !hole) return;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const int k = g * 16 + 2 * i;
-                            if (k < lo || k > hi) y[i].x = -INFINITY;
-                            if (k + 1 < lo || k + 1 > hi) y[i].y = -INFINITY;
-                        }
-                        // a run has 16 keys or more
-                        if ((flags & kHoles) && !((f->box_ok >> ((ck * kChunk + g * 16) >> box_log2)) & 1)) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = make_float2(-INFINITY, -INFINITY);
+                            if (hole || 2 * i < lo || 2 * i > hi) y[i].x = -INFINITY;
+                            if (hole || 2 * i + 1 < lo || 2 * i + 1 > hi) y[i].y = -INFINITY;
                         }
                     };
                     // The chunk's part of M: the maximum of s + log2 sv, and of s - 100, which keeps P
                     // finite where a row sees little but tokens whose values are all zero.
                     auto find_m = [&]() -> float {
                         float mj = -INFINITY, ms = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                         for (int g = 0; g < kChunk / 16; ++g) {
                             uint32_t s[16];
                             float2 y[8];
@@ -715,8 +721,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             wa *= inv;
             wb *= inv;
             const Partials part = partials_at(ws, RT, D);
-            float* po = part.o + ((size_t)slot * RT + (there ? tr : 0)) * D;
-            uint16_t* dst = a.O + (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
+            const int64_t o_off = (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
+            // Rows go through shared memory (the warp's part of the queries, which no product reads
+            // any more), so that what leaves are whole lines: 32 channels at a time, each row's
+            // 16-byte pieces turned by the row.
+            float4* stage = reinterpret_cast<float4*>(smem + C::OFF_Q + 2 * X * C::QB) + q * 256;
+            const int piece = lane & 7;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t oa[32];
@@ -731,22 +741,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(oa[i]), wb, v[i]);
                 }
-                if (there && split) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *reinterpret_cast<float4*>(po + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                } else if (there) {
+                for (int i = 0; i < 8; ++i)
+                    stage[lane * 8 + (i ^ (lane & 7))] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w4[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[i + 2 * k], v[i + 2 * k + 1]);
-                            w4[k] = *reinterpret_cast<const uint32_t*>(&b2);
-                        }
-                        *reinterpret_cast<uint4*>(dst + c0 + i) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = 4 * i + lane / 8, row_t = tr - lane + rr;  // of the warp's rows, of the tile's
+                    const float4 x = stage[rr * 8 + (piece ^ (rr & 7))];
+                    const int64_t off = __shfl_sync(0xffffffffu, o_off, rr);
+                    if (row_t >= rows) continue;
+                    if (split) {
+                        *reinterpret_cast<float4*>(part.o + ((size_t)slot * RT + row_t) * D + c0 + 4 * piece) = x;
+                    } else {
+                        const __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x, x.y), b1 = __floats2bfloat162_rn(x.z, x.w);
+                        *reinterpret_cast<uint2*>(a.O + off + c0 + 4 * piece) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
                     }
                 }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();

@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                     const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
                     if (it >= NS &&
-                        !mbar_wait_suspended(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                        !mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
                         ok = false;
                         break;
                     }
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 // the stage that ends the consumers' loop
                 const int st = it % NS;
                 if (it < NS ||
-                    mbar_wait_suspended(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) {
+                    mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
                     if (lane == 0 && warp == kKeyWarp)
                         reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
                     if (lane == 0) mbar_arrive(full + 8 * st);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
             // this CTA's own copies land before it can exit
-            for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait(full + 8 * (j % NS), (j / NS) & 1, kTimeoutNs);
+            for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1);
         }
     } else {
         // ------------------------------------------------------------ consumers
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         int it = 0, items = 0;
         while (true) {
             const int st = it % NS;
-            if (!mbar_wait_suspended(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (!mbar_wait_counted(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status)) break;
             const StageInfo* info = reinterpret_cast<const StageInfo*>(smem + C::OFF_INFO + st * 64);
             const int flags = info->flags;
             if (flags & kEnd) break;
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
             // ------------------------------------------------------------ the item's end
             // the accumulators are free to overwrite once the last item's were read
-            if (items > 0 && !mbar_wait_suspended(read, (items - 1) & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (items > 0 && !mbar_wait_counted(read, (items - 1) & 1, abort_flag, c.dev_status)) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(written);
-            if (!mbar_wait_suspended(written, items & 1, abort_flag, c.dev_status, kTimeoutNs)) break;
+            if (!mbar_wait_counted(written, items & 1, abort_flag, c.dev_status)) break;
             const bool split = flags & (kHead | kTail);
             const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
             for (int i = threadIdx.x; i < rows * (D / 4); i += kConsumers * 32) {

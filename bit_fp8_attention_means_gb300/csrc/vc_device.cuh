@@ -105,33 +105,28 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, dev_status, timeout_ns));
 }
 
-// mbar_wait_warp that leaves the issue slots to the other warps: an attempt may
-// suspend the thread for up to 20 us, and the timer (a slow read) is looked at
-// only after a failed one.  With attempts that return at once, five waiting
-// warps spent half of a CTA's instructions.
-__device__ __forceinline__ bool mbar_wait_suspended(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                    int32_t* dev_status, uint64_t timeout_ns) {
-    bool ok = mbar_test_wait(bar, parity);
-    for (uint64_t t0 = 0; !ok;) {
-        uint32_t got;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(got)
-            : "r"(bar), "r"(parity), "r"(20000u)
-            : "memory");
-        ok = got != 0;
-        if (ok || *abort_flag) break;
-        const uint64_t t = globaltimer_ns();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > timeout_ns) {
-            *abort_flag = 1;
-            if (dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
-            break;
-        }
+// mbar_wait_warp in a few instructions: the bound is a number of attempts (each of
+// some 30 ns and more: 2^27 of them pass the 4 s of the timed waits), not a time.  A
+// kernel with twenty waits and the timed loop in each place is large enough to
+// run out of the instruction cache.
+constexpr uint32_t kWaitAttempts = 1u << 27;
+__device__ __forceinline__ bool mbar_wait_counted(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                  int32_t* dev_status) {
+    bool ok = true;
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 1023u) continue;
+        if (!*abort_flag && n < kWaitAttempts) continue;
+        if (!*abort_flag && dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+        break;
     }
     return __all_sync(0xffffffffu, ok);
+}
+// The same for teardown: not ended by another thread's giving up.
+__device__ __forceinline__ void drain_wait_counted(uint32_t bar, uint32_t parity) {
+    for (uint32_t n = 0; !mbar_try_wait(bar, parity) && n < kWaitAttempts; ++n) {
+    }
 }
 
 // ------------------------------------------------------------ TMA
@@ -177,6 +172,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
         if (globaltimer_ns() - t0 > timeout_ns) return;
     }
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Programmatic dependent launch: lets the next kernel of the stream start its
 // blocks now; waits until the kernel before has ended and its writes are visible.

@@ -309,7 +309,6 @@ __device__ __forceinline__ float part_weight(float m_part, float m) {
 
 constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
 constexpr float kZeroLog2 = -60.f;     // log2 sv of a token whose values are all zero
-constexpr uint64_t kTimeoutNs = 4000000000ull;  // bound of every wait
 
 // What a producer tells the other warps of a CTA about a unit.
 struct StageInfo {
