@@ -455,17 +455,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[i] = nx[i];
                         nx[i] = load(i0 + BATCH + i);
                     }
+                    // step by step over the batch: four chains of shuffles side by side
+                    uint32_t top[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                          __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+                        top[i] = max(top[i] & 0xFFFFu, top[i] >> 16);
+                    }
+#pragma unroll
+                    for (int o = LR / 2; o; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+                    float fac[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        fac[i] = row_factor(top[i]);
+                        // to the row's own thread
+                        const float g = __shfl_sync(0xffffffffu, fac[i], (lane % NR) * LR);
+                        if (lane / NR == i0 + i) qs = a.scale_log2 / g;
+                    }
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
                         const uint32_t w4[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = __vmaxu2(top, w4[k] & 0x7FFF7FFFu);
-                        top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-                        for (int o = LR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const float fac = row_factor(top);
-                        const __nv_bfloat162 f2 = __float2bfloat162_rn(fac);  // a power of two
+                        const __nv_bfloat162 f2 = __float2bfloat162_rn(fac[i]);  // a power of two
                         uint32_t hw[2], lw[2];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -482,9 +495,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int at = C::chunk(q * 32 + rr, sub / 2) + (sub & 1) * 8;
                         *reinterpret_cast<uint2*>(qh + at) = make_uint2(hw[0], hw[1]);
                         *reinterpret_cast<uint2*>(qh + C::QB + at) = make_uint2(lw[0], lw[1]);
-                        // to the row's own thread
-                        const float g = __shfl_sync(0xffffffffu, fac, (lane % NR) * LR);
-                        if (lane / NR == i0 + i) qs = a.scale_log2 / g;
                     }
                 }
                 const int r = r0 + (tr < rows ? tr : 0), tok = r / a.G;
@@ -721,12 +731,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             wa *= inv;
             wb *= inv;
             const Partials part = partials_at(ws, RT, D);
-            const int64_t o_off = (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
+            const int64_t o_off = split ? ((int64_t)slot * RT + tr) * D
+                                        : (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
             // Rows go through shared memory (the warp's part of the queries, which no product reads
             // any more), so that what leaves are whole lines: 32 channels at a time, each row's
             // 16-byte pieces turned by the row.
             float4* stage = reinterpret_cast<float4*>(smem + C::OFF_Q + 2 * X * C::QB) + q * 256;
             const int piece = lane & 7;
+            int64_t off[8];  // of the rows that this lane stores a piece of
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + lane / 8;  // of the warp's rows
+                const int64_t o = __shfl_sync(0xffffffffu, o_off, rr);
+                off[i] = tr - lane + rr < rows ? o + 4 * piece : -1;
+            }
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t oa[32];
@@ -747,15 +765,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int rr = 4 * i + lane / 8, row_t = tr - lane + rr;  // of the warp's rows, of the tile's
+                    const int rr = 4 * i + lane / 8;
                     const float4 x = stage[rr * 8 + (piece ^ (rr & 7))];
-                    const int64_t off = __shfl_sync(0xffffffffu, o_off, rr);
-                    if (row_t >= rows) continue;
+                    if (off[i] < 0) continue;
                     if (split) {
-                        *reinterpret_cast<float4*>(part.o + ((size_t)slot * RT + row_t) * D + c0 + 4 * piece) = x;
+                        *reinterpret_cast<float4*>(part.o + off[i] + c0) = x;
                     } else {
                         const __nv_bfloat162 b0 = __floats2bfloat162_rn(x.x, x.y), b1 = __floats2bfloat162_rn(x.z, x.w);
-                        *reinterpret_cast<uint2*>(a.O + off + c0 + 4 * piece) =
+                        *reinterpret_cast<uint2*>(a.O + off[i] + c0) =
                             make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
                     }
                 }
