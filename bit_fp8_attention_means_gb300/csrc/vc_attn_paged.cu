@@ -471,63 +471,82 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // ------------------------------------------------------------ joining
 //
 // join_kernel: blocks (i, .) take the item that begins in CTA i's part and goes
-// on in the next ones, kJoinRows rows each, and add their parts in key order;
-// the blocks also share out the rows whose tiles see no key at all, which no CTA
-// had.  A launch and a few L2 round trips (one block an item took 45 us for
-// tiles of 256 rows).
-constexpr int kJoinThreads = 256, kJoinRows = 8;
+// on in the next ones, share its rows out among their warps, and add a row's
+// parts in key order; the blocks also share out the rows whose tiles see no key
+// at all, which no CTA had.  A launch and four L2 round trips: the headers, the
+// parts' maxima and sums (a lane each), the accumulators (eight parts at a time).
+// Small enough (96 threads of 40 registers) to wait on the SMs beside the kernel
+// for few rows.  One block an item with a thread for each piece of a row took
+// 12 us more for the 19 parts of one token against 75,600 keys.
+constexpr int kJoinThreads = 96;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 16)  // 40 registers
     join_kernel(const PagedAttn a, const CacheView c, void* ws, int RT, int parts) {
+    constexpr int E = D / 32;  // channels of a lane
     __shared__ int s_end;
     const Partials part = partials_at(ws, RT, D);
-    const int mine = blockIdx.x, i0 = 2 * mine + 1;
+    const int mine = blockIdx.x, i0 = 2 * mine + 1, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) s_end = parts;
     __syncthreads();
     wait_for_primary();
-    const PartHeader hd = part.head[i0];
-    if (hd.valid) {
-        // the parts of CTAs mine .. end - 1: the first later one that has the item's end
-        for (int k = mine + 1 + threadIdx.x; k < parts; k += kJoinThreads) {
-            const PartHeader next = part.head[2 * k];
-            if (next.valid && next.last) atomicMin(&s_end, k + 1);
-        }
+    if (part.head[i0].valid) {
+        // the parts of CTAs mine .. end - 1: up to the first later one that has the item's end
+        for (int k = mine + 1 + threadIdx.x; k < parts; k += kJoinThreads)
+            if (part.head[2 * k].valid && part.head[2 * k].last) atomicMin(&s_end, k + 1);
         __syncthreads();
-        const int end = s_end;
-        const int first_row = blockIdx.y * kJoinRows, some = min(hd.rows - first_row, kJoinRows);
-        for (int i = threadIdx.x; i < some * (D / 4); i += kJoinThreads) {
-            const int row = first_row + i / (D / 4), ch = (i % (D / 4)) * 4;
-            const float* pm = part.m + row;
-            float m = pm[(size_t)i0 * RT], l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-            for (int k = mine + 1; k < end; ++k) m = fmaxf(m, pm[(size_t)(2 * k) * RT]);
-#pragma unroll 4
-            for (int k = mine; k < end; ++k) {
-                const size_t at = (size_t)(k == mine ? i0 : 2 * k) * RT + row;
-                const float w = part_weight(part.m[at], m);
-                l = fmaf(w, part.l[at], l);
-                const float4 u = *reinterpret_cast<const float4*>(part.o + at * D + ch);
-                acc[0] = fmaf(w, u.x, acc[0]);
-                acc[1] = fmaf(w, u.y, acc[1]);
-                acc[2] = fmaf(w, u.z, acc[2]);
-                acc[3] = fmaf(w, u.w, acc[3]);
+        const PartHeader hd = part.head[i0];
+        const int n = s_end - mine;
+        auto slot = [&](int k) { return (size_t)(k ? 2 * (mine + k) : i0) * RT; };
+        for (int row = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; row < hd.rows;
+             row += gridDim.y * (kJoinThreads / 32)) {
+            float m = -INFINITY, l = 0.f, acc[E];
+            for (int k = lane; k < n; k += 32) m = fmaxf(m, part.m[slot(k) + row]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = 0.f;
+            for (int k0 = 0; k0 < n; k0 += 32) {
+                float w = 0.f, lw = 0.f;
+                if (k0 + lane < n) {
+                    w = part_weight(part.m[slot(k0 + lane) + row], m);
+                    lw = w * part.l[slot(k0 + lane) + row];
+                }
+                const int some = min(n - k0, 32);
+#pragma unroll 8
+                for (int k = 0; k < some; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k);
+                    l += __shfl_sync(0xffffffffu, lw, k);
+                    const float* o = part.o + (slot(k0 + k) + row) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 u = *reinterpret_cast<const float4*>(o);
+                        acc[0] = fmaf(wk, u.x, acc[0]);
+                        acc[1] = fmaf(wk, u.y, acc[1]);
+                        acc[2] = fmaf(wk, u.z, acc[2]);
+                        acc[3] = fmaf(wk, u.w, acc[3]);
+                    } else {
+                        const float2 u = *reinterpret_cast<const float2*>(o);
+                        acc[0] = fmaf(wk, u.x, acc[0]);
+                        acc[1] = fmaf(wk, u.y, acc[1]);
+                    }
+                }
             }
-            store_row(a, hd.q0, hd.h, hd.r0 + row, ch, acc, inverse_sum(l));
-            if (ch == 0) store_lse(a, c, hd.q0, hd.h, hd.r0 + row, m, l);
+            store_row(a, hd.q0, hd.h, hd.r0 + row, lane * E, acc, inverse_sum(l));
+            if (lane == 0) store_lse(a, c, hd.q0, hd.h, hd.r0 + row, m, l);
         }
     }
-    const float none[4] = {0.f, 0.f, 0.f, 0.f};
+    float none[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) none[e] = 0.f;
     for (int b = blockIdx.y * gridDim.x + blockIdx.x; b < c.B; b += gridDim.x * gridDim.y) {
         const SeqInfo s = seq_info(c, b);
         const int nt = seq_tiles(a, s, RT);
         for (int t = 0; t < nt; ++t) {
             if (item_range(a, s, t, RT).units()) continue;
             const int r0 = t * RT, rows = min(RT, s.n * a.G - r0);
-            for (int i = threadIdx.x; i < c.H * rows * (D / 4); i += kJoinThreads) {
-                const int h = i / (rows * (D / 4)), row = i / (D / 4) % rows, ch = (i % (D / 4)) * 4;
-                store_row(a, s.q0, h, r0 + row, ch, none, 0.f);
-                if (ch == 0) store_lse(a, c, s.q0, h, r0 + row, 0.f, 0.f);
+            for (int i = threadIdx.x / 32; i < c.H * rows; i += kJoinThreads / 32) {
+                store_row(a, s.q0, i / rows, r0 + i % rows, lane * E, none, 0.f);
+                if (lane == 0) store_lse(a, c, s.q0, i / rows, r0 + i % rows, 0.f, 0.f);
             }
         }
     }
@@ -563,7 +582,7 @@ vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(parts, (RT + kJoinRows - 1) / kJoinRows);
+    cfg.gridDim = dim3(parts, RT / 8 + 1);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cfg.attrs = &attr;

@@ -349,13 +349,20 @@ __device__ __forceinline__ float row_factor(uint32_t top) {
     return __int_as_float((134 - e) << 23);
 }
 
-// Channels ch .. ch + 3 of row r (a (token, head) pair of its sequence), acc * inv as bf16.
-__device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int r, int ch, const float (&acc)[4],
+// Channels ch .. ch + N - 1 (N = 2 or 4) of row r (a (token, head) pair of its sequence), acc * inv as bf16.
+template <int N>
+__device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int r, int ch, const float (&acc)[N],
                                           float inv) {
-    const __nv_bfloat162 v0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-    const __nv_bfloat162 v1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2*>(a.O + (int64_t)(q0 + r / a.G) * a.o_sn + (int64_t)(h * a.G + r % a.G) * a.o_sh + ch) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&v0), *reinterpret_cast<const uint32_t*>(&v1));
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(acc[i] * inv, acc[i + 1] * inv);
+        w[i / 2] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const int tok = r / a.G;
+    uint16_t* dst = a.O + (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + r - tok * a.G) * a.o_sh + ch;
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
 __device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c, int q0, int h, int r, float m,
