@@ -28,8 +28,8 @@ namespace {
 //
 // attn_few_kernel: tiles of 8 RG rows.  What bounds it is reading the cache
 // once (2d + 8 bytes per key and head), so everything else is arranged around a
-// full memory pipe: one persistent CTA on each SM, three producer warps (keys,
-// values, scales) that keep NS stages of 128 keys in flight, and sixteen
+// full memory pipe: one persistent CTA on each SM, four producer warps (two for
+// keys, two for values) that keep NS stages of 128 keys in flight, and sixteen
 // consumer warps that share nothing until an item ends.  A consumer warp owns 8
 // rows and blocks of 16 keys, with its own M, l and A in registers.  Keys and
 // channels are the wide side of the products (K q^T, V^T P^T as m16n8k16 fp16),
@@ -43,10 +43,16 @@ namespace {
 // What an item costs besides its units, in units: the queries, and adding up the warps' parts.
 constexpr int kItemCost = 3;
 constexpr int kConsumers = 16;
-constexpr int kFewThreads = (kConsumers + 4) * 32;  // the producers' warpgroup has an idle warp
-constexpr int kKeyWarp = kConsumers, kValueWarp = kConsumers + 1, kScaleWarp = kConsumers + 2;
+constexpr int kFewThreads = (kConsumers + 4) * 32;
 // 640 threads start with 96 registers each; 4 x 128 x 104 + 128 x 56 = 60,416 fit into those 61,440
 constexpr int kFewRegsUp = 104, kFewRegsDown = 56;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 template <int D>
 struct FewCfg {
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(full + 8 * s, 3);  // keys and info, values, scales
+            mbar_init(full + 8 * s, 4 + 64);  // the producers, and each lane of the two that load scales
             mbar_init(empty + 8 * s, kConsumers);
         }
         mbar_init(written, kConsumers);
@@ -130,93 +136,90 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int box_log2 = min(c.page_log2, 7);  // runs of keys in one page
     if (warp >= kConsumers) {
         regs_down<kFewRegsDown>();
-        if (warp <= kScaleWarp) {
-            // ------------------------------------------------------------ producers
-            if (lane == 0 && warp != kScaleWarp) prefetch_tensormap(warp == kKeyWarp ? &tmK : &tmV);
-            const int boxes = kUnit >> box_log2;
-            ItemWalk<kItemCost> w;
-            bool more = w.start(c, a, RT, p), ok = true;
-            int it = 0;
-            while (more && ok) {
-                const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
-                // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
-                auto entry = [&](int u) -> int {
-                    const int k = u * kUnit + (lane << box_log2);
-                    if (lane >= boxes || u >= w.end || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
-                    const int pg = __ldg(c.table + (int64_t)w.b * c.s_table + (k >> c.page_log2));
-                    return pg < 0 ? -2 : pg;
-                };
-                int ahead = entry(w.unit);
-                for (int u = w.unit; u < w.end; ++u, ++it) {
-                    const int st = it % NS, key0 = u * kUnit;
-                    int pg = ahead;
-                    ahead = entry(u + 1);
-                    if (pg == -2 || pg >= c.pages) {
-                        flag_invalid(c.dev_status);
-                        pg = -1;
-                    }
-                    const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
-                    if (it >= NS &&
-                        !mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
-                        ok = false;
-                        break;
-                    }
-                    if (warp == kScaleWarp) {
-                        // scales of the runs that are there; the others are masked
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(full + 8 * st, (uint32_t)__popc(box_ok) << (box_log2 + 3));
-                        __syncwarp();
-                        if (pg >= 0) {
-                            const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
-                            const int64_t off = (int64_t)pg * c.t_page + (int64_t)w.h * c.t_head + in;
-                            const uint32_t dst = sbase + C::OFF_SC + st * (2 * kUnit * 4) + (lane << (box_log2 + 2));
-                            bulk_load(dst, c.sk + off, 4u << box_log2, full + 8 * st);
-                            bulk_load(dst + kUnit * 4, c.sv + off, 4u << box_log2, full + 8 * st);
-                        }
-                        continue;
-                    }
-                    if (lane == 0) {
-                        if (warp == kKeyWarp) {
-                            StageInfo* f = reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64);
-                            const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all &&
-                                                  box_ok == (1 << boxes) - 1;
-                            f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) |
-                                       (all_seen ? 0 : kMasked) | (w.head ? kHead : 0) | (w.tail ? kTail : 0);
-                            f->key0 = key0;
-                            f->q0 = w.s.q0;
-                            f->n = w.s.n;
-                            f->L = w.s.L;
-                            f->h = w.h;
-                            f->r0 = r0;
-                            f->rows = rows;
-                            f->box_ok = box_ok;
-                        }
-                        mbar_arrive_expect_tx(full + 8 * st, C::TILE);
-                    }
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const uint32_t at = sbase + (warp == kKeyWarp ? C::OFF_K : C::OFF_V) + st * C::TILE +
-                                            (uint32_t)(lane << box_log2) * D;
-                        const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
-                        tma_load_4d(at, warp == kKeyWarp ? &tmK : &tmV, 0, in, w.h, pg, full + 8 * st);
-                    }
+        // ------------------------------------------------------------ producers
+        // Warps 0 and 1 of them load keys, 2 and 3 values, every other run of keys in one page
+        // each (a run is a TMA load, and a thread's loads are issued one after the other: eight
+        // runs of 16 keys in one warp took longer than the data); the odd ones load the scales.
+        const int role = warp - kConsumers, odd = role & 1;
+        const CUtensorMap* map = role < 2 ? &tmK : &tmV;
+        if (lane == 0) prefetch_tensormap(map);
+        const int boxes = kUnit >> box_log2;
+        const bool mine = lane < boxes && (lane & 1) == odd;
+        ItemWalk<kItemCost> w;
+        bool more = w.start(c, a, RT, p), ok = true;
+        int it = 0;
+        while (more && ok) {
+            const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
+            // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
+            auto entry = [&](int u) -> int {
+                const int k = u * kUnit + (lane << box_log2);
+                if (lane >= boxes || u >= w.end || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
+                const int pg = __ldg(c.table + (int64_t)w.b * c.s_table + (k >> c.page_log2));
+                return pg < 0 ? -2 : pg;
+            };
+            int ahead = entry(w.unit);
+            for (int u = w.unit; u < w.end; ++u, ++it) {
+                const int st = it % NS, key0 = u * kUnit;
+                int pg = ahead;
+                ahead = entry(u + 1);
+                if (pg == -2 || pg >= c.pages) {
+                    flag_invalid(c.dev_status);
+                    pg = -1;
                 }
-                if (ok) more = w.next(c, a, RT);
-            }
-            if (ok) {
-                // the stage that ends the consumers' loop
-                const int st = it % NS;
-                if (it < NS ||
-                    mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
-                    if (lane == 0 && warp == kKeyWarp)
-                        reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
-                    if (lane == 0) mbar_arrive(full + 8 * st);
-                    ++it;
+                const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
+                if (it >= NS && !mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (role == 0) {
+                        StageInfo* f = reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64);
+                        const bool all_seen = key0 >= w.r.lo_all && key0 + kUnit - 1 <= w.r.hi_all &&
+                                              box_ok == (1 << boxes) - 1;
+                        f->flags = (u == w.unit ? kFirst : 0) | (u == w.end - 1 ? kLast : 0) |
+                                   (all_seen ? 0 : kMasked) | (w.head ? kHead : 0) | (w.tail ? kTail : 0);
+                        f->key0 = key0;
+                        f->q0 = w.s.q0;
+                        f->n = w.s.n;
+                        f->L = w.s.L;
+                        f->h = w.h;
+                        f->r0 = r0;
+                        f->rows = rows;
+                        f->box_ok = box_ok;
+                    }
+                    mbar_arrive_expect_tx(full + 8 * st, (uint32_t)((boxes + 1 - odd) >> 1 << box_log2) * D);
+                }
+                __syncwarp();
+                if (mine) {
+                    const uint32_t at = sbase + (role < 2 ? C::OFF_K : C::OFF_V) + st * C::TILE +
+                                        (uint32_t)(lane << box_log2) * D;
+                    const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
+                    tma_load_4d(at, map, 0, in, w.h, pg, full + 8 * st);
+                }
+                if (odd) {
+                    // four keys' scales a lane; 0 where the page is not there
+                    const int spg = __shfl_sync(0xffffffffu, pg, (4 * lane) >> box_log2);
+                    const int in = (key0 + 4 * lane) & ((1 << c.page_log2) - 1);
+                    const int64_t off = spg < 0 ? 0 : (int64_t)spg * c.t_page + (int64_t)w.h * c.t_head + in;
+                    cp_async16(sbase + C::OFF_SC + (2 * st + role / 2) * (kUnit * 4) + lane * 16,
+                               (role < 2 ? c.sk : c.sv) + off, spg < 0 ? 0 : 16);
+                    cp_async_arrive(full + 8 * st);
                 }
             }
-            // this CTA's own copies land before it can exit
-            for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1);
+            if (ok) more = w.next(c, a, RT);
         }
+        if (ok) {
+            // the stage that ends the consumers' loop
+            const int st = it % NS;
+            if (it < NS || mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
+                if (lane == 0 && role == 0) reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
+                if (lane == 0) mbar_arrive(full + 8 * st);
+                if (odd) mbar_arrive(full + 8 * st);
+                ++it;
+            }
+        }
+        // this CTA's own copies land before it can exit
+        for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1);
     } else {
         // ------------------------------------------------------------ consumers
         regs_up<kFewRegsUp>();
