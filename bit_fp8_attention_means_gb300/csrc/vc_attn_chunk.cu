@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_barrier_init();
         const Partials part = partials_at(ws, RT, D);
-        part.head[2 * blockIdx.x].valid = 0;
-        part.head[2 * blockIdx.x + 1].valid = 0;
+        part.head[2 * blockIdx.x].parts = 0;
+        part.head[2 * blockIdx.x + 1].parts = 0;
     }
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < c.B; b += kThreads)
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool more = w.start(c, a, RT, p), ok = true;
             int it = 0, loaded_k = 0, loaded_v = 0;
             while (more && ok) {
-                const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
+                const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0), on = w.parts_on(p, blockIdx.x);
                 // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
                 auto entry = [&](int u) -> int {
                     const int k = u * kUnit + (lane << box_log2);
@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f->rows = rows;
                         f->box_ok = box_ok;
                         f->pad[0] = u - w.unit;
+                        f->pad[1] = on;
                         mbar_arrive(bar(C::IF + it % C::NI));
                     }
                     __syncwarp();
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::CE + sc));
-            const int q0 = f->q0, h = f->h, r0 = f->r0, rows = f->rows;
+            const int q0 = f->q0, h = f->h, r0 = f->r0, rows = f->rows, on = f->pad[1];
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(C::IE + it % C::NI));
             if (!(flags & kLast)) continue;
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store_lse(a, c, q0, h, r, M, l);
             }
             if (split && threadIdx.x == 0)
-                part.head[slot] = PartHeader{1, (flags & kTail) ? 0 : 1, q0, h, r0, rows};
+                part.head[slot] = PartHeader{on, q0, h, r0, rows};
             ++items;
         }
     }

@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_init(read, kConsumers);
         *abort_flag = 0;
         fence_barrier_init();
-        part.head[2 * blockIdx.x].valid = 0;
-        part.head[2 * blockIdx.x + 1].valid = 0;
+        part.head[2 * blockIdx.x].parts = 0;
+        part.head[2 * blockIdx.x + 1].parts = 0;
     }
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < c.B; b += kFewThreads)
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         bool more = w.start(c, a, RT, p), ok = true;
         int it = 0;
         while (more && ok) {
-            const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0);
+            const int r0 = w.tile * RT, rows = min(RT, w.s.n * a.G - r0), on = w.parts_on(p, blockIdx.x);
             // table entry of run `lane` of unit u, asked for one unit ahead; -1 where no row sees the run
             auto entry = [&](int u) -> int {
                 const int k = u * kUnit + (lane << box_log2);
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         f->r0 = r0;
                         f->rows = rows;
                         f->box_ok = box_ok;
+                        f->pad[1] = on;
                     }
                     mbar_arrive_expect_tx(full + 8 * st, (uint32_t)((boxes + 1 - odd) >> 1 << box_log2) * D);
                 }
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     }
                 }
             const int key_end = flags & kLast;
-            const int q0 = info->q0, h = info->h, r0 = info->r0, rows = info->rows;
+            const int q0 = info->q0, h = info->h, r0 = info->r0, rows = info->rows, on = info->pad[1];
             __syncwarp();
             if (lane == 0) mbar_arrive(empty + 8 * st);
             ++it;
@@ -462,7 +463,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
             if (split && threadIdx.x == 0)
-                part.head[slot] = PartHeader{1, (flags & kTail) ? 0 : 1, q0, h, r0, rows};
+                part.head[slot] = PartHeader{on, q0, h, r0, rows};
             __syncwarp();
             if (lane == 0) mbar_arrive(read);
             ++items;
@@ -474,35 +475,27 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // ------------------------------------------------------------ joining
 //
 // join_kernel: blocks (i, .) take the item that begins in CTA i's part and goes
-// on in the next ones, share its rows out among their warps, and add a row's
-// parts in key order; the blocks also share out the rows whose tiles see no key
-// at all, which no CTA had.  A launch and four L2 round trips: the headers, the
-// parts' maxima and sums (a lane each), the accumulators (eight parts at a time).
-// Small enough (96 threads of 40 registers) to wait on the SMs beside the kernel
-// for few rows.  One block an item with a thread for each piece of a row took
-// 12 us more for the 19 parts of one token against 75,600 keys.
-constexpr int kJoinThreads = 96;
+// on in the next ones, and add its rows' parts in key order; the blocks also
+// share out the rows whose tiles see no key at all, which no CTA had.  A launch
+// and two L2 round trips: the header, then the parts' maxima and sums (a lane
+// each) with the first accumulators.  A block has WR warps a row, which take every
+// WR-th part: 4 for tiles of few rows, of which a long cache makes many parts, 1
+// for those of many.
+constexpr int kJoinThreads = 128;
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads, 16)  // 40 registers
+template <int D, int WR>
+__global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const PagedAttn a, const CacheView c, void* ws, int RT, int parts) {
-    constexpr int E = D / 32;  // channels of a lane
-    __shared__ int s_end;
+    constexpr int E = D / 32, NW = kJoinThreads / 32;  // channels of a lane; warps
+    __shared__ float sums[WR > 1 ? NW : 1][D];
     const Partials part = partials_at(ws, RT, D);
-    const int mine = blockIdx.x, i0 = 2 * mine + 1, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_end = parts;
-    __syncthreads();
+    const int i0 = 2 * blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     wait_for_primary();
-    if (part.head[i0].valid) {
-        // the parts of CTAs mine .. end - 1: up to the first later one that has the item's end
-        for (int k = mine + 1 + threadIdx.x; k < parts; k += kJoinThreads)
-            if (part.head[2 * k].valid && part.head[2 * k].last) atomicMin(&s_end, k + 1);
-        __syncthreads();
-        const PartHeader hd = part.head[i0];
-        const int n = s_end - mine;
-        auto slot = [&](int k) { return (size_t)(k ? 2 * (mine + k) : i0) * RT; };
-        for (int row = blockIdx.y * (kJoinThreads / 32) + threadIdx.x / 32; row < hd.rows;
-             row += gridDim.y * (kJoinThreads / 32)) {
+    const PartHeader hd = part.head[i0];
+    const int n = min(hd.parts, parts - (int)blockIdx.x);
+    auto slot = [&](int k) { return (size_t)(k ? 2 * ((int)blockIdx.x + k) : i0) * RT; };
+    if (n > 0)
+        for (int row = blockIdx.y * (NW / WR) + warp / WR; row < hd.rows; row += gridDim.y * (NW / WR)) {
             float m = -INFINITY, l = 0.f, acc[E];
             for (int k = lane; k < n; k += 32) m = fmaxf(m, part.m[slot(k) + row]);
 #pragma unroll
@@ -516,10 +509,12 @@ __global__ void __launch_bounds__(kJoinThreads, 16)  // 40 registers
                     lw = w * part.l[slot(k0 + lane) + row];
                 }
                 const int some = min(n - k0, 32);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+                l += lw;
 #pragma unroll 8
-                for (int k = 0; k < some; ++k) {
+                for (int k = warp % WR; k < some; k += WR) {
                     const float wk = __shfl_sync(0xffffffffu, w, k);
-                    l += __shfl_sync(0xffffffffu, lw, k);
                     const float* o = part.o + (slot(k0 + k) + row) * D + lane * E;
                     if constexpr (E == 4) {
                         const float4 u = *reinterpret_cast<const float4*>(o);
@@ -534,10 +529,22 @@ __global__ void __launch_bounds__(kJoinThreads, 16)  // 40 registers
                     }
                 }
             }
+            if (WR > 1) {
+                // one row a block at a time: all four warps are here
+#pragma unroll
+                for (int e = 0; e < E; ++e) sums[warp][lane * E + e] = acc[e];
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    acc[e] = 0.f;
+                    for (int k = 0; k < WR; ++k) acc[e] += sums[k][lane * E + e];
+                }
+                __syncthreads();
+                if (warp) continue;
+            }
             store_row(a, hd.q0, hd.h, hd.r0 + row, lane * E, acc, inverse_sum(l));
             if (lane == 0) store_lse(a, c, hd.q0, hd.h, hd.r0 + row, m, l);
         }
-    }
     float none[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) none[e] = 0.f;
@@ -585,12 +592,14 @@ vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(parts, RT / 8 + 1);
+    // few rows: a row a block; many: 32 blocks an item
+    cfg.gridDim = dim3(parts, RT <= 32 ? RT : 32);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, join_kernel<D>, a, c, ws, RT, parts));
+    return cuda_status(RT <= 32 ? cudaLaunchKernelEx(&cfg, join_kernel<D, 4>, a, c, ws, RT, parts)
+                                : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, c, ws, RT, parts));
 }
 
 template <int D, int RG>

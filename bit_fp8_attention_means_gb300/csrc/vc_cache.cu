@@ -120,48 +120,97 @@ __device__ __forceinline__ void check_batch(const CacheView& c) {
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
 }
 
+// A group of lanes takes kRows consecutive rows (heads of one token, as a rule),
+// whose loads are on their way while the place of the token is looked up, once.
+// Measured, for 3,600 tokens of 40 heads written (112 MB) and 75,600 read back
+// (2.35 GB): one row 26.0 and 391 us, two 23.3 us (4.8 TB/s) and 342 us (6.9 TB/s),
+// four 25.1 and 347 us, eight 32.1 and 389 us; one token each of 96 sequences of 8
+// heads takes 3.5 us with one or two.
+constexpr int kRows = 2;
+
 template <int D, bool READ>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(const RowArgs a, const CacheView c) {
-    constexpr int W = D / 8;  // lanes of a row
+    constexpr int W = D / 8, U = kRows;  // lanes of a row, rows of a group
     check_batch(c);
     const int lane = threadIdx.x & 31, sub = lane & (W - 1);
     const unsigned mask = ((W == 16) ? 0xFFFFu : 0xFFu) << (lane & ~(W - 1));
-    const int64_t row = (int64_t)blockIdx.x * (kThreads / W) + threadIdx.x / W;
-    if (row >= (int64_t)c.T * c.H) return;
-    const int tok = (int)(row / c.H), h = (int)(row % c.H);
-    int64_t at = 0, st = 0;
-    bool found;
-    const bool there = locate<W>(c, tok, h, sub, mask, &at, &st, &found);
-    const int64_t x = (int64_t)tok * a.s_n + (int64_t)h * a.s_h + sub * 8;
+    const int64_t rows = (int64_t)c.T * c.H, row0 = ((int64_t)blockIdx.x * (kThreads / W) + threadIdx.x / W) * U;
+    if (row0 >= rows) return;
+    int tok = (int)(row0 / c.H), h = (int)(row0 - (int64_t)tok * c.H);
+    // rows of the group: token and head, and where their bf16 lie
+    int toks[U], hs[U];
+    int64_t x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        toks[u] = tok;
+        hs[u] = h;
+        x[u] = (int64_t)tok * a.s_n + (int64_t)h * a.s_h + sub * 8;
+        if (++h == c.H) {
+            h = 0;
+            ++tok;
+        }
+    }
+    uint4 kx[U], vx[U];
     if (!READ) {
-        if (!there) return;
-        const uint4 kx = __ldcs(reinterpret_cast<const uint4*>(a.K + x));
-        const uint4 vx = __ldcs(reinterpret_cast<const uint4*>(a.V + x));
-        float ks, vs;
-        const uint2 kc = quantize_row<W>(kx, mask, &ks), vc = quantize_row<W>(vx, mask, &vs);
-        *reinterpret_cast<uint2*>(c.K8 + at + sub * 8) = kc;
-        *reinterpret_cast<uint2*>(c.V8 + at + sub * 8) = vc;
-        if (sub == 0) {
-            c.sk[st] = ks;
-            c.sv[st] = vs;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (row0 + u >= rows) break;
+            kx[u] = __ldcs(reinterpret_cast<const uint4*>(a.K + x[u]));
+            vx[u] = __ldcs(reinterpret_cast<const uint4*>(a.V + x[u]));
+        }
+    }
+    int64_t at[U], st[U];
+    bool found[U], there[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        found[u] = there[u] = false;
+        if (row0 + u >= rows) continue;
+        if (u == 0 || toks[u] != toks[u - 1]) {
+            there[u] = locate<W>(c, toks[u], hs[u], sub, mask, &at[u], &st[u], &found[u]);
+        } else {
+            found[u] = found[u - 1];
+            there[u] = there[u - 1];
+            at[u] = at[u - 1] + c.s_head;
+            st[u] = st[u - 1] + c.t_head;
+        }
+    }
+    if (!READ) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!there[u]) continue;
+            float ks, vs;
+            const uint2 kc = quantize_row<W>(kx[u], mask, &ks), vc = quantize_row<W>(vx[u], mask, &vs);
+            *reinterpret_cast<uint2*>(c.K8 + at[u] + sub * 8) = kc;
+            *reinterpret_cast<uint2*>(c.V8 + at[u] + sub * 8) = vc;
+            if (sub == 0) {
+                c.sk[st[u]] = ks;
+                c.sv[st[u]] = vs;
+            }
         }
     } else {
-        if (!found) return;
-        uint4 ko = make_uint4(0, 0, 0, 0), vo = ko;
-        if (there) {
-            const uint2 kc = __ldcs(reinterpret_cast<const uint2*>(c.K8 + at + sub * 8));
-            const uint2 vc = __ldcs(reinterpret_cast<const uint2*>(c.V8 + at + sub * 8));
-            ko = dequantize_row(kc, __ldg(c.sk + st));
-            vo = dequantize_row(vc, __ldg(c.sv + st));
+        uint2 kc[U], vc[U];
+        float ks[U], vs[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!there[u]) continue;
+            kc[u] = __ldcs(reinterpret_cast<const uint2*>(c.K8 + at[u] + sub * 8));
+            vc[u] = __ldcs(reinterpret_cast<const uint2*>(c.V8 + at[u] + sub * 8));
+            ks[u] = __ldg(c.sk + st[u]);
+            vs[u] = __ldg(c.sv + st[u]);
         }
-        __stcs(reinterpret_cast<uint4*>(a.Kout + x), ko);
-        __stcs(reinterpret_cast<uint4*>(a.Vout + x), vo);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!found[u]) continue;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            __stcs(reinterpret_cast<uint4*>(a.Kout + x[u]), there[u] ? dequantize_row(kc[u], ks[u]) : zero);
+            __stcs(reinterpret_cast<uint4*>(a.Vout + x[u]), there[u] ? dequantize_row(vc[u], vs[u]) : zero);
+        }
     }
 }
 
 template <bool READ>
 vc_status launch_rows(const RowArgs& a, const CacheView& c, int d, cudaStream_t st) {
-    const int rows_per_block = kThreads / (d / 8);
+    const int rows_per_block = kThreads / (d / 8) * kRows;
     const unsigned grid = (unsigned)(((int64_t)c.T * c.H + rows_per_block - 1) / rows_per_block);
     if (d == 128) cache_rows_kernel<128, READ><<<grid, kThreads, 0, st>>>(a, c);
     else cache_rows_kernel<64, READ><<<grid, kThreads, 0, st>>>(a, c);

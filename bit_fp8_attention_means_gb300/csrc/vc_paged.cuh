@@ -114,6 +114,8 @@ struct Part {
     int64_t g0, g1;
     int b;        // sequence of g0
     int64_t off;  // g0's place in its sequence (all heads)
+    int64_t total;  // length of the line, and number of parts
+    int parts;
 };
 
 // Called by all NT threads of a block; the result is the same in all of them.
@@ -138,7 +140,7 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
         }
         return b0 + (int)threadIdx.x < c.B ? seq_cost(c, a, b0 + threadIdx.x, RT, IC) * c.H : 0;
     };
-    if (threadIdx.x == 0) found = Part{0, 0, 0, 0};
+    if (threadIdx.x == 0) found = Part{};
     const int64_t first_u = costs(0);
     int64_t mine = first_u;
     for (int b0 = NT; b0 < c.B; b0 += NT) {
@@ -154,6 +156,8 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     if (total < parts) parts = (int)total;  // no empty part between two others
     p.b = 0;
     p.off = 0;
+    p.total = total;
+    p.parts = parts;
     if (part >= parts) {
         p.g0 = p.g1 = 0;
         return p;
@@ -194,16 +198,22 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
 // warps; all members are uniform over the warp.
 template <int IC>
 struct ItemWalk {
-    int64_t left;    // of the part's length
+    int64_t at, left;  // place in the line, and what is left of the part
     int b, h, tile;  // the item
     SeqInfo s;
     ItemRange r;
     int unit, end;   // units [unit, end) of 128 keys, of this item in this part
+    int64_t item_end;  // the item's end in the line
     bool head;       // an earlier CTA has the item's first units
     bool tail;       // a later CTA has its last units
 
+    // Parts from this one on that have units of the item.
+    __device__ int parts_on(const Part& p, int part) const {
+        return tail ? (int)((item_end * p.parts - 1) / p.total) - part + 1 : 1;
+    }
     // To the first item; false where the part holds no unit at all.
     __device__ bool start(const CacheView& c, const PagedAttn& a, int RT, const Part& p) {
+        at = p.g0;
         left = p.g1 - p.g0;
         b = p.b;
         s = seq_info(c, b);
@@ -234,6 +244,8 @@ struct ItemWalk {
     __device__ bool take(int off) {
         const int u = r.units(), all = u + IC;
         const int to = left < all - off ? off + (int)left : all;
+        item_end = at + all - off;
+        at += to - off;
         left -= to - off;
         const int u0 = max(off - IC, 0), u1 = to - IC;
         head = u0 > 0;
@@ -267,8 +279,7 @@ struct ItemWalk {
 // What a CTA leaves in the workspace for an item that it shares: a header and,
 // for its rows, the running maximum (log2 units), the sum, the accumulator.
 struct PartHeader {
-    int valid;       // 0: nothing here
-    int last;        // the item's last units are in this part
+    int parts;       // from this one on that have units of the item; 0: nothing here
     int q0, h, r0, rows;  // first row of the sequence, head, first (token, head) pair and number of pairs
 };
 

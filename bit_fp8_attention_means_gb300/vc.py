@@ -5,6 +5,7 @@ kernels.  PyTorch supplies device memory and the current stream.  There is no
 fallback: if the library has not been built, every call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -309,6 +310,9 @@ def vc_attn_fwd(qz, shape: VcShape, softmax_scale=0.0, expcast=1, vsmooth=1, O=N
 
 # ------------------------------------------------------------ paged cache
 
+_U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+
+
 def alloc_cache(pages, page_size, H, d, device):
     """A page pool for vc_cache_append, vc_cache_read and vc_attn_paged: dict of K8, V8 (E4M3 bytes
     [pages, H, page_size, d]) and their scales sk, sv (fp32 [pages, H, page_size]), zeroed.
@@ -327,14 +331,13 @@ def alloc_cache(pages, page_size, H, d, device):
 def _cache_parts(cache):
     """Checks a dict of K8, sk, V8, sv (see alloc_cache): its vc_cache_shape, the four pointers, the device's index."""
     K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
-    shape, k, t = tuple(K8.shape), K8.stride(), sk.stride()
-    if len(shape) != 4 or K8.dtype != torch.uint8 or V8.dtype != torch.uint8 or tuple(V8.shape) != shape:
+    shape, k, t = K8.shape, K8.stride(), sk.stride()
+    if len(shape) != 4 or K8.dtype is not _U8 or V8.dtype is not _U8 or V8.shape != shape:
         raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
-    if sk.dtype != torch.float32 or sv.dtype != torch.float32 or tuple(sk.shape) != shape[:3] or \
-            tuple(sv.shape) != shape[:3]:
+    pages, H, page, d = shape
+    if sk.dtype is not _F32 or sv.dtype is not _F32 or sk.shape != (pages, H, page) or sv.shape != (pages, H, page):
         raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
     v, u = V8.stride(), sv.stride()
-    pages, H, page, d = shape
     if pages < 2 or H < 2:  # a dimension of one element may have any stride: it gets a legal one
         k, v = _plain_strides(shape, k, d), _plain_strides(shape, v, d)
         t, u = _plain_strides(shape[:3], t, page), _plain_strides(shape[:3], u, page)
@@ -360,24 +363,25 @@ def cache_shape_of(cache) -> VcCacheShape:
 
 
 def _batch_of(cu, kv_len, table, T, dev) -> VcBatch:
-    i32 = torch.int32
-    n, B, c = tuple(cu.shape), tuple(kv_len.shape), tuple(table.shape)
-    if cu.dtype != i32 or kv_len.dtype != i32 or table.dtype != i32 or len(n) != 1 or len(B) != 1 or len(c) != 2:
+    c = table.shape
+    if cu.dtype is not _I32 or kv_len.dtype is not _I32 or table.dtype is not _I32 or len(c) != 2 or \
+            cu.dim() != 1 or kv_len.dim() != 1:
         raise ValueError("cu [B+1], kv_len [B] and table [B, cols] must be int32")
-    if n[0] != c[0] + 1 or B[0] != c[0]:
+    B, cols = c
+    if cu.numel() != B + 1 or kv_len.numel() != B:
         raise ValueError("cu, kv_len and table disagree on the number of sequences")
-    s, cols = table.stride(), c[1]
-    if cu.stride()[0] != 1 or (kv_len.stride()[0] != 1 and c[0] > 1) or (s[1] != 1 and cols > 1):
+    s = table.stride()
+    if cu.stride(0) != 1 or (B > 1 and kv_len.stride(0) != 1) or (s[1] != 1 and cols > 1):
         raise ValueError("cu, kv_len and the rows of table must be contiguous")
     if cu.get_device() != dev or kv_len.get_device() != dev or table.get_device() != dev:
         raise ValueError("cu, kv_len or table is not on the cache's device")
-    return VcBatch(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), c[0], T, cols, s[0] if c[0] > 1 else max(cols, 1))
+    return VcBatch(cu.data_ptr(), kv_len.data_ptr(), table.data_ptr(), B, T, cols, s[0] if B > 1 else max(cols, 1))
 
 
 def _rows(name, t, H, d, dev):
     """Checks a bf16 [T, H, d] tensor with contiguous channels: its row and head strides."""
-    shape, s = tuple(t.shape), t.stride()
-    if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != H or shape[2] != d:
+    shape, s = t.shape, t.stride()
+    if t.dtype is not _BF16 or len(shape) != 3 or shape[1] != H or shape[2] != d:
         raise ValueError("%s must be bf16 [T, %d, %d]" % (name, H, d))
     if s[2] != 1:
         raise ValueError("%s must have contiguous channels" % name)
@@ -397,7 +401,7 @@ def _status_ptr(dev_status, dev):
 def _on_device(dev, stream, fn, args, where, made):
     """Calls fn(*args, stream) with device `dev` current, and keeps the tensors in `made` (made here, on
     the current stream) for a stream that is not the current one."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     if here != dev:
         torch.cuda.set_device(dev)
     try:
@@ -446,10 +450,10 @@ def vc_cache_read(cache, cu, kv_len, table, T, K=None, V=None, dev_status=None, 
     _need_cuda(dev)
     made = []
     if K is None:
-        K = torch.empty((T, s.H, s.d), dtype=torch.bfloat16, device=cache["K8"].device)
+        K = cache["K8"].new_empty((T, s.H, s.d), dtype=_BF16)
         made.append(K)
     if V is None:
-        V = torch.empty_strided(K.shape, K.stride(), dtype=torch.bfloat16, device=K.device)
+        V = torch.empty_like(K) if K.is_contiguous() else K.new_empty_strided(K.shape, K.stride())
         made.append(V)
     strides = _rows("K", K, s.H, s.d, dev)
     if K.shape[0] != T or V.shape != K.shape or _rows("V", V, s.H, s.d, dev) != strides:
@@ -457,6 +461,13 @@ def vc_cache_read(cache, cu, kv_len, table, T, K=None, V=None, dev_status=None, 
     _on_device(dev, stream, L.vc_cache_read, (s, K8, sk, V8, sv, batch, K.data_ptr(), V.data_ptr(), *strides, status),
                "vc_cache_read", made)
     return K, V
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_paged_bytes(page_size, H, d, Hq, B, T, max_q):
+    """vc_attn_paged_workspace, which depends on these numbers alone."""
+    s = VcCacheShape(1, page_size, H, d, H * page_size * d, page_size * d, d, H * page_size, page_size)
+    return lib().vc_attn_paged_workspace(s, Hq, B, T, max_q)
 
 
 def attn_paged_workspace_bytes(cache, Hq, B, T, max_q=0) -> int:
@@ -474,7 +485,7 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
     kernel, nothing else).  Rows of no sequence stay as they are in O and lse."""
     L = lib()
     s, (K8, sk, V8, sv), dev = _cache_parts(cache)
-    shape = tuple(Q.shape)
+    shape = Q.shape
     if len(shape) != 3:
         raise ValueError("Q must be bf16 [T, Hq, %d]" % s.d)
     T, Hq, d = shape
@@ -484,22 +495,21 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
     _need_cuda(dev)
     made = []
     if O is None:
-        O = torch.empty(shape, dtype=torch.bfloat16, device=Q.device)
+        O = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty(shape)
         o_strides = (Hq * d, d)
         made.append(O)
     else:
         o_strides = _rows("O", O, Hq, d, dev)
-        if tuple(O.shape) != shape:
+        if O.shape != shape:
             raise ValueError("O must have Q's shape")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty((T, Hq), dtype=_F32)
         made.append(lse)
     elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or \
             lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
     if workspace is None:
-        workspace = torch.empty(max(L.vc_attn_paged_workspace(s, Hq, batch.B, T, max_q), 256), dtype=torch.uint8,
-                                device=Q.device)
+        workspace = Q.new_empty(max(_attn_paged_bytes(s.page_size, s.H, d, Hq, batch.B, T, max_q), 256), dtype=_U8)
         made.append(workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
