@@ -158,6 +158,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 return pg < 0 ? -2 : pg;
             };
             int ahead = entry(w.unit);
+            if (role == 0)
+                // the item's queries on their way to L2 while the last item's units are under way
+                for (int i = lane; i < rows; i += 32) {
+                    const int tok = (r0 + i) / a.G;
+                    const uint16_t* src =
+                        a.Q + (int64_t)(w.s.q0 + tok) * a.q_sn + (int64_t)(w.h * a.G + r0 + i - tok * a.G) * a.q_sh;
+                    prefetch_l2(src);
+                    if (D == 128) prefetch_l2(src + 64);
+                }
             for (int u = w.unit; u < w.end; ++u, ++it) {
                 const int st = it % NS, key0 = u * kUnit;
                 int pg = ahead;

@@ -109,6 +109,12 @@ __device__ __forceinline__ int64_t seq_cost_warp(const PagedAttn& a, const SeqIn
     return u;
 }
 
+// a / b of numbers that are small as a rule: a 64-bit division is a long subroutine,
+// and a CTA's first microsecond.
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The part of a CTA: [g0, g1) of the line, and where g0 lies.
 struct Part {
     int64_t g0, g1;
@@ -162,8 +168,8 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
         p.g0 = p.g1 = 0;
         return p;
     }
-    p.g0 = total * part / parts;
-    p.g1 = total * (part + 1) / parts;
+    p.g0 = div_small(total * part, parts);
+    p.g1 = div_small(total * (part + 1), parts);
     int64_t before = 0;  // cost of the sequences of earlier rounds
     for (int b0 = 0; b0 < c.B; b0 += NT) {
         __syncthreads();
@@ -209,7 +215,7 @@ struct ItemWalk {
 
     // Parts from this one on that have units of the item.
     __device__ int parts_on(const Part& p, int part) const {
-        return tail ? (int)((item_end * p.parts - 1) / p.total) - part + 1 : 1;
+        return tail ? (int)div_small(item_end * p.parts - 1, p.total) - part + 1 : 1;
     }
     // To the first item; false where the part holds no unit at all.
     __device__ bool start(const CacheView& c, const PagedAttn& a, int RT, const Part& p) {
@@ -218,8 +224,8 @@ struct ItemWalk {
         b = p.b;
         s = seq_info(c, b);
         const int64_t per_head = seq_cost_warp(a, s, RT, IC);
-        h = (int)(p.off / per_head);
-        int64_t off = p.off % per_head;
+        h = (int)div_small(p.off, per_head);
+        int64_t off = p.off - h * per_head;
         const int nt = seq_tiles(a, s, RT), lane = threadIdx.x & 31;
         for (int t0 = 0;; t0 += 32) {
             int64_t scan = t0 + lane < nt ? item_cost(a, s, t0 + lane, RT, IC) : 0;
