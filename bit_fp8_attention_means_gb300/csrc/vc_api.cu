@@ -236,6 +236,7 @@ static vc_status check_cache_shape(const vc_cache_shape& c) {
     if (c.pages < 1 || c.page_size < 1 || c.H < 1 || c.d < 1) return VC_ERR_INVALID_ARG;
     if (c.s_page <= 0 || c.s_head <= 0 || c.s_tok <= 0 || c.s_page % 16 || c.s_head % 16 || c.s_tok % 16)
         return VC_ERR_INVALID_ARG;
+    if (c.s_page >> 40 || c.s_head >> 40 || c.s_tok >> 40) return VC_ERR_INVALID_ARG;  // what a tensor map holds
     if (c.t_page <= 0 || c.t_head <= 0 || c.t_page % 4 || c.t_head % 4) return VC_ERR_INVALID_ARG;
     if (c.d != 64 && c.d != 128) return VC_ERR_UNSUPPORTED;
     if (c.page_size < 16 || c.page_size > 4096 || (c.page_size & (c.page_size - 1))) return VC_ERR_UNSUPPORTED;
@@ -249,7 +250,8 @@ static vc_status cache_view(const vc_cache_shape& c, const uint8_t* K8, const fl
     if (!K8 || !sk || !V8 || !sv || !b.cu || !b.kv_len || !b.table) return VC_ERR_INVALID_ARG;
     if (!aligned16(K8) || !aligned16(V8) || !aligned16(sk) || !aligned16(sv)) return VC_ERR_INVALID_ARG;
     if (b.s_table < b.cols) return VC_ERR_INVALID_ARG;
-    if ((int64_t)b.cols * c.page_size >= (int64_t(1) << 31) || (int64_t)b.T * c.H >= (int64_t(1) << 31))
+    // positions and rows are 32-bit, with room for a unit of keys and a tile of rows past the end
+    if ((int64_t)b.cols * c.page_size >= (int64_t(1) << 30) || (int64_t)b.T * c.H >= (int64_t(1) << 31))
         return VC_ERR_UNSUPPORTED;
     out->K8 = const_cast<uint8_t*>(K8);
     out->sk = const_cast<float*>(sk);
@@ -310,7 +312,7 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
 
 static vc_status check_paged_heads(const vc_cache_shape& c, int Hq, int T, int max_q) {
     if (Hq < 1 || Hq % c.H || max_q < 0) return VC_ERR_INVALID_ARG;
-    if ((int64_t)T * Hq >= (int64_t(1) << 31)) return VC_ERR_UNSUPPORTED;
+    if ((int64_t)T * Hq >= (int64_t(1) << 30)) return VC_ERR_UNSUPPORTED;
     return VC_OK;
 }
 

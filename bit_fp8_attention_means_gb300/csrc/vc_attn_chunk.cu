@@ -3,17 +3,18 @@
 // Per row, over its keys t, with the cached codes k8, v8 and scales sk, sv:
 //   s_t = (q . k8_t) sk_t scale log2 e,   P_t = 2^(s_t - M),   l = sum_t P_t,
 //   A = sum_t (P_t sv_t) v8_t,            O = A / l,
-// M being the running maximum of s_t + log2 sv_t: P sv, which goes to the product
-// as fp16, is then at most 1 whatever the scales are.  M follows only where the
-// unit's sum of P times its largest sv passes 2^15, so that P sv stays finite in
-// fp16 (whose precision is the same up to there) without a maximum being taken;
-// then a pass of its own over the unit finds the new M.
+// M being the running maximum of s_t + log2 sv_t, rounded down to a whole number:
+// P sv, which goes to the product as fp16, is then below 2 whatever the scales
+// are.  M follows only where the unit's sum of P times its largest sv passes 2^15,
+// so that P sv stays finite in fp16 (whose precision is the same up to there)
+// without a maximum being taken; then a pass of its own over the unit finds the
+// new M, and what was summed before is scaled by a power of two.
 //
-// One persistent CTA on each SM
-// takes tiles of 256 rows as two pipelines A and B of 128 rows, which share the
-// keys and values and the tensor core, so that the softmax of one overlaps the
-// products of the other; a tile of up to 128 rows is given to both, which then
-// take its units of 128 keys in turn and are added up at its end.
+// One persistent CTA on each SM takes tiles of 256 rows as two pipelines A and B
+// of 128 rows, which share the keys and values and the tensor core, so that the
+// softmax of one overlaps the products of the other; a tile of up to 128 rows is
+// given to both, which then take its units of 128 keys in turn and are added up at
+// its end.
 //
 // Per unit and pipeline, 128 rows x 128 keys:
 //   S = q K8^T in kind::f8f6f4, straight from the cached codes: the query row,
@@ -25,9 +26,14 @@
 //       which a warpgroup converts once a unit for both pipelines.  (P as two
 //       E4M3 numbers would spare that, but lose everything below 2^-17 of the
 //       row's largest: a few thousand keys there are a visible part of a sum.)
-// What bounds it is the tensor core: 4 x 512 clocks a unit for both pipelines;
-// the softmax needs about 700 issue slots a warp and unit, two such warps and a
-// converting one on each scheduler.
+// The floor is the tensor core's 4 x 512 clocks a unit of both pipelines (d = 128).
+// Measured: 3,640 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.40 ms, 1,270
+// TFLOP/s.  Without any softmax arithmetic a unit took 3,150 clocks (the products
+// read 192 KB of shared memory a unit, 1,536 clocks of its bandwidth, beside the
+// conversion's and the scales'), without products 3,100: what is left is the chain
+// from scores to P and back, half hidden by the other pipeline, and instructions
+// that have to be fetched (the softmax loop, the issuer and the converter together
+// run out of the first instruction cache).  With d = 64 the chain alone bounds it.
 //
 // 16 warps:
 //   0-3, 4-7  softmax of A and B: a thread owns a row (its TMEM lane).
@@ -282,8 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // One warp issues for both pipelines, in turn: the product P V of a pipeline's last
             // unit, then its next scores, then the same for the other.  So the two stay half a
             // step apart, one in its softmax while the tensor core works for the other.  (Two
-            // issuers side by side fell into step, each waiting for both pipelines' products:
-            // 6.3 ms against XX ms for a 3,600-token chunk over 75,600 keys of 40 heads.)
+            // issuers side by side fell into step, each waiting for both pipelines' products.)
             constexpr uint32_t IDESC_QK = idesc_f8_e4m3(128, 128), IDESC_PV = idesc_f16_bn(128, D);
             int items = 0;                           // items ended
             int own[2] = {0, 0};                     // units whose P V has been issued
@@ -544,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (hole || 2 * i + 1 < lo || 2 * i + 1 > hi) y[i].y = -INFINITY;
                         }
                     };
-                    // The chunk's part of M: the maximum of s + log2 sv, and of s - 100, which keeps P
-                    // finite where a row sees little but tokens whose values are all zero.
+                    // The chunk's part of M: the maximum of s + log2 sv, and of s - kZeroLog2.
                     auto find_m = [&]() -> float {
                         float mj = -INFINITY, ms = -INFINITY;
 #pragma unroll 1
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           fmaf(y[i + 1].y, qs, lg2_approx(sv.w)));
                             }
                         }
-                        return fmaxf(mj, ms * qs - 100.f);
+                        return floorf(fmaxf(mj, ms * qs - kZeroLog2));
                     };
                     // P sv of the chunk against M, as fp16 in pw; returns the sum of P.  16 keys at a time,
                     // the next scores and key scales on their way, eight independent operations behind
@@ -656,8 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                         sum = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
-                        // (an infinite sum: a token whose values are all zero far above M)
-                        raise = sum * sv_top > 32768.f || sum == INFINITY;
+                        // (a sum of over 2^96: tokens whose values are all zero far above M)
+                        raise = sum * sv_top > 32768.f || sum > 0x1p96f;
                         if (!__any_sync(0xffffffffu, raise)) break;
                     }
                     l += sum;

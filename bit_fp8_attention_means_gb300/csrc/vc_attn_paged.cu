@@ -37,8 +37,10 @@ namespace {
 // Codes become fp16 on the way from shared memory to registers; the channels of
 // q . k and the keys and channels of P V are permuted so that each thread reads
 // 16 consecutive bytes, in an order without bank conflicts under the TMA
-// swizzle.  Rows as the wide side, 8 warps and one producer took 251 us where
-// this takes XX us (one token of 96 sequences, 747 MB).
+// swizzle.  One token of 96 sequences of 100 to 8,192 keys (747 MB, pages of 16):
+// 151 us, 4.9 TB/s; rows as the wide side, 8 warps and one producer took 251 us.
+// One token against 75,600 keys (160 MB): 40 us, of which 25 us at 6.4 TB/s lie
+// between the first data (6 us) and the joining (6 us).
 
 // What an item costs besides its units, in units: the queries, and adding up the warps' parts.
 constexpr int kItemCost = 3;
@@ -319,15 +321,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             mma_f16((k & 1) ? z : x, ka, q[hf * 4 + k][0], q[hf * 4 + k][1]);
                         }
                     }
-                    // x = (q . k8) sk scale log2 e + log2 sv
-                    float isv[2];
+                    // x = (q . k8) sk scale log2 e + log2 sv.  A token whose values are all zero
+                    // raises M only where it would pass 2^kZeroLog2 of P; its P counts in l alone,
+                    // and what fp16 makes of it (no infinity) meets codes of zero.
+                    float isv[2], up[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int k = kb + 8 * t + krg;
                         const float sk = sks[k], sv = svs[k];
-                        const float lv = sv == 0.f ? kZeroLog2 : lg2_approx(sv);
+                        up[t] = sv == 0.f ? kZeroLog2 : 0.f;
+                        const float lv = sv == 0.f ? -kZeroLog2 : lg2_approx(sv);
                         // a NaN scale makes x NaN where it is seen; elsewhere 0 * isv has to stay 0
-                        isv[t] = sv == 0.f ? 0x1p60f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
+                        isv[t] = sv == 0.f ? 1.f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
                         x[2 * t] = fmaf((x[2 * t] + z[2 * t]) * sk, qs[0], lv);
                         x[2 * t + 1] = fmaf((x[2 * t + 1] + z[2 * t + 1]) * sk, qs[1], lv);
                     }
@@ -366,13 +371,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        x[2 * t] = ex2_approx(x[2 * t] - m0);
-                        x[2 * t + 1] = ex2_approx(x[2 * t + 1] - m1);
+                        x[2 * t] = ex2_approx(x[2 * t] + (up[t] - m0));
+                        x[2 * t + 1] = ex2_approx(x[2 * t + 1] + (up[t] - m1));
                         l[0] = fmaf(x[2 * t], isv[t], l[0]);
                         l[1] = fmaf(x[2 * t + 1], isv[t], l[1]);
                     }
                     // P^T: keys as the products' inner index, this thread's row g
-                    const uint32_t p0 = transpose8(pack_f16(x[0], x[1])), p1 = transpose8(pack_f16(x[2], x[3]));
+                    const uint32_t p0 = transpose8(pack_f16_sat(x[0], x[1])), p1 = transpose8(pack_f16_sat(x[2], x[3]));
                     // V^T P^T: the four keys of this thread, D/8 channels of each
                     uint32_t v[4][D / 32];
 #pragma unroll

@@ -367,13 +367,15 @@ vc_status vc_attn_fwd_hybrid(const uint8_t* Q8, const float* sq, const uint8_t* 
  * of the first three (byte strides below, channel stride 1; the two share
  * strides).  sk, sv: fp32 scales [page, head, token], token stride 1.  The
  * value of a code is code * scale.  K8 and V8 may be two halves of one
- * allocation.
+ * allocation.  The codes of tokens that a sequence holds are numbers (NaN codes,
+ * 0x7F and 0xFF, are never written); what lies in slots that hold no token of
+ * the sequence is never looked at and may be anything.
  */
 typedef struct {
     int32_t pages;     /* pages in the pool, >= 1 */
     int32_t page_size; /* tokens of a page: a power of two, 16 .. 4096 */
     int32_t H, d;      /* key/value heads; channels of a head, 64 or 128 */
-    int64_t s_page, s_head, s_tok; /* strides of K8 and V8 in bytes, positive multiples of 16 */
+    int64_t s_page, s_head, s_tok; /* strides of K8 and V8 in bytes, positive multiples of 16 below 2^40 */
     int64_t t_page, t_head;        /* strides of sk and sv in floats, positive multiples of 4 */
 } vc_cache_shape;
 
@@ -422,7 +424,7 @@ typedef struct {
  * Errors, before any launch: VC_ERR_INVALID_ARG (a null pointer, a misaligned
  * K, V, K8, V8, sk or sv (16 bytes), a stride or size out of the ranges above,
  * B < 1, T < 0, cols < 1), VC_ERR_UNSUPPORTED (d not 64 or 128, a page_size
- * outside the list, T * H >= 2^31, cols * page_size >= 2^31); VC_ERR_CUDA if
+ * outside the list, T * H >= 2^31, cols * page_size >= 2^30); VC_ERR_CUDA if
  * a launch fails.
  */
 vc_status vc_cache_append(const void* K, const void* V, int64_t s_n, int64_t s_h, vc_cache_shape cache,
@@ -453,10 +455,14 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
  *   row (i, h) sees:
  *     s_t = softmax_scale q . k_t,  O = sum_t e^(s_t) v_t / sum_t e^(s_t),
  *     lse = ln sum_t e^(s_t).
- *   Sums, maxima and the scores' scaling are fp32; the probabilities enter the
- *   product with the value codes as fp16 (relative error <= 2^-11 above 2^-14
- *   of the row's largest), after the tokens' value scales are folded into
- *   their exponents.  A row that sees no key gets O = 0 and lse = -inf.
+ *   Sums, maxima and the scores' scaling are fp32.  The probabilities enter the
+ *   product with the value codes as fp16, each times its token's value scale
+ *   (relative error <= 2^-11 above 2^-14 of the row's largest such product).  A
+ *   query enters the scores exactly or, for many rows, as two E4M3 parts
+ *   (within 2^-17 of its largest channel).  Where a token whose values are all
+ *   zero has 2^88 times the weight of every other times that one's value scale,
+ *   the others' values may count as zero.  A row that sees no key gets O = 0
+ *   and lse = -inf.
  *   Tokens of pages that are not there count as unseen (*dev_status).
  *   max_q    the largest n_b, as far as the caller knows it (0: unknown).  It
  *            chooses among kernels and sizes the workspace's share of each; a
@@ -472,7 +478,7 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
  * bits.  softmax_scale <= 0 stands for 1/sqrt(d).  T = 0 does nothing.
  * Errors as vc_cache_append, plus VC_ERR_INVALID_ARG for Hq not a positive
  * multiple of cache.H, causal not in {0, 1}, window < 0, max_q < 0, a
- * softmax_scale that is not finite; VC_ERR_UNSUPPORTED for T * Hq >= 2^31;
+ * softmax_scale that is not finite; VC_ERR_UNSUPPORTED for T * Hq >= 2^30;
  * VC_ERR_WORKSPACE.
  */
 size_t vc_attn_paged_workspace(vc_cache_shape cache, int Hq, int B, int T, int max_q);

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from bit_fp8_attention_means_gb300 import vc
-from paged_case import Case, quantize
+from paged_case import LOG2E, Case, quantize
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -420,3 +420,64 @@ def test_scale_of_new_values_reaches_the_output():
     codes, scale = quantize(c.V)
     value = codes.view(torch.float8_e4m3fn).float() * scale[..., None]
     assert torch.all((O.float().cpu() - value).abs() <= 2.0 ** -8 * value.abs() + 2.0 ** -20 * value.abs())
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (90, 1), (300, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_heavy_tokens_without_values(n, G, d):
+    """Tokens whose values are all zero take nearly all of the weight: the others' share stays right as
+    long as they have no more than 2^88 times the others' weights times value scales; beyond, it may
+    vanish, and nothing overflows."""
+    c = Case(n=[n, n], kv=[900, 400], H=2, G=G, d=d, seed=33)
+    zero = torch.rand(c.sv.shape, generator=torch.Generator().manual_seed(3)) < 0.5
+    c.V8[zero], c.sv[zero] = 0, 0.0
+    keys = c.sk.clone()
+    for times in (14.0, 120.0):
+        c.sk = torch.where(zero, keys * times, keys)
+        cache = c.cache()
+        over = torch.zeros(c.T, 2 * G, dtype=torch.float64)   # log2 of that ratio
+        for b in range(2):
+            last = c.kv[b] - n + torch.arange(n)
+            for h in range(2):
+                (k, ks, _), (_, vs, _) = (c.sequence(cache, a, e, b, h) for a, e in (("K8", "sk"), ("V8", "sv")))
+                unseen = torch.arange(c.kv[b]) > last[:, None]
+                for j in range(G):
+                    q = c.Q.double()[b * n:(b + 1) * n, h * G + j]
+                    s = (q @ (k * ks[:, None]).T / math.sqrt(d) * LOG2E).masked_fill(unseen, -math.inf)
+                    over[b * n:(b + 1) * n, h * G + j] = s[:, vs == 0].amax(-1) - (s + vs.log2())[:, vs > 0].amax(-1)
+        O, lse = (t.double().cpu() for t in attend(c))
+        O_ref, tol, lse_ref, told = c.attend(cache)
+        assert torch.all((lse - lse_ref).abs() <= told)
+        within = over <= 88
+        assert torch.all((O - O_ref).abs()[within] <= tol[within])
+        assert torch.isfinite(O).all() and torch.all(O[over > 120].abs() <= 1e-30)
+        assert within.any() if times < 100 else (over > 120).any()
+
+
+def test_calls_of_two_host_threads():
+    """Two threads, each with its own stream, cache and outputs, at the same time."""
+    import threading
+    cases = [Case(n=[n] * 2, kv=[800, 300], H=2, G=G, seed=40 + n) for n, G in ((1, 4), (150, 1))]
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            c, stream = cases[i], torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                cache, args, Q, K, V = c.cache(DEV), c.args(DEV), c.Q.to(DEV), c.K.to(DEV), c.V.to(DEV)
+                for _ in range(20):
+                    vc.vc_cache_append(K, V, cache, *args)
+                    got[i].append(vc.vc_attn_paged(Q, cache, *args, max_q=max(c.n)))
+            stream.synchronize()
+        except Exception as e:                              # carried to the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for c, outs in zip(cases, got):
+        c.check(outs[0], c.appended())
+        for O, lse in outs[1:]:
+            assert same_bits(O, outs[0][0]) and same_bits(lse, outs[0][1])

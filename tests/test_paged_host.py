@@ -34,9 +34,11 @@ def _batch(**kw):
 
 BAD_SHAPES = [(dict(pages=0), 1), (dict(H=0), 1), (dict(d=0), 1), (dict(page_size=-16), 1), (dict(d=96), 2), (dict(d=256), 2),
               (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=8192), 2), (dict(s_tok=0), 1),
-              (dict(s_tok=8), 1), (dict(s_page=-4096), 1), (dict(s_head=24), 1), (dict(t_page=0), 1), (dict(t_head=6), 1)]
+              (dict(s_tok=8), 1), (dict(s_page=-4096), 1), (dict(s_head=24), 1), (dict(t_page=0), 1), (dict(t_head=6), 1),
+              (dict(s_page=1 << 40), 1), (dict(s_head=1 << 41), 1), (dict(s_tok=1 << 40), 1)]
 BAD_BATCHES = [(dict(B=0), 1), (dict(T=-1), 1), (dict(cols=0), 1), (dict(cu=None), 1), (dict(kv_len=None), 1),
-               (dict(table=None), 1), (dict(s_table=3), 1), (dict(cols=1 << 27, s_table=1 << 27), 2), (dict(T=1 << 30), 2)]
+               (dict(table=None), 1), (dict(s_table=3), 1), (dict(cols=1 << 27, s_table=1 << 27), 2), (dict(T=1 << 30), 2),
+               (dict(cols=1 << 26, s_table=1 << 26), 2)]
 
 
 def _append(L, cache, batch, K=FAKE, V=FAKE, s_n=256, s_h=128, codes=(FAKE,) * 4):
@@ -79,6 +81,7 @@ def test_attention_refusals(L):
                dict(window=-1), dict(max_q=-1), dict(lse=ctypes.c_void_p(0x10002))):
         assert _attn(L, _cache(), _batch(), **kw) == 1, kw
     assert _attn(L, _cache(), _batch(T=1 << 28), Hq=16) == 2
+    assert _attn(L, _cache(), _batch(T=1 << 28), Hq=4) == 2
     need = L.vc_attn_paged_workspace(_cache(), 4, 3, 7, 0)
     if need:
         assert _attn(L, _cache(), _batch(), ws=None) == 3
