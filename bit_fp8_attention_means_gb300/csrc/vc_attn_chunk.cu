@@ -741,10 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Partials part = partials_at(ws, RT, D);
             const int64_t o_off = split ? ((int64_t)slot * RT + tr) * D
                                         : (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
-            // Rows go through shared memory (the warp's part of the queries, which no product reads
-            // any more), so that what leaves are whole lines: 32 channels at a time, each row's
-            // 16-byte pieces turned by the row.
-            float4* stage = reinterpret_cast<float4*>(smem + C::OFF_Q + 2 * X * C::QB) + q * 256;
+            // Rows go through shared memory (the warp's own rows of the queries, which no product reads
+            // any more and no other warp writes for the next item), so that what leaves are whole
+            // lines: 32 channels at a time, each row's 16-byte pieces turned by the row.
+            uint8_t* stage = smem + C::OFF_Q + 2 * X * C::QB + q * 32 * D;
+            auto staged = [&](int r, int piece) -> float4& {  // d = 64: 16 rows fit in each of the two parts
+                return *reinterpret_cast<float4*>(stage + r * 128 + (D == 64 && r >= 16 ? C::QB - 2048 : 0) +
+                                                  ((piece ^ (r & 7)) << 4));
+            };
             const int piece = lane & 7;
             int64_t off[8];  // of the rows that this lane stores a piece of
 #pragma unroll
@@ -769,12 +773,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    stage[lane * 8 + (i ^ (lane & 7))] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    staged(lane, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int rr = 4 * i + lane / 8;
-                    const float4 x = stage[rr * 8 + (piece ^ (rr & 7))];
+                    const float4 x = staged(rr, piece);
                     if (off[i] < 0) continue;
                     if (split) {
                         *reinterpret_cast<float4*>(part.o + off[i] + c0) = x;
