@@ -27,13 +27,12 @@
 //       E4M3 numbers would spare that, but lose everything below 2^-17 of the
 //       row's largest: a few thousand keys there are a visible part of a sum.)
 // The floor is the tensor core's 4 x 512 clocks a unit of both pipelines (d = 128).
-// Measured: 3,640 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.40 ms, 1,270
-// TFLOP/s.  Without any softmax arithmetic a unit took 3,150 clocks (the products
-// read 192 KB of shared memory a unit, 1,536 clocks of its bandwidth, beside the
-// conversion's and the scales'), without products 3,100: what is left is the chain
-// from scores to P and back, half hidden by the other pipeline, and instructions
-// that have to be fetched (the softmax loop, the issuer and the converter together
-// run out of the first instruction cache).  With d = 64 the chain alone bounds it.
+// Measured: 3,640 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.39 ms, 1,270
+// TFLOP/s.  Shared memory's data path is the busiest part (products 35 %, loads and
+// stores 50 %, TMA besides): without softmax arithmetic a unit still took 3,150 clocks.
+// Two threads a row (5.9 ms), loads that need fewer scales (16x256b, 4.6 ms) and a
+// converter of two thirds the instructions (4.5 ms) gained nothing.  With d = 64 the
+// chain from scores to P bounds it as well (tensor core 23 % busy).
 //
 // 16 warps:
 //   0-3, 4-7  softmax of A and B: a thread owns a row (its TMEM lane).
