@@ -27,12 +27,13 @@
 //       E4M3 numbers would spare that, but lose everything below 2^-17 of the
 //       row's largest: a few thousand keys there are a visible part of a sum.)
 // The floor is the tensor core's 4 x 512 clocks a unit of both pipelines (d = 128).
-// Measured: 3,640 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.39 ms, 1,270
-// TFLOP/s.  Shared memory's data path is the busiest part (products 35 %, loads and
-// stores 50 %, TMA besides): without softmax arithmetic a unit still took 3,150 clocks.
-// Two threads a row (5.9 ms), loads that need fewer scales (16x256b, 4.6 ms) and a
-// converter of two thirds the instructions (4.5 ms) gained nothing.  With d = 64 the
-// chain from scores to P bounds it as well (tensor core 23 % busy).
+// Measured: 3,560 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.30 ms, 1,297
+// TFLOP/s.  Without softmax arithmetic a unit still took 3,150 clocks.  Shared memory's data
+// path is the busiest part (products 35 %, loads and stores 50 %, TMA besides), and code
+// that runs beside other code costs instruction fetches: two threads a row (5.9 ms), loads
+// that need fewer scales (16x256b, 4.6 ms) and warps of their own for the scales (4.8 ms)
+// all lost.  With d = 64 the chain from scores to P bounds it as well (tensor core 23 %
+// busy).
 //
 // 16 warps:
 //   0-3, 4-7  softmax of A and B: a thread owns a row (its TMEM lane).
@@ -111,15 +112,19 @@ __device__ __forceinline__ int no_hoist(int x) {
     return x;
 }
 
-template <int D>
+template <int D, int kChunk>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedAttn a, const CacheView c, int RT, void* ws) {
     using C = ManyCfg<D>;
-    // Keys that the softmax takes at a time, by what fits the instruction cache beside the rest:
-    // 64 with d = 128 (32: 5.1 ms against 4.7 for 3,600 rows over 75,600 keys; 128: 5.6), 32 with
-    // d = 64, where the products hide less of it (windowed chunks 0.82 ms against 0.93).
-    constexpr int kChunk = D == 128 ? 64 : 32;
+    // Keys that the softmax takes between two decisions about M: kChunk, and in units with a mask,
+    // whose code is longer, kMaskedChunk.  The less code, the better the instruction caches hold it
+    // beside the other pipeline's; the longer a chunk, the more overlaps within it.
+    //   d = 128, tiles of 256 rows, 3,600 rows over 75,600 keys: 64 keys 4.30 ms, 32 4.64, 16 5.13,
+    //     all 128 5.95; masked 16 against 32: ragged chunks 112 against 121 us.
+    //   d = 128, tiles of 128 rows, a few tokens of 24 sequences: 16 keys 48.8 us, 32 51.4, 64 56.9.
+    //   d = 64, windowed chunks: 32 keys 0.755 ms, 64 (masked 16) 0.842, 16 0.795.
+    constexpr int kMaskedChunk = D == 128 ? 16 : 32;
     // offsets from the array itself: through an integer the compiler would lose sight of
     // the address space, and generic loads take the slow road to shared memory
     extern __shared__ uint8_t smem_raw[];
@@ -362,6 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ converter
         regs_down<kRegsConv>();
         const int t = threadIdx.x - kConvWarp * 32;
+        // Pieces of 16 codes: this thread's are piece ch of tokens row0 + i ROWS, whose swizzle is the
+        // same for all i.  As fp16 a piece is two of 16 bytes: 64 channels a half, 128 bytes a token,
+        // 128-byte swizzle; the halves' threads write theirs in opposite order, which keeps them on
+        // different banks.
+        constexpr int PIECES = D / 16, ROWS = 128 / PIECES;
+        static_assert(ROWS % 8 == 0, "one swizzle");
+        const int row0 = t / PIECES, ch = t % PIECES;
+        const bool swap = ch >= 4;
+        const int from = C::chunk(row0, ch);
+        const int lo = (((ch & 3) * 2) ^ (row0 & 7)) << 4, hi = (((ch & 3) * 2 + 1) ^ (row0 & 7)) << 4;
+        const int to = (ch / 4) * (kUnit * 128) + row0 * 128 + (swap ? hi : lo), other = swap ? lo - hi : hi - lo;
         for (int it = 0;; ++it) {
             if (!wait(C::IF + it % C::NI, it / C::NI)) break;
             const StageInfo* f = info_at(it);
@@ -388,26 +404,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(C::CF + sc));
             }
             if (it >= C::NW && !wait(C::WE + sw, it / C::NW - 1)) break;
-            const uint8_t* vs = smem + C::OFF_V + sv * C::TILE;
-            uint8_t* wd = smem + C::OFF_W + sw * C::WB;
-            constexpr int PIECES = D / 16;  // 16 codes each
+            const uint8_t* src = smem + C::OFF_V + sv * C::TILE + from;
+            uint8_t* dst = smem + C::OFF_W + sw * C::WB + to;
 #pragma unroll 1
             for (int i = 0; i < PIECES; ++i) {
-                const int r = (i * 128 + t) / PIECES, ch = t % PIECES;
-                uint4 x = *reinterpret_cast<const uint4*>(vs + C::chunk(r, ch));
-                if ((flags & kMasked) && key0 + r >= L) x = make_uint4(0, 0, 0, 0);  // any bits behind the last token
-                uint4 lo, hi;
-                e4m3x4_to_f16(x.x, lo.x, lo.y);
-                e4m3x4_to_f16(x.y, lo.z, lo.w);
-                e4m3x4_to_f16(x.z, hi.x, hi.y);
-                e4m3x4_to_f16(x.w, hi.z, hi.w);
-                // 64 channels a half, 128 bytes a token, 128-byte swizzle; the halves' threads
-                // write their two pieces in opposite order, which keeps them on different banks
-                uint8_t* row = wd + (ch / 4) * (kUnit * 128) + r * 128;
-                const int c0 = ((ch & 3) * 2) ^ (r & 7), c1 = ((ch & 3) * 2 + 1) ^ (r & 7);
-                const bool swap = ch >= 4;
-                *reinterpret_cast<uint4*>(row + ((swap ? c1 : c0) << 4)) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(row + ((swap ? c0 : c1) << 4)) = swap ? lo : hi;
+                uint4 x = *reinterpret_cast<const uint4*>(src + i * ROWS * D);
+                if ((flags & kMasked) && key0 + row0 + i * ROWS >= L) x = make_uint4(0, 0, 0, 0);  // any bits behind the last token
+                uint4 y0, y1;
+                e4m3x4_to_f16(swap ? x.z : x.x, y0.x, y0.y);
+                e4m3x4_to_f16(swap ? x.w : x.y, y0.z, y0.w);
+                e4m3x4_to_f16(swap ? x.x : x.z, y1.x, y1.y);
+                e4m3x4_to_f16(swap ? x.y : x.w, y1.z, y1.w);
+                *reinterpret_cast<uint4*>(dst + i * ROWS * 128) = y0;
+                *reinterpret_cast<uint4*>(dst + i * ROWS * 128 + other) = y1;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -527,89 +536,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4 tops = ld_shared4(scl + 2 * kUnit * 4);
                 const float sv_top = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
                 float alpha = 1.f;
-                // kChunk keys at a time, in a loop: straight-line code for all 128 keys, run by the two
-                // pipelines' warps at different times, spent a third of their time waiting for
-                // instructions.  P of a chunk takes the place of scores that have been read.
+                const uint32_t scores = la + D;
+                // -inf for those of the unit's keys 16 g .. 16 g + 15 that the row does not see.  Most groups
+                // of a masked unit are seen by all of the warp's rows or by none.  Returns whether the row
+                // sees one.
+                auto hide = [&](float2(&y)[8], int g) -> bool {
+                    // computed here: comparisons taken out of a loop would be made for every unit
+                    const int at = key0 + g * 16, lo = no_hoist(first - at), hi = no_hoist(last - at);
+                    // a run has 16 keys or more
+                    const bool hole = (flags & kHoles) && !((f->box_ok >> ((g * 16) >> box_log2)) & 1);
+                    if (__all_sync(0xffffffffu, lo <= 0 && hi >= 15) && !hole) return true;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (hole || 2 * i < lo || 2 * i > hi) y[i].x = -INFINITY;
+                        if (hole || 2 * i + 1 < lo || 2 * i + 1 > hi) y[i].y = -INFINITY;
+                    }
+                    return !hole && lo <= 15 && hi >= 0;
+                };
+                // kChunk keys at a time in a loop, 16 of them side by side with the next scores and key scales on
+                // their way.  P of a chunk takes the place of scores that have been read.
+                auto softmax = [&](auto masked_tag) {
+                    constexpr bool MASKED = decltype(masked_tag)::value;
+                    constexpr int NG = (MASKED ? kMaskedChunk : kChunk) / 16;
+                    uint32_t x[2][16];
+                    float4 sk[4], sv[4];
+                    bool raised = false;
+                    tmem_ld16(scores, x[0]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scl + i * 16);
+                    tmem_wait_ld();
 #pragma unroll 1
-                for (int ck = 0; ck < kUnit / kChunk; ++ck) {
-                    const uint32_t scores = la + D + ck * kChunk, scales = scl + ck * kChunk * 4;
-                    const int at = key0 + ck * kChunk;  // position of the chunk's first key
-                    // -inf for those of the chunk's keys 16 g .. 16 g + 15 that the row does not see.  Most
-                    // groups of a masked unit are seen by all of the warp's rows or by none.
-                    auto hide = [&](float2(&y)[8], int g) {
-                        // computed here: comparisons taken out of a loop would be made for every unit
-                        const int lo = no_hoist(first - at) - g * 16, hi = no_hoist(last - at) - g * 16;
-                        // a run has 16 keys or more
-                        const bool hole = (flags & kHoles) && !((f->box_ok >> ((ck * kChunk + g * 16) >> box_log2)) & 1);
-                        if (__all_sync(0xffffffffu, lo <= 0 && hi >= 15) && !hole) return;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (hole || 2 * i < lo || 2 * i > hi) y[i].x = -INFINITY;
-                            if (hole || 2 * i + 1 < lo || 2 * i + 1 > hi) y[i].y = -INFINITY;
-                        }
-                    };
-                    // The chunk's part of M: the maximum of s + log2 sv, and of s - kZeroLog2.
-                    auto find_m = [&]() -> float {
-                        float mj = -INFINITY, ms = -INFINITY;
-#pragma unroll 1
-                        for (int g = 0; g < kChunk / 16; ++g) {
-                            uint32_t s[16];
-                            float2 y[8];
-                            tmem_ld16(scores + g * 16, s);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const float4 sk = ld_shared4(scales + g * 64 + i * 8);
-                                y[i] = make_float2(__uint_as_float(s[2 * i]) * sk.x, __uint_as_float(s[2 * i + 1]) * sk.y);
-                                y[i + 1] =
-                                    make_float2(__uint_as_float(s[2 * i + 2]) * sk.z, __uint_as_float(s[2 * i + 3]) * sk.w);
-                            }
-                            if (flags & kMasked) hide(y, g);
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const float4 sv = ld_shared4(scales + kUnit * 4 + g * 64 + i * 8);
-                                ms = max3(ms, fmaxf(y[i].x, y[i].y), fmaxf(y[i + 1].x, y[i + 1].y));
-                                mj = max3(mj, fmaf(y[i].x, qs, lg2_approx(sv.x)), fmaf(y[i].y, qs, lg2_approx(sv.y)));
-                                mj = max3(mj, fmaf(y[i + 1].x, qs, lg2_approx(sv.z)),
-                                          fmaf(y[i + 1].y, qs, lg2_approx(sv.w)));
-                            }
-                        }
-                        return floorf(fmaxf(mj, ms * qs - kZeroLog2));
-                    };
-                    // P sv of the chunk against M, as fp16 in pw; returns the sum of P.  16 keys at a time,
-                    // the next scores and key scales on their way, eight independent operations behind
-                    // one another.
-                    uint32_t pw[kChunk / 2];
-                    auto find_p = [&](auto masked_tag) -> float {
-                        constexpr bool MASKED = decltype(masked_tag)::value;
-                        const float m = M == -INFINITY ? 0.f : M;
-                        const float2 nm2 = make_float2(-m, -m);
+                    for (int g = 0; g < kUnit / 16;) {
+                        uint32_t pw[8 * NG];
                         float2 l2 = make_float2(0.f, 0.f), l3 = l2;
-                        uint32_t s[2][16];
-                        float4 sk[4], sv[4];
-                        tmem_ld16(scores, s[0]);
+                        bool seen = !MASKED;
+                        const float m = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scales + i * 16);
-                        tmem_wait_ld();
+                        for (int j = 0; j < NG; ++j) {
+                            const int next = j + 1 < NG || g + NG < kUnit / 16 ? g + j + 1 : g + j;
+                            if (NG > 1) tmem_ld16(scores + next * 16, x[(j + 1) & 1]);
 #pragma unroll
-                        for (int g = 0; g < kChunk / 16; ++g) {
-                            if (g + 1 < kChunk / 16) tmem_ld16(scores + (g + 1) * 16, s[(g + 1) & 1]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sv[i] = ld_shared4(scales + kUnit * 4 + g * 64 + i * 16);
-                            const uint32_t(&x)[16] = s[g & 1];
+                            for (int i = 0; i < 4; ++i) sv[i] = ld_shared4(scl + kUnit * 4 + (g + j) * 64 + i * 16);
                             float2 y[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                y[i] = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                y[i] = __fmul2_rn(make_float2(__uint_as_float(x[j & 1][2 * i]), __uint_as_float(x[j & 1][2 * i + 1])),
                                                   (i & 1) ? make_float2(sk[i / 2].z, sk[i / 2].w)
                                                           : make_float2(sk[i / 2].x, sk[i / 2].y));
-                            if (g + 1 < kChunk / 16) {
+                            if (NG == 1) tmem_ld16(scores + next * 16, x[0]);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scales + (g + 1) * 64 + i * 16);
-                            }
+                            for (int i = 0; i < 4; ++i) sk[i] = ld_shared4(scl + next * 64 + i * 16);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = __ffma2_rn(y[i], qs2, nm2);
-                            if (MASKED) hide(y, g);
+                            for (int i = 0; i < 8; ++i) y[i] = __ffma2_rn(y[i], qs2, make_float2(-m, -m));
+                            if (MASKED) seen |= hide(y, g + j);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) y[i] = make_float2(ex2_approx(y[i].x), ex2_approx(y[i].y));
 #pragma unroll
@@ -621,18 +600,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 8; ++i) {
                                 y[i] = __fmul2_rn(y[i], (i & 1) ? make_float2(sv[i / 2].z, sv[i / 2].w)
                                                                 : make_float2(sv[i / 2].x, sv[i / 2].y));
-                                pw[g * 8 + i] = pack_f16(y[i].x, y[i].y);
+                                pw[j * 8 + i] = pack_f16(y[i].x, y[i].y);
                             }
-                            if (g + 1 < kChunk / 16) tmem_wait_ld();
+                            tmem_wait_ld();
                         }
-                        return (l2.x + l2.y) + (l3.x + l3.y);
-                    };
-                    bool raise = M == -INFINITY;
-                    float sum = 0.f;
+                        const float sum = (l2.x + l2.y) + (l3.x + l3.y);
+                        // (a sum of over 2^96: tokens whose values are all zero far above M)
+                        const bool raise = (M == -INFINITY && seen) || sum * sv_top > 32768.f || sum > 0x1p96f;
+                        if (!raised && __any_sync(0xffffffffu, raise)) {
+                            raised = true;
+                            // M: the maximum of s + log2 sv, and of s - kZeroLog2; then these keys again
+                            float mj = -INFINITY, ms = -INFINITY;
 #pragma unroll 1
-                    for (int rep = 0; rep < 2; ++rep) {
-                        if (__any_sync(0xffffffffu, raise)) {
-                            const float mu = find_m();
+                            for (int j = NG - 1; j >= 0; --j) {
+                                float2 y[8];
+                                tmem_ld16(scores + (g + j) * 16, x[0]);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    sk[i] = ld_shared4(scl + (g + j) * 64 + i * 16);
+                                    y[2 * i] = make_float2(__uint_as_float(x[0][4 * i]) * sk[i].x,
+                                                           __uint_as_float(x[0][4 * i + 1]) * sk[i].y);
+                                    y[2 * i + 1] = make_float2(__uint_as_float(x[0][4 * i + 2]) * sk[i].z,
+                                                               __uint_as_float(x[0][4 * i + 3]) * sk[i].w);
+                                }
+                                if (MASKED) hide(y, g + j);
+#pragma unroll
+                                for (int i = 0; i < 8; i += 2) {
+                                    const float4 v = ld_shared4(scl + kUnit * 4 + (g + j) * 64 + i * 8);
+                                    ms = max3(ms, fmaxf(y[i].x, y[i].y), fmaxf(y[i + 1].x, y[i + 1].y));
+                                    mj = max3(mj, fmaf(y[i].x, qs, lg2_approx(v.x)), fmaf(y[i].y, qs, lg2_approx(v.y)));
+                                    mj = max3(mj, fmaf(y[i + 1].x, qs, lg2_approx(v.z)), fmaf(y[i + 1].y, qs, lg2_approx(v.w)));
+                                }
+                            }
+                            const float mu = floorf(fmaxf(mj, ms * qs - kZeroLog2));
                             float w = 1.f;
                             if (raise && mu > M) {
                                 w = part_weight(M, mu);
@@ -640,38 +641,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             l *= w;
                             alpha *= w;
-                            if (ck > 0) {
-                                // the unit's P so far
-                                const __half2 w2 = __half2half2(__float2half_rn(w));
-                                tmem_wait_st();
+                            // the unit's P so far (and, at 16 keys a chunk, of scores that have been read)
+                            const __half2 w2 = __half2half2(__float2half_rn(w));
+                            tmem_wait_st();
 #pragma unroll 1
-                                for (int c0 = 0; c0 < ck * kChunk / 2; c0 += 16) {
-                                    uint32_t x[16];
-                                    tmem_ld16(la + D + c0, x);
-                                    tmem_wait_ld();
+                            for (int c0 = 0; c0 < g * 8; c0 += 16) {
+                                uint32_t z[16];
+                                tmem_ld16(scores + c0, z);
+                                tmem_wait_ld();
 #pragma unroll
-                                    for (int i = 0; i < 16; ++i) {
-                                        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x[i]), w2);
-                                        x[i] = *reinterpret_cast<const uint32_t*>(&v);
-                                    }
-                                    tmem_st16(la + D + c0, x);
+                                for (int i = 0; i < 16; ++i) {
+                                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&z[i]), w2);
+                                    z[i] = *reinterpret_cast<const uint32_t*>(&v);
                                 }
+                                tmem_st16(scores + c0, z);
                             }
+                            tmem_wait_st();
+                            continue;
                         }
-                        sum = (flags & kMasked) ? find_p(std::true_type{}) : find_p(std::false_type{});
-                        // (a sum of over 2^96: tokens whose values are all zero far above M)
-                        raise = sum * sv_top > 32768.f || sum > 0x1p96f;
-                        if (!__any_sync(0xffffffffu, raise)) break;
-                    }
-                    l += sum;
+                        raised = false;
+                        l += sum;
 #pragma unroll
-                    for (int c0 = 0; c0 < kChunk / 2; c0 += 16) {
-                        uint32_t x[16];
+                        for (int j = 0; j < NG; ++j) {
+                            uint32_t z[8];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = pw[c0 + i];
-                        tmem_st16(la + D + ck * kChunk / 2 + c0, x);
+                            for (int i = 0; i < 8; ++i) z[i] = pw[j * 8 + i];
+                            tmem_st8(scores + (g + j) * 8, z);
+                        }
+                        g += NG;
                     }
-                }
+                };
+                if (flags & kMasked)
+                    softmax(std::true_type{});
+                else
+                    softmax(std::false_type{});
                 if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
                     // O holds every product up to the pipeline's last unit: the scores' completion
                     // covers what was issued before them
@@ -815,10 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D>
+template <int D, int kChunk>
 vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
                       int ctas, void* ws, cudaStream_t st) {
-    auto kern = attn_many_kernel<D>;
+    auto kern = attn_many_kernel<D, kChunk>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
     if (s != VC_OK) return s;
     kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
@@ -829,8 +832,9 @@ vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedA
 
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, void* ws, cudaStream_t st) {
-    return d == 128 ? launch_many<128>(mk, mv, a, c, RT, ctas, ws, st)
-                    : launch_many<64>(mk, mv, a, c, RT, ctas, ws, st);
+    if (d == 64) return launch_many<64, 32>(mk, mv, a, c, RT, ctas, ws, st);
+    return RT == 256 ? launch_many<128, 64>(mk, mv, a, c, RT, ctas, ws, st)
+                     : launch_many<128, 16>(mk, mv, a, c, RT, ctas, ws, st);
 }
 
 }  // namespace vc
