@@ -594,9 +594,9 @@ bool make_cache_map(CUtensorMap* map, const uint8_t* base, int d, const CacheVie
 
 // Rows of a tile, by the rows of the longest chunk as far as the caller told: up to
 // 32 go to the kernel for few rows, more to the one for many.  Measured on 24
-// sequences of 500 to 6,000 keys, d = 128, few rows against many: 16 rows 31.9
-// against 53.9 us, 32 rows 43.5 against 54.1 (d = 64: 32.5 against 43.1).  Tiles of
-// 128 rows take 1.35 us a unit of keys, of 256 rows 2.0.
+// sequences of 500 to 6,000 keys, d = 128, few rows against many: 16 rows 33.8
+// against 46.7 us, 32 rows 45.9 against 47.6 (d = 64: 33.4 against 43.7).  128 rows
+// take 53.5 us in tiles of 128 and 56.9 in tiles of 256.
 int tile_rows(int G, int B, int T, int max_q) {
     const int64_t q = max_q > 0 ? max_q : ((int64_t)T + B - 1) / B;
     const int64_t rows = q * G;
