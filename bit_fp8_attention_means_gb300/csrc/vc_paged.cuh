@@ -69,7 +69,7 @@ __device__ __forceinline__ int row_last(const PagedAttn& a, const SeqInfo& s, in
     return a.causal ? s.L - s.n + token : s.L - 1;
 }
 __device__ __forceinline__ int row_first(const PagedAttn& a, int last) {
-    return a.window ? max(0, last - a.window + 1) : 0;
+    return a.window && last >= a.window ? last - a.window + 1 : 0;  // no overflow for any window
 }
 
 __device__ __forceinline__ ItemRange item_range(const PagedAttn& a, const SeqInfo& s, int tile, int RT) {

@@ -416,6 +416,11 @@ def _on_device(dev, stream, fn, args, where, made):
             t.record_stream(stream)
 
 
+def _int32(x):
+    """The number itself or the nearest that a C int holds: ctypes would drop the upper bits."""
+    return x if -1 <= x <= 0x7FFFFFFF else max(-1, min(x, 0x7FFFFFFF))
+
+
 def _need_cuda(dev):
     if dev < 0:
         raise ValueError("the cache must be on a CUDA device")
@@ -471,7 +476,7 @@ def _attn_paged_bytes(page_size, H, d, Hq, B, T, max_q):
 
 
 def attn_paged_workspace_bytes(cache, Hq, B, T, max_q=0) -> int:
-    return lib().vc_attn_paged_workspace(cache_shape_of(cache), Hq, B, T, max_q)
+    return lib().vc_attn_paged_workspace(cache_shape_of(cache), Hq, B, T, _int32(max_q))
 
 
 def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, window=0, max_q=0, O=None, lse=None,
@@ -493,6 +498,7 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
     batch = _batch_of(cu, kv_len, table, T, dev)
     status = _status_ptr(dev_status, dev)
     _need_cuda(dev)
+    window, max_q = _int32(window), _int32(max_q)
     made = []
     if O is None:
         O = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty(shape)

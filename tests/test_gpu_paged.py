@@ -481,3 +481,41 @@ def test_calls_of_two_host_threads():
         c.check(outs[0], c.appended())
         for O, lse in outs[1:]:
             assert same_bits(O, outs[0][0]) and same_bits(lse, outs[0][1])
+
+
+@pytest.mark.parametrize("n,kv", [([3, 9], [2, 40]), ([200, 40], [150, 500])])
+def test_windows_of_any_size(n, kv):
+    """The largest window that a C int holds and larger ones see what no window sees, with rows before the
+    first key in the same tile."""
+    c = Case(n=n, kv=kv, H=2, G=2, seed=50)
+    whole = attend(c)
+    c.check(whole, c.cache())
+    for window in (2 ** 31 - 1, 2 ** 31 - 50, 2 ** 32 + 3, 2 ** 40):
+        got = attend(c, window=window)
+        assert same_bits(got[0], whole[0]) and same_bits(got[1], whole[1]), window
+    got = attend(c, max_q=2 ** 32 + 1)
+    c.check(got, c.cache())
+
+
+@pytest.mark.parametrize("n,G,d", [(1, 4, 128), (100, 1, 128), (300, 1, 64)])
+def test_without_lse_and_with_given_outputs(n, G, d):
+    """Strided O, a workspace kept by the caller, and the C entry without lse."""
+    c = Case(n=[n, n], kv=[500, 310], H=2, G=G, d=d, seed=51)
+    cache, args, Q = c.cache(DEV), c.args(DEV), c.Q.to(DEV)
+    want = vc.vc_attn_paged(Q, cache, *args, max_q=n)
+    c.check(want, c.cache())
+    big = torch.full((c.T, 2 * G + 1, d + 8), 3.0, dtype=torch.bfloat16, device=DEV)
+    O = big[:, :2 * G, :d]
+    ws = torch.empty(vc.attn_paged_workspace_bytes(cache, 2 * G, 2, c.T, n), dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        vc.vc_attn_paged(Q, cache, *args, max_q=n, O=O, workspace=ws)
+    assert same_bits(O, want[0])
+    assert torch.all(big[:, 2 * G] == 3.0) and torch.all(big[:, :, d:] == 3.0)
+    O2 = torch.zeros_like(Q)
+    shape, batch = vc.cache_shape_of(cache), vc._batch_of(*args, c.T, 0)
+    rc = vc.lib().vc_attn_paged(Q.data_ptr(), 2 * G * d, d, 2 * G, shape, cache["K8"].data_ptr(), cache["sk"].data_ptr(),
+                                cache["V8"].data_ptr(), cache["sv"].data_ptr(), batch, 0.0, 1, 0, n, O2.data_ptr(),
+                                2 * G * d, d, None, ws.data_ptr(), ws.numel(), None,
+                                torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and same_bits(O2, want[0])
