@@ -455,7 +455,7 @@ def vc_cache_read(cache, cu, kv_len, table, T, K=None, V=None, dev_status=None, 
     _need_cuda(dev)
     made = []
     if K is None:
-        K = cache["K8"].new_empty((T, s.H, s.d), dtype=_BF16)
+        K = torch.empty((T, s.H, s.d), dtype=_BF16, device=dev)  # half the time of new_empty
         made.append(K)
     if V is None:
         V = torch.empty_like(K) if K.is_contiguous() else K.new_empty_strided(K.shape, K.stride())
@@ -501,7 +501,7 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
     window, max_q = _int32(window), _int32(max_q)
     made = []
     if O is None:
-        O = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty(shape)
+        O = torch.empty(shape, dtype=_BF16, device=dev)
         o_strides = (Hq * d, d)
         made.append(O)
     else:
@@ -509,13 +509,14 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
         if O.shape != shape:
             raise ValueError("O must have Q's shape")
     if lse is None:
-        lse = Q.new_empty((T, Hq), dtype=_F32)
+        lse = torch.empty((T, Hq), dtype=_F32, device=dev)
         made.append(lse)
     elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or \
             lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
     if workspace is None:
-        workspace = Q.new_empty(max(_attn_paged_bytes(s.page_size, s.H, d, Hq, batch.B, T, max_q), 256), dtype=_U8)
+        workspace = torch.empty(max(_attn_paged_bytes(s.page_size, s.H, d, Hq, batch.B, T, max_q), 256), dtype=_U8,
+                                device=dev)
         made.append(workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
