@@ -5,10 +5,10 @@
 //   A = sum_t (P_t sv_t) v8_t,            O = A / l,
 // M being the running maximum of s_t + log2 sv_t, rounded down to a whole number:
 // P sv, which goes to the product as fp16, is then below 2 whatever the scales
-// are.  M follows only where the unit's sum of P times its largest sv passes 2^15,
-// so that P sv stays finite in fp16 (whose precision is the same up to there)
-// without a maximum being taken; then a pass of its own over the unit finds the
-// new M, and what was summed before is scaled by a power of two.
+// are.  M follows only where the sum of P over the 16 to 64 keys at hand times their
+// unit's largest sv passes 2^15, so that P sv stays finite in fp16 (whose precision is
+// the same up to there) without a maximum being taken; then a pass of its own over
+// these keys finds the new M, and what was summed before is scaled by a power of two.
 //
 // One persistent CTA on each SM takes tiles of 256 rows as two pipelines A and B
 // of 128 rows, which share the keys and values and the tensor core, so that the
@@ -29,10 +29,10 @@
 // The floor is the tensor core's 4 x 512 clocks a unit of both pipelines (d = 128).
 // Measured: 3,560 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.30 ms, 1,297
 // TFLOP/s.  Without softmax arithmetic a unit still took 3,150 clocks.  Shared memory's data
-// path is the busiest part (products 35 %, loads and stores 50 %, TMA besides), and code
+// path is the busiest part (products 36 %, loads and stores 55 %, TMA besides), and code
 // that runs beside other code costs instruction fetches: two threads a row (5.9 ms), loads
 // that need fewer scales (16x256b, 4.6 ms) and warps of their own for the scales (4.8 ms)
-// all lost.  With d = 64 the chain from scores to P bounds it as well (tensor core 23 %
+// all lost.  With d = 64 the chain from scores to P bounds it as well (tensor core 25 %
 // busy).
 //
 // 16 warps:
