@@ -398,22 +398,41 @@ def _status_ptr(dev_status, dev):
     return dev_status.data_ptr()
 
 
-def _on_device(dev, stream, fn, args, where, made):
-    """Calls fn(*args, stream) with device `dev` current, and keeps the tensors in `made` (made here, on
-    the current stream) for a stream that is not the current one."""
+def _on_device(dev, stream, fn, args, where):
+    """Calls fn(*args, stream) with device `dev` current."""
     here = torch._C._cuda_getDevice()
     if here != dev:
         torch.cuda.set_device(dev)
     try:
-        current = torch._C._cuda_getCurrentRawStream(dev)
-        handle = current if stream is None else stream.cuda_stream
-        _check(fn(*args, handle), where)
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream), where)
     finally:
         if here != dev:
             torch.cuda.set_device(here)
-    if handle != current:
-        for t in made:
-            t.record_stream(stream)
+
+
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` as the current one, for an entry point that makes outputs or a workspace.
+
+    They come from the memory of `stream` then.  From that of the caller's stream they could be
+    what its kernels, still under way, read or write: `stream` does not wait for those.  The
+    caller's stream is to use the outputs, so their memory is kept until it has."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
+
+def _is_other(stream):
+    """Whether a call's `stream` is another than the current one."""
+    return stream is not None and stream != torch.cuda.current_stream(stream.device)
+
+
+def _check_stream(stream, dev):
+    if stream is not None and stream.device.index != dev:
+        raise ValueError("stream is not on the cache's device")
 
 
 def _int32(x):
@@ -431,7 +450,9 @@ def vc_cache_append(K, V, cache, cu, kv_len, table, dev_status=None, stream=None
 
     cu int32 [B+1], kv_len int32 [B], table int32 [B, cols]: sequence b has
     rows cu[b] .. cu[b+1]-1 of the call and kv_len[b] tokens in the cache with
-    these included; position p lies in page table[b, p // page_size]."""
+    these included; position p lies in page table[b, p // page_size].
+    stream: where this and the other calls run, if not the current one.  It has to have waited for
+    what is handed in; what a call makes itself, its workspace too, is of that stream's memory."""
     L = lib()
     s, (K8, sk, V8, sv), dev = _cache_parts(cache)
     strides = _rows("K", K, s.H, s.d, dev)
@@ -440,8 +461,9 @@ def vc_cache_append(K, V, cache, cu, kv_len, table, dev_status=None, stream=None
     batch = _batch_of(cu, kv_len, table, K.shape[0], dev)
     status = _status_ptr(dev_status, dev)
     _need_cuda(dev)
+    _check_stream(stream, dev)
     _on_device(dev, stream, L.vc_cache_append, (K.data_ptr(), V.data_ptr(), *strides, s, K8, sk, V8, sv, batch, status),
-               "vc_cache_append", ())
+               "vc_cache_append")
     return cache
 
 
@@ -453,18 +475,18 @@ def vc_cache_read(cache, cu, kv_len, table, T, K=None, V=None, dev_status=None, 
     batch = _batch_of(cu, kv_len, table, T, dev)
     status = _status_ptr(dev_status, dev)
     _need_cuda(dev)
-    made = []
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_cache_read, cache, cu, kv_len, table, T, K, V, dev_status)
     if K is None:
         K = torch.empty((T, s.H, s.d), dtype=_BF16, device=dev)  # half the time of new_empty
-        made.append(K)
     if V is None:
         V = torch.empty_like(K) if K.is_contiguous() else K.new_empty_strided(K.shape, K.stride())
-        made.append(V)
     strides = _rows("K", K, s.H, s.d, dev)
     if K.shape[0] != T or V.shape != K.shape or _rows("V", V, s.H, s.d, dev) != strides:
         raise ValueError("K and V must have T rows and share strides")
     _on_device(dev, stream, L.vc_cache_read, (s, K8, sk, V8, sv, batch, K.data_ptr(), V.data_ptr(), *strides, status),
-               "vc_cache_read", made)
+               "vc_cache_read")
     return K, V
 
 
@@ -498,32 +520,32 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
     batch = _batch_of(cu, kv_len, table, T, dev)
     status = _status_ptr(dev_status, dev)
     _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_attn_paged, Q, cache, cu, kv_len, table, softmax_scale, causal, window, max_q, O,
+                          lse, workspace, dev_status)
     window, max_q = _int32(window), _int32(max_q)
-    made = []
     if O is None:
         O = torch.empty(shape, dtype=_BF16, device=dev)
         o_strides = (Hq * d, d)
-        made.append(O)
     else:
         o_strides = _rows("O", O, Hq, d, dev)
         if O.shape != shape:
             raise ValueError("O must have Q's shape")
     if lse is None:
         lse = torch.empty((T, Hq), dtype=_F32, device=dev)
-        made.append(lse)
     elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or \
             lse.get_device() != dev:
         raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
     if workspace is None:
         workspace = torch.empty(max(_attn_paged_bytes(s.page_size, s.H, d, Hq, batch.B, T, max_q), 256), dtype=_U8,
                                 device=dev)
-        made.append(workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
     _on_device(dev, stream, L.vc_attn_paged,
                (Q.data_ptr(), *q_strides, Hq, s, K8, sk, V8, sv, batch, softmax_scale, causal, window, max_q,
                 O.data_ptr(), *o_strides, lse.data_ptr(), workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), status), "vc_attn_paged", made)
+                workspace.numel() * workspace.element_size(), status), "vc_attn_paged")
     return O, lse
 
 

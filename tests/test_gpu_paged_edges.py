@@ -1,0 +1,28 @@
+"""GPU: the ends of what the paged cache's calls take, against the definitions in fp64 (paged_case.py)."""
+import pytest
+import torch
+
+from bit_fp8_attention_means_gb300 import vc
+from paged_case import Case
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (200, 1)])
+def test_calls_on_two_streams_at_once(n, G):
+    """Calls on the current stream and, without a wait, on another one: each has its own workspace and outputs."""
+    cases = [Case(n=[n] * 3, kv=[4000, 700, 300], H=2, G=G, seed=70 + i) for i in range(2)]
+    data = [(c.Q.to(DEV), c.cache(DEV), *c.args(DEV)) for c in cases]
+    want = [vc.vc_attn_paged(*d, max_q=n) for d in data]
+    back = [vc.vc_cache_read(*d[1:], c.T) for c, d in zip(cases, data)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(30):
+        here = [vc.vc_attn_paged(*data[0], max_q=n) for _ in range(3)]
+        there = vc.vc_attn_paged(*data[1], max_q=n, stream=side)
+        kv = vc.vc_cache_read(*data[1][1:], cases[1].T, stream=side)
+        here.append(vc.vc_attn_paged(*data[0], max_q=n))
+        torch.cuda.synchronize()
+        for got, ref in [(x, want[0]) for x in here] + [(there, want[1]), (kv, back[1])]:
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
