@@ -124,6 +124,26 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` as the current one, for an entry point that makes outputs or a workspace.
+
+    They come from the memory of `stream` then.  From that of the caller's stream they could be
+    what its kernels, still under way, read or write: `stream` does not wait for those.  The
+    caller's stream is to use the outputs, so their memory is kept until it has."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
+
+def _is_other(stream):
+    """Whether a call's `stream` is another than the current one."""
+    return stream is not None and stream != torch.cuda.current_stream(stream.device)
+
+
 def nblk_of(N):
     return (N + BLOCK - 1) // BLOCK
 
@@ -161,6 +181,9 @@ def vc_cluster(V, k, iters, warm_start=False, centroids=None, labels=None, perm=
 
     block_fill=1 calls vc_cluster_ex: perm keeps whole 128-token blocks per
     cluster and chains the clusters' leftovers by centroid distance."""
+    if _is_other(stream):
+        return _on_stream(stream, vc_cluster, V, k, iters, warm_start, centroids, labels, perm, workspace, dev_status,
+                          block_fill=block_fill)
     s = shape_of(V)
     dev = V.device
     if centroids is None:
@@ -232,6 +255,8 @@ def vc_quantize(Q, K, V, perm=None, vsmooth=1, out=None, workspace=None, stream=
     """Fused quantizer. Returns a dict with Q8, sq, K8, sk, V8T, sv, mu (mu is bf16 bits as int16).
     vbits=4 calls vc_quantize_v4: the V residual in 4 bits (E2M1 with a power-of-two
     scale per 32 tokens of a channel), stored as E4M3 bytes for vc_attn_fwd."""
+    if _is_other(stream):
+        return _on_stream(stream, vc_quantize, Q, K, V, perm, vsmooth, out, workspace, vbits=vbits)
     L = lib()
     s = _check_qkv(Q, K, V)
     dev = Q.device
@@ -253,6 +278,8 @@ def vc_quantize(Q, K, V, perm=None, vsmooth=1, out=None, workspace=None, stream=
 def vc_quantize_ex(Q, K, V, perm=None, vsmooth=1, rope=None, hadamard=0, out=None, workspace=None, stream=None):
     """vc_quantize with the rotary transform (``rope``: fp32 [N, d/2, 2] (cos, sin)
     table on the device) and/or the Hadamard rotation of Q and K fused in."""
+    if _is_other(stream):
+        return _on_stream(stream, vc_quantize_ex, Q, K, V, perm, vsmooth, rope, hadamard, out, workspace)
     L = lib()
     return _quantize_call(L.vc_quantize_ex, "vc_quantize_ex", Q, K, V, perm, vsmooth, rope, hadamard, out,
                           workspace, L.vc_quantize_workspace, stream)
@@ -262,6 +289,8 @@ def vc_quantize_staged(Q, K, V, perm=None, vsmooth=1, rope=None, hadamard=0, out
                        stream=None):
     """The same computation as vc_quantize_ex as the unfused chain of kernels
     (intermediates in device memory); bit-identical outputs."""
+    if _is_other(stream):
+        return _on_stream(stream, vc_quantize_staged, Q, K, V, perm, vsmooth, rope, hadamard, out, workspace)
     L = lib()
     return _quantize_call(L.vc_quantize_staged, "vc_quantize_staged", Q, K, V, perm, vsmooth, rope, hadamard, out,
                           workspace, L.vc_quantize_staged_workspace, stream)
@@ -283,6 +312,9 @@ def vc_attn_fwd(qz, shape: VcShape, softmax_scale=0.0, expcast=1, vsmooth=1, O=N
     debug=(bh, qtile) additionally returns the fp32 scores and probability bytes
     of that one query tile: (O, S_dump [128, Npad], P_dump [128, Npad]).
     """
+    if _is_other(stream):
+        return _on_stream(stream, vc_attn_fwd, qz, shape, softmax_scale, expcast, vsmooth, O, dev_status, debug=debug,
+                          exact_margin=exact_margin)
     dev = qz["Q8"].device
     if O is None:
         O = torch.empty((shape.B, shape.N, shape.H, shape.d), dtype=torch.bfloat16, device=dev)
@@ -410,26 +442,6 @@ def _on_device(dev, stream, fn, args, where):
             torch.cuda.set_device(here)
 
 
-def _on_stream(stream, call, *args, **kw):
-    """call(*args, **kw) with `stream` as the current one, for an entry point that makes outputs or a workspace.
-
-    They come from the memory of `stream` then.  From that of the caller's stream they could be
-    what its kernels, still under way, read or write: `stream` does not wait for those.  The
-    caller's stream is to use the outputs, so their memory is kept until it has."""
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        out = call(*args, **kw)
-    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-        if t is not None:
-            t.record_stream(caller)
-    return out
-
-
-def _is_other(stream):
-    """Whether a call's `stream` is another than the current one."""
-    return stream is not None and stream != torch.cuda.current_stream(stream.device)
-
-
 def _check_stream(stream, dev):
     if stream is not None and stream.device.index != dev:
         raise ValueError("stream is not on the cache's device")
@@ -550,6 +562,8 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
 
 
 def vc_debug_e4m3_encode(x: torch.Tensor, out=None, stream=None):
+    if _is_other(stream):
+        return _on_stream(stream, vc_debug_e4m3_encode, x, out)
     if out is None:
         out = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
     _check(lib().vc_debug_e4m3_encode(_ptr(x), x.numel(), _ptr(out), _stream(stream)), "vc_debug_e4m3_encode")
@@ -565,6 +579,8 @@ def vc_debug_attn_timeout(qz, shape: VcShape, dev_status: torch.Tensor, skip_k_t
     """vc_attn_fwd whose K loader never delivers key tile `skip_k_tile`, every
     device wait bounded by timeout_us: the kernel must record VC_ERR_TIMEOUT in
     dev_status and return.  Returns O (unspecified contents)."""
+    if _is_other(stream):
+        return _on_stream(stream, vc_debug_attn_timeout, qz, shape, dev_status, skip_k_tile, timeout_us, vsmooth, O)
     if O is None:
         O = torch.empty((shape.B, shape.N, shape.H, shape.d), dtype=torch.bfloat16, device=qz["Q8"].device)
     _check(lib().vc_debug_attn_timeout(_ptr(qz["Q8"]), _ptr(qz["sq"]), _ptr(qz["K8"]), _ptr(qz["sk"]),

@@ -63,7 +63,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: w["current"].cuda_stream)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: w["used"].append((t.data_ptr(), s.cuda_stream)), raising=False)
-    for name in ("empty", "empty_like", "empty_strided"):
+    for name in ("empty", "empty_like", "empty_strided", "zeros"):
         monkeypatch.setattr(torch, name, recording(getattr(torch, name)))
     yield w
     vc._attn_paged_bytes.cache_clear()
@@ -82,7 +82,8 @@ def on_side(w, call, made):
     out = call(stream=side)
     (name, args), = w["launches"]
     w["launches"].clear()
-    handle = args[-1].value if isinstance(args[-1], ctypes.c_void_p) else args[-1]
+    handle = args[13 if name == "vc_attn_fwd_debug" else -1]
+    handle = handle.value if isinstance(handle, ctypes.c_void_p) else handle
     assert handle == 2, name
     new = pointers(args) & set(w["made"])
     assert len(new) == made and all(w["made"][p] == 2 for p in new), name
@@ -106,6 +107,22 @@ def test_paged_calls_make_their_memory_on_the_given_stream(world):
     for stream in (None, Stream(1)):
         vc.vc_attn_paged(c.Q, cache, *args, stream=stream)
         assert world["launches"].pop()[1][-1] == 1
+
+
+def test_whole_sequence_calls_make_their_memory_on_the_given_stream(world):
+    x = torch.zeros((1, 256, 2, 64), dtype=torch.bfloat16)
+    shape = vc.shape_of(x)
+    cent, labels, perm = on_side(world, lambda stream: vc.vc_cluster(x, 4, 1, stream=stream), 4)
+    on_side(world, lambda stream: vc.vc_cluster(x, 4, 1, True, cent, labels, perm, stream=stream, block_fill=1), 1)
+    qz = on_side(world, lambda stream: vc.vc_quantize(x, x, x, perm, stream=stream), 8)
+    on_side(world, lambda stream: vc.vc_quantize(x, x, x, perm, out=qz, vbits=4, stream=stream), 1)
+    for fn in (vc.vc_quantize_ex, vc.vc_quantize_staged):
+        on_side(world, lambda stream: fn(x, x, x, hadamard=1, stream=stream), 8)
+    O = on_side(world, lambda stream: vc.vc_attn_fwd(qz, shape, stream=stream), 1)
+    on_side(world, lambda stream: vc.vc_attn_fwd(qz, shape, O=O, exact_margin=2.0, stream=stream), 0)
+    on_side(world, lambda stream: vc.vc_attn_fwd(qz, shape, debug=(0, 0), stream=stream), 3)
+    values = torch.zeros(8)
+    on_side(world, lambda stream: vc.vc_debug_e4m3_encode(values, stream=stream), 1)
 
 
 def test_stream_of_another_device_is_refused(world):
