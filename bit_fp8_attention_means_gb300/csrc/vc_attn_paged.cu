@@ -10,7 +10,7 @@
 // Folding sv into the exponent lets P, at most 2^8 above the running maximum M
 // of x, enter the product with the value codes as fp16 whatever the scales are;
 // E4M3 codes are fp16 numbers exactly.  A token whose values are all zero
-// (sv = 0) has log2 sv = -60 instead: it counts in l and neither in A nor,
+// (sv = 0) has log2 sv = -88 instead: it counts in l and neither in A nor,
 // beside other tokens, in M.  M moves only when the maximum has risen by more
 // than 8 (P then stays below 2^8, far inside fp16), which saves most of the
 // rescaling of A.
@@ -322,8 +322,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         }
                     }
                     // x = (q . k8) sk scale log2 e + log2 sv.  A token whose values are all zero
-                    // raises M only where it would pass 2^kZeroLog2 of P; its P counts in l alone,
-                    // and what fp16 makes of it (no infinity) meets codes of zero.
+                    // raises M only where it would pass 2^kZeroLog2 of P; its P counts in l alone.
                     float isv[2], up[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
@@ -377,7 +376,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         l[1] = fmaf(x[2 * t + 1], isv[t], l[1]);
                     }
                     // P^T: keys as the products' inner index, this thread's row g
-                    const uint32_t p0 = transpose8(pack_f16_sat(x[0], x[1])), p1 = transpose8(pack_f16_sat(x[2], x[3]));
+                    const uint32_t p0 = transpose8(up[0] == 0.f ? pack_f16_sat(x[0], x[1]) : 0u);
+                    const uint32_t p1 = transpose8(up[1] == 0.f ? pack_f16_sat(x[2], x[3]) : 0u);
                     // V^T P^T: the four keys of this thread, D/8 channels of each
                     uint32_t v[4][D / 32];
 #pragma unroll

@@ -365,9 +365,10 @@ vc_status vc_attn_fwd_hybrid(const uint8_t* Q8, const float* sq, const uint8_t* 
  *
  * The cache.  K8, V8: E4M3 codes, page x head x token x channel, in any order
  * of the first three (byte strides below, channel stride 1; the two share
- * strides).  sk, sv: fp32 scales [page, head, token], token stride 1.  The
- * value of a code is code * scale.  K8 and V8 may be two halves of one
- * allocation.  The codes of tokens that a sequence holds are numbers (NaN codes,
+ * strides).  sk, sv: fp32 scales [page, head, token], token stride 1, of the
+ * kind that vc_cache_append writes: 0, or positive from 2^-109 to 2^120, or NaN.
+ * The value of a code is code * scale, whatever the code is.  K8 and V8 may be
+ * two halves of one allocation.  The codes of tokens that a sequence holds are numbers (NaN codes,
  * 0x7F and 0xFF, are never written); what lies in slots that hold no token of
  * the sequence is never looked at and may be anything.
  */

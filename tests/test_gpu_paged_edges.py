@@ -7,6 +7,16 @@ from paged_case import Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+TILES = [(1, 4), (3, 4), (5, 5), (90, 1), (150, 2)]    # (tokens, query heads a key head): tiles of 8, 16, 32, 128, 256 rows
+
+
+def attend(c, cache=None, **kw):
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    kw.setdefault("max_q", max(c.n))
+    out = vc.vc_attn_paged(c.Q.to(DEV), cache or c.cache(DEV), *c.args(DEV), dev_status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    return out
 
 
 @pytest.mark.parametrize("n,G", [(1, 4), (200, 1)])
@@ -26,3 +36,16 @@ def test_calls_on_two_streams_at_once(n, G):
         torch.cuda.synchronize()
         for got, ref in [(x, want[0]) for x in here] + [(there, want[1]), (kv, back[1])]:
             assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("n,G", TILES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_scale_zero_is_value_zero(n, G, d):
+    """A value is code * scale: codes under a scale of 0 count in the sum of weights and nowhere else."""
+    c = Case(n=[n, n], kv=[600, 333], H=2, G=G, d=d, seed=60)
+    c.sv[torch.rand(c.sv.shape, generator=torch.Generator().manual_seed(4)) < 0.5] = 0.0
+    for p in range(0, 333, c.page):
+        c.sv[c.table[1, p // c.page], 1] = 0.0
+    got = attend(c)
+    c.check(got, c.cache())
+    assert torch.all(got[0][n:, G:] == 0) and torch.isfinite(got[1]).all()
