@@ -641,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             l *= w;
                             alpha *= w;
-                            // the unit's P so far (and, at 16 keys a chunk, of scores that have been read)
-                            const __half2 w2 = __half2half2(__float2half_rn(w));
+                            // the unit's P sv so far (and, at 16 keys a chunk, of scores that have been read), in
+                            // fp32: they may be 2^15 and w 2^-29 with 2^-14 of the new largest left of them
                             tmem_wait_st();
 #pragma unroll 1
                             for (int c0 = 0; c0 < g * 8; c0 += 16) {
@@ -651,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
-                                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&z[i]), w2);
-                                    z[i] = *reinterpret_cast<const uint32_t*>(&v);
+                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&z[i]));
+                                    z[i] = pack_f16(v.x * w, v.y * w);
                                 }
                                 tmem_st16(scores + c0, z);
                             }

@@ -1,4 +1,6 @@
 """GPU: the ends of what the paged cache's calls take, against the definitions in fp64 (paged_case.py)."""
+import math
+
 import pytest
 import torch
 
@@ -49,3 +51,28 @@ def test_scale_zero_is_value_zero(n, G, d):
     got = attend(c)
     c.check(got, c.cache())
     assert torch.all(got[0][n:, G:] == 0) and torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("n,d", [(90, 64), (90, 128), (200, 64), (200, 128)])
+def test_weights_before_a_large_rise(n, d):
+    """A key whose product stays just below the bound of P sv, then one of 2^10.5 times its weight in the same
+    unit of keys, with values on different channels."""
+    B, L = 80, 384                                       # more items than CTAs: some lie whole in one
+    c = Case(n=[n] * B, kv=[L] * B, H=2, d=d, page=128, seed=61, spare=0)
+    c.Q[:] = 0
+    c.Q[..., 0] = 1.0
+    c.K8[:], c.V8[:], c.sv[:], c.sk[:] = 0, 0, 1.0, 0.0
+    c.K8[..., 0] = 0x38                                   # 1.0
+    c.V8[..., 2] = 0x38
+    last = c.table[:, 2].long()                           # the third unit of each sequence
+    for key, score, channel in ((5, 14.5, 0), (5 + 64, 25.0, 1)):
+        c.sk[last, :, key] = score * math.log(2.0)        # scores in log2 units, 0 elsewhere
+        c.V8[last, :, key] = 0
+        c.V8[last, :, key, channel] = 0x38
+    O, lse = attend(c, causal=0, softmax_scale=1.0)
+    one = Case(n=[n], kv=[L], H=2, d=d, page=128, seed=61, spare=0)   # all sequences are the same
+    one.Q, one.table = c.Q[:n], torch.arange(3, dtype=torch.int32)[None]
+    for k in ("K8", "sk", "V8", "sv"):
+        setattr(one, k, getattr(c, k)[c.table[0].long()])
+    for b in range(B):
+        one.check((O[b * n:(b + 1) * n], lse[b * n:(b + 1) * n]), one.cache(), causal=0, scale=1.0)
