@@ -9,6 +9,9 @@
 // unit's largest sv passes 2^15, so that P sv stays finite in fp16 (whose precision is
 // the same up to there) without a maximum being taken; then a pass of its own over
 // these keys finds the new M, and what was summed before is scaled by a power of two.
+// l may then have terms of up to 2^111 (1 / sv of the smallest values), or sums of 2^118
+// before M follows: where it passes 2^100 it is kept as l lf with lf = 2^-64, and at an
+// item's end M, l and O are brought to l < 2, so that parts of any maxima can be added up.
 //
 // One persistent CTA on each SM takes tiles of 256 rows as two pipelines A and B
 // of 128 rows, which share the keys and values and the tensor core, so that the
@@ -64,6 +67,9 @@ constexpr int kRegsSoftmax = 152, kRegsConv = 104, kRegsOther = 104;
 // What an item costs besides its units, in units: its queries (5 us), the first scores and the
 // last rows, with both pipelines empty, against 2 us a unit.
 constexpr int kItemCost = 7;
+// The value scale, as -log2, up to which M follows s + log2 sv: below those of the cache that are not 0
+// (2^-109), and so that the P of 64 keys whose values are all zero sum up to less than 2^118.
+constexpr float kLeastLog2 = 110.f;
 // A unit's scales: sk[128], sv[128] (0 where there is no token), the largest sv of each 32.
 constexpr int kScaleBytes = (2 * kUnit + 4) * 4;
 
@@ -79,8 +85,8 @@ struct ManyCfg {
     static constexpr int OFF_W = OFF_V + NV * TILE;
     static constexpr int OFF_RAW = OFF_W + NW * WB;       // [NV][sk | sv][128]
     static constexpr int OFF_SC = OFF_RAW + NV * 2 * kUnit * 4;  // [NC]
-    static constexpr int OFF_ML = OFF_SC + NC * kScaleBytes;   // [m | l][128] of B, for A
-    static constexpr int OFF_INFO = OFF_ML + 2 * 128 * 4;
+    static constexpr int OFF_ML = OFF_SC + NC * kScaleBytes;   // [m | l | factor of O][128] of B, for A
+    static constexpr int OFF_INFO = OFF_ML + 3 * 128 * 4;
     static constexpr int OFF_BAR = OFF_INFO + NI * 64;
     static constexpr int OFF_MISC = OFF_BAR + 48 * 8;
     static constexpr int USED = OFF_MISC + 32;
@@ -105,6 +111,12 @@ struct ManyCfg {
 __host__ __device__ constexpr uint32_t idesc_f16_bn(uint32_t M, uint32_t N) {
     return (1u << 4) | (1u << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+
+// 2^e for a whole e <= 127, exactly; 0 below 2^-149.
+__device__ __forceinline__ float pow2_whole(int e) {
+    return __int_as_float(e >= -126 ? (e + 127) << 23 : e >= -149 ? 1 << (e + 149) : 0);
+}
+__device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23) - 127; }  // x >= 2^-126
 
 // The same value, as far as the compiler may know another one each time.
 __device__ __forceinline__ int no_hoist(int x) {
@@ -430,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_up<kRegsSoftmax>();
         const int X = warp >> 2, q = warp & 3, row = q * 32 + lane;
         const uint32_t la = tmem + ((uint32_t)(q * 32) << 16) + C::base(X);
-        float M = -INFINITY, l = 0.f, qs = 0.f;
+        float M = -INFINITY, l = 0.f, lf = 1.f, qs = 0.f;
         int last = -1, first = 0, items = 0, own = 0, shared = 0;
         bool fresh = true, begin = true;
         for (int it = 0;; ++it) {
@@ -523,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 first = row_first(a, last);
                 M = -INFINITY;
                 l = 0.f;
+                lf = 1.f;
                 fresh = true;
             }
             if (begin && !wait(C::CF + sc, it / C::NC)) break;
@@ -605,12 +618,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_wait_ld();
                         }
                         const float sum = (l2.x + l2.y) + (l3.x + l3.y);
-                        // (a sum of over 2^96: tokens whose values are all zero far above M)
-                        const bool raise = (M == -INFINITY && seen) || sum * sv_top > 32768.f || sum > 0x1p96f;
+                        // (a sum of over 2^118: tokens whose values are all zero far above M)
+                        const bool raise = (M == -INFINITY && seen) || sum * sv_top > 32768.f || sum > 0x1p118f;
                         if (!raised && __any_sync(0xffffffffu, raise)) {
                             raised = true;
-                            // M: the maximum of s + log2 sv, and of s - kZeroLog2; then these keys again
-                            float mj = -INFINITY, ms = -INFINITY;
+                            // M: the maximum of s + log2 sv, log2 0 counting as -kLeastLog2; then these keys again
+                            float mj = -INFINITY;
 #pragma unroll 1
                             for (int j = NG - 1; j >= 0; --j) {
                                 float2 y[8];
@@ -628,18 +641,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 8; i += 2) {
                                     const float4 v = ld_shared4(scl + kUnit * 4 + (g + j) * 64 + i * 8);
-                                    ms = max3(ms, fmaxf(y[i].x, y[i].y), fmaxf(y[i + 1].x, y[i + 1].y));
-                                    mj = max3(mj, fmaf(y[i].x, qs, lg2_approx(v.x)), fmaf(y[i].y, qs, lg2_approx(v.y)));
-                                    mj = max3(mj, fmaf(y[i + 1].x, qs, lg2_approx(v.z)), fmaf(y[i + 1].y, qs, lg2_approx(v.w)));
+                                    auto lg = [](float x) -> float { return fmaxf(lg2_approx(x), -kLeastLog2); };
+                                    mj = max3(mj, fmaf(y[i].x, qs, lg(v.x)), fmaf(y[i].y, qs, lg(v.y)));
+                                    mj = max3(mj, fmaf(y[i + 1].x, qs, lg(v.z)), fmaf(y[i + 1].y, qs, lg(v.w)));
                                 }
                             }
-                            const float mu = floorf(fmaxf(mj, ms * qs - kZeroLog2));
+                            const float mu = floorf(mj);
                             float w = 1.f;
                             if (raise && mu > M) {
-                                w = part_weight(M, mu);
+                                // M may rise by 228 (values of 2^-100, then of 2^127): l, which is as far below 1
+                                // for large values as above it for small ones, in two steps, lf = 1 first if that fits
+                                float dn = fmaxf(M - mu, -250.f);
+                                w = ex2_approx(dn);
+                                if (lf < 1.f && (dn < -32.f || l < 1.f)) {
+                                    dn += 64.f;
+                                    lf = 1.f;
+                                }
+                                const float d1 = fmaxf(dn, -120.f);
+                                l = l * ex2_approx(d1) * ex2_approx(dn - d1);
                                 M = mu;
                             }
-                            l *= w;
                             alpha *= w;
                             // the unit's P sv so far (and, at 16 keys a chunk, of scores that have been read), in
                             // fp32: they may be 2^15 and w 2^-29 with 2^-14 of the new largest left of them
@@ -660,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             continue;
                         }
                         raised = false;
-                        l += sum;
+                        l = fmaf(sum, lf, l);
 #pragma unroll
                         for (int j = 0; j < NG; ++j) {
                             uint32_t z[8];
@@ -675,6 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     softmax(std::true_type{});
                 else
                     softmax(std::false_type{});
+                if (l > 0x1p100f) {
+                    l *= 0x1p-64f;
+                    lf *= 0x1p-64f;
+                }
                 if (!fresh && __any_sync(0xffffffffu, alpha != 1.f)) {
                     // O holds every product up to the pipeline's last unit: the scores' completion
                     // covers what was issued before them
@@ -709,27 +734,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------------ the item's end
             float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
             if (!wait(C::OD + X, items)) break;
+            // l below 2, M by as much higher; wa is what O is multiplied by
+            const int le = l >= 2.f ? exponent_of(l) : 0, oe = le - exponent_of(lf);
+            l *= pow2_whole(-le);
+            M += (float)oe;
+            float wa = pow2_whole(-oe), wb = 0.f;
             if (!both && X == 1) {
                 // A adds the two halves of the keys up; it reads this row's O in tensor memory
                 // itself and gets M and l here, once it has read the last ones
                 if (items > 0 && !wait(C::OE + 1, items - 1)) break;
                 ml[row] = M;
                 ml[128 + row] = l;
+                ml[256 + row] = wa;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::MB));
                 ++items;
                 continue;
             }
             const bool add = !both && place > 0;  // B had units of this item
-            float wa = 1.f, wb = 0.f;
             if (!both) {
                 if (!wait(C::OD + 1, items) || !wait(C::MB, shared)) break;
                 ++shared;
                 if (add) {
                     const float mb = ml[row], lb = ml[128 + row], m = fmaxf(M, mb);
-                    wa = part_weight(M, m);
-                    wb = part_weight(mb, m);
-                    l = wa * l + wb * lb;
+                    const float fa = part_weight(M, m), fb = part_weight(mb, m);
+                    l = fa * l + fb * lb;
+                    wa *= fa;
+                    wb = fb * ml[256 + row];
                     M = m;
                 }
             }
@@ -738,8 +769,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
             const int r = r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
             const float inv = split ? 1.f : inverse_sum(l);
-            wa *= inv;
-            wb *= inv;
             const Partials part = partials_at(ws, RT, D);
             const int64_t o_off = split ? ((int64_t)slot * RT + tr) * D
                                         : (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
@@ -775,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    staged(lane, i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    staged(lane, i) = make_float4(v[4 * i] * inv, v[4 * i + 1] * inv, v[4 * i + 2] * inv, v[4 * i + 3] * inv);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {

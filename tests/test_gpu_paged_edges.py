@@ -76,3 +76,29 @@ def test_weights_before_a_large_rise(n, d):
         setattr(one, k, getattr(c, k)[c.table[0].long()])
     for b in range(B):
         one.check((O[b * n:(b + 1) * n], lse[b * n:(b + 1) * n]), one.cache(), causal=0, scale=1.0)
+
+
+def sized(n, G, d, exponents, order):
+    """Values times 2^e, down to what vc_cache_append still writes (2^-100): e mixed, or in the keys' order."""
+    c = Case(n=[n, n], kv=[1700, 700], H=2, G=G, d=d, seed=62)
+    e = torch.tensor(exponents, dtype=torch.float32)
+    if order == "mixed":
+        c.sv *= torch.exp2(e)[torch.randint(len(exponents), c.sv.shape, generator=torch.Generator().manual_seed(5))]
+    else:
+        for b in range(2):
+            step = torch.arange(c.kv[b]) * len(exponents) // c.kv[b]
+            for p in range(c.kv[b]):
+                c.sv[c.table[b, p // c.page], :, p % c.page] *= 2.0 ** float(e[step[p]])
+    return c
+
+
+SIZES = [((-100,), "mixed"), ((-90,), "mixed"), ((-100, -60, 0, 100), "mixed"), ((-100, -30, 40, 100), "rising"), ((100, 40, -30, -100), "falling")]
+
+
+@pytest.mark.parametrize("n,G", TILES[3:])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("exponents,order", SIZES, ids=str)
+def test_values_of_any_size_many_rows(n, G, d, exponents, order):
+    c = sized(n, G, d, exponents, order)
+    for mask in (dict(), dict(causal=0, window=300)):
+        c.check(attend(c, **mask), c.cache(), **mask)
