@@ -4,16 +4,15 @@
 //
 // Row (token, query head) sees keys t with scores s_t = scale q . k_t; with the
 // cached codes k8, v8 and the tokens' scales sk, sv,
-//   x_t = (q . k8_t) sk_t scale log2 e + log2 sv_t,   P_t = 2^(x_t - M),
-//   A = sum_t P_t v8_t,   l = sum_t P_t / sv_t,   O = A / l,
-//   lse = ln 2 (M + log2 l).
-// Folding sv into the exponent lets P, at most 2^8 above the running maximum M
-// of x, enter the product with the value codes as fp16 whatever the scales are;
-// E4M3 codes are fp16 numbers exactly.  A token whose values are all zero
-// (sv = 0) has log2 sv = -88 instead: it counts in l and neither in A nor,
-// beside other tokens, in M.  M moves only when the maximum has risen by more
-// than 8 (P then stays below 2^8, far inside fp16), which saves most of the
-// rescaling of A.
+//   y_t = (q . k8_t) sk_t scale log2 e,   x_t = y_t + log2 sv_t,
+//   A = sum_t 2^(x_t - M) v8_t,   l = sum_t 2^(y_t - N),
+//   O = 2^(M - N) A / l,   lse = ln 2 (N + log2 l),
+// M and N being the running maxima of x and of y.  Folding sv into the exponent lets
+// P = 2^(x - M) enter the product with the value codes as fp16 whatever the scales are;
+// E4M3 codes are fp16 numbers exactly.  (A single exponential, with l the sum of P / sv,
+// would lose the weight of small values beside large ones and leave fp32's range for many
+// small ones.)  M and N move only when their maximum has risen by more than 8 (P then stays
+// below 2^8, far inside fp16), which saves most of the rescaling of A.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
         const int kr0 = C::key_of(2 * tig), kr1 = C::key_of(2 * tig + 1), krg = C::key_of(g);
         uint32_t q[KSTEPS][2];
-        float o[MT][4], M[2], l[2], qs[2];  // rows 2 tig and 2 tig + 1 of the warp's 8
+        float o[MT][4], M[2], N[2], l[2], qs[2];  // rows 2 tig and 2 tig + 1 of the warp's 8
         int last[2], first[2];
         int it = 0, items = 0;
         while (true) {
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     qs[e] = __shfl_sync(0xffffffffu, qg, (2 * tig + e) * 4);
                     last[e] = __shfl_sync(0xffffffffu, lg, (2 * tig + e) * 4);
                     first[e] = row_first(a, last[e]);
-                    M[e] = -INFINITY;
+                    M[e] = N[e] = -INFINITY;
                     l[e] = 0.f;
                 }
 #pragma unroll
@@ -321,19 +320,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                             mma_f16((k & 1) ? z : x, ka, q[hf * 4 + k][0], q[hf * 4 + k][1]);
                         }
                     }
-                    // x = (q . k8) sk scale log2 e + log2 sv.  A token whose values are all zero
-                    // raises M only where it would pass 2^kZeroLog2 of P; its P counts in l alone.
-                    float isv[2], up[2];
+                    // y = (q . k8) sk scale log2 e, x = y + log2 sv: -inf where a token's values are all
+                    // zero, NaN both where they are no numbers
+                    float y[4];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const int k = kb + 8 * t + krg;
-                        const float sk = sks[k], sv = svs[k];
-                        up[t] = sv == 0.f ? kZeroLog2 : 0.f;
-                        const float lv = sv == 0.f ? -kZeroLog2 : lg2_approx(sv);
-                        // a NaN scale makes x NaN where it is seen; elsewhere 0 * isv has to stay 0
-                        isv[t] = sv == 0.f ? 1.f : sv > 0.f ? __fdividef(1.f, sv) : 0.f;
-                        x[2 * t] = fmaf((x[2 * t] + z[2 * t]) * sk, qs[0], lv);
-                        x[2 * t + 1] = fmaf((x[2 * t + 1] + z[2 * t + 1]) * sk, qs[1], lv);
+                        const float sv = svs[k], lv = lg2_approx(sv);
+                        const float sk = sv < INFINITY ? sks[k] : __int_as_float(0x7FFFFFFF);
+                        y[2 * t] = (x[2 * t] + z[2 * t]) * sk * qs[0];
+                        y[2 * t + 1] = (x[2 * t + 1] + z[2 * t + 1]) * sk * qs[1];
+                        x[2 * t] = y[2 * t] + lv;
+                        x[2 * t + 1] = y[2 * t + 1] + lv;
                     }
                     if (flags & kMasked) {
                         const int key0 = info->key0, L = info->L, box_ok = info->box_ok;
@@ -341,24 +339,31 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         for (int t = 0; t < 2; ++t) {
                             const int k = kb + 8 * t + krg, pos = key0 + k;
                             const bool there = pos < L && ((box_ok >> (k >> box_log2)) & 1);
-                            if (!there || pos > last[0] || pos < first[0]) x[2 * t] = -INFINITY;
-                            if (!there || pos > last[1] || pos < first[1]) x[2 * t + 1] = -INFINITY;
-                            if (!there) isv[t] = 0.f;  // whatever lies behind the last token
+                            if (!there || pos > last[0] || pos < first[0]) x[2 * t] = y[2 * t] = -INFINITY;
+                            if (!there || pos > last[1] || pos < first[1]) x[2 * t + 1] = y[2 * t + 1] = -INFINITY;
                         }
                     }
                     float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-                    if (__any_sync(0xffffffffu, mx0 > M[0] + kStale || mx1 > M[1] + kStale)) {
+                    float my0 = fmaxf(y[0], y[2]), my1 = fmaxf(y[1], y[3]);
+                    if (__any_sync(0xffffffffu, mx0 > M[0] + kStale || mx1 > M[1] + kStale || my0 > N[0] + kStale ||
+                                                    my1 > N[1] + kStale)) {
 #pragma unroll
                         for (int i = 4; i < 32; i <<= 1) {
                             mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, i));
                             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, i));
+                            my0 = fmaxf(my0, __shfl_xor_sync(0xffffffffu, my0, i));
+                            my1 = fmaxf(my1, __shfl_xor_sync(0xffffffffu, my1, i));
                         }
                         const float n0 = fmaxf(M[0], mx0), n1 = fmaxf(M[1], mx1);
                         const float a0 = part_weight(M[0], n0), a1 = part_weight(M[1], n1);
                         M[0] = n0;
                         M[1] = n1;
-                        l[0] *= a0;
-                        l[1] *= a1;
+                        my0 = fmaxf(N[0], my0);
+                        my1 = fmaxf(N[1], my1);
+                        l[0] *= part_weight(N[0], my0);
+                        l[1] *= part_weight(N[1], my1);
+                        N[0] = my0;
+                        N[1] = my1;
 #pragma unroll
                         for (int m = 0; m < MT; ++m) {
                             o[m][0] *= a0;
@@ -368,16 +373,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         }
                     }
                     const float m0 = M[0] == -INFINITY ? 0.f : M[0], m1 = M[1] == -INFINITY ? 0.f : M[1];
+                    const float n0 = N[0] == -INFINITY ? 0.f : N[0], n1 = N[1] == -INFINITY ? 0.f : N[1];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        x[2 * t] = ex2_approx(x[2 * t] + (up[t] - m0));
-                        x[2 * t + 1] = ex2_approx(x[2 * t + 1] + (up[t] - m1));
-                        l[0] = fmaf(x[2 * t], isv[t], l[0]);
-                        l[1] = fmaf(x[2 * t + 1], isv[t], l[1]);
+                        x[2 * t] = ex2_approx(x[2 * t] - m0);
+                        x[2 * t + 1] = ex2_approx(x[2 * t + 1] - m1);
+                        l[0] += ex2_approx(y[2 * t] - n0);
+                        l[1] += ex2_approx(y[2 * t + 1] - n1);
                     }
                     // P^T: keys as the products' inner index, this thread's row g
-                    const uint32_t p0 = transpose8(up[0] == 0.f ? pack_f16_sat(x[0], x[1]) : 0u);
-                    const uint32_t p1 = transpose8(up[1] == 0.f ? pack_f16_sat(x[2], x[3]) : 0u);
+                    const uint32_t p0 = transpose8(pack_f16(x[0], x[1])), p1 = transpose8(pack_f16(x[2], x[3]));
                     // V^T P^T: the four keys of this thread, D/8 channels of each
                     uint32_t v[4][D / 32];
 #pragma unroll
@@ -432,13 +437,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int i = 4; i < 32; i <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], i);
+                // one maximum for both from here on
+                const float m = fmaxf(M[e], N[e]), wo = part_weight(M[e], m);
+                l[e] *= part_weight(N[e], m);
                 float* dst = scr + ((size_t)warp * 8 + 2 * tig + e) * D + C::channel_of(g);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i)
                     *reinterpret_cast<float4*>(dst + 4 * i) =
-                        make_float4(o[2 * i][e], o[2 * i][2 + e], o[2 * i + 1][e], o[2 * i + 1][2 + e]);
+                        make_float4(o[2 * i][e] * wo, o[2 * i][2 + e] * wo, o[2 * i + 1][e] * wo, o[2 * i + 1][2 + e] * wo);
                 if (g == 0) {
-                    ml[warp * 8 + 2 * tig + e] = M[e];
+                    ml[warp * 8 + 2 * tig + e] = m;
                     ml[kConsumers * 8 + warp * 8 + 2 * tig + e] = l[e];
                 }
             }

@@ -325,9 +325,6 @@ __device__ __forceinline__ float part_weight(float m_part, float m) {
 // ------------------------------------------------------------ shared by the attention kernels
 
 constexpr float kStale = 8.f;          // how far the maximum may rise before M follows
-// The maximum M of s + log2 sv leaves P = 2^(s - M) of a token whose values are all zero unbounded;
-// it counts as if log2 sv were -kZeroLog2.  P then stays below 2^98 and the sum of 2^30 of them finite.
-constexpr float kZeroLog2 = 88.f;
 
 // What a producer tells the other warps of a CTA about a unit.
 struct StageInfo {
@@ -351,13 +348,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& a, uint32_t&
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// the same with 65504 for what is beyond
-__device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 

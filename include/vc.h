@@ -461,7 +461,7 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
  *   (relative error <= 2^-11 above 2^-14 of the row's largest such product).  A
  *   query enters the scores exactly or, for many rows, as two E4M3 parts
  *   (within 2^-17 of its largest channel).  Where a token whose values are all
- *   zero has 2^88 times the weight of every other times that one's value scale,
+ *   zero has 2^110 times the weight of every other times that one's value scale,
  *   the others' values may count as zero.  A row that sees no key gets O = 0
  *   and lse = -inf.
  *   Tokens of pages that are not there count as unseen (*dev_status).

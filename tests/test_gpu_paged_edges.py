@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from bit_fp8_attention_means_gb300 import vc
-from paged_case import Case
+from paged_case import LOG2E, Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -102,3 +102,60 @@ def test_values_of_any_size_many_rows(n, G, d, exponents, order):
     c = sized(n, G, d, exponents, order)
     for mask in (dict(), dict(causal=0, window=300)):
         c.check(attend(c, **mask), c.cache(), **mask)
+
+
+@pytest.mark.parametrize("n,G", TILES[:3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("exponents,order", SIZES, ids=str)
+def test_values_of_any_size_few_rows(n, G, d, exponents, order):
+    c = sized(n, G, d, exponents, order)
+    for mask in (dict(), dict(causal=0, window=300)):
+        c.check(attend(c, **mask), c.cache(), **mask)
+
+
+@pytest.mark.parametrize("n", [1, 90, 150])
+def test_many_small_values_above_the_first(n):
+    """Long sequences of values near 2^-100 whose weights lie a little above those of the first keys."""
+    H, d, page, L = 304, 64, 256, 16384                   # more items than CTAs: some lie whole in one
+    pages = L // page
+    g = torch.Generator().manual_seed(6)
+    V8 = (torch.randint(0x30, 0x40, (pages, page, d), generator=g) + 128 * torch.randint(2, (pages, page, d), generator=g)).to(torch.uint8)
+    s = torch.full((L,), 7.4)
+    s[:256] = 0.0                                         # log2 units
+    cache = vc.alloc_cache(pages, page, H, d, DEV)
+    cache["K8"][..., 0] = 0x38                            # 1.0
+    cache["V8"].copy_(V8[:, None])
+    cache["sk"].copy_((s * math.log(2.0)).view(pages, 1, page))
+    cache["sv"].fill_(2.0 ** -108)
+    Q = torch.zeros((n, H, d), dtype=torch.bfloat16, device=DEV)
+    Q[..., 0] = 1.0
+    cu, kv = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, n], [L]))
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+    O, lse = vc.vc_attn_paged(Q, cache, cu, kv, table, softmax_scale=1.0, causal=0, max_q=n)
+    sd = cache["sk"][:, 0].double().reshape(-1)
+    p = torch.softmax(sd, 0)
+    v = V8.to(DEV).view(torch.float8_e4m3fn).double().reshape(L, d) * 2.0 ** -108
+    # P to fp16, O to bf16; the scores' products, scaling and exponential; sums of L terms
+    want, rel = p @ v, 2.0 ** -11 + 3 * (2.0 ** -21 * 24 + 2 * (d + 16) * 2.0 ** -24 * 8) + (L + 64) * 2.0 ** -24
+    tol = 2.0 ** -8 * want.abs() + rel * (p @ v.abs())
+    assert torch.all((O.double() - want).abs() <= tol)
+    assert torch.all((lse.double() - torch.logsumexp(sd, 0)).abs() <= rel)
+
+
+@pytest.mark.parametrize("n,G", TILES)
+@pytest.mark.parametrize("times", [20.0, 24.0])
+def test_heavy_tokens_without_values_to_the_stated_end(n, G, times):
+    """Tokens whose values are all zero with up to 2^110 times the others' weight times value scale."""
+    c = Case(n=[n], kv=[900], H=1, G=G, d=64, seed=33)
+    zero = torch.rand(c.sv.shape, generator=torch.Generator().manual_seed(3)) < 0.5
+    c.V8[zero], c.sv[zero] = 0, 0.0
+    c.sk = torch.where(zero, c.sk * times, c.sk)
+    cache = c.cache()
+    (k, ks, _), (_, vs, _) = (c.sequence(cache, a, e, 0, 0) for a, e in (("K8", "sk"), ("V8", "sv")))
+    s = torch.einsum("tjd,kd->tjk", c.Q.double(), k * ks[:, None]) / math.sqrt(64) * LOG2E
+    s.masked_fill_((torch.arange(900) > 900 - n + torch.arange(n)[:, None])[:, None], -math.inf)
+    within = s[..., vs == 0].amax(-1) - (s + vs.log2())[..., vs > 0].amax(-1) <= 110
+    O, lse = (t.double().cpu() for t in attend(c))
+    want, tol, lse_want, lse_tol = c.attend(cache)
+    assert within.any() and torch.isfinite(O).all()
+    assert torch.all((O - want).abs()[within] <= tol[within]) and torch.all((lse - lse_want).abs() <= lse_tol)
