@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     for (int k = 0; k < 4; ++k) top = max(top, max(wd[i][k] & 0x7FFFu, (wd[i][k] >> 16) & 0x7FFFu));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float f = row_factor(top), qg = a.scale_log2 / f;
+                // a query that is not finite gives NaN, also where all its scores are -inf
+                const float f = row_factor(top), qg = top < 0x7F80u ? a.scale_log2 / f : __int_as_float(0x7FFFFFFF);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i)
 #pragma unroll

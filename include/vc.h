@@ -463,7 +463,8 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
  *   (within 2^-17 of its largest channel).  Where a token whose values are all
  *   zero has 2^110 times the weight of every other times that one's value scale,
  *   the others' values may count as zero.  A row that sees no key gets O = 0
- *   and lse = -inf.
+ *   and lse = -inf; one whose query holds a NaN or an infinity, and that sees a
+ *   key, gets NaN, and no other does.
  *   Tokens of pages that are not there count as unseen (*dev_status).
  *   max_q    the largest n_b, as far as the caller knows it (0: unknown).  It
  *            chooses among kernels and sizes the workspace's share of each; a

@@ -159,3 +159,16 @@ def test_heavy_tokens_without_values_to_the_stated_end(n, G, times):
     want, tol, lse_want, lse_tol = c.attend(cache)
     assert within.any() and torch.isfinite(O).all()
     assert torch.all((O - want).abs()[within] <= tol[within]) and torch.all((lse - lse_want).abs() <= lse_tol)
+
+
+@pytest.mark.parametrize("n,G", TILES)
+def test_queries_that_are_not_finite(n, G):
+    """They give NaN whatever the keys' signs, and only in their own rows; a row that sees no key stays empty."""
+    c = Case(n=[n, n], kv=[300, n - 1], H=2, G=G, seed=63)
+    c.K8[..., 7] = 0xB8                                   # -1.0: a score of -inf for an infinite channel 7
+    c.Q[:n, 0, 7] = math.inf
+    c.Q[n - 1, -1, 3] = math.nan
+    c.Q[n, 0, 7] = math.inf                               # at position -1
+    got = attend(c)
+    c.check(got, c.cache())
+    assert torch.isnan(got[0][:n, 0].float()).all() and torch.all(got[0][n] == 0)
