@@ -330,7 +330,11 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
     if (st != VC_OK) return st;
     if ((st = check_batch_sizes(batch)) != VC_OK) return st;
     if ((st = check_paged_heads(cache, Hq, batch.T, max_q)) != VC_OK) return st;
-    if ((causal != 0 && causal != 1) || window < 0 || !__builtin_isfinite(softmax_scale)) return VC_ERR_INVALID_ARG;
+    const double sc = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / __builtin_sqrt((double)cache.d);
+    const float scale_log2 = (float)(sc * 1.4426950408889634);
+    if ((causal != 0 && causal != 1) || window < 0 || !__builtin_isfinite(softmax_scale) ||
+        !__builtin_isfinite(scale_log2))
+        return VC_ERR_INVALID_ARG;
     if (!row_strides_ok(q_sn, q_sh) || !row_strides_ok(o_sn, o_sh)) return VC_ERR_INVALID_ARG;
     if (batch.T == 0) return VC_OK;
     if (!Q || !O || !aligned16(Q) || !aligned16(O) || (reinterpret_cast<uintptr_t>(lse) & 3u))
@@ -348,8 +352,7 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
     a.o_sh = o_sh;
     a.lse = lse;
     a.G = Hq / cache.H;
-    const double sc = softmax_scale > 0.f ? (double)softmax_scale : 1.0 / __builtin_sqrt((double)cache.d);
-    a.scale_log2 = (float)(sc * 1.4426950408889634);
+    a.scale_log2 = scale_log2;
     a.causal = causal;
     a.window = window;
     a.max_q = max_q;

@@ -343,6 +343,7 @@ def vc_attn_fwd(qz, shape: VcShape, softmax_scale=0.0, expcast=1, vsmooth=1, O=N
 # ------------------------------------------------------------ paged cache
 
 _U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+_LEAST_FP32 = 2.0 ** -149
 
 
 def alloc_cache(pages, page_size, H, d, device):
@@ -537,6 +538,8 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
         return _on_stream(stream, vc_attn_paged, Q, cache, cu, kv_len, table, softmax_scale, causal, window, max_q, O,
                           lse, workspace, dev_status)
     window, max_q = _int32(window), _int32(max_q)
+    if 0 < softmax_scale < _LEAST_FP32:  # as fp32 it would be 0, the default
+        softmax_scale = _LEAST_FP32
     if O is None:
         O = torch.empty(shape, dtype=_BF16, device=dev)
         o_strides = (Hq * d, d)

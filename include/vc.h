@@ -480,8 +480,8 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
  * bits.  softmax_scale <= 0 stands for 1/sqrt(d).  T = 0 does nothing.
  * Errors as vc_cache_append, plus VC_ERR_INVALID_ARG for Hq not a positive
  * multiple of cache.H, causal not in {0, 1}, window < 0, max_q < 0, a
- * softmax_scale that is not finite; VC_ERR_UNSUPPORTED for T * Hq >= 2^30;
- * VC_ERR_WORKSPACE.
+ * softmax_scale that is not finite or whose product with log2 e is not;
+ * VC_ERR_UNSUPPORTED for T * Hq >= 2^30; VC_ERR_WORKSPACE.
  */
 size_t vc_attn_paged_workspace(vc_cache_shape cache, int Hq, int B, int T, int max_q);
 vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,

@@ -172,3 +172,10 @@ def test_queries_that_are_not_finite(n, G):
     got = attend(c)
     c.check(got, c.cache())
     assert torch.isnan(got[0][:n, 0].float()).all() and torch.all(got[0][n] == 0)
+
+
+@pytest.mark.parametrize("scale", [1e-60, 1e-46, 1e-30])
+def test_small_softmax_scales(scale):
+    """A scale that fp32 does not hold is not the default one."""
+    c = Case(n=[2], kv=[200], H=2, seed=64)
+    c.check(attend(c, softmax_scale=scale), c.cache(), scale=scale)
