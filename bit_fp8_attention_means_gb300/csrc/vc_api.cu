@@ -322,10 +322,11 @@ size_t vc_attn_paged_workspace(vc_cache_shape cache, int Hq, int B, int T, int m
     return attn_paged_workspace(cache, Hq, B, T, max_q);
 }
 
-vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache, const uint8_t* K8,
-                        const float* sk, const uint8_t* V8, const float* sv, vc_batch batch, float softmax_scale,
+static vc_status attn_paged_call(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache, const uint8_t* K8,
+                                 const float* sk, const uint8_t* V8, const float* sv, vc_batch batch, float softmax_scale,
                         int causal, int window, int max_q, void* O, int64_t o_sn, int64_t o_sh, float* lse,
-                        void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+                        void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream,
+                                 int skip_unit) {
     vc_status st = check_cache_shape(cache);
     if (st != VC_OK) return st;
     if ((st = check_batch_sizes(batch)) != VC_OK) return st;
@@ -356,7 +357,26 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
     a.causal = causal;
     a.window = window;
     a.max_q = max_q;
+    a.skip_unit = skip_unit;
     return launch_attn_paged(a, v, cache.d, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache, const uint8_t* K8,
+                        const float* sk, const uint8_t* V8, const float* sv, vc_batch batch, float softmax_scale,
+                        int causal, int window, int max_q, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                        void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+    return attn_paged_call(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, softmax_scale, causal, window, max_q, O,
+                           o_sn, o_sh, lse, workspace, workspace_bytes, dev_status, stream, -1);
+}
+
+vc_status vc_debug_attn_paged_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
+                                      const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                                      vc_batch batch, int max_q, void* O, int64_t o_sn, int64_t o_sh, void* workspace,
+                                      size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream,
+                                      int skip_unit) {
+    if (!dev_status || skip_unit < 0) return VC_ERR_INVALID_ARG;
+    return attn_paged_call(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, 0.f, 1, 0, max_q, O, o_sn, o_sh, nullptr,
+                           workspace, workspace_bytes, dev_status, stream, skip_unit);
 }
 
 vc_status vc_attn_fwd_debug(const uint8_t* Q8, const float* sq, const uint8_t* K8, const float* sk,

@@ -124,7 +124,9 @@ __device__ __forceinline__ int no_hoist(int x) {
     return x;
 }
 
-template <int D, int kChunk>
+// SKIP: the test hook that leaves out the keys of unit a.skip_unit, in instances of its own (in the others
+// these few instructions of the loader cost 4 % of the time of windowed chunks).
+template <int D, int kChunk, bool SKIP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedAttn a, const CacheView c, int RT, void* ws) {
@@ -264,9 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int sk = it % C::NK, sv = it % C::NV;
                     ok = it < C::NK || wait(C::KE + sk, it / C::NK - 1);
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(C::KF + sk), C::TILE);
+                    const bool skip = SKIP && it == a.skip_unit;
+                    if (lane == 0 && !skip) mbar_arrive_expect_tx(bar(C::KF + sk), C::TILE);
                     __syncwarp();
-                    if (lane < boxes)
+                    if (lane < boxes && !skip)
                         tma_load_4d(sbase + C::OFF_K + sk * C::TILE + at, &tmK, 0, in, w.h, pg, bar(C::KF + sk));
                     loaded_k = it + 1;
                     ok = it < C::NV || wait(C::VE + sv, it / C::NV - 1);
@@ -295,10 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             // this CTA's own copies land before it can exit
+            uint32_t left = kWaitAttempts;
             for (int j = max(loaded_k - C::NK, 0); j < loaded_k; ++j)
-                drain_wait_counted(bar(C::KF + j % C::NK), (j / C::NK) & 1);
+                if (!SKIP || j != a.skip_unit) drain_wait_counted(bar(C::KF + j % C::NK), (j / C::NK) & 1, left);
             for (int j = max(loaded_v - C::NV, 0); j < loaded_v; ++j)
-                drain_wait_counted(bar(C::VF + j % C::NV), (j / C::NV) & 1);
+                drain_wait_counted(bar(C::VF + j % C::NV), (j / C::NV) & 1, left);
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ MMA issuer
             // One warp issues for both pipelines, in turn: the product P V of a pipeline's last
@@ -372,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every MMA this warp issued has completed once this phase flips
             mma_commit_w(bar(C::TD));
-            drain_wait_counted(bar(C::TD), 0);
+            uint32_t left = kWaitAttempts;
+            drain_wait_counted(bar(C::TD), 0, left);
             __syncwarp();
         }
     } else if (warp >= kConvWarp) {
@@ -847,14 +852,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, int kChunk>
-vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
-                      int ctas, void* ws, cudaStream_t st) {
-    auto kern = attn_many_kernel<D, kChunk>;
+template <int D, int kChunk, bool SKIP>
+vc_status launch_many_as(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
+                         int ctas, void* ws, cudaStream_t st) {
+    auto kern = attn_many_kernel<D, kChunk, SKIP>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
     if (s != VC_OK) return s;
     kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
     return cuda_status(cudaGetLastError());
+}
+
+template <int D, int kChunk>
+vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
+                      int ctas, void* ws, cudaStream_t st) {
+    return a.skip_unit < 0 ? launch_many_as<D, kChunk, false>(mk, mv, a, c, RT, ctas, ws, st)
+                           : launch_many_as<D, kChunk, true>(mk, mv, a, c, RT, ctas, ws, st);
 }
 
 }  // namespace

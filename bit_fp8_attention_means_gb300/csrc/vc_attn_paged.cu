@@ -98,7 +98,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return r;
 }
 
-template <int D, int RG>
+// SKIP: the test hook that leaves out the keys of unit a.skip_unit, in instances of its own.
+template <int D, int RG, bool SKIP>
 __global__ void __launch_bounds__(kFewThreads, 1)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedAttn a, const CacheView c, void* ws) {
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             for (int u = w.unit; u < w.end; ++u, ++it) {
                 const int st = it % NS, key0 = u * kUnit;
+                const bool skip = SKIP && it == a.skip_unit && role < 2;
                 int pg = ahead;
                 ahead = entry(u + 1);
                 if (pg == -2 || pg >= c.pages) {
@@ -198,16 +200,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         f->box_ok = box_ok;
                         f->pad[1] = on;
                     }
-                    mbar_arrive_expect_tx(full + 8 * st, (uint32_t)((boxes + 1 - odd) >> 1 << box_log2) * D);
+                    if (!skip) mbar_arrive_expect_tx(full + 8 * st, (uint32_t)((boxes + 1 - odd) >> 1 << box_log2) * D);
                 }
                 __syncwarp();
-                if (mine) {
+                if (mine && !skip) {
                     const uint32_t at = sbase + (role < 2 ? C::OFF_K : C::OFF_V) + st * C::TILE +
                                         (uint32_t)(lane << box_log2) * D;
                     const int in = (key0 + (lane << box_log2)) & ((1 << c.page_log2) - 1);
                     tma_load_4d(at, map, 0, in, w.h, pg, full + 8 * st);
                 }
-                if (odd) {
+                if (odd && !skip) {
                     // four keys' scales a lane; 0 where the page is not there
                     const int spg = __shfl_sync(0xffffffffu, pg, (4 * lane) >> box_log2);
                     const int in = (key0 + 4 * lane) & ((1 << c.page_log2) - 1);
@@ -230,7 +232,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
         }
         // this CTA's own copies land before it can exit
-        for (int j = it > NS ? it - NS : 0; j < it; ++j) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1);
+        uint32_t left = kWaitAttempts;
+        for (int j = it > NS ? it - NS : 0; j < it; ++j)
+            if (!SKIP || j != a.skip_unit) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1, left);
     } else {
         // ------------------------------------------------------------ consumers
         regs_up<kFewRegsUp>();
@@ -628,10 +632,10 @@ vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, 
                                 : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, c, ws, RT, parts));
 }
 
-template <int D, int RG>
+template <int D, int RG, bool SKIP = false>
 vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
                      int ctas, cudaStream_t st) {
-    auto kern = attn_few_kernel<D, RG>;
+    auto kern = attn_few_kernel<D, RG, SKIP>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
     if (s != VC_OK) return s;
     kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
@@ -649,10 +653,15 @@ int part_count(const PagedAttn& a, const CacheView& c, int RT) {
 template <int D>
 vc_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
                    cudaStream_t st) {
-    const int RT = tile_rows(a.G, c.B, c.T, a.max_q), ctas = part_count(a, c, RT);
+    int RT = tile_rows(a.G, c.B, c.T, a.max_q);
+    const bool skip = a.skip_unit >= 0 && RT <= 32;
+    if (skip) RT = 8;  // of the kernel for few rows, one instance with the hook
+    const int ctas = part_count(a, c, RT);
     vc_status s;
     switch (RT) {
-        case 8: s = launch_few<D, 1>(mk, mv, a, c, ws, ctas, st); break;
+        case 8:
+            s = skip ? launch_few<D, 1, true>(mk, mv, a, c, ws, ctas, st) : launch_few<D, 1>(mk, mv, a, c, ws, ctas, st);
+            break;
         case 16: s = launch_few<D, 2>(mk, mv, a, c, ws, ctas, st); break;
         case 32: s = launch_few<D, 4>(mk, mv, a, c, ws, ctas, st); break;
         default: s = launch_attn_many(mk, mv, a, c, D, RT, ctas, ws, st);

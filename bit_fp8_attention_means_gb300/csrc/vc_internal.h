@@ -93,6 +93,7 @@ struct PagedAttn {
     int G;             // query heads of a key/value head
     float scale_log2;  // softmax_scale * log2 e
     int causal, window, max_q;
+    int skip_unit;     // test hook: each CTA's loaders of keys neither load nor signal this unit of theirs; -1 = off
 };
 vc_status launch_cache_append(const uint16_t* K, const uint16_t* V, int64_t s_n, int64_t s_h, int d,
                               const CacheView& c, cudaStream_t st);

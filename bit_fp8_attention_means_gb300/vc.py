@@ -98,6 +98,10 @@ def lib():
         L.vc_attn_paged.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp, _vp, _vp,
                                     _vp, VcBatch, ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp,
                                     ctypes.c_int64, ctypes.c_int64, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        L.vc_debug_attn_paged_timeout.restype = ctypes.c_int
+        L.vc_debug_attn_paged_timeout.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp,
+                                                  _vp, _vp, _vp, VcBatch, ctypes.c_int, _vp, ctypes.c_int64,
+                                                  ctypes.c_int64, _vp, ctypes.c_size_t, _vp, _vp, ctypes.c_int]
         L.vc_debug_e4m3_encode.restype = ctypes.c_int
         L.vc_debug_e4m3_encode.argtypes = [_vp, ctypes.c_int64, _vp, _vp]
         L.vc_debug_wait_timeout.restype = ctypes.c_int
@@ -590,4 +594,25 @@ def vc_debug_attn_timeout(qz, shape: VcShape, dev_status: torch.Tensor, skip_k_t
                                        _ptr(qz["V8T"]), _ptr(qz["sv"]), _ptr(qz["mu"]) if vsmooth else None, shape,
                                        int(vsmooth), _ptr(O), _ptr(dev_status), _stream(stream), int(skip_k_tile),
                                        int(timeout_us)), "vc_debug_attn_timeout")
+    return O
+
+
+def vc_debug_attn_paged_timeout(Q, cache, cu, kv_len, table, dev_status, skip_unit, max_q=0, stream=None):
+    """vc_attn_paged whose loaders leave out the keys of each CTA's unit `skip_unit`: it must record
+    VC_ERR_TIMEOUT in dev_status after about a second and return.  Returns O (unspecified)."""
+    L = lib()
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    T, Hq, d = Q.shape
+    strides, batch = _rows("Q", Q, Hq, s.d, dev), _batch_of(cu, kv_len, table, T, dev)
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_debug_attn_paged_timeout, Q, cache, cu, kv_len, table, dev_status, skip_unit,
+                          max_q)
+    O = torch.empty((T, Hq, d), dtype=_BF16, device=dev)
+    ws = _workspace(L.vc_attn_paged_workspace(s, Hq, batch.B, T, max_q), O.device)
+    _on_device(dev, stream, lambda *args: L.vc_debug_attn_paged_timeout(*args, skip_unit),
+               (Q.data_ptr(), *strides, Hq, s, K8, sk, V8, sv, batch, max_q, O.data_ptr(), Hq * d, d, ws.data_ptr(),
+                ws.numel(), status), "vc_debug_attn_paged_timeout")
     return O

@@ -179,3 +179,27 @@ def test_small_softmax_scales(scale):
     """A scale that fp32 does not hold is not the default one."""
     c = Case(n=[2], kv=[200], H=2, seed=64)
     c.check(attend(c, softmax_scale=scale), c.cache(), scale=scale)
+
+
+@pytest.mark.parametrize("n,G", TILES)
+@pytest.mark.parametrize("d,skip", [(64, 1), (128, 0)])
+def test_wait_timeout_and_recovery(n, G, d, skip):
+    """The kernels' failure path: loaders that leave out a unit's keys.  The wait for them runs out and is
+    recorded, every CTA ends, and the next call in the context is right."""
+    c = Case(n=[n] * 40, kv=[1500] * 40, H=2, G=G, d=d, page=64, seed=66)
+    Q, cache, args = c.Q.to(DEV), c.cache(DEV), c.args(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    vc.vc_debug_attn_paged_timeout(Q, cache, *args, status, skip, max_q=n)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(status) == 5
+    # 2^18 attempts of 3.7 us, or twice that where something in flight never arrives
+    assert start.elapsed_time(end) < 4000
+    got = attend(c)
+    one = Case(n=[n], kv=[1500], H=2, G=G, d=d, page=64, seed=66)
+    one.Q, one.table, one.pages = c.Q[:n], c.table[:1], c.pages
+    for k in ("K8", "sk", "V8", "sv"):
+        setattr(one, k, getattr(c, k))
+    one.check((got[0][:n], got[1][:n]), c.cache())
