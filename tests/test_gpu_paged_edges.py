@@ -203,3 +203,65 @@ def test_wait_timeout_and_recovery(n, G, d, skip):
     for k in ("K8", "sk", "V8", "sv"):
         setattr(one, k, getattr(c, k))
     one.check((got[0][:n], got[1][:n]), c.cache())
+
+
+BROKEN = [([0, 4, 2, 12], [20, 30, 40]), ([-3, 4, 8, 12], [20, 30, 40]), ([5, 4, 3, 2], [20, 30, 40]), ([0, 4, 8, 2 ** 31 - 1], [20, 30, 40]),
+          ([-2 ** 31, -1, 2 ** 31 - 1, 0], [20, 30, 40]), ([0, 4, 8, 12], [20, -1, 40]), ([0, 4, 8, 12], [20, 30, 2 ** 31 - 1]),
+          ([0, 4, 8, 12], [-2 ** 31, 3, 1]), ([2, 4, 8, 11], [20, 30, 48])]
+
+
+@pytest.mark.parametrize("cu,kv", BROKEN, ids=str)
+@pytest.mark.parametrize("max_q", [1, 4, 500])
+def test_broken_batches_touch_nothing_outside(cu, kv, max_q):
+    """Offsets and lengths out of range, with guards around every buffer: nothing there is written, nor, as it
+    would spread NaN, read; within them only the rows and slots that the clamped numbers name are written."""
+    c = Case(n=[4, 4, 4], kv=[20, 30, 48], H=2, G=8, seed=19, cols=3)
+    c.table[c.table < 0] = 0                              # what a length beyond the sequence's own finds
+    guard = 64
+
+    def guarded(t, fill):
+        big = torch.full((t.shape[0] + 2 * guard, *t.shape[1:]), fill, dtype=t.dtype, device=DEV)
+        inner = big[guard:-guard]
+        inner.copy_(t)
+        return inner, big
+
+    nan = math.nan
+    seven = torch.full((), 7.0)
+    bufs = {"K8": guarded(c.K8, 0x7F), "V8": guarded(c.V8, 0x7F), "sk": guarded(c.sk, nan), "sv": guarded(c.sv, nan),
+            "Q": guarded(c.Q, nan), "K": guarded(c.K, nan), "V": guarded(c.V, nan),
+            "O": guarded(seven.to(torch.bfloat16).expand(c.T, 16, 128), 7.0), "lse": guarded(seven.expand(c.T, 16), 7.0),
+            "K2": guarded(seven.to(torch.bfloat16).expand(c.T, 2, 128), 7.0), "V2": guarded(seven.to(torch.bfloat16).expand(c.T, 2, 128), 7.0)}
+    cache = {k: bufs[k][0] for k in ("K8", "V8", "sk", "sv")}
+    args = tuple(torch.tensor(x, dtype=torch.int32, device=DEV) for x in (cu, kv)) + (c.table.to(DEV),)
+    before = {k: b[1].clone() for k, b in bufs.items()}
+    rows, slots = torch.zeros(c.T, dtype=torch.bool), torch.zeros(c.pages, c.page, dtype=torch.bool)
+    for b in range(3):
+        first = min(max(cu[b], 0), c.T)
+        n, length = min(max(cu[b + 1], first), c.T) - first, min(max(kv[b], 0), 3 * c.page)
+        rows[first:first + n] = True
+        for p in range(max(length - n, 0), length):
+            slots[c.table[b, p // c.page], p % c.page] = True
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    vc.vc_attn_paged(bufs["Q"][0], cache, *args, max_q=max_q, O=bufs["O"][0], lse=bufs["lse"][0], dev_status=status)
+    vc.vc_cache_read(cache, *args, c.T, K=bufs["K2"][0], V=bufs["V2"][0], dev_status=status)
+    vc.vc_cache_append(bufs["K"][0], bufs["V"][0], cache, *args, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == (0 if kv[2] == 48 else 1)
+    for k, (inner, big) in bufs.items():
+        same = (big == before[k]) | (big != big) & (before[k] != before[k])
+        assert same[:guard].all() and same[-guard:].all(), k
+        assert not torch.isnan(inner.float()).any(), k
+        same = same[guard:-guard].cpu()
+        if k in ("K8", "V8", "sk", "sv"):
+            assert same.transpose(1, 2)[~slots].all(), k
+        else:
+            assert same[~rows].all(), k
+
+
+@pytest.mark.parametrize("n,G", TILES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_items_of_many_parts(n, G, d):
+    """One sequence over all CTAs: more parts of an item than a warp has lanes to join."""
+    c = Case(n=[n], kv=[12000], H=1, G=G, d=d, page=64, seed=65)
+    for mask in (dict(), dict(causal=0, window=9000)):
+        c.check(attend(c, **mask), c.cache(), **mask)
