@@ -30,9 +30,10 @@
 //       E4M3 numbers would spare that, but lose everything below 2^-17 of the
 //       row's largest: a few thousand keys there are a visible part of a sum.)
 // The floor is the tensor core's 4 x 512 clocks a unit of both pipelines (d = 128).
-// Measured: 3,560 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.30 ms, 1,297
-// TFLOP/s.  Without softmax arithmetic a unit still took 3,150 clocks.  Shared memory's data
-// path is the busiest part (products 36 %, loads and stores 55 %, TMA besides), and code
+// Measured: 3,770 clocks; 3,600 tokens of 40 heads over 75,600 keys take 4.53 ms call after
+// call, 1,229 TFLOP/s at the 1,940 MHz of the power cap, and 4.30 ms for ten calls.  Without
+// softmax arithmetic a unit still took 3,150 clocks.  Shared memory's data path is the
+// busiest part (products 37 %, loads and stores 56 %, TMA besides), and code
 // that runs beside other code costs instruction fetches: two threads a row (5.9 ms), loads
 // that need fewer scales (16x256b, 4.6 ms) and warps of their own for the scales (4.8 ms)
 // all lost.  With d = 64 the chain from scores to P bounds it as well (tensor core 25 %
@@ -134,10 +135,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Keys that the softmax takes between two decisions about M: kChunk, and in units with a mask,
     // whose code is longer, kMaskedChunk.  The less code, the better the instruction caches hold it
     // beside the other pipeline's; the longer a chunk, the more overlaps within it.
-    //   d = 128, tiles of 256 rows, 3,600 rows over 75,600 keys: 64 keys 4.30 ms, 32 4.64, 16 5.13,
-    //     all 128 5.95; masked 16 against 32: ragged chunks 112 against 121 us.
-    //   d = 128, tiles of 128 rows, a few tokens of 24 sequences: 16 keys 48.8 us, 32 51.4, 64 56.9.
-    //   d = 64, windowed chunks: 32 keys 0.755 ms, 64 (masked 16) 0.842, 16 0.795.
+    //   d = 128, tiles of 256 rows, 3,600 rows over 75,600 keys: 64 keys 4.51 ms, 32 4.95, 16 5.22,
+    //     all 128 5.10; masked 16 against 32: ragged chunks 115 against 124 us.
+    //   d = 128, tiles of 128 rows, a few tokens of 24 sequences: 16 keys 53.1 us, 32 54.8, 64 58.4.
+    //   d = 64, windowed chunks: 32 keys 0.750 ms, 64 0.918, 16 0.797; masked 16 0.759.
+    // (The instance of 16 keys has 8 bytes of spill stores and 136 of spill loads, the others none.)
     constexpr int kMaskedChunk = D == 128 ? 16 : 32;
     // offsets from the array itself: through an integer the compiler would lose sight of
     // the address space, and generic loads take the slow road to shared memory

@@ -37,7 +37,7 @@ namespace {
 // q . k and the keys and channels of P V are permuted so that each thread reads
 // 16 consecutive bytes, in an order without bank conflicts under the TMA
 // swizzle.  One token of 96 sequences of 100 to 8,192 keys (747 MB, pages of 16):
-// 151 us, 4.9 TB/s; rows as the wide side, 8 warps and one producer took 251 us.
+// 153 us, 4.9 TB/s; rows as the wide side, 8 warps and one producer took 251 us.
 // One token against 75,600 keys (160 MB): 40 us, of which 25 us at 6.4 TB/s lie
 // between the first data (6 us) and the joining (6 us).
 
@@ -607,9 +607,11 @@ bool make_cache_map(CUtensorMap* map, const uint8_t* base, int d, const CacheVie
 
 // Rows of a tile, by the rows of the longest chunk as far as the caller told: up to
 // 32 go to the kernel for few rows, more to the one for many.  Measured on 24
-// sequences of 500 to 6,000 keys, d = 128, few rows against many: 16 rows 33.8
-// against 46.7 us, 32 rows 45.9 against 47.6 (d = 64: 33.4 against 43.7).  128 rows
-// take 53.5 us in tiles of 128 and 56.9 in tiles of 256.
+// sequences of 500 to 6,000 keys, d = 128, few rows against many: 16 rows 36.0
+// against 51.0 us, 32 rows 47.0 against 51.3 (d = 64: 34.8 against 45.3), 64 rows 75.5
+// in tiles of 32 against 52.5.  128 rows take 56.0 us in tiles of 128 and 60.9 in
+// tiles of 256.  One choice for the whole call: a chunk of 2,000 tokens beside 60 single
+// ones (8 x 4 heads) takes 250 us, in two calls 200.
 int tile_rows(int G, int B, int T, int max_q) {
     const int64_t q = max_q > 0 ? max_q : ((int64_t)T + B - 1) / B;
     const int64_t rows = q * G;
