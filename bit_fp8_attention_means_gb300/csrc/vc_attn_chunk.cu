@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const PagedAttn a, const CacheView c, int RT, void* ws) {
     using C = ManyCfg<D>;
+    constexpr uint32_t ATTEMPTS = SKIP ? kHookAttempts : kWaitAttempts;
     // Keys that the softmax takes between two decisions about M: kChunk, and in units with a mask,
     // whose code is longer, kMaskedChunk.  The less code, the better the instruction caches hold it
     // beside the other pipeline's; the longer a chunk, the more overlaps within it.
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     auto wait = [&](int i, int phase) -> bool {
-        return mbar_wait_counted(bar(i), phase & 1, abort_flag, c.dev_status);
+        return mbar_wait_counted<ATTEMPTS>(bar(i), phase & 1, abort_flag, c.dev_status);
     };
 
     if (threadIdx.x == 0) {
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             // this CTA's own copies land before it can exit
-            uint32_t left = kWaitAttempts;
+            uint32_t left = ATTEMPTS;
             for (int j = max(loaded_k - C::NK, 0); j < loaded_k; ++j)
                 if (!SKIP || j != a.skip_unit) drain_wait_counted(bar(C::KF + j % C::NK), (j / C::NK) & 1, left);
             for (int j = max(loaded_v - C::NV, 0); j < loaded_v; ++j)
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every MMA this warp issued has completed once this phase flips
             mma_commit_w(bar(C::TD));
-            uint32_t left = kWaitAttempts;
+            uint32_t left = ATTEMPTS;
             drain_wait_counted(bar(C::TD), 0, left);
             __syncwarp();
         }

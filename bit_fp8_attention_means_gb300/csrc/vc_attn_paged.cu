@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     const PagedAttn a, const CacheView c, void* ws) {
     using C = FewCfg<D>;
     constexpr int NS = C::NS, RT = 8 * RG;
+    constexpr uint32_t ATTEMPTS = SKIP ? kHookAttempts : kWaitAttempts;
     // offsets from the array itself: through an integer the compiler would lose sight of
     // the address space, and generic loads take the slow road to shared memory
     extern __shared__ uint8_t smem_raw[];
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     pg = -1;
                 }
                 const int box_ok = (int)__ballot_sync(0xffffffffu, pg >= 0);
-                if (it >= NS && !mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
+                if (it >= NS && !mbar_wait_counted<ATTEMPTS>(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
                     ok = false;
                     break;
                 }
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (ok) {
             // the stage that ends the consumers' loop
             const int st = it % NS;
-            if (it < NS || mbar_wait_counted(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
+            if (it < NS || mbar_wait_counted<ATTEMPTS>(empty + 8 * st, (it / NS - 1) & 1, abort_flag, c.dev_status)) {
                 if (lane == 0 && role == 0) reinterpret_cast<StageInfo*>(smem + C::OFF_INFO + st * 64)->flags = kEnd;
                 if (lane == 0) mbar_arrive(full + 8 * st);
                 if (odd) mbar_arrive(full + 8 * st);
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
         }
         // this CTA's own copies land before it can exit
-        uint32_t left = kWaitAttempts;
+        uint32_t left = ATTEMPTS;
         for (int j = it > NS ? it - NS : 0; j < it; ++j)
             if (!SKIP || j != a.skip_unit) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1, left);
     } else {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         int it = 0, items = 0;
         while (true) {
             const int st = it % NS;
-            if (!mbar_wait_counted(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status)) break;
+            if (!mbar_wait_counted<ATTEMPTS>(full + 8 * st, (it / NS) & 1, abort_flag, c.dev_status)) break;
             const StageInfo* info = reinterpret_cast<const StageInfo*>(smem + C::OFF_INFO + st * 64);
             const int flags = info->flags;
             if (flags & kEnd) break;
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
             // ------------------------------------------------------------ the item's end
             // the accumulators are free to overwrite once the last item's were read
-            if (items > 0 && !mbar_wait_counted(read, (items - 1) & 1, abort_flag, c.dev_status)) break;
+            if (items > 0 && !mbar_wait_counted<ATTEMPTS>(read, (items - 1) & 1, abort_flag, c.dev_status)) break;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(written);
-            if (!mbar_wait_counted(written, items & 1, abort_flag, c.dev_status)) break;
+            if (!mbar_wait_counted<ATTEMPTS>(written, items & 1, abort_flag, c.dev_status)) break;
             const bool split = flags & (kHead | kTail);
             const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
             for (int i = threadIdx.x; i < rows * (D / 4); i += kConsumers * 32) {
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 // and two L2 round trips: the header, then the parts' maxima and sums (a lane
 // each) with the first accumulators.  A block has WR warps a row, which take every
 // WR-th part: 4 for tiles of few rows, of which a long cache makes many parts, 1
-// for those of many.
+// for those of many.  (4 to 20 bytes of spill loads in each instance.)
 constexpr int kJoinThreads = 128;
 
 template <int D, int WR>

@@ -107,17 +107,19 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
 
 // mbar_wait_warp in a few instructions: the bound is a number of attempts, not a
 // time.  One that stays in vain suspends the thread for 3.7 us (measured: 2^14 of
-// them took 61 ms), so 2^18 are a second; every 1024th looks whether another thread
-// gave up.  A kernel with twenty waits and the timed loop in each place is large enough
-// to run out of the instruction cache, and with the bound as an argument of the kernel
-// instead of a constant windowed chunks took 804 us instead of 782.
-constexpr uint32_t kWaitAttempts = 1u << 18;
+// them took 61 ms), so 2^20 are the 4 s of the timed waits; every 1024th looks whether
+// another thread gave up.  A kernel with twenty waits and the timed loop in each place
+// is large enough to run out of the instruction cache, and with the bound as an argument
+// of the kernel instead of a constant windowed chunks took 804 us instead of 782.
+constexpr uint32_t kWaitAttempts = 1u << 20;
+constexpr uint32_t kHookAttempts = 1u << 16;  // of the test hook's instances
+template <uint32_t ATTEMPTS>
 __device__ __forceinline__ bool mbar_wait_counted(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                   int32_t* dev_status) {
     bool ok = true;
     for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
         if (n & 1023u) continue;
-        if (!*abort_flag && n < kWaitAttempts) continue;
+        if (!*abort_flag && n < ATTEMPTS) continue;
         if (!*abort_flag && dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
         *abort_flag = 1;
         ok = false;
@@ -125,8 +127,8 @@ __device__ __forceinline__ bool mbar_wait_counted(uint32_t bar, uint32_t parity,
     }
     return __all_sync(0xffffffffu, ok);
 }
-// The same for teardown: not ended by another thread's giving up; `left` attempts (kWaitAttempts at first) for all
-// of a thread's waits.
+// The same for teardown: not ended by another thread's giving up; `left` attempts for all of a
+// thread's waits.
 __device__ __forceinline__ void drain_wait_counted(uint32_t bar, uint32_t parity, uint32_t& left) {
     for (; !mbar_try_wait(bar, parity) && left; --left) {
     }

@@ -599,7 +599,7 @@ def vc_debug_attn_timeout(qz, shape: VcShape, dev_status: torch.Tensor, skip_k_t
 
 def vc_debug_attn_paged_timeout(Q, cache, cu, kv_len, table, dev_status, skip_unit, max_q=0, stream=None):
     """vc_attn_paged whose loaders leave out the keys of each CTA's unit `skip_unit`: it must record
-    VC_ERR_TIMEOUT in dev_status after about a second and return.  Returns O (unspecified)."""
+    VC_ERR_TIMEOUT in dev_status, after about a quarter of a second, and return.  Returns O (unspecified)."""
     L = lib()
     s, (K8, sk, V8, sv), dev = _cache_parts(cache)
     T, Hq, d = Q.shape

@@ -543,10 +543,10 @@ vc_status vc_debug_attn_timeout(const uint8_t* Q8, const float* sq, const uint8_
  * Test hook for the failure path of the paged attention's kernels: runs
  * vc_attn_paged (causal, no window, default scale, no lse) except that every CTA's
  * loaders neither load nor signal the keys of its unit `skip_unit` (>= 0; a unit is
- * 128 keys of an item, counted from the CTA's first).  The waits of vc_attn_paged give
- * up after about a second: a CTA with that many units then writes VC_ERR_TIMEOUT to
- * *dev_status (required here) and ends as vc_debug_attn_timeout describes, within
- * another second; O is left unspecified.  Other arguments as vc_attn_paged, whose errors
+ * 128 keys of an item, counted from the CTA's first), and every device wait gives up
+ * after about a quarter of a second (4 s in vc_attn_paged): a CTA with that many units
+ * then writes VC_ERR_TIMEOUT to *dev_status (required here) and ends as
+ * vc_debug_attn_timeout describes, within as long again; O is left unspecified.  Other arguments as vc_attn_paged, whose errors
  * it returns too.
  */
 vc_status vc_debug_attn_paged_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,

@@ -195,8 +195,8 @@ def test_wait_timeout_and_recovery(n, G, d, skip):
     end.record()
     torch.cuda.synchronize()
     assert int(status) == 5
-    # 2^18 attempts of 3.7 us, or twice that where something in flight never arrives
-    assert start.elapsed_time(end) < 4000
+    # 2^16 attempts of 3.7 us, or twice that where something in flight never arrives
+    assert start.elapsed_time(end) < 1000
     got = attend(c)
     one = Case(n=[n], kv=[1500], H=2, G=G, d=d, page=64, seed=66)
     one.Q, one.table, one.pages = c.Q[:n], c.table[:1], c.pages
