@@ -8,5 +8,6 @@ as hand-written CUDA kernels behind the C ABI in ``include/vc.h``.
 does not load the CUDA library; the first call does, and raises if it is
 missing.
 """
-from .vc import (VcError, VcShape, alloc_cache, alloc_quantized, shape_of, vc_attn_fwd,  # noqa: F401
-                 vc_attn_paged, vc_cache_append, vc_cache_read, vc_cluster, vc_quantize)
+from .vc import (VcError, VcShape, alloc_cache, alloc_pool, alloc_quantized, make_rope, shape_of, vc_attn_fwd,  # noqa: F401
+                 vc_attn_paged, vc_cache_append, vc_cache_append_rope, vc_cache_copy, vc_cache_read, vc_cluster,
+                 vc_pages_compact, vc_pages_fork, vc_pages_reserve, vc_pages_trim, vc_quantize, vc_rope)

@@ -94,6 +94,7 @@ const char* vc_status_string(vc_status s) {
         case VC_ERR_WORKSPACE: return "VC_ERR_WORKSPACE";
         case VC_ERR_CUDA: return "VC_ERR_CUDA";
         case VC_ERR_TIMEOUT: return "VC_ERR_TIMEOUT";
+        case VC_ERR_PAGES: return "VC_ERR_PAGES";
     }
     return "VC_ERR_UNKNOWN";
 }
@@ -308,6 +309,229 @@ vc_status vc_cache_read(vc_cache_shape cache, const uint8_t* K8, const float* sk
     if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
     return launch_cache_read(v, cache.d, static_cast<uint16_t*>(K), static_cast<uint16_t*>(V), s_n, s_h,
                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------ rotary positions
+
+static vc_status check_rope(const vc_rope_spec& r, int d) {
+    if (d < 1) return VC_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return VC_ERR_UNSUPPORTED;
+    if (r.rot < 16 || r.rot > d || r.rot % 16 || (r.layout != 0 && r.layout != 1)) return VC_ERR_INVALID_ARG;
+    if (!(r.magnitude > 0.f) || !__builtin_isfinite(r.magnitude)) return VC_ERR_INVALID_ARG;
+    return VC_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static vc_status rope_rows(const vc_rope_spec& r, const int32_t* pos, int inverse, RopeRows* a) {
+    if (!r.turns || (reinterpret_cast<uintptr_t>(r.turns) & 7u) || !aligned4(pos)) return VC_ERR_INVALID_ARG;
+    *a = RopeRows{};
+    a->turns = r.turns;
+    a->pos = pos;
+    a->rot = r.rot;
+    a->pairs = r.layout;
+    a->magnitude = r.magnitude;
+    a->sign = inverse ? -r.magnitude : r.magnitude;
+    return VC_OK;
+}
+
+vc_status vc_rope(const void* X, int64_t s_n, int64_t s_h, int T, int H, int d, vc_rope_spec rope, const int32_t* pos,
+                  const int32_t* cu, const int32_t* kv_len, int B, int inverse, void* out, int64_t o_sn, int64_t o_sh,
+                  int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_rope(rope, d);
+    if (st != VC_OK) return st;
+    if (T < 0 || H < 1 || (inverse != 0 && inverse != 1)) return VC_ERR_INVALID_ARG;
+    if (!row_strides_ok(s_n, s_h) || !row_strides_ok(o_sn, o_sh)) return VC_ERR_INVALID_ARG;
+    if ((int64_t)T * H >= (int64_t(1) << 31)) return VC_ERR_UNSUPPORTED;
+    if (T == 0) return VC_OK;
+    if (!X || !out || !aligned16(X) || !aligned16(out) || (!cu) != (!kv_len) || (!pos && !cu) || (cu && B < 1))
+        return VC_ERR_INVALID_ARG;
+    RopeRows a;
+    if ((st = rope_rows(rope, pos, inverse, &a)) != VC_OK) return st;
+    a.Q = static_cast<const uint16_t*>(X);
+    a.q_sn = s_n;
+    a.q_sh = s_h;
+    a.out = static_cast<uint16_t*>(out);
+    a.o_sn = o_sn;
+    a.o_sh = o_sh;
+    a.Hq = H;
+    CacheView v{};  // no cache: sequences of up to 2^30 - 1 tokens
+    v.cu = cu;
+    v.kv_len = kv_len;
+    v.cols = (1 << 30) - 1;
+    v.B = B;
+    v.T = T;
+    v.dev_status = dev_status;
+    return launch_rope(a, v, d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_cache_append_rope(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, const void* K, const void* V,
+                               int64_t s_n, int64_t s_h, vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8,
+                               float* sv, vc_batch batch, vc_rope_spec rope, const int32_t* pos, void* Q_out,
+                               int64_t o_sn, int64_t o_sh, int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    if ((st = check_batch_sizes(batch)) != VC_OK) return st;
+    if ((st = check_rope(rope, cache.d)) != VC_OK) return st;
+    if (Hq < 0 || !row_strides_ok(s_n, s_h)) return VC_ERR_INVALID_ARG;
+    if (Hq && (!row_strides_ok(q_sn, q_sh) || !row_strides_ok(o_sn, o_sh))) return VC_ERR_INVALID_ARG;
+    if ((int64_t)batch.T * ((int64_t)Hq + 2 * (int64_t)cache.H) >= (int64_t(1) << 31)) return VC_ERR_UNSUPPORTED;
+    if (batch.T == 0) return VC_OK;
+    if (!K || !V || !aligned16(K) || !aligned16(V)) return VC_ERR_INVALID_ARG;
+    if (Hq && (!Q || !Q_out || !aligned16(Q) || !aligned16(Q_out))) return VC_ERR_INVALID_ARG;
+    RopeRows a;
+    if ((st = rope_rows(rope, pos, 0, &a)) != VC_OK) return st;
+    CacheView v;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    a.Q = static_cast<const uint16_t*>(Q);
+    a.K = static_cast<const uint16_t*>(K);
+    a.V = static_cast<const uint16_t*>(V);
+    a.out = static_cast<uint16_t*>(Q_out);
+    a.q_sn = q_sn;
+    a.q_sh = q_sh;
+    a.k_sn = s_n;
+    a.k_sh = s_h;
+    a.o_sn = o_sn;
+    a.o_sh = o_sh;
+    a.Hq = Hq;
+    return launch_append_rope(a, v, cache.d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------ pages of a cache
+
+static vc_status check_pool(const vc_cache_shape& c, const vc_pool& p, Pool* out) {
+    if (!p.refs || !p.free_pages || !aligned4(p.refs) || !aligned4(p.free_pages)) return VC_ERR_INVALID_ARG;
+    if (c.pages > (1 << 30)) return VC_ERR_UNSUPPORTED;
+    out->refs = p.refs;
+    out->free = p.free_pages;
+    return VC_OK;
+}
+
+// Pieces of a page are counted in 32 bits.
+static vc_status check_page_bytes(const vc_cache_shape& c) {
+    return (int64_t)c.H * c.page_size * c.d >= (int64_t(1) << 31) ? VC_ERR_UNSUPPORTED : VC_OK;
+}
+
+static vc_status check_table(const vc_cache_shape& c, const int32_t* table, int64_t s_table, int rows, int cols) {
+    if (!table || !aligned4(table) || rows < 1 || cols < 1 || s_table < cols) return VC_ERR_INVALID_ARG;
+    if ((int64_t)cols * c.page_size >= (int64_t(1) << 30)) return VC_ERR_UNSUPPORTED;
+    return VC_OK;
+}
+
+static bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uint64_t)m * 4 && y < x + (uint64_t)n * 4;
+}
+
+size_t vc_pages_reserve_workspace(vc_cache_shape cache, int B, int T) {
+    if (check_cache_shape(cache) != VC_OK || B < 1 || T < 1) return 0;
+    return pages_reserve_workspace(B, T, __builtin_ctz((unsigned)cache.page_size));
+}
+
+vc_status vc_pages_reserve(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8, float* sv, vc_pool pool,
+                           vc_batch batch, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    if ((st = check_batch_sizes(batch)) != VC_OK) return st;
+    Pool p;
+    if ((st = check_pool(cache, pool, &p)) != VC_OK || (st = check_page_bytes(cache)) != VC_OK) return st;
+    if (batch.T == 0) return VC_OK;
+    CacheView v;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    if (!workspace_ok(workspace, workspace_bytes, pages_reserve_workspace(v.B, v.T, v.page_log2))) return VC_ERR_WORKSPACE;
+    return launch_pages_reserve(v, cache.d, p, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_pages_fork(vc_cache_shape cache, vc_pool pool, const int32_t* table, int64_t s_table, int B, int cols,
+                        const int32_t* kv_len, const int32_t* parents, const int32_t* lens, int N, int32_t* new_table,
+                        int64_t s_new, int new_cols, int32_t* new_len, int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    Pool p;
+    if ((st = check_pool(cache, pool, &p)) != VC_OK) return st;
+    if (N < 0) return VC_ERR_INVALID_ARG;
+    if (N == 0) return VC_OK;
+    if ((st = check_table(cache, table, s_table, B, cols)) != VC_OK) return st;
+    if ((st = check_table(cache, new_table, s_new, N, new_cols)) != VC_OK) return st;
+    if (!kv_len || !parents || !new_len || !aligned4(kv_len) || !aligned4(parents) || !aligned4(lens) || !aligned4(new_len))
+        return VC_ERR_INVALID_ARG;
+    if (overlap(table, (B - 1) * s_table + cols, new_table, (N - 1) * s_new + new_cols) || overlap(kv_len, B, new_len, N))
+        return VC_ERR_INVALID_ARG;
+    ForkArgs f;
+    f.table_in = table;
+    f.kv_in = kv_len;
+    f.parents = parents;
+    f.lens = lens;
+    f.table_out = new_table;
+    f.kv_out = new_len;
+    f.s_in = s_table;
+    f.s_out = s_new;
+    f.B = B;
+    f.cols_in = cols;
+    f.cols_out = new_cols;
+    f.pages = cache.pages;
+    f.page_log2 = __builtin_ctz((unsigned)cache.page_size);
+    f.dev_status = dev_status;
+    return launch_pages_fork(f, p, N, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_pages_trim(vc_cache_shape cache, vc_pool pool, int32_t* table, int64_t s_table, int B, int cols,
+                        int32_t* kv_len, const int32_t* lens, int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    Pool p;
+    if ((st = check_pool(cache, pool, &p)) != VC_OK) return st;
+    if ((st = check_table(cache, table, s_table, B, cols)) != VC_OK) return st;
+    if (!kv_len || !lens || !aligned4(kv_len) || !aligned4(lens)) return VC_ERR_INVALID_ARG;
+    TrimArgs t;
+    t.table = table;
+    t.kv_len = kv_len;
+    t.lens = lens;
+    t.s_table = s_table;
+    t.cols = cols;
+    t.pages = cache.pages;
+    t.page_log2 = __builtin_ctz((unsigned)cache.page_size);
+    t.dev_status = dev_status;
+    return launch_pages_trim(t, p, B, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t vc_pages_compact_workspace(vc_cache_shape cache) {
+    return check_cache_shape(cache) == VC_OK ? pages_compact_workspace(cache.pages) : 0;
+}
+
+vc_status vc_pages_compact(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8, float* sv, vc_pool pool,
+                           int32_t* table, int64_t s_table, int B, int cols, int32_t* used, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_cache_shape(cache);
+    if (st != VC_OK) return st;
+    Pool p;
+    if ((st = check_pool(cache, pool, &p)) != VC_OK || (st = check_page_bytes(cache)) != VC_OK) return st;
+    if ((st = check_table(cache, table, s_table, B, cols)) != VC_OK) return st;
+    if (!aligned4(used)) return VC_ERR_INVALID_ARG;
+    const vc_batch batch{table, table, table, B, 0, cols, s_table};  // no tokens: cu and kv_len are not read
+    CacheView v;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    if (!workspace_ok(workspace, workspace_bytes, pages_compact_workspace(cache.pages))) return VC_ERR_WORKSPACE;
+    return launch_pages_compact(v, cache.d, p, used, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_cache_copy(vc_cache_shape source, const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                        vc_cache_shape target, uint8_t* K8_to, float* sk_to, uint8_t* V8_to, float* sv_to,
+                        const int32_t* from, const int32_t* to, int N, int32_t* dev_status, vc_stream_t stream) {
+    vc_status st = check_cache_shape(source);
+    if (st != VC_OK || (st = check_cache_shape(target)) != VC_OK) return st;
+    if (source.page_size != target.page_size || source.H != target.H || source.d != target.d || N < 0)
+        return VC_ERR_INVALID_ARG;
+    if ((st = check_page_bytes(source)) != VC_OK) return st;
+    if (N == 0) return VC_OK;
+    if (!from || !to || !aligned4(from) || !aligned4(to)) return VC_ERR_INVALID_ARG;
+    const vc_batch none{from, from, from, 1, 0, 1, 1};  // no batch: not read
+    CacheView s, t;
+    if ((st = cache_view(source, K8, sk, V8, sv, none, dev_status, &s)) != VC_OK ||
+        (st = cache_view(target, K8_to, sk_to, V8_to, sv_to, none, dev_status, &t)) != VC_OK)
+        return st;
+    return launch_cache_copy(s, t, source.d, from, to, N, reinterpret_cast<cudaStream_t>(stream));
 }
 
 static vc_status check_paged_heads(const vc_cache_shape& c, int Hq, int T, int max_q) {

@@ -29,23 +29,6 @@ struct RowArgs {
     int64_t s_n, s_h;
 };
 
-// The sequence of row `tok`: the last b with cu[b] <= tok.  W lanes (a group
-// with mask `mask`) probe W places a round, so B <= W^2 takes two rounds.
-template <int W>
-__device__ __forceinline__ int find_seq(const CacheView& c, int tok, int sub, unsigned mask) {
-    int lo = 0, hi = c.B;  // the answer lies in [lo, hi)
-    while (hi - lo > 1) {
-        const int step = (hi - lo + W - 1) / W;
-        const int at = lo + sub * step;
-        const bool le = at < hi && __ldg(c.cu + at) <= tok;
-        const unsigned votes = (__ballot_sync(mask, le) & mask) >> (__ffs(mask) - 1);
-        const int k = max(31 - __clz((int)(votes | 1u)), 0);
-        lo += k * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
-
 // Where row (tok, h) of the call lies: the element offsets of its codes and
 // its scale.  False where the row belongs to no sequence (*found = false too),
 // has a negative position or a page that is not there.

@@ -105,4 +105,60 @@ vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void*
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, void* ws, cudaStream_t st);
 
+// rotary positions (vc_rope.cu)
+struct RopeRows {
+    const uint16_t* Q;             // rows to turn (and the queries of an append)
+    const uint16_t* K;
+    const uint16_t* V;
+    uint16_t* out;
+    int64_t q_sn, q_sh, k_sn, k_sh, o_sn, o_sh;
+    const int64_t* turns;          // [rot / 2] turns a position, as fractions of 2^64
+    const int32_t* pos;            // [T], or null: the positions in the cache
+    int Hq, rot, pairs;            // rows of a token in Q, turned channels, layout
+    float magnitude, sign;         // what cos and sin are multiplied by
+};
+vc_status launch_rope(const RopeRows& a, const CacheView& c, int d, cudaStream_t st);
+vc_status launch_append_rope(const RopeRows& a, const CacheView& c, int d, cudaStream_t st);
+
+// pages of a cache (vc_pages.cu)
+struct Pool {
+    int32_t* refs;                 // [pages] table entries that name a page
+    uint32_t* free;                // a bit for each page that none names
+};
+struct ForkArgs {
+    const int32_t* table_in;
+    const int32_t* kv_in;
+    const int32_t* parents;
+    const int32_t* lens;           // or null: the parents' lengths
+    int32_t* table_out;
+    int32_t* kv_out;
+    int64_t s_in, s_out;
+    int B, cols_in, cols_out, pages, page_log2;
+    int32_t* dev_status;
+};
+struct TrimArgs {
+    int32_t* table;
+    int32_t* kv_len;
+    const int32_t* lens;
+    int64_t s_table;
+    int cols, pages, page_log2;
+    int32_t* dev_status;
+};
+struct ReserveWs {                 // entry w of the call: its page, what becomes of it, the w-th new page;
+    int32_t *page, *cls, *fresh;   // sequence b: what is to be copied, its first entry
+    int32_t *from, *to, *off;
+};
+struct CompactWs {
+    int32_t *head, *number, *from, *to;  // pages in use and to move; a page's place in the lists; the lists
+};
+vc_status launch_pages_fork(const ForkArgs& f, const Pool& pool, int N, cudaStream_t st);
+vc_status launch_pages_trim(const TrimArgs& t, const Pool& pool, int B, cudaStream_t st);
+size_t pages_reserve_workspace(int B, int T, int page_log2);
+vc_status launch_pages_reserve(const CacheView& c, int d, const Pool& pool, void* workspace, cudaStream_t st);
+vc_status launch_cache_copy(const CacheView& s, const CacheView& t, int d, const int32_t* from, const int32_t* to,
+                            int count, cudaStream_t st);
+size_t pages_compact_workspace(int pages);
+vc_status launch_pages_compact(const CacheView& c, int d, const Pool& pool, int32_t* count, void* workspace,
+                               cudaStream_t st);
+
 }  // namespace vc

@@ -42,6 +42,48 @@ __device__ __forceinline__ int page_of(const CacheView& c, int b, int p) {
     return (pg >= 0 && pg < c.pages) ? pg : -1;
 }
 
+// The sequence of row `tok`: the last b with cu[b] <= tok.  W lanes (a group
+// with mask `mask`) probe W places a round, so B <= W^2 takes two rounds.
+template <int W>
+__device__ __forceinline__ int find_seq(const CacheView& c, int tok, int sub, unsigned mask) {
+    int lo = 0, hi = c.B;  // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + W - 1) / W;
+        const int at = lo + sub * step;
+        const bool le = at < hi && __ldg(c.cu + at) <= tok;
+        const unsigned votes = (__ballot_sync(mask, le) & mask) >> (__ffs(mask) - 1);
+        const int k = max(31 - __clz((int)(votes | 1u)), 0);
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// Eight fp32 values of a row that W lanes share -> eight codes; the row's scale.  The largest
+// magnitude comes from the bit patterns with the sign off, which order like the magnitudes and put
+// infinities and NaN above every number.
+template <int W>
+__device__ __forceinline__ uint2 quantize_row8(const float (&x)[8], unsigned mask, float* scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
+    const float amax = __uint_as_float(top);
+    if (top >= 0x7F800000u || amax < 0x1p-100f) {
+        *scale = top >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : 0.f;
+        return make_uint2(0u, 0u);
+    }
+    *scale = __fdiv_rn(amax, 448.f);
+    const float inv = __fdiv_rn(448.f, amax);
+    uint32_t o[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        o[i] = cvt_e4m3x2(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv)) |
+               (cvt_e4m3x2(__fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv)) << 16);
+    return make_uint2(o[0], o[1]);
+}
+
 // ------------------------------------------------------------ work of the attention kernels
 //
 // The rows of a sequence for one key/value head are its n * G (token, query

@@ -6,6 +6,7 @@ fallback: if the library has not been built, every call raises.
 """
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -15,7 +16,7 @@ LIB_PATH = os.path.join(_PKG, "libvc_gb300.so")
 BLOCK = 128
 
 STATUS = {0: "VC_OK", 1: "VC_ERR_INVALID_ARG", 2: "VC_ERR_UNSUPPORTED", 3: "VC_ERR_WORKSPACE",
-          4: "VC_ERR_CUDA", 5: "VC_ERR_TIMEOUT"}
+          4: "VC_ERR_CUDA", 5: "VC_ERR_TIMEOUT", 6: "VC_ERR_PAGES"}
 
 
 class VcError(RuntimeError):
@@ -38,6 +39,14 @@ class VcCacheShape(ctypes.Structure):
 class VcBatch(ctypes.Structure):
     _fields_ = [("cu", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
                 ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("cols", ctypes.c_int32), ("s_table", ctypes.c_int64)]
+
+
+class VcRopeSpec(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+
+
+class VcPool(ctypes.Structure):
+    _fields_ = [("refs", ctypes.c_void_p), ("free_pages", ctypes.c_void_p)]
 
 
 _lib = None
@@ -98,6 +107,27 @@ def lib():
         L.vc_attn_paged.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp, _vp, _vp,
                                     _vp, VcBatch, ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp,
                                     ctypes.c_int64, ctypes.c_int64, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        i32, i64 = ctypes.c_int, ctypes.c_int64
+        L.vc_rope.restype = i32
+        L.vc_rope.argtypes = [_vp, i64, i64, i32, i32, i32, VcRopeSpec, _vp, _vp, _vp, i32, i32, _vp, i64, i64, _vp, _vp]
+        L.vc_cache_append_rope.restype = i32
+        L.vc_cache_append_rope.argtypes = [_vp, i64, i64, i32, _vp, _vp, i64, i64, VcCacheShape, _vp, _vp, _vp, _vp, VcBatch,
+                                           VcRopeSpec, _vp, _vp, i64, i64, _vp, _vp]
+        L.vc_pages_reserve_workspace.restype = ctypes.c_size_t
+        L.vc_pages_reserve_workspace.argtypes = [VcCacheShape, i32, i32]
+        L.vc_pages_reserve.restype = i32
+        L.vc_pages_reserve.argtypes = [VcCacheShape, _vp, _vp, _vp, _vp, VcPool, VcBatch, _vp, ctypes.c_size_t, _vp, _vp]
+        L.vc_pages_fork.restype = i32
+        L.vc_pages_fork.argtypes = [VcCacheShape, VcPool, _vp, i64, i32, i32, _vp, _vp, _vp, i32, _vp, i64, i32, _vp, _vp, _vp]
+        L.vc_pages_trim.restype = i32
+        L.vc_pages_trim.argtypes = [VcCacheShape, VcPool, _vp, i64, i32, i32, _vp, _vp, _vp, _vp]
+        L.vc_pages_compact_workspace.restype = ctypes.c_size_t
+        L.vc_pages_compact_workspace.argtypes = [VcCacheShape]
+        L.vc_pages_compact.restype = i32
+        L.vc_pages_compact.argtypes = [VcCacheShape, _vp, _vp, _vp, _vp, VcPool, _vp, i64, i32, i32, _vp, _vp,
+                                       ctypes.c_size_t, _vp, _vp]
+        L.vc_cache_copy.restype = i32
+        L.vc_cache_copy.argtypes = [VcCacheShape, _vp, _vp, _vp, _vp, VcCacheShape, _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp, _vp]
         L.vc_debug_attn_paged_timeout.restype = ctypes.c_int
         L.vc_debug_attn_paged_timeout.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp,
                                                   _vp, _vp, _vp, VcBatch, ctypes.c_int, _vp, ctypes.c_int64,
@@ -566,6 +596,279 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
                 O.data_ptr(), *o_strides, lse.data_ptr(), workspace.data_ptr(),
                 workspace.numel() * workspace.element_size(), status), "vc_attn_paged")
     return O, lse
+
+
+# ------------------------------------------------------------ rotary positions
+
+_LAYOUTS = {"halves": 0, "pairs": 1}
+
+
+def make_rope(rot, base=10000.0, layout="halves", scaling="none", factor=1.0, original=4096, slow=1.0, fast=32.0,
+              magnitude=None, device="cuda"):
+    """The angles of vc_rope and vc_cache_append_rope: a dict of turns (int64 [rot/2], turns a position as 64-bit
+    fractions), layout and magnitude.
+
+    rot: turned channels of a head (a multiple of 16).  layout "halves": pair i is channels (i, i + rot/2),
+    "pairs": (2i, 2i + 1).  Pair i turns by w_i = base^(-2i/rot) radians a position, computed in fp64;
+    scaling, for contexts `factor` times as long as the `original` ones:
+      "positions"  w_i / factor;
+      "base"       base times factor^(rot / (rot - 2)), so that the slowest pair turns 1/factor as fast;
+      "ramp"       pairs that turn `fast` times or more over the original positions stay, those that turn `slow`
+                   times or less are divided by factor, linear in the turns between, and magnitude is
+                   0.1 ln factor + 1 unless it is given (1 for the others).
+    A dict with other turns, made by hand, does as well."""
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be 'halves' or 'pairs'")
+    if rot < 16 or rot % 16:
+        raise ValueError("rot must be a multiple of 16")
+    if not (base > 0 and factor > 0 and original > 0 and fast > slow):
+        raise ValueError("base, factor and original must be positive, fast above slow")
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2.0))
+    w = base ** (torch.arange(rot // 2, dtype=torch.float64) * (-2.0 / rot))
+    if scaling == "positions":
+        w = w / factor
+    elif scaling == "ramp":
+        keep = ((original * w / (2.0 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        w = w * keep + w / factor * (1.0 - keep)
+        magnitude = 0.1 * math.log(factor) + 1.0 if magnitude is None else magnitude
+    elif scaling not in ("none", "base"):
+        raise ValueError("scaling must be 'none', 'positions', 'base' or 'ramp'")
+    turns = torch.round(torch.remainder(w / (2.0 * math.pi), 1.0) * 2.0 ** 62).to(torch.int64) << 2
+    return dict(turns=turns.to(device), layout=layout, magnitude=1.0 if magnitude is None else float(magnitude))
+
+
+def _rope_spec(rope, dev):
+    turns = rope["turns"]
+    if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous() or turns.numel() < 1:
+        raise ValueError("rope's turns must be contiguous int64 [rot/2]")
+    if turns.get_device() != dev:
+        raise ValueError("rope's turns are not on the rows' device")
+    if rope["layout"] not in _LAYOUTS:
+        raise ValueError("rope's layout must be 'halves' or 'pairs'")
+    return VcRopeSpec(turns.data_ptr(), 2 * turns.shape[0], _LAYOUTS[rope["layout"]], rope["magnitude"])
+
+
+def _int32_vector(name, t, n, dev):
+    """Checks an int32 vector of n elements: its pointer."""
+    if t.dtype is not _I32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be contiguous int32 [%d]" % (name, n))
+    if t.get_device() != dev:
+        raise ValueError("%s is not on the other tensors' device" % name)
+    return t.data_ptr()
+
+
+def vc_rope(X, rope, pos=None, cu=None, kv_len=None, inverse=0, out=None, dev_status=None, stream=None):
+    """X (bf16 [T, H, d]) turned by its rows' positions, for a `rope` of make_rope: pos int32 [T], or those of a
+    batch (cu, kv_len as in vc_cache_append; rows of no sequence stay as they are in `out`).
+    inverse=1: the transposed map, as for the gradient.  out: X itself to turn it in place."""
+    L = lib()
+    if X.dim() != 3:
+        raise ValueError("X must be bf16 [T, H, d]")
+    T, H, d = X.shape
+    dev = X.get_device()
+    strides = _rows("X", X, H, d, dev)
+    spec = _rope_spec(rope, dev)
+    if pos is None and cu is None:
+        raise ValueError("vc_rope needs pos, or cu and kv_len")
+    if (cu is None) != (kv_len is None):
+        raise ValueError("cu and kv_len belong together")
+    at = None if pos is None else _int32_vector("pos", pos, T, dev)
+    B = 0 if cu is None else kv_len.numel()
+    batch = (None, None) if cu is None else (_int32_vector("cu", cu, B + 1, dev), _int32_vector("kv_len", kv_len, B, dev))
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_rope, X, rope, pos, cu, kv_len, inverse, out, dev_status)
+    if out is None:
+        out = torch.empty((T, H, d), dtype=_BF16, device=dev)
+        o_strides = (H * d, d)
+    else:
+        o_strides = _rows("out", out, H, d, dev)
+        if out.shape[0] != T:
+            raise ValueError("out must have X's shape")
+    _on_device(dev, stream, L.vc_rope, (X.data_ptr(), *strides, T, H, d, spec, at, *batch, B, inverse, out.data_ptr(),
+                                        *o_strides, status), "vc_rope")
+    return out
+
+
+def vc_cache_append_rope(Q, K, V, cache, cu, kv_len, table, rope, pos=None, out=None, dev_status=None, stream=None):
+    """What comes before a step's attention, in one launch: returns Q (bf16 [T, Hq, d], or None) turned as by
+    vc_rope, and quantizes the turned K and V (bf16 [T, H, d]) into the pages of `cache` as vc_cache_append does.
+    pos int32 [T]: other positions to turn by than the tokens' places in the cache.  out: where the turned
+    queries go (Q itself: in place)."""
+    L = lib()
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    strides = _rows("K", K, s.H, s.d, dev)
+    if V.shape != K.shape or _rows("V", V, s.H, s.d, dev) != strides:
+        raise ValueError("K and V must share shape and strides")
+    T = K.shape[0]
+    Hq, q_strides, o_strides = 0, (0, 0), (0, 0)
+    if Q is not None:
+        if Q.dim() != 3 or Q.shape[0] != T:
+            raise ValueError("Q must be bf16 [%d, Hq, %d]" % (T, s.d))
+        Hq = Q.shape[1]
+        q_strides = _rows("Q", Q, Hq, s.d, dev)
+    elif out is not None:
+        raise ValueError("out without Q")
+    batch = _batch_of(cu, kv_len, table, T, dev)
+    spec = _rope_spec(rope, dev)
+    at = None if pos is None else _int32_vector("pos", pos, T, dev)
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_cache_append_rope, Q, K, V, cache, cu, kv_len, table, rope, pos, out, dev_status)
+    if out is not None:
+        o_strides = _rows("out", out, Hq, s.d, dev)
+        if out.shape[0] != T:
+            raise ValueError("out must have Q's shape")
+    elif Q is not None:
+        out = torch.empty((T, Hq, s.d), dtype=_BF16, device=dev)
+        o_strides = (Hq * s.d, s.d)
+    _on_device(dev, stream, L.vc_cache_append_rope,
+               (None if Q is None else Q.data_ptr(), *q_strides, Hq, K.data_ptr(), V.data_ptr(), *strides, s, K8, sk, V8, sv,
+                batch, spec, at, None if out is None else out.data_ptr(), *o_strides, status), "vc_cache_append_rope")
+    return out
+
+
+# ------------------------------------------------------------ pages of a cache
+
+
+def alloc_pool(pages, device):
+    """The state of a cache's pages, all free: dict of refs (int32 [pages], table entries that name a page) and free
+    (int32 words, a bit for each page that none names).  Tables of the pool begin as -1."""
+    bits = torch.full((-(-pages // 32),), -1, dtype=_I32, device=device)
+    if pages % 32:
+        bits[-1] = (1 << pages % 32) - 1
+    return dict(refs=torch.zeros(pages, dtype=_I32, device=device), free=bits)
+
+
+def _pool_of(pool, pages, dev) -> VcPool:
+    return VcPool(_int32_vector("refs", pool["refs"], pages, dev), _int32_vector("free", pool["free"], -(-pages // 32), dev))
+
+
+def _table_of(name, table, dev):
+    """Checks an int32 [rows, cols] table: its pointer and what the C calls take beside it (stride, rows, cols)."""
+    if table.dtype is not _I32 or table.dim() != 2:
+        raise ValueError("%s must be int32 [rows, cols]" % name)
+    if table.get_device() != dev:
+        raise ValueError("%s is not on the cache's device" % name)
+    (rows, cols), (s, one) = table.shape, table.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    return table.data_ptr(), s if rows > 1 else max(cols, 1), rows, cols
+
+
+def pages_reserve_workspace_bytes(cache, B, T) -> int:
+    return lib().vc_pages_reserve_workspace(cache_shape_of(cache), B, T)
+
+
+def pages_compact_workspace_bytes(cache) -> int:
+    return lib().vc_pages_compact_workspace(cache_shape_of(cache))
+
+
+def _given_workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=_U8, device=dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    return workspace
+
+
+def _launch_side(stream, call):
+    """call(), which returns nothing to the caller but may make a workspace, with `stream` as the current one."""
+    with torch.cuda.stream(stream):
+        call()
+
+
+def vc_pages_reserve(cache, pool, cu, kv_len, table, T, workspace=None, dev_status=None, stream=None):
+    """Pages of their own for the tokens of a call (cu, kv_len, table as that call gets them, T rows in all): entries of
+    -1 in `table` get the lowest free pages of `pool` (see alloc_pool), pages that others name too are replaced by a
+    copy.  With too few free pages nothing is taken and dev_status becomes 6 (VC_ERR_PAGES)."""
+    L = lib()
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    batch = _batch_of(cu, kv_len, table, T, dev)
+    p = _pool_of(pool, s.pages, dev)
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _launch_side(stream, lambda: vc_pages_reserve(cache, pool, cu, kv_len, table, T, workspace, dev_status))
+    workspace = _given_workspace(workspace, L.vc_pages_reserve_workspace(s, batch.B, T), dev)
+    _on_device(dev, stream, L.vc_pages_reserve, (s, K8, sk, V8, sv, p, batch, workspace.data_ptr(),
+                                                 workspace.numel() * workspace.element_size(), status), "vc_pages_reserve")
+
+
+def vc_pages_fork(cache, pool, table, kv_len, parents, new_table, new_len, lens=None, dev_status=None, stream=None):
+    """Rows of new_table (int32 [N, cols]) and new_len (int32 [N]) become sequences that name the pages of the first
+    lens[i] tokens (all of them without lens) of sequence parents[i] of `table`; parents[i] = -1: an empty one.
+    Nothing is copied before vc_pages_reserve.  What the rows held is not given back: vc_pages_trim does that."""
+    L = lib()
+    s, _, dev = _cache_parts(cache)
+    p = _pool_of(pool, s.pages, dev)
+    at, s_table, B, cols = _table_of("table", table, dev)
+    to, s_new, N, new_cols = _table_of("new_table", new_table, dev)
+    args = (s, p, at, s_table, B, cols, _int32_vector("kv_len", kv_len, B, dev), _int32_vector("parents", parents, N, dev),
+            None if lens is None else _int32_vector("lens", lens, N, dev), N, to, s_new, new_cols,
+            _int32_vector("new_len", new_len, N, dev), _status_ptr(dev_status, dev))
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    _on_device(dev, stream, L.vc_pages_fork, args, "vc_pages_fork")
+
+
+def vc_pages_trim(cache, pool, table, kv_len, lens, dev_status=None, stream=None):
+    """Each sequence keeps the pages of its first lens[b] tokens (int32 [B]; 0 ends it, a negative one leaves it
+    alone): its other entries of `table` become -1, kv_len at most lens."""
+    L = lib()
+    s, _, dev = _cache_parts(cache)
+    p = _pool_of(pool, s.pages, dev)
+    at, s_table, B, cols = _table_of("table", table, dev)
+    args = (s, p, at, s_table, B, cols, _int32_vector("kv_len", kv_len, B, dev), _int32_vector("lens", lens, B, dev),
+            _status_ptr(dev_status, dev))
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    _on_device(dev, stream, L.vc_pages_trim, args, "vc_pages_trim")
+
+
+def vc_pages_compact(cache, pool, table, used=None, workspace=None, dev_status=None, stream=None):
+    """Moves the pages in use to the lowest numbers and renames them in `table`, which has to hold all entries of the
+    pool.  Returns how many are in use (int32 [1] on the device): the pages from there on are free."""
+    L = lib()
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    p = _pool_of(pool, s.pages, dev)
+    at, s_table, B, cols = _table_of("table", table, dev)
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_pages_compact, cache, pool, table, used, workspace, dev_status)
+    if used is None:
+        used = torch.empty(1, dtype=_I32, device=dev)
+    out = _int32_vector("used", used, 1, dev)
+    workspace = _given_workspace(workspace, L.vc_pages_compact_workspace(s), dev)
+    _on_device(dev, stream, L.vc_pages_compact,
+               (s, K8, sk, V8, sv, p, at, s_table, B, cols, out, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), status), "vc_pages_compact")
+    return used
+
+
+def vc_cache_copy(source, target, from_pages, to_pages, dev_status=None, stream=None):
+    """Copies whole pages: from_pages[i] of `source` to to_pages[i] of `target` (int32 [N]; a -1 leaves the pair out),
+    caches of one page size, heads and channels, or one cache."""
+    L = lib()
+    s, parts, dev = _cache_parts(source)
+    t, to_parts, to_dev = _cache_parts(target)
+    if to_dev != dev:
+        raise ValueError("the caches are on different devices")
+    N = from_pages.numel()
+    args = (s, *parts, t, *to_parts, _int32_vector("from_pages", from_pages, N, dev), _int32_vector("to_pages", to_pages, N, dev), N,
+            _status_ptr(dev_status, dev))
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    _on_device(dev, stream, L.vc_cache_copy, args, "vc_cache_copy")
+    return target
 
 
 def vc_debug_e4m3_encode(x: torch.Tensor, out=None, stream=None):

@@ -55,7 +55,8 @@ typedef enum {
     VC_ERR_UNSUPPORTED = 2, /* d not in {64, 128}, k outside [1, 1024], N > 2^24 */
     VC_ERR_WORKSPACE = 3,   /* workspace pointer null or smaller than the query says */
     VC_ERR_CUDA = 4,        /* a CUDA launch or driver call failed */
-    VC_ERR_TIMEOUT = 5      /* a bounded device wait ran out (written to *dev_status) */
+    VC_ERR_TIMEOUT = 5,     /* a bounded device wait ran out (written to *dev_status) */
+    VC_ERR_PAGES = 6        /* a pool has too few free pages (written to *dev_status) */
 } vc_status;
 
 /*
@@ -489,6 +490,156 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
                         float softmax_scale, int causal, int window, int max_q, void* O, int64_t o_sn,
                         int64_t o_sh, float* lse, void* workspace, size_t workspace_bytes,
                         int32_t* dev_status, vc_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  The pairs' frequencies are the caller's, so every way to
+ * stretch a context is a matter of the numbers in `turns`; no table of angles
+ * is read, and far positions are as exact as near ones.
+ */
+typedef struct {
+    const int64_t* turns; /* device int64 [rot/2], 8-byte aligned: turns a position of each pair, the fraction
+                             w - floor(w) times 2^64 (as an unsigned number); position p turns pair i by
+                             (p turns[i] mod 2^64) 2^-64 of a turn, exact for every p */
+    int32_t rot;          /* turned channels, the first of a head: a multiple of 16, 16 .. d; the others stay */
+    int32_t layout;       /* 0, halves: pair i is channels (i, i + rot/2); 1, pairs: channels (2i, 2i + 1) */
+    float magnitude;      /* m > 0, finite: what the turned channels are multiplied by */
+} vc_rope_spec;
+
+/*
+ * Turns rows by their positions:  with a the pair's angle, c = m cos a and s = m sin a in fp32,
+ *   y0 = x0 c - x1 s,  y1 = x0 s + x1 c,   each rounded to bf16 once.
+ *   X        bf16 [T, H, d], element strides s_n, s_h (positive multiples of 8, channel stride 1),
+ *            16-byte aligned.
+ *   pos      int32 [T], any positions, or NULL: then those that the batch gives (below).
+ *   cu, kv_len  int32 [B+1] and [B] of a batch as in vc_batch, kv_len up to 2^30 - 1, or both NULL
+ *            (with pos only): row cu[b] + i is at position kv_len[b] - n_b + i.  Where they are
+ *            given, rows of no sequence stay as they are in `out`, with pos too.
+ *   inverse  1: s = -m sin a, the transposed map: with m = 1 it takes vc_rope back, and the gradient
+ *            of a loss in X is vc_rope with inverse = 1 of its gradient in `out`.
+ *   out      bf16 [T, H, d], strides o_sn, o_sh as X's, 16-byte aligned: X itself with X's strides,
+ *            or not overlapping it.
+ * A row that is not finite gives what the formula gives.  T = 0 does nothing.
+ * Errors, before any launch: VC_ERR_INVALID_ARG (a null or misaligned pointer, a stride or size out
+ * of the ranges above, inverse not in {0, 1}, rot, layout or magnitude out of theirs, neither pos
+ * nor cu and kv_len, B < 1 with cu), VC_ERR_UNSUPPORTED (d not 64 or 128, T * H >= 2^31);
+ * VC_ERR_CUDA if a launch fails.  cu or kv_len that break their rules are clamped and reported
+ * through *dev_status as for the cache.
+ */
+vc_status vc_rope(const void* X, int64_t s_n, int64_t s_h, int T, int H, int d, vc_rope_spec rope,
+                  const int32_t* pos, const int32_t* cu, const int32_t* kv_len, int B, int inverse,
+                  void* out, int64_t o_sn, int64_t o_sh, int32_t* dev_status, vc_stream_t stream);
+
+/*
+ * What a step does before its attention, in one launch: the queries turned (Q_out = vc_rope(Q)),
+ * and vc_cache_append of the turned keys and of the values.  The keys are quantized from the
+ * turned fp32 values, not rounded to bf16 in between; values and their scales are as
+ * vc_cache_append writes them, bit for bit.
+ *   Q, Q_out bf16 [T, Hq, d] as X and out of vc_rope; Hq = 0: no queries (the pointers may be NULL).
+ *   pos      int32 [T], or NULL: the tokens' positions in the cache, kv_len[b] - n_b + i.
+ * Where a token is written does not depend on pos.  A key row whose turned values are not all
+ * finite numbers is written as zeros with a NaN scale, as vc_cache_append does with such rows.
+ * Everything else as vc_cache_append and vc_rope; VC_ERR_UNSUPPORTED for T (Hq + 2 H) >= 2^31.
+ */
+vc_status vc_cache_append_rope(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, const void* K, const void* V,
+                               int64_t s_n, int64_t s_h, vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8,
+                               float* sv, vc_batch batch, vc_rope_spec rope, const int32_t* pos, void* Q_out,
+                               int64_t o_sn, int64_t o_sh, int32_t* dev_status, vc_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of a cache.  A pool says who holds them, in device memory, so that
+ * sequences fork, grow and end without the host, also in captured graphs.
+ *
+ * The entries of all tables of a pool name its pages: -1 none, p >= 0 page p.
+ * An entry -2 - p holds page p without the right to write it (see
+ * vc_pages_reserve); the cache's other calls take it for a page that is not
+ * there.  A new pool has refs = 0 and all pages' bits set, and tables of -1.
+ * The page calls keep both up to date; the state that they leave depends on
+ * what was called, not on the order of anything inside a call.
+ */
+typedef struct {
+    int32_t* refs;        /* int32 [pages]: entries that name the page */
+    uint32_t* free_pages; /* uint32 [ceil(pages/32)], 4-byte aligned: bit p % 32 of word p / 32 is set where
+                             there is none; bits behind the last page are not looked at */
+} vc_pool;
+
+/*
+ * Pages for a call's tokens, before they are written: after it the positions
+ * kv_len[b] - n_b .. kv_len[b] - 1 of every sequence lie in pages that it alone names
+ * (vc_batch as the calls after it get it, with its table's entries written by this one;
+ * batch.T is what bounds cu).  An entry of -1 there gets a new page.  One whose page others
+ * name too gets a new page as well, into which what the old one holds of the positions before
+ * is copied; if all that name a page are entries that this call writes, the last of them, in
+ * the order of the sequences and their positions, keeps it.  New pages are the lowest free
+ * ones, in that order.
+ *   If the pool has too few, none is taken: VC_ERR_PAGES is written to *dev_status, the counts
+ * stay, and entries that needed a copy become -2 - p, so that what follows in the stream writes
+ * into no page of others (it finds a page that is not there, which it reports); calling again
+ * with enough free pages makes up for it, and vc_pages_trim frees such a page like any other.
+ *   Nothing at all is done for a batch that breaks its rules (reported).  kv_len[b] < n_b counts
+ * the positions from 0 on.
+ *   workspace  >= vc_pages_reserve_workspace(cache, B, T) bytes, 256-byte aligned.
+ * Errors as vc_cache_append (without K and V), VC_ERR_INVALID_ARG for a null or misaligned pool,
+ * VC_ERR_UNSUPPORTED for pages > 2^30 or H * page_size * d >= 2^31, VC_ERR_WORKSPACE.
+ */
+size_t vc_pages_reserve_workspace(vc_cache_shape cache, int B, int T);
+vc_status vc_pages_reserve(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8, float* sv, vc_pool pool,
+                           vc_batch batch, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           vc_stream_t stream);
+
+/*
+ * Sequences that begin as others are: row i of new_table names the pages of the first len_i
+ * tokens of sequence parents[i] of `table`, -1 behind them, and new_len[i] = len_i =
+ * min(lens[i], kv_len[parents[i]]) (lens NULL: the parent's length).  No data is copied: the page
+ * that a fork ends in is shared too, until vc_pages_reserve of one that goes on.  parents[i] = -1
+ * makes an empty row.  What the rows of new_table and new_len held before is overwritten, not
+ * given back.  Parents may come several times.
+ *   table    int32 [B, cols], row stride s_table (>= cols); kv_len int32 [B]; parents, lens int32 [N].
+ *   new_table  int32 [N, new_cols], row stride s_new; new_len int32 [N].  The memory from the first
+ *            to the last row of the two tables must not overlap, nor kv_len and new_len.
+ * A parent outside -1 .. B - 1, a length below 0 or beyond either table's columns gives an empty
+ * row, an entry that names no page -1; both are reported.  N = 0 does nothing.
+ * Errors: VC_ERR_INVALID_ARG (null or misaligned pointers, B < 1, N < 0, cols or strides out of
+ * range, overlap), VC_ERR_UNSUPPORTED as vc_pages_reserve and vc_cache_append; VC_ERR_CUDA.
+ */
+vc_status vc_pages_fork(vc_cache_shape cache, vc_pool pool, const int32_t* table, int64_t s_table, int B, int cols,
+                        const int32_t* kv_len, const int32_t* parents, const int32_t* lens, int N, int32_t* new_table,
+                        int64_t s_new, int new_cols, int32_t* new_len, int32_t* dev_status, vc_stream_t stream);
+
+/*
+ * Sequences that end, or are taken back to what they were: sequence b keeps the pages of its
+ * first lens[b] tokens; its other entries become -1, and pages that nobody names any more are
+ * free.  kv_len[b] becomes lens[b] where it was more.  lens[b] = 0 ends the sequence, a negative
+ * one leaves it alone.  An entry that names a page which nobody is counted for, or none, is
+ * reported.  Errors as vc_pages_fork.
+ */
+vc_status vc_pages_trim(vc_cache_shape cache, vc_pool pool, int32_t* table, int64_t s_table, int B, int cols,
+                        int32_t* kv_len, const int32_t* lens, int32_t* dev_status, vc_stream_t stream);
+
+/*
+ * Moves the pages in use together: with U of them, those of numbers from U on go to the free
+ * numbers below U, in ascending order on both sides, with their codes, scales and counts, and the
+ * entries of `table` follow; pages U .. pages - 1 are free then, and U is written to *used (nullable,
+ * device int32).  `table` must hold all entries that name pages of the pool: one that names a page
+ * which nobody is counted for stays and is reported.
+ *   workspace  >= vc_pages_compact_workspace(cache) bytes, 256-byte aligned.
+ * Errors as vc_pages_reserve.
+ */
+size_t vc_pages_compact_workspace(vc_cache_shape cache);
+vc_status vc_pages_compact(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8, float* sv, vc_pool pool,
+                           int32_t* table, int64_t s_table, int B, int cols, int32_t* used, void* workspace,
+                           size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream);
+
+/*
+ * Copies whole pages between caches of one page_size, H and d (strides may differ), or within
+ * one: page from[i] of the source to page to[i] of the target, i < N, int32 in device memory.  A
+ * pair with a -1 is left out, other numbers out of range are reported.  A page that is copied to
+ * must not be in `from` too, nor twice in `to` (the order of the copies is open).
+ * Errors: as vc_cache_append for both caches, VC_ERR_INVALID_ARG for caches of different kind or
+ * N < 0, VC_ERR_UNSUPPORTED for H * page_size * d >= 2^31.
+ */
+vc_status vc_cache_copy(vc_cache_shape source, const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                        vc_cache_shape target, uint8_t* K8_to, float* sk_to, uint8_t* V8_to, float* sv_to,
+                        const int32_t* from, const int32_t* to, int N, int32_t* dev_status, vc_stream_t stream);
 
 /*
  * Test hook for the ExpCast byte check: runs vc_attn_fwd and additionally,
