@@ -9,5 +9,5 @@ does not load the CUDA library; the first call does, and raises if it is
 missing.
 """
 from .vc import (VcError, VcShape, alloc_cache, alloc_pool, alloc_quantized, make_rope, shape_of, vc_attn_fwd,  # noqa: F401
-                 vc_attn_paged, vc_cache_append, vc_cache_append_rope, vc_cache_copy, vc_cache_read, vc_cluster,
-                 vc_pages_compact, vc_pages_fork, vc_pages_reserve, vc_pages_trim, vc_quantize, vc_rope)
+                 vc_attn_paged, vc_attn_paged_shared, vc_cache_append, vc_cache_append_rope,
+                 vc_cache_copy, vc_cache_read, vc_cluster, vc_pages_compact, vc_pages_fork, vc_pages_reserve, vc_pages_trim, vc_quantize, vc_rope)

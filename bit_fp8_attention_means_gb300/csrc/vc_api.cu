@@ -546,11 +546,12 @@ size_t vc_attn_paged_workspace(vc_cache_shape cache, int Hq, int B, int T, int m
     return attn_paged_workspace(cache, Hq, B, T, max_q);
 }
 
-static vc_status attn_paged_call(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache, const uint8_t* K8,
-                                 const float* sk, const uint8_t* V8, const float* sv, vc_batch batch, float softmax_scale,
-                        int causal, int window, int max_q, void* O, int64_t o_sn, int64_t o_sh, float* lse,
-                        void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream,
-                                 int skip_unit) {
+// Checks what the paged attention's calls share and fills the kernels' arguments; *nothing: no rows.
+static vc_status paged_args(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, const vc_cache_shape& cache,
+                            const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                            const vc_batch& batch, float softmax_scale, int causal, int window, int max_q, void* O,
+                            int64_t o_sn, int64_t o_sh, float* lse, int32_t* dev_status, PagedAttn* a, CacheView* v,
+                            bool* nothing) {
     vc_status st = check_cache_shape(cache);
     if (st != VC_OK) return st;
     if ((st = check_batch_sizes(batch)) != VC_OK) return st;
@@ -561,26 +562,39 @@ static vc_status attn_paged_call(const void* Q, int64_t q_sn, int64_t q_sh, int 
         !__builtin_isfinite(scale_log2))
         return VC_ERR_INVALID_ARG;
     if (!row_strides_ok(q_sn, q_sh) || !row_strides_ok(o_sn, o_sh)) return VC_ERR_INVALID_ARG;
-    if (batch.T == 0) return VC_OK;
+    *nothing = batch.T == 0;
+    if (*nothing) return VC_OK;
     if (!Q || !O || !aligned16(Q) || !aligned16(O) || (reinterpret_cast<uintptr_t>(lse) & 3u))
         return VC_ERR_INVALID_ARG;
+    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, v)) != VC_OK) return st;
+    a->Q = static_cast<const uint16_t*>(Q);
+    a->q_sn = q_sn;
+    a->q_sh = q_sh;
+    a->O = static_cast<uint16_t*>(O);
+    a->o_sn = o_sn;
+    a->o_sh = o_sh;
+    a->lse = lse;
+    a->G = Hq / cache.H;
+    a->scale_log2 = scale_log2;
+    a->causal = causal;
+    a->window = window;
+    a->max_q = max_q;
+    return VC_OK;
+}
+
+static vc_status attn_paged_call(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache, const uint8_t* K8,
+                                 const float* sk, const uint8_t* V8, const float* sv, vc_batch batch, float softmax_scale,
+                                 int causal, int window, int max_q, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream,
+                                 int skip_unit) {
+    PagedAttn a{};
     CacheView v;
-    if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    bool nothing = false;
+    const vc_status st = paged_args(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, softmax_scale, causal, window, max_q,
+                                    O, o_sn, o_sh, lse, dev_status, &a, &v, &nothing);
+    if (st != VC_OK || nothing) return st;
     const size_t need = attn_paged_workspace(cache, Hq, batch.B, batch.T, max_q);
     if (need && !workspace_ok(workspace, workspace_bytes, need)) return VC_ERR_WORKSPACE;
-    PagedAttn a;
-    a.Q = static_cast<const uint16_t*>(Q);
-    a.q_sn = q_sn;
-    a.q_sh = q_sh;
-    a.O = static_cast<uint16_t*>(O);
-    a.o_sn = o_sn;
-    a.o_sh = o_sh;
-    a.lse = lse;
-    a.G = Hq / cache.H;
-    a.scale_log2 = scale_log2;
-    a.causal = causal;
-    a.window = window;
-    a.max_q = max_q;
     a.skip_unit = skip_unit;
     return launch_attn_paged(a, v, cache.d, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -591,6 +605,37 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
                         void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
     return attn_paged_call(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, softmax_scale, causal, window, max_q, O,
                            o_sn, o_sh, lse, workspace, workspace_bytes, dev_status, stream, -1);
+}
+
+static vc_status check_groups(int N, int max_rows) { return N < 0 || max_rows < 0 ? VC_ERR_INVALID_ARG : VC_OK; }
+
+size_t vc_attn_paged_shared_workspace(vc_cache_shape cache, int Hq, int B, int T, int N, int max_q, int max_rows) {
+    if (check_cache_shape(cache) != VC_OK || B < 1 || T < 1 || check_paged_heads(cache, Hq, T, max_q) != VC_OK ||
+        check_groups(N, max_rows) != VC_OK)
+        return 0;
+    return attn_shared_workspace(cache, Hq, B, T, N, max_q, max_rows);
+}
+
+vc_status vc_attn_paged_shared(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
+                               const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv, vc_batch batch,
+                               const int32_t* groups, const int32_t* prefix, int N, float softmax_scale, int causal,
+                               int max_q, int max_rows, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+    SharedAttn a{};
+    CacheView v;
+    bool nothing = false;
+    if (check_groups(N, max_rows) != VC_OK) return VC_ERR_INVALID_ARG;
+    vc_status st = paged_args(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, softmax_scale, causal, 0, max_q, O, o_sn,
+                              o_sh, lse, dev_status, &a, &v, &nothing);
+    if (st != VC_OK || nothing) return st;
+    if (N > 0 && (!groups || !prefix || !aligned4(groups) || !aligned4(prefix))) return VC_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, attn_shared_workspace(cache, Hq, v.B, v.T, N, max_q, max_rows)))
+        return VC_ERR_WORKSPACE;
+    a.groups = groups;
+    a.prefix = prefix;
+    a.N = N;
+    a.skip_unit = -1;
+    return launch_attn_shared(a, v, cache.d, max_rows, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 vc_status vc_debug_attn_paged_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,

@@ -67,7 +67,7 @@ constexpr int kRegsSoftmax = 152, kRegsConv = 104, kRegsOther = 104;
 
 // What an item costs besides its units, in units: its queries (5 us), the first scores and the
 // last rows, with both pipelines empty, against 2 us a unit.
-constexpr int kItemCost = 7;
+constexpr int kItemCost = kManyItemCost;
 // The value scale, as -log2, up to which M follows s + log2 sv: below those of the cache that are not 0
 // (2^-109), and so that the P of 64 keys whose values are all zero sum up to less than 2^118.
 constexpr float kLeastLog2 = 110.f;
@@ -127,10 +127,11 @@ __device__ __forceinline__ int no_hoist(int x) {
 
 // SKIP: the test hook that leaves out the keys of unit a.skip_unit, in instances of its own (in the others
 // these few instructions of the loader cost 4 % of the time of windowed chunks).
-template <int D, int kChunk, bool SKIP>
+// SHARED: a pass of the attention over shared prefixes.
+template <int D, int kChunk, bool SKIP, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_many_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const PagedAttn a, const CacheView c, int RT, void* ws) {
+                     const AttnOf<SHARED> a, const CacheView c, int RT, void* ws) {
     using C = ManyCfg<D>;
     constexpr uint32_t ATTEMPTS = SKIP ? kHookAttempts : kWaitAttempts;
     // Keys that the softmax takes between two decisions about M: kChunk, and in units with a mask,
@@ -178,17 +179,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         init(C::TD, 1, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        const Partials part = partials_at(ws, RT, D);
-        part.head[2 * blockIdx.x].parts = 0;
-        part.head[2 * blockIdx.x + 1].parts = 0;
+        if constexpr (!SHARED) {
+            const Partials part = partials_at(ws, RT, D);
+            part.head[2 * blockIdx.x].parts = 0;
+            part.head[2 * blockIdx.x + 1].parts = 0;
+        }
     }
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < c.B; b += kThreads)
-            if (!seq_valid(c, b)) flag_invalid(c.dev_status);
-    const Part p = plan_part<kThreads>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
+            if (!seq_valid_in<SHARED>(c, a, b)) flag_invalid(c.dev_status);
+    if constexpr (SHARED)
+        if (blockIdx.x == 0)
+            for (int g = threadIdx.x; g < a.N; g += kThreads)
+                if (!group_valid(c, a, g)) flag_invalid(c.dev_status);
+    const Part p = plan_part<kThreads, SHARED>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
     __syncthreads();
     launch_dependents();
-    if (p.g0 == p.g1) return;
+    if (p.g0 == p.g1) {
+        if (SHARED) wait_for_primary();
+        return;
+    }
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -211,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 prefetch_tensormap(&tmV);
             }
             const int boxes = kUnit >> box_log2;
-            ItemWalk<kItemCost> w;
+            ItemWalk<kItemCost, SHARED> w;
             bool more = w.start(c, a, RT, p), ok = true;
             int it = 0, loaded_k = 0, loaded_v = 0;
             while (more && ok) {
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto entry = [&](int u) -> int {
                     const int k = u * kUnit + (lane << box_log2);
                     if (lane >= boxes || u >= w.end || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
-                    const int pg = __ldg(c.table + (int64_t)w.b * c.s_table + (k >> c.page_log2));
+                    const int pg = __ldg(c.table + (int64_t)w.table_row() * c.s_table + (k >> c.page_log2));
                     return pg < 0 ? -2 : pg;
                 };
                 int ahead = entry(w.unit);
@@ -261,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f->box_ok = box_ok;
                         f->pad[0] = u - w.unit;
                         f->pad[1] = on;
+                        if (SHARED) f->pad[2] = first_of<SHARED>(w.s);
                         mbar_arrive(bar(C::IF + it % C::NI));
                     }
                     __syncwarp();
@@ -539,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(C::QF + X));
                 const SeqInfo s{f->q0, f->n, f->L};
-                last = row_last(a, s, tok);
-                first = row_first(a, last);
+                last = row_last(a, s, tok, pass_of(a));
+                first = SHARED ? f->pad[2] : row_first(a, last);
                 M = -INFINITY;
                 l = 0.f;
                 lf = 1.f;
@@ -773,12 +784,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_after();
-            const bool split = flags & (kHead | kTail), there = tr < rows;
+            const bool split = SHARED || flags & (kHead | kTail), there = tr < rows;
             const int slot = 2 * blockIdx.x + ((flags & kHead) ? 0 : 1);
             const int r = r0 + (there ? tr : 0), tok = r / a.G, j = r - tok * a.G;
             const float inv = split ? 1.f : inverse_sum(l);
-            const Partials part = partials_at(ws, RT, D);
-            const int64_t o_off = split ? ((int64_t)slot * RT + tr) * D
+            const auto part = partials_of<SHARED>(c, a, ws, RT, D);
+            // place of this thread's row in the workspace
+            auto at_row = [&]() -> int64_t {
+                if (!SHARED || flags & (kHead | kTail)) return (int64_t)slot * RT + tr;
+                return own_slot(RT, (int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + j);
+            };
+            const int64_t o_off = split ? at_row() * D
                                         : (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
             // Rows go through shared memory (the warp's own rows of the queries, which no product reads
             // any more and no other warp writes for the next item), so that what leaves are whole
@@ -836,13 +852,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!both) mbar_arrive(bar(C::OE + 1));
             }
             if (there && split) {
-                part.m[(size_t)slot * RT + tr] = M;
-                part.l[(size_t)slot * RT + tr] = l;
+                part.m[at_row()] = M;
+                part.l[at_row()] = l;
+                if constexpr (SHARED)
+                    if (!(flags & kHead)) part.word[(int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + j] = row_word(blockIdx.x, on);
             } else if (there) {
                 store_lse(a, c, q0, h, r, M, l);
             }
-            if (split && threadIdx.x == 0)
-                part.head[slot] = PartHeader{on, q0, h, r0, rows};
+            if constexpr (!SHARED)
+                if (split && threadIdx.x == 0)
+                    part.head[slot] = PartHeader{on, q0, h, r0, rows};
             ++items;
         }
     }
@@ -853,32 +872,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (SHARED) wait_for_primary();  // the second pass's end is the first one's too
 }
 
-template <int D, int kChunk, bool SKIP>
-vc_status launch_many_as(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
+template <int D, int kChunk, bool SKIP, bool SHARED>
+vc_status launch_many_as(const CUtensorMap& mk, const CUtensorMap& mv, const AttnOf<SHARED>& a, const CacheView& c, int RT,
                          int ctas, void* ws, cudaStream_t st) {
-    auto kern = attn_many_kernel<D, kChunk, SKIP>;
+    auto kern = attn_many_kernel<D, kChunk, SKIP, SHARED>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
     if (s != VC_OK) return s;
-    kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
+    if constexpr (SHARED) return launch_pass(kern, ctas, kThreads, ManyCfg<D>::SMEM, a.pass, st, mk, mv, a, c, RT, ws);
+    else kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
     return cuda_status(cudaGetLastError());
 }
 
-template <int D, int kChunk>
-vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
+template <int D, int kChunk, class Attn>
+vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const Attn& a, const CacheView& c, int RT,
                       int ctas, void* ws, cudaStream_t st) {
-    return a.skip_unit < 0 ? launch_many_as<D, kChunk, false>(mk, mv, a, c, RT, ctas, ws, st)
-                           : launch_many_as<D, kChunk, true>(mk, mv, a, c, RT, ctas, ws, st);
+    if constexpr (std::is_same_v<Attn, SharedAttn>) return launch_many_as<D, kChunk, false, true>(mk, mv, a, c, RT, ctas, ws, st);
+    else
+        return a.skip_unit < 0 ? launch_many_as<D, kChunk, false, false>(mk, mv, a, c, RT, ctas, ws, st)
+                               : launch_many_as<D, kChunk, true, false>(mk, mv, a, c, RT, ctas, ws, st);
+}
+
+template <class Attn>
+vc_status launch_any(const CUtensorMap& mk, const CUtensorMap& mv, const Attn& a, const CacheView& c, int d, int RT,
+                     int ctas, void* ws, cudaStream_t st) {
+    if (d == 64) return launch_many<64, 32>(mk, mv, a, c, RT, ctas, ws, st);
+    return RT == 256 ? launch_many<128, 64>(mk, mv, a, c, RT, ctas, ws, st)
+                     : launch_many<128, 16>(mk, mv, a, c, RT, ctas, ws, st);
 }
 
 }  // namespace
 
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, void* ws, cudaStream_t st) {
-    if (d == 64) return launch_many<64, 32>(mk, mv, a, c, RT, ctas, ws, st);
-    return RT == 256 ? launch_many<128, 64>(mk, mv, a, c, RT, ctas, ws, st)
-                     : launch_many<128, 16>(mk, mv, a, c, RT, ctas, ws, st);
+    return launch_any(mk, mv, a, c, d, RT, ctas, ws, st);
+}
+
+vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c,
+                           int d, int RT, int ctas, void* ws, cudaStream_t st) {
+    return launch_any(mk, mv, a, c, d, RT, ctas, ws, st);
 }
 
 }  // namespace vc

@@ -99,10 +99,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // SKIP: the test hook that leaves out the keys of unit a.skip_unit, in instances of its own.
-template <int D, int RG, bool SKIP>
+// SHARED: a pass of the attention over shared prefixes.
+template <int D, int RG, bool SKIP, bool SHARED>
 __global__ void __launch_bounds__(kFewThreads, 1)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const PagedAttn a, const CacheView c, void* ws) {
+                    const AttnOf<SHARED> a, const CacheView c, void* ws) {
     using C = FewCfg<D>;
     constexpr int NS = C::NS, RT = 8 * RG;
     constexpr uint32_t ATTEMPTS = SKIP ? kHookAttempts : kWaitAttempts;
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const uint32_t full = sbase + C::OFF_BAR, empty = full + 8 * NS, written = empty + 8 * NS, read = written + 8;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
     const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-    const Partials part = partials_at(ws, RT, D);
+    const auto part = partials_of<SHARED>(c, a, ws, RT, D);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -125,16 +126,25 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_init(read, kConsumers);
         *abort_flag = 0;
         fence_barrier_init();
-        part.head[2 * blockIdx.x].parts = 0;
-        part.head[2 * blockIdx.x + 1].parts = 0;
+        if constexpr (!SHARED) {
+            part.head[2 * blockIdx.x].parts = 0;
+            part.head[2 * blockIdx.x + 1].parts = 0;
+        }
     }
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < c.B; b += kFewThreads)
-            if (!seq_valid(c, b)) flag_invalid(c.dev_status);
-    const Part p = plan_part<kFewThreads>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
+            if (!seq_valid_in<SHARED>(c, a, b)) flag_invalid(c.dev_status);
+    if constexpr (SHARED)
+        if (blockIdx.x == 0)
+            for (int g = threadIdx.x; g < a.N; g += kFewThreads)
+                if (!group_valid(c, a, g)) flag_invalid(c.dev_status);
+    const Part p = plan_part<kFewThreads, SHARED>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
     __syncthreads();
     launch_dependents();
-    if (p.g0 == p.g1) return;
+    if (p.g0 == p.g1) {
+        if (SHARED) wait_for_primary();
+        return;
+    }
 
     const int box_log2 = min(c.page_log2, 7);  // runs of keys in one page
     if (warp >= kConsumers) {
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (lane == 0) prefetch_tensormap(map);
         const int boxes = kUnit >> box_log2;
         const bool mine = lane < boxes && (lane & 1) == odd;
-        ItemWalk<kItemCost> w;
+        ItemWalk<kItemCost, SHARED> w;
         bool more = w.start(c, a, RT, p), ok = true;
         int it = 0;
         while (more && ok) {
@@ -157,7 +167,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             auto entry = [&](int u) -> int {
                 const int k = u * kUnit + (lane << box_log2);
                 if (lane >= boxes || u >= w.end || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
-                const int pg = __ldg(c.table + (int64_t)w.b * c.s_table + (k >> c.page_log2));
+                const int pg = __ldg(c.table + (int64_t)w.table_row() * c.s_table + (k >> c.page_log2));
                 return pg < 0 ? -2 : pg;
             };
             int ahead = entry(w.unit);
@@ -200,6 +210,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         f->rows = rows;
                         f->box_ok = box_ok;
                         f->pad[1] = on;
+                        if (SHARED) f->pad[2] = first_of<SHARED>(w.s);
                     }
                     if (!skip) mbar_arrive_expect_tx(full + 8 * st, (uint32_t)((boxes + 1 - odd) >> 1 << box_log2) * D);
                 }
@@ -289,12 +300,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                         q[2 * i + k / 2][k & 1] = pack_f16(bf16_bits_to_f32(wd[i][k] & 0xFFFFu) * f,
                                                            __uint_as_float(wd[i][k] & 0xFFFF0000u) * f);
                 const SeqInfo s{q0, info->n, info->L};
-                const int lg = row_last(a, s, tok);
+                const int lg = row_last(a, s, tok, pass_of(a));
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     qs[e] = __shfl_sync(0xffffffffu, qg, (2 * tig + e) * 4);
                     last[e] = __shfl_sync(0xffffffffu, lg, (2 * tig + e) * 4);
-                    first[e] = row_first(a, last[e]);
+                    first[e] = SHARED ? info->pad[2] : row_first(a, last[e]);
                     M[e] = N[e] = -INFINITY;
                     l[e] = 0.f;
                 }
@@ -478,7 +489,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     acc[2] = fmaf(w, u.z, acc[2]);
                     acc[3] = fmaf(w, u.w, acc[3]);
                 }
-                if (split) {
+                if constexpr (SHARED) {
+                    const int r = r0 + row, tok = r / a.G;
+                    const int64_t whole = (int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + r - tok * a.G;
+                    const int64_t at = split ? (int64_t)slot * RT + row : own_slot(RT, whole);
+                    *reinterpret_cast<float4*>(part.o + at * D + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                    if (ch == 0) {
+                        part.m[at] = m;
+                        part.l[at] = lsum;
+                        if (!(flags & kHead)) part.word[whole] = row_word(blockIdx.x, on);
+                    }
+                } else if (split) {
                     *reinterpret_cast<float4*>(part.o + ((size_t)slot * RT + row) * D + ch) =
                         make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (ch == 0) {
@@ -490,14 +511,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     if (ch == 0) store_lse(a, c, q0, h, r0 + row, m, lsum);
                 }
             }
-            if (split && threadIdx.x == 0)
-                part.head[slot] = PartHeader{on, q0, h, r0, rows};
+            if constexpr (!SHARED)
+                if (split && threadIdx.x == 0)
+                    part.head[slot] = PartHeader{on, q0, h, r0, rows};
             __syncwarp();
             if (lane == 0) mbar_arrive(read);
             ++items;
         }
     }
     __syncthreads();
+    if (SHARED) wait_for_primary();  // the second pass's end is the first one's too
 }
 
 // ------------------------------------------------------------ joining
@@ -580,7 +603,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         const SeqInfo s = seq_info(c, b);
         const int nt = seq_tiles(a, s, RT);
         for (int t = 0; t < nt; ++t) {
-            if (item_range(a, s, t, RT).units()) continue;
+            if (item_range<false>(a, s, t, RT, 0).units()) continue;
             const int r0 = t * RT, rows = min(RT, s.n * a.G - r0);
             for (int i = threadIdx.x / 32; i < c.H * rows; i += kJoinThreads / 32) {
                 store_row(a, s.q0, i / rows, r0 + i % rows, lane * E, none, 0.f);
@@ -635,14 +658,26 @@ vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, 
                                 : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, c, ws, RT, parts));
 }
 
-template <int D, int RG, bool SKIP = false>
-vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
+template <int D, int RG, bool SKIP = false, bool SHARED = false>
+vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const AttnOf<SHARED>& a, const CacheView& c, void* ws,
                      int ctas, cudaStream_t st) {
-    auto kern = attn_few_kernel<D, RG, SKIP>;
+    auto kern = attn_few_kernel<D, RG, SKIP, SHARED>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
     if (s != VC_OK) return s;
-    kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
+    if constexpr (SHARED) return launch_pass(kern, ctas, kFewThreads, FewCfg<D>::SMEM, a.pass, st, mk, mv, a, c, ws);
+    else kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
     return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+vc_status launch_pass_d(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, void* ws,
+                        cudaStream_t st) {
+    switch (a.rt[a.pass - 1]) {
+        case 8: return launch_few<D, 1, false, true>(mk, mv, a, c, ws, kMaxCtas, st);
+        case 16: return launch_few<D, 2, false, true>(mk, mv, a, c, ws, kMaxCtas, st);
+        case 32: return launch_few<D, 4, false, true>(mk, mv, a, c, ws, kMaxCtas, st);
+        default: return launch_attn_many(mk, mv, a, c, D, a.rt[a.pass - 1], kMaxCtas, ws, st);
+    }
 }
 
 // CTAs of a call: one on each SM, fewer where there cannot be that much work.
@@ -682,6 +717,49 @@ vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void*
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, c.K8, d, c) || !make_cache_map(&mv, c.V8, d, c)) return VC_ERR_CUDA;
     return d == 128 ? launch_d<128>(mk, mv, a, c, ws, st) : launch_d<64>(mk, mv, a, c, ws, st);
+}
+
+// ------------------------------------------------------------ shared prefixes
+//
+// Two passes with kernels as above, each over the keys that are its own: pass 1 takes the rows of a
+// group's sequences together over the prefix, which is read once for all of them, pass 2 each
+// sequence over what follows.  Both leave unscaled results in the workspace, which a third launch
+// joins.  The second pass is launched to run beside the first one: the SMs are shared out by the
+// passes' lengths, so each finds about as many free as it has parts.
+
+// A unit's time in tiles of RT rows, in hundredths of microseconds.
+static int unit_time(int RT) { return RT <= 16 ? 80 : RT == 32 ? 100 : RT == 128 ? 120 : 200; }
+
+// A pass's part of the workspace.
+static size_t shared_bytes(int RT, int d, size_t rows) { return (shared_partials_bytes(RT, d, rows) + 255) & ~(size_t)255; }
+
+size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int N, int max_q, int max_rows) {
+    const int G = Hq / c.H;
+    size_t n = 0;
+    for (int pass = 1; pass <= 2; ++pass) {
+        const int RT = pass == 1 ? tile_rows(G, N > 0 ? N : 1, T, max_rows) : tile_rows(G, B, T, max_q);
+        n += shared_bytes(RT, c.d, (size_t)T * Hq);
+    }
+    return n;
+}
+
+vc_status launch_attn_shared(const SharedAttn& args, const CacheView& c, int d, int max_rows, void* ws, cudaStream_t st) {
+    CUtensorMap mk, mv;
+    if (!make_cache_map(&mk, c.K8, d, c) || !make_cache_map(&mv, c.V8, d, c)) return VC_ERR_CUDA;
+    SharedAttn a = args;
+    a.rt[0] = tile_rows(a.G, a.N > 0 ? a.N : 1, c.T, max_rows);
+    a.rt[1] = tile_rows(a.G, c.B, c.T, a.max_q);
+    for (int i = 0; i < 2; ++i) {
+        a.ic[i] = a.rt[i] <= 32 ? kItemCost : kManyItemCost;
+        a.unit[i] = unit_time(a.rt[i]);
+    }
+    void* const at[2] = {ws, static_cast<uint8_t*>(ws) + shared_bytes(a.rt[0], d, (size_t)c.T * c.H * a.G)};
+    for (a.pass = 1; a.pass <= 2; ++a.pass) {
+        const vc_status s = d == 128 ? launch_pass_d<128>(mk, mv, a, c, at[a.pass - 1], st)
+                                     : launch_pass_d<64>(mk, mv, a, c, at[a.pass - 1], st);
+        if (s != VC_OK) return s;
+    }
+    return launch_shared_join(a, c, d, at[0], at[1], st);
 }
 
 }  // namespace vc

@@ -4,6 +4,7 @@
 // or checked here, so that no value in them leads outside the caller's buffers.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -16,6 +17,14 @@ struct SeqInfo {
     int q0, n;  // first row of the call and number of rows
     int L;      // tokens in the cache
 };
+// In attention over shared prefixes: the first key of the pass over it, and its row of the table.
+struct SeqPass : SeqInfo {
+    int lo, row;
+};
+template <bool SHARED>
+using SeqOf = std::conditional_t<SHARED, SeqPass, SeqInfo>;
+template <bool SHARED>
+using AttnOf = std::conditional_t<SHARED, SharedAttn, PagedAttn>;
 
 __device__ __forceinline__ void flag_invalid(int32_t* dev_status) {
     if (dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_INVALID_ARG);
@@ -34,6 +43,78 @@ __device__ __forceinline__ SeqInfo seq_info(const CacheView& c, int b) {
 __device__ __forceinline__ bool seq_valid(const CacheView& c, int b) {
     const int a = __ldg(c.cu + b), e = __ldg(c.cu + b + 1), len = __ldg(c.kv_len + b);
     return a >= 0 && e >= a && e <= c.T && len >= 0 && len <= (c.cols << c.page_log2);
+}
+
+// Attention over shared prefixes (SHARED kernels) takes two passes over the same rows.  Pass 1:
+// "sequence" g is group g, its rows those of all its sequences, its keys the prefix, found through
+// the first sequence's row of the table.  Pass 2: sequence b, keys from its group's prefix on.
+
+// Of the N groups, the one that sequence b belongs to; -1: none.
+__device__ __forceinline__ int group_of(const SharedAttn& a, int b) {
+    int lo = 0, hi = a.N;  // the last g with groups[g] <= b
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(a.groups + mid) <= b) lo = mid;
+        else hi = mid;
+    }
+    return a.N > 0 && b >= __ldg(a.groups + lo) && b < __ldg(a.groups + lo + 1) ? lo : -1;
+}
+
+__device__ __forceinline__ int prefix_of(const CacheView& c, const SharedAttn& a, int g) {
+    return g < 0 ? 0 : min(max(__ldg(a.prefix + g), 0), c.cols << c.page_log2);
+}
+
+// Group g as pass 1 sees it.
+__device__ __forceinline__ SeqPass group_info(const CacheView& c, const SharedAttn& a, int g) {
+    SeqPass s;
+    const int b0 = min(max(__ldg(a.groups + g), 0), c.B), b1 = min(max(__ldg(a.groups + g + 1), b0), c.B);
+    s.q0 = min(max(__ldg(c.cu + b0), 0), c.T);
+    s.n = min(max(__ldg(c.cu + b1), s.q0), c.T) - s.q0;
+    s.L = prefix_of(c, a, g);
+    s.lo = 0;
+    s.row = min(b0, c.B - 1);
+    return s;
+}
+
+template <bool SHARED>
+__device__ __forceinline__ SeqOf<SHARED> seq_of(const CacheView& c, const AttnOf<SHARED>& a, int b, int pass) {
+    if constexpr (SHARED) {
+        if (pass == 1) return group_info(c, a, b);
+        SeqPass s;
+        static_cast<SeqInfo&>(s) = seq_info(c, b);
+        s.lo = prefix_of(c, a, group_of(a, b));
+        s.row = b;
+        return s;
+    } else {
+        return seq_info(c, b);
+    }
+}
+template <bool SHARED>
+__device__ __forceinline__ int first_of(const SeqOf<SHARED>& s) {
+    if constexpr (SHARED) return s.lo;
+    else return 0;
+}
+template <bool SHARED>
+__device__ __forceinline__ int seq_count(const CacheView& c, const AttnOf<SHARED>& a, int pass) {
+    if constexpr (SHARED) return pass == 1 ? a.N : c.B;
+    else return c.B;
+}
+
+// Whether sequence b keeps the rules of its batch, and of its group.
+template <bool SHARED>
+__device__ __forceinline__ bool seq_valid_in(const CacheView& c, const AttnOf<SHARED>& a, int b) {
+    if (!seq_valid(c, b)) return false;
+    if constexpr (SHARED) {
+        const int g = group_of(a, b);
+        if (g < 0) return true;
+        const int prefix = __ldg(a.prefix + g), n = __ldg(c.cu + b + 1) - __ldg(c.cu + b);
+        return prefix >= 0 && (n == 0 || prefix <= max(__ldg(c.kv_len + b) - n, 0));
+    }
+    return true;
+}
+__device__ __forceinline__ bool group_valid(const CacheView& c, const SharedAttn& a, int g) {
+    const int b0 = __ldg(a.groups + g), b1 = __ldg(a.groups + g + 1);
+    return b0 >= 0 && b1 >= b0 && b1 <= c.B && __ldg(a.prefix + g) <= (c.cols << c.page_log2);
 }
 
 // Page of position p (0 <= p < cols * page_size), or -1 where it is not there.
@@ -107,20 +188,24 @@ struct ItemRange {
     __device__ int units() const { return hi < lo ? 0 : hi / kUnit - lo / kUnit + 1; }
 };
 
-__device__ __forceinline__ int row_last(const PagedAttn& a, const SeqInfo& s, int token) {
-    return a.causal ? s.L - s.n + token : s.L - 1;
+// The pass of this launch; 0: the only one.
+__device__ __forceinline__ constexpr int pass_of(const PagedAttn&) { return 0; }
+__device__ __forceinline__ int pass_of(const SharedAttn& a) { return a.pass; }
+__device__ __forceinline__ int row_last(const PagedAttn& a, const SeqInfo& s, int token, int pass) {
+    return a.causal && pass != 1 ? s.L - s.n + token : s.L - 1;
 }
 __device__ __forceinline__ int row_first(const PagedAttn& a, int last) {
     return a.window && last >= a.window ? last - a.window + 1 : 0;  // no overflow for any window
 }
 
-__device__ __forceinline__ ItemRange item_range(const PagedAttn& a, const SeqInfo& s, int tile, int RT) {
+template <bool SHARED>
+__device__ __forceinline__ ItemRange item_range(const AttnOf<SHARED>& a, const SeqOf<SHARED>& s, int tile, int RT, int pass) {
     const int r0 = tile * RT, r1 = min(r0 + RT, s.n * a.G) - 1;
-    const int h0 = row_last(a, s, r0 / a.G), h1 = row_last(a, s, r1 / a.G);
+    const int h0 = row_last(a, s, r0 / a.G, pass), h1 = row_last(a, s, r1 / a.G, pass);
     ItemRange r;
-    r.lo = row_first(a, h0);
+    r.lo = SHARED ? first_of<SHARED>(s) : row_first(a, h0);
     r.hi = h1;
-    r.lo_all = row_first(a, h1);
+    r.lo_all = SHARED ? first_of<SHARED>(s) : row_first(a, h1);
     r.hi_all = h0;
     return r;
 }
@@ -130,23 +215,26 @@ __device__ __forceinline__ int seq_tiles(const PagedAttn& a, const SeqInfo& s, i
     return (int)(((int64_t)s.n * a.G + RT - 1) / RT);
 }
 
-__device__ __forceinline__ int item_cost(const PagedAttn& a, const SeqInfo& s, int tile, int RT, int IC) {
-    const int u = item_range(a, s, tile, RT).units();
+template <bool SHARED>
+__device__ __forceinline__ int item_cost(const AttnOf<SHARED>& a, const SeqOf<SHARED>& s, int tile, int RT, int IC, int pass) {
+    const int u = item_range<SHARED>(a, s, tile, RT, pass).units();
     return u ? u + IC : 0;
 }
 
 // Cost of one head's tiles of a sequence: by one thread, or by a warp.
-__device__ __forceinline__ int64_t seq_cost(const CacheView& c, const PagedAttn& a, int b, int RT, int IC) {
-    const SeqInfo s = seq_info(c, b);
+template <bool SHARED>
+__device__ __forceinline__ int64_t seq_cost(const CacheView& c, const AttnOf<SHARED>& a, int b, int RT, int IC, int pass) {
+    const SeqOf<SHARED> s = seq_of<SHARED>(c, a, b, pass);
     const int nt = seq_tiles(a, s, RT);
     int64_t u = 0;
-    for (int t = 0; t < nt; ++t) u += item_cost(a, s, t, RT, IC);
+    for (int t = 0; t < nt; ++t) u += item_cost<SHARED>(a, s, t, RT, IC, pass);
     return u;
 }
-__device__ __forceinline__ int64_t seq_cost_warp(const PagedAttn& a, const SeqInfo& s, int RT, int IC) {
+template <bool SHARED>
+__device__ __forceinline__ int64_t seq_cost_warp(const AttnOf<SHARED>& a, const SeqOf<SHARED>& s, int RT, int IC, int pass) {
     const int nt = seq_tiles(a, s, RT);
     int64_t u = 0;
-    for (int t = threadIdx.x & 31; t < nt; t += 32) u += item_cost(a, s, t, RT, IC);
+    for (int t = threadIdx.x & 31; t < nt; t += 32) u += item_cost<SHARED>(a, s, t, RT, IC, pass);
     for (int o = 16; o; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
     return u;
 }
@@ -166,32 +254,58 @@ struct Part {
     int parts;
 };
 
+// Length of a pass's line; called by all NT threads of a block, the same in all of them.
+template <int NT>
+__device__ __forceinline__ int64_t line_length(const CacheView& c, const SharedAttn& a, int pass) {
+    const int RT = pass == 1 ? a.rt[0] : a.rt[1], IC = pass == 1 ? a.ic[0] : a.ic[1];
+    __shared__ int64_t sums[NT / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = seq_count<true>(c, a, pass);
+    int64_t mine = 0;
+    if ((int64_t)c.T * a.G > (int64_t)n * RT * 4) {
+        for (int b = warp; b < n; b += NT / 32) {
+            const int64_t u = seq_cost_warp<true>(a, seq_of<true>(c, a, b, pass), RT, IC, pass);
+            if (lane == 0) mine += u * c.H;
+        }
+    } else {
+        for (int b = threadIdx.x; b < n; b += NT) mine += seq_cost<true>(c, a, b, RT, IC, pass) * c.H;
+    }
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) sums[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < NT / 32; ++w) total += sums[w];
+    return total;
+}
+
 // Called by all NT threads of a block; the result is the same in all of them.
 // Two passes over the sequences, NT at a time: the total, then the one that
 // holds g0.  Sequences of many tiles are added up by a warp each.
-template <int NT>
-__device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a, int RT, int IC, int part, int parts) {
+// SHARED: the two passes run side by side, each on a share of the SMs that goes by its length and what
+// a unit costs it.
+template <int NT, bool SHARED>
+__device__ __forceinline__ Part plan_part(const CacheView& c, const AttnOf<SHARED>& a, int RT, int IC, int part, int parts) {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ int64_t cost[NT];
     __shared__ Part found;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool by_warp = (int64_t)c.T * a.G > (int64_t)c.B * RT * 4;
+    const int pass = pass_of(a), seqs = seq_count<SHARED>(c, a, pass);
+    const bool by_warp = (int64_t)c.T * a.G > (int64_t)seqs * RT * 4;
     // cost of sequence b0 + threadIdx.x
     auto costs = [&](int b0) -> int64_t {
         if (by_warp) {
-            for (int i = warp; i < NT && b0 + i < c.B; i += NT / 32) {
-                const int64_t u = seq_cost_warp(a, seq_info(c, b0 + i), RT, IC);
+            for (int i = warp; i < NT && b0 + i < seqs; i += NT / 32) {
+                const int64_t u = seq_cost_warp<SHARED>(a, seq_of<SHARED>(c, a, b0 + i, pass), RT, IC, pass);
                 if (lane == 0) cost[i] = u * c.H;
             }
             __syncthreads();
-            return b0 + (int)threadIdx.x < c.B ? cost[threadIdx.x] : 0;
+            return b0 + (int)threadIdx.x < seqs ? cost[threadIdx.x] : 0;
         }
-        return b0 + (int)threadIdx.x < c.B ? seq_cost(c, a, b0 + threadIdx.x, RT, IC) * c.H : 0;
+        return b0 + (int)threadIdx.x < seqs ? seq_cost<SHARED>(c, a, b0 + threadIdx.x, RT, IC, pass) * c.H : 0;
     };
     if (threadIdx.x == 0) found = Part{};
     const int64_t first_u = costs(0);
     int64_t mine = first_u;
-    for (int b0 = NT; b0 < c.B; b0 += NT) {
+    for (int b0 = NT; b0 < seqs; b0 += NT) {
         __syncthreads();
         mine += costs(b0);
     }
@@ -201,6 +315,17 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     int64_t total = 0;
     for (int w = 0; w < NT / 32; ++w) total += warp_sum[w];
     Part p;
+    if constexpr (SHARED) {
+        const bool first = pass == 1;
+        const int64_t mine_w = total * (first ? a.unit[0] : a.unit[1]);
+        const int64_t other_w = line_length<NT>(c, a, 3 - pass) * (first ? a.unit[1] : a.unit[0]);
+        // pass 1's share, rounded; both have one part at least where they have work
+        const int64_t w1 = first ? mine_w : other_w, w2 = first ? other_w : mine_w;
+        int p1 = w1 ? (int)((w1 * parts + (w1 + w2) / 2) / (w1 + w2)) : 0;
+        if (w1) p1 = max(p1, 1);
+        if (w2) p1 = min(p1, parts - 1);
+        parts = first ? p1 : parts - p1;
+    }
     if (total < parts) parts = (int)total;  // no empty part between two others
     p.b = 0;
     p.off = 0;
@@ -213,7 +338,7 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
     p.g0 = div_small(total * part, parts);
     p.g1 = div_small(total * (part + 1), parts);
     int64_t before = 0;  // cost of the sequences of earlier rounds
-    for (int b0 = 0; b0 < c.B; b0 += NT) {
+    for (int b0 = 0; b0 < seqs; b0 += NT) {
         __syncthreads();
         const int64_t u = b0 ? costs(b0) : first_u;
         int64_t scan = u;
@@ -244,33 +369,38 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
 
 // Walks the items of a CTA's part that have units in it, in order.  For whole
 // warps; all members are uniform over the warp.
-template <int IC>
+template <int IC, bool SHARED>
 struct ItemWalk {
     int64_t at, left;  // place in the line, and what is left of the part
     int b, h, tile;  // the item
-    SeqInfo s;
+    SeqOf<SHARED> s;
     ItemRange r;
     int unit, end;   // units [unit, end) of 128 keys, of this item in this part
     int64_t item_end;  // the item's end in the line
     bool head;       // an earlier CTA has the item's first units
     bool tail;       // a later CTA has its last units
 
+    __device__ int table_row() const {
+        if constexpr (SHARED) return s.row;
+        else return b;
+    }
     // Parts from this one on that have units of the item.
     __device__ int parts_on(const Part& p, int part) const {
         return tail ? (int)div_small(item_end * p.parts - 1, p.total) - part + 1 : 1;
     }
     // To the first item; false where the part holds no unit at all.
-    __device__ bool start(const CacheView& c, const PagedAttn& a, int RT, const Part& p) {
+    __device__ bool start(const CacheView& c, const AttnOf<SHARED>& a, int RT, const Part& p) {
         at = p.g0;
         left = p.g1 - p.g0;
         b = p.b;
-        s = seq_info(c, b);
-        const int64_t per_head = seq_cost_warp(a, s, RT, IC);
+        const int pass = pass_of(a);
+        s = seq_of<SHARED>(c, a, b, pass);
+        const int64_t per_head = seq_cost_warp<SHARED>(a, s, RT, IC, pass);
         h = (int)div_small(p.off, per_head);
         int64_t off = p.off - h * per_head;
         const int nt = seq_tiles(a, s, RT), lane = threadIdx.x & 31;
         for (int t0 = 0;; t0 += 32) {
-            int64_t scan = t0 + lane < nt ? item_cost(a, s, t0 + lane, RT, IC) : 0;
+            int64_t scan = t0 + lane < nt ? item_cost<SHARED>(a, s, t0 + lane, RT, IC, pass) : 0;
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(0xffffffffu, scan, o);
                 if (lane >= o) scan += v;
@@ -285,7 +415,7 @@ struct ItemWalk {
             }
             off -= __shfl_sync(0xffffffffu, scan, 31);
         }
-        r = item_range(a, s, tile, RT);
+        r = item_range<SHARED>(a, s, tile, RT, pass_of(a));
         return take((int)off) || next(c, a, RT);
     }
     // The item from place `off` of its length on; false where that holds none of its units.
@@ -303,21 +433,21 @@ struct ItemWalk {
         return u1 > u0;
     }
     // To the next item with units in the part; false at its end.
-    __device__ bool next(const CacheView& c, const PagedAttn& a, int RT) {
+    __device__ bool next(const CacheView& c, const AttnOf<SHARED>& a, int RT) {
         while (left > 0) {
             if (++tile >= seq_tiles(a, s, RT)) {
                 tile = 0;
                 if (++h >= c.H) {
                     h = 0;
-                    if (++b >= c.B) return false;
-                    s = seq_info(c, b);
+                    if (++b >= seq_count<SHARED>(c, a, pass_of(a))) return false;
+                    s = seq_of<SHARED>(c, a, b, pass_of(a));
                 }
                 if (seq_tiles(a, s, RT) == 0) {  // a sequence without rows has no heads to walk
                     h = c.H;
                     continue;
                 }
             }
-            r = item_range(a, s, tile, RT);
+            r = item_range<SHARED>(a, s, tile, RT, pass_of(a));
             if (r.units() && take(0)) return true;
         }
         return false;
@@ -339,11 +469,23 @@ struct Partials {
     float* l;
     float* o;          // [2 * kMaxCtas][RT][D]
 };
+// SHARED: every row's result goes there, those of items that are not cut to a slot of the row's own
+// behind the others', and the part that an item begins in leaves a word for each of its rows.
+struct SharedPartials {
+    float* m;          // [2 * kMaxCtas * RT + rows]
+    float* l;
+    float* o;          // [2 * kMaxCtas * RT + rows][D]
+    uint32_t* word;    // [rows]
+};
 
 inline __host__ __device__ size_t partials_bytes(int RT, int D) {
     return 2 * (size_t)kMaxCtas * (32 + (size_t)RT * (D + 2) * sizeof(float));
 }
+inline __host__ __device__ size_t shared_partials_bytes(int RT, int D, size_t rows) {
+    return ((2 * (size_t)kMaxCtas * RT + rows) * (D + 2) + rows) * sizeof(float);
+}
 static_assert(sizeof(PartHeader) <= 32, "header slots");
+static_assert(kMaxCtas < 256, "parts of an item in a row's word");
 
 inline __host__ __device__ Partials partials_at(void* ws, int RT, int D) {
     Partials p;
@@ -353,6 +495,26 @@ inline __host__ __device__ Partials partials_at(void* ws, int RT, int D) {
     p.head = reinterpret_cast<PartHeader*>(p.l + 2 * (size_t)kMaxCtas * RT);
     return p;
 }
+
+inline __host__ __device__ SharedPartials shared_partials_at(void* ws, int RT, int D, size_t rows) {
+    const size_t slots = 2 * (size_t)kMaxCtas * RT + rows;
+    SharedPartials p;
+    p.o = static_cast<float*>(ws);
+    p.m = p.o + slots * D;
+    p.l = p.m + slots;
+    p.word = reinterpret_cast<uint32_t*>(p.l + slots);
+    return p;
+}
+template <bool SHARED>
+__device__ __forceinline__ auto partials_of(const CacheView& c, const PagedAttn& a, void* ws, int RT, int D) {
+    if constexpr (SHARED) return shared_partials_at(ws, RT, D, (size_t)c.T * c.H * a.G);
+    else return partials_at(ws, RT, D);
+}
+
+// SHARED: the word of a row whose item begins in CTA i and has parts in n CTAs (n = 1: not cut).
+__device__ __forceinline__ uint32_t row_word(int cta, int parts) { return (uint32_t)cta << 8 | (uint32_t)parts; }
+// A row's own place.
+__device__ __forceinline__ int64_t own_slot(int RT, int64_t row) { return 2 * (int64_t)kMaxCtas * RT + row; }
 
 // 1 / l for a row's sum: 0 for a row that saw nothing, NaN kept.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
@@ -426,6 +588,22 @@ __device__ __forceinline__ void store_row(const PagedAttn& a, int q0, int h, int
 __device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c, int q0, int h, int r, float m,
                                           float l) {
     if (a.lse) a.lse[(int64_t)(q0 + r / a.G) * (c.H * a.G) + h * a.G + r % a.G] = lse_of(m, l);
+}
+
+// Launches a pass of the attention over shared prefixes; the second one while the first one runs.
+template <class... P, class... A>
+vc_status launch_pass(void (*kern)(P...), int ctas, int threads, int smem, int pass, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = pass == 2 ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 
 }  // namespace vc

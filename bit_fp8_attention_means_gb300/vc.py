@@ -128,6 +128,11 @@ def lib():
                                        ctypes.c_size_t, _vp, _vp]
         L.vc_cache_copy.restype = i32
         L.vc_cache_copy.argtypes = [VcCacheShape, _vp, _vp, _vp, _vp, VcCacheShape, _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp, _vp]
+        L.vc_attn_paged_shared_workspace.restype = ctypes.c_size_t
+        L.vc_attn_paged_shared_workspace.argtypes = [VcCacheShape, i32, i32, i32, i32, i32, i32]
+        L.vc_attn_paged_shared.restype = i32
+        L.vc_attn_paged_shared.argtypes = [_vp, i64, i64, i32, VcCacheShape, _vp, _vp, _vp, _vp, VcBatch, _vp, _vp, i32,
+                                           ctypes.c_float, i32, i32, i32, _vp, i64, i64, _vp, _vp, ctypes.c_size_t, _vp, _vp]
         L.vc_debug_attn_paged_timeout.restype = ctypes.c_int
         L.vc_debug_attn_paged_timeout.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp,
                                                   _vp, _vp, _vp, VcBatch, ctypes.c_int, _vp, ctypes.c_int64,
@@ -595,6 +600,69 @@ def vc_attn_paged(Q, cache, cu, kv_len, table, softmax_scale=0.0, causal=1, wind
                (Q.data_ptr(), *q_strides, Hq, s, K8, sk, V8, sv, batch, softmax_scale, causal, window, max_q,
                 O.data_ptr(), *o_strides, lse.data_ptr(), workspace.data_ptr(),
                 workspace.numel() * workspace.element_size(), status), "vc_attn_paged")
+    return O, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_shared_bytes(page_size, H, d, Hq, B, T, N, max_q, max_rows):
+    """vc_attn_paged_shared_workspace, which depends on these numbers alone."""
+    s = VcCacheShape(1, page_size, H, d, H * page_size * d, page_size * d, d, H * page_size, page_size)
+    return lib().vc_attn_paged_shared_workspace(s, Hq, B, T, N, max_q, max_rows)
+
+
+def attn_paged_shared_workspace_bytes(cache, Hq, B, T, N, max_q=0, max_rows=0) -> int:
+    return lib().vc_attn_paged_shared_workspace(cache_shape_of(cache), Hq, B, T, N, _int32(max_q), _int32(max_rows))
+
+
+def vc_attn_paged_shared(Q, cache, cu, kv_len, table, groups, prefix, softmax_scale=0.0, causal=1, max_q=0, max_rows=0,
+                         O=None, lse=None, workspace=None, dev_status=None, stream=None):
+    """vc_attn_paged (without a window) for sequences that begin alike, as forks do: groups int32 [N+1] are offsets of
+    N runs of sequences, prefix int32 [N] how many tokens a run's sequences have in common, in the same pages but for
+    the page that the prefix ends in.  Each prefix is read once for all rows of its run.  Returns (O, lse).
+
+    A prefix holds none of the call's tokens; 0 and runs of one sequence are fine, as are sequences of no run.
+    max_q: the longest chunk among the sequences, max_rows: the most tokens of this call in one run, if known (they
+    choose kernels, nothing else)."""
+    L = lib()
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    shape = Q.shape
+    if len(shape) != 3:
+        raise ValueError("Q must be bf16 [T, Hq, %d]" % s.d)
+    T, Hq, d = shape
+    q_strides = _rows("Q", Q, Hq, s.d, dev)
+    batch = _batch_of(cu, kv_len, table, T, dev)
+    N = prefix.numel()
+    runs = _int32_vector("groups", groups, N + 1, dev), _int32_vector("prefix", prefix, N, dev)
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    _check_stream(stream, dev)
+    if _is_other(stream):
+        return _on_stream(stream, vc_attn_paged_shared, Q, cache, cu, kv_len, table, groups, prefix, softmax_scale, causal,
+                          max_q, max_rows, O, lse, workspace, dev_status)
+    max_q, max_rows = _int32(max_q), _int32(max_rows)
+    if 0 < softmax_scale < _LEAST_FP32:  # as fp32 it would be 0, the default
+        softmax_scale = _LEAST_FP32
+    if O is None:
+        O = torch.empty(shape, dtype=_BF16, device=dev)
+        o_strides = (Hq * d, d)
+    else:
+        o_strides = _rows("O", O, Hq, d, dev)
+        if O.shape != shape:
+            raise ValueError("O must have Q's shape")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=_F32, device=dev)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or \
+            lse.get_device() != dev:
+        raise ValueError("lse must be contiguous fp32 [T, Hq] on the cache's device")
+    if workspace is None:
+        workspace = torch.empty(max(_attn_shared_bytes(s.page_size, s.H, d, Hq, batch.B, T, N, max_q, max_rows), 256),
+                                dtype=_U8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    _on_device(dev, stream, L.vc_attn_paged_shared,
+               (Q.data_ptr(), *q_strides, Hq, s, K8, sk, V8, sv, batch, *runs, N, softmax_scale, causal, max_q, max_rows,
+                O.data_ptr(), *o_strides, lse.data_ptr(), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), status), "vc_attn_paged_shared")
     return O, lse
 
 

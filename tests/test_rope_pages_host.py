@@ -235,3 +235,27 @@ def test_model_walks_stay_consistent():
                 m.fork(parents, rows, lens)
             assert m.consistent()
     assert refused
+
+
+def test_shared_prefix_refusals(L):
+    def call(c=cache(), b=batch(), Q=FAKE, O=FAKE, Hq=4, q=(512, 128), o=(512, 128), groups=FAKE, prefix=FAKE, N=2, scale=0.0, causal=1, max_q=0, max_rows=0, lse=FAKE, ws=FAKE,
+             ws_bytes=1 << 40, codes=(FAKE,) * 4):
+        return L.vc_attn_paged_shared(Q, *q, Hq, c, *codes, b, groups, prefix, N, scale, causal, max_q, max_rows, O, *o, lse, ws, ws_bytes, None, None)
+    for bad in (dict(groups=None), dict(prefix=None), dict(groups=TWO), dict(prefix=TWO), dict(N=-1), dict(max_rows=-1), dict(max_q=-1), dict(Q=None), dict(Q=ODD), dict(O=ODD),
+                dict(Hq=3), dict(q=(0, 128)), dict(o=(512, 4)), dict(scale=math.nan), dict(scale=3.4e38), dict(causal=2), dict(lse=TWO), dict(codes=(FAKE, FAKE, None, FAKE)),
+                dict(c=cache(pages=0)), dict(b=batch(B=0)), dict(b=batch(cu=None)), dict(b=batch(s_table=3))):
+        assert call(**bad) == 1, bad
+    for bad in (dict(c=cache(d=96)), dict(b=batch(T=1 << 28)), dict(b=batch(cols=1 << 26, s_table=1 << 26))):
+        assert call(**bad) == 2, bad
+    for N in (0, 2):
+        need = L.vc_attn_paged_shared_workspace(cache(), 4, 3, 7, N, 0, 0)
+        assert need > 0 and call(N=N, ws=None) == 3 and call(N=N, ws_bytes=need - 1) == 3 and call(N=N, ws=ctypes.c_void_p(0x10080)) == 3
+    assert L.vc_attn_paged_shared_workspace(cache(), 3, 3, 7, 2, 0, 0) == 0 and L.vc_attn_paged_shared_workspace(cache(), 4, 3, 7, -1, 0, 0) == 0
+    assert call(b=batch(T=0, cu=None), groups=None, Q=None, codes=(None,) * 4) == 0
+    c = Case(n=[2], kv=[5], H=2)
+    groups, prefix = torch.tensor([0, 1], dtype=torch.int32), torch.tensor([3], dtype=torch.int32)
+    for bad in ((groups[:1], prefix), (groups.long(), prefix), (groups, prefix.float()), (groups, prefix.repeat(2))):
+        with pytest.raises(ValueError):
+            vc.vc_attn_paged_shared(c.Q, c.cache(), *c.args("cpu"), *bad)
+    with pytest.raises(ValueError, match="CUDA"):
+        vc.vc_attn_paged_shared(c.Q, c.cache(), *c.args("cpu"), groups, prefix)
