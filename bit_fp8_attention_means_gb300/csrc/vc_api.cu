@@ -635,7 +635,7 @@ vc_status vc_attn_paged_shared(const void* Q, int64_t q_sn, int64_t q_sh, int Hq
     a.prefix = prefix;
     a.N = N;
     a.skip_unit = -1;
-    return launch_attn_shared(a, v, cache.d, max_rows, workspace, reinterpret_cast<cudaStream_t>(stream));
+    return launch_attn_shared(a, cache, v, max_rows, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 vc_status vc_debug_attn_paged_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,

@@ -185,14 +185,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             part.head[2 * blockIdx.x + 1].parts = 0;
         }
     }
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < c.B; b += kThreads)
-            if (!seq_valid_in<SHARED>(c, a, b)) flag_invalid(c.dev_status);
-    if constexpr (SHARED)
-        if (blockIdx.x == 0)
-            for (int g = threadIdx.x; g < a.N; g += kThreads)
-                if (!group_valid(c, a, g)) flag_invalid(c.dev_status);
-    const Part p = plan_part<kThreads, SHARED>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
+    auto plan = [&] {
+        if constexpr (SHARED) {
+            if (a.pass == 1) wait_for_primary();  // the plan; the second pass starts when all of the first have it
+            return load_part(a.plan + (a.pass == 1 ? 0 : kMaxCtas * a.per_sm[0]) + blockIdx.x);
+        } else {
+            if (blockIdx.x == 0)
+                for (int b = threadIdx.x; b < c.B; b += kThreads)
+                    if (!seq_valid(c, b)) flag_invalid(c.dev_status);
+            return plan_part<kThreads>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
+        }
+    };
+    const auto p = plan();
     __syncthreads();
     launch_dependents();
     if (p.g0 == p.g1) {
@@ -791,8 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto part = partials_of<SHARED>(c, a, ws, RT, D);
             // place of this thread's row in the workspace
             auto at_row = [&]() -> int64_t {
-                if (!SHARED || flags & (kHead | kTail)) return (int64_t)slot * RT + tr;
-                return own_slot(RT, (int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + j);
+                if constexpr (!SHARED) return (int64_t)slot * RT + tr;
+                else if (flags & (kHead | kTail)) return (int64_t)slot * RT + tr;
+                else
+                    return own_slot(a, (int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + j);
             };
             const int64_t o_off = split ? at_row() * D
                                         : (int64_t)(q0 + tok) * a.o_sn + (int64_t)(h * a.G + j) * a.o_sh;
@@ -855,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 part.m[at_row()] = M;
                 part.l[at_row()] = l;
                 if constexpr (SHARED)
-                    if (!(flags & kHead)) part.word[(int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + j] = row_word(blockIdx.x, on);
+                    if (!(flags & kHead)) part.word[(int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + j] = row_word(tr, blockIdx.x, on);
             } else if (there) {
                 store_lse(a, c, q0, h, r, M, l);
             }
@@ -875,44 +881,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (SHARED) wait_for_primary();  // the second pass's end is the first one's too
 }
 
-template <int D, int kChunk, bool SKIP, bool SHARED>
-vc_status launch_many_as(const CUtensorMap& mk, const CUtensorMap& mv, const AttnOf<SHARED>& a, const CacheView& c, int RT,
+template <int D, int kChunk, bool SKIP>
+vc_status launch_many_as(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
                          int ctas, void* ws, cudaStream_t st) {
-    auto kern = attn_many_kernel<D, kChunk, SKIP, SHARED>;
+    auto kern = attn_many_kernel<D, kChunk, SKIP, false>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
     if (s != VC_OK) return s;
-    if constexpr (SHARED) return launch_pass(kern, ctas, kThreads, ManyCfg<D>::SMEM, a.pass, st, mk, mv, a, c, RT, ws);
-    else kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
+    kern<<<ctas, kThreads, ManyCfg<D>::SMEM, st>>>(mk, mv, a, c, RT, ws);
     return cuda_status(cudaGetLastError());
 }
 
-template <int D, int kChunk, class Attn>
-vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const Attn& a, const CacheView& c, int RT,
+template <int D, int kChunk>
+vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, int RT,
                       int ctas, void* ws, cudaStream_t st) {
-    if constexpr (std::is_same_v<Attn, SharedAttn>) return launch_many_as<D, kChunk, false, true>(mk, mv, a, c, RT, ctas, ws, st);
-    else
-        return a.skip_unit < 0 ? launch_many_as<D, kChunk, false, false>(mk, mv, a, c, RT, ctas, ws, st)
-                               : launch_many_as<D, kChunk, true, false>(mk, mv, a, c, RT, ctas, ws, st);
+    return a.skip_unit < 0 ? launch_many_as<D, kChunk, false>(mk, mv, a, c, RT, ctas, ws, st)
+                           : launch_many_as<D, kChunk, true>(mk, mv, a, c, RT, ctas, ws, st);
 }
 
-template <class Attn>
-vc_status launch_any(const CUtensorMap& mk, const CUtensorMap& mv, const Attn& a, const CacheView& c, int d, int RT,
-                     int ctas, void* ws, cudaStream_t st) {
-    if (d == 64) return launch_many<64, 32>(mk, mv, a, c, RT, ctas, ws, st);
-    return RT == 256 ? launch_many<128, 64>(mk, mv, a, c, RT, ctas, ws, st)
-                     : launch_many<128, 16>(mk, mv, a, c, RT, ctas, ws, st);
+template <int D, int kChunk>
+vc_status launch_many_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, int RT,
+                           int ctas, cudaStream_t st) {
+    auto kern = attn_many_kernel<D, kChunk, false, true>;
+    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
+    if (s != VC_OK) return s;
+    return launch_after(kern, dim3(ctas), kThreads, ManyCfg<D>::SMEM, st, mk, mv, a, c, RT, (void*)nullptr);
 }
 
 }  // namespace
 
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, void* ws, cudaStream_t st) {
-    return launch_any(mk, mv, a, c, d, RT, ctas, ws, st);
+    if (d == 64) return launch_many<64, 32>(mk, mv, a, c, RT, ctas, ws, st);
+    return RT == 256 ? launch_many<128, 64>(mk, mv, a, c, RT, ctas, ws, st)
+                     : launch_many<128, 16>(mk, mv, a, c, RT, ctas, ws, st);
 }
 
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c,
-                           int d, int RT, int ctas, void* ws, cudaStream_t st) {
-    return launch_any(mk, mv, a, c, d, RT, ctas, ws, st);
+                           int d, int RT, int ctas, cudaStream_t st) {
+    if (d == 64) return launch_many_pass<64, 32>(mk, mv, a, c, RT, ctas, st);
+    return RT == 256 ? launch_many_pass<128, 64>(mk, mv, a, c, RT, ctas, st)
+                     : launch_many_pass<128, 16>(mk, mv, a, c, RT, ctas, st);
 }
 
 }  // namespace vc

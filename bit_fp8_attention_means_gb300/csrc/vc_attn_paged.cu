@@ -43,10 +43,15 @@ namespace {
 
 // What an item costs besides its units, in units: the queries, and adding up the warps' parts.
 constexpr int kItemCost = 3;
-constexpr int kConsumers = 16;
-constexpr int kFewThreads = (kConsumers + 4) * 32;
-// 640 threads start with 96 registers each; 4 x 128 x 104 + 128 x 56 = 60,416 fit into those 61,440
-constexpr int kFewRegsUp = 104, kFewRegsDown = 56;
+constexpr int kFewConsumers = 16;
+// Shared prefixes leave many sequences a few units each, whose beginnings and ends a CTA waits out: two
+// CTAs of half the size on an SM fill each other's waits.
+constexpr int kShortConsumers = 8;
+constexpr int few_threads(int consumers) { return (consumers + 4) * 32; }
+// 640 threads start with 96 registers each; 4 x 128 x 104 + 128 x 56 = 60,416 fit into those 61,440.
+// 384 start with 80; 2 x 128 x 96 + 128 x 48 = 30,720.
+constexpr int few_regs_up(int consumers) { return consumers == 16 ? 104 : 96; }
+constexpr int few_regs_down(int consumers) { return consumers == 16 ? 56 : 48; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -55,14 +60,17 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-template <int D>
+template <int D, int kConsumers>
 struct FewCfg {
-    static constexpr int NS = D == 128 ? 4 : 8;
+    static constexpr int NS = (D == 128 ? 4 : 8) * kConsumers / 16;
     static constexpr int TILE = kUnit * D;                       // codes of K or V in a stage
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = OFF_K + NS * TILE;
-    static constexpr int OFF_SCR = OFF_V + NS * TILE;            // [warp][8][D] accumulators at an item's end
-    static constexpr int OFF_SC = OFF_SCR + kConsumers * 8 * D * 4;  // [stage][sk | sv][128]
+    // [warp][8][PITCH] accumulators at an item's end.  Two CTAs on an SM: rows 4 floats apart in the
+    // banks and odd groups' halves swapped, without which 8 lanes would store to one bank.
+    static constexpr int PITCH = kConsumers == 16 ? D : D + 4;
+    static constexpr int OFF_SCR = OFF_V + NS * TILE;
+    static constexpr int OFF_SC = OFF_SCR + kConsumers * 8 * PITCH * 4;  // [stage][sk | sv][128]
     static constexpr int OFF_ML = OFF_SC + NS * 2 * kUnit * 4;   // [m | l][warp][8]
     static constexpr int OFF_INFO = OFF_ML + 2 * kConsumers * 8 * 4;
     static constexpr int OFF_BAR = OFF_INFO + NS * 64;           // full[NS], empty[NS], written, read
@@ -80,6 +88,8 @@ struct FewCfg {
     __device__ static int chunk(int r, int ch) {
         return D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
     }
+    // Where channel ch of an accumulator's row lies.
+    __device__ static int scr(int ch) { return kConsumers == 16 ? ch : ch ^ ((D == 128 ? ch >> 6 : ch >> 3) & 1) * 4; }
     // First of the D/8 consecutive channels that rows n and n + 8 of the output tiles stand for.
     __device__ static int channel_of(int n) { return D == 128 ? ((n >> 1) + 4 * (n & 1)) * 16 : n * 8; }
 };
@@ -101,10 +111,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // SKIP: the test hook that leaves out the keys of unit a.skip_unit, in instances of its own.
 // SHARED: a pass of the attention over shared prefixes.
 template <int D, int RG, bool SKIP, bool SHARED>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(few_threads(SHARED ? kShortConsumers : kFewConsumers), SHARED ? 2 : 1)
     attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const AttnOf<SHARED> a, const CacheView c, void* ws) {
-    using C = FewCfg<D>;
+    constexpr int kConsumers = SHARED ? kShortConsumers : kFewConsumers, kFewThreads = few_threads(kConsumers);
+    using C = FewCfg<D, kConsumers>;
     constexpr int NS = C::NS, RT = 8 * RG;
     constexpr uint32_t ATTEMPTS = SKIP ? kHookAttempts : kWaitAttempts;
     // offsets from the array itself: through an integer the compiler would lose sight of
@@ -131,14 +142,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             part.head[2 * blockIdx.x + 1].parts = 0;
         }
     }
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < c.B; b += kFewThreads)
-            if (!seq_valid_in<SHARED>(c, a, b)) flag_invalid(c.dev_status);
-    if constexpr (SHARED)
-        if (blockIdx.x == 0)
-            for (int g = threadIdx.x; g < a.N; g += kFewThreads)
-                if (!group_valid(c, a, g)) flag_invalid(c.dev_status);
-    const Part p = plan_part<kFewThreads, SHARED>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
+    auto plan = [&] {
+        if constexpr (SHARED) {
+            if (a.pass == 1) wait_for_primary();  // the plan; the second pass starts when all of the first have it
+            return load_part(a.plan + (a.pass == 1 ? 0 : kMaxCtas * a.per_sm[0]) + blockIdx.x);
+        } else {
+            if (blockIdx.x == 0)
+                for (int b = threadIdx.x; b < c.B; b += kFewThreads)
+                    if (!seq_valid(c, b)) flag_invalid(c.dev_status);
+            return plan_part<kFewThreads>(c, a, RT, kItemCost, blockIdx.x, gridDim.x);
+        }
+    };
+    const auto p = plan();
     __syncthreads();
     launch_dependents();
     if (p.g0 == p.g1) {
@@ -148,7 +163,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
     const int box_log2 = min(c.page_log2, 7);  // runs of keys in one page
     if (warp >= kConsumers) {
-        regs_down<kFewRegsDown>();
+        regs_down<few_regs_down(kConsumers)>();
         // ------------------------------------------------------------ producers
         // Warps 0 and 1 of them load keys, 2 and 3 values, every other run of keys in one page
         // each (a run is a TMA load, and a thread's loads are issued one after the other: eight
@@ -170,7 +185,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const int pg = __ldg(c.table + (int64_t)w.table_row() * c.s_table + (k >> c.page_log2));
                 return pg < 0 ? -2 : pg;
             };
-            int ahead = entry(w.unit);
+            int ahead = -1;
+            Runs runs;
+            if constexpr (SHARED) runs.start(c, w, box_log2);
+            else ahead = entry(w.unit);
             if (role == 0)
                 // the item's queries on their way to L2 while the last item's units are under way
                 for (int i = lane; i < rows; i += 32) {
@@ -184,7 +202,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const int st = it % NS, key0 = u * kUnit;
                 const bool skip = SKIP && it == a.skip_unit && role < 2;
                 int pg = ahead;
-                ahead = entry(u + 1);
+                if constexpr (SHARED) pg = runs.at(c, w, u, box_log2);
+                else ahead = entry(u + 1);
                 if (pg == -2 || pg >= c.pages) {
                     flag_invalid(c.dev_status);
                     pg = -1;
@@ -249,8 +268,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             if (!SKIP || j != a.skip_unit) drain_wait_counted(full + 8 * (j % NS), (j / NS) & 1, left);
     } else {
         // ------------------------------------------------------------ consumers
-        regs_up<kFewRegsUp>();
-        constexpr int SLICES = RG <= 2 ? 8 : kConsumers / RG, SLICE = kUnit / SLICES;  // of a stage's keys
+        regs_up<few_regs_up(kConsumers)>();
+        constexpr int SLICES = kConsumers / RG < 8 ? kConsumers / RG : 8, SLICE = kUnit / SLICES;  // of a stage's keys
         constexpr int SETS = kConsumers / (RG * SLICES);  // sets of warps that take turns at the stages
         constexpr int KSTEPS = D / 16, MT = D / 16;
         const int g = lane >> 2, tig = lane & 3;
@@ -457,10 +476,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 // one maximum for both from here on
                 const float m = fmaxf(M[e], N[e]), wo = part_weight(M[e], m);
                 l[e] *= part_weight(N[e], m);
-                float* dst = scr + ((size_t)warp * 8 + 2 * tig + e) * D + C::channel_of(g);
+                float* dst = scr + ((size_t)warp * 8 + 2 * tig + e) * C::PITCH;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i)
-                    *reinterpret_cast<float4*>(dst + 4 * i) =
+                    *reinterpret_cast<float4*>(dst + C::scr(C::channel_of(g) + 4 * i)) =
                         make_float4(o[2 * i][e] * wo, o[2 * i][2 + e] * wo, o[2 * i + 1][e] * wo, o[2 * i + 1][2 + e] * wo);
                 if (g == 0) {
                     ml[warp * 8 + 2 * tig + e] = m;
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     const int at = at0 + s * RG * 8;
                     const float w = part_weight(ml[at], m);
                     lsum = fmaf(w, ml[kConsumers * 8 + at], lsum);
-                    const float4 u = *reinterpret_cast<const float4*>(scr + (size_t)at * D + ch);
+                    const float4 u = *reinterpret_cast<const float4*>(scr + (size_t)at * C::PITCH + C::scr(ch));
                     acc[0] = fmaf(w, u.x, acc[0]);
                     acc[1] = fmaf(w, u.y, acc[1]);
                     acc[2] = fmaf(w, u.z, acc[2]);
@@ -492,12 +511,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 if constexpr (SHARED) {
                     const int r = r0 + row, tok = r / a.G;
                     const int64_t whole = (int64_t)(q0 + tok) * (c.H * a.G) + h * a.G + r - tok * a.G;
-                    const int64_t at = split ? (int64_t)slot * RT + row : own_slot(RT, whole);
+                    const int64_t at = split ? (int64_t)slot * RT + row : own_slot(a, whole);
                     *reinterpret_cast<float4*>(part.o + at * D + ch) = make_float4(acc[0], acc[1], acc[2], acc[3]);
                     if (ch == 0) {
                         part.m[at] = m;
                         part.l[at] = lsum;
-                        if (!(flags & kHead)) part.word[whole] = row_word(blockIdx.x, on);
+                        if (!(flags & kHead)) part.word[whole] = row_word(row, blockIdx.x, on);
                     }
                 } else if (split) {
                     *reinterpret_cast<float4*>(part.o + ((size_t)slot * RT + row) * D + ch) =
@@ -658,25 +677,36 @@ vc_status launch_join(const PagedAttn& a, const CacheView& c, void* ws, int RT, 
                                 : cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, a, c, ws, RT, parts));
 }
 
-template <int D, int RG, bool SKIP = false, bool SHARED = false>
-vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const AttnOf<SHARED>& a, const CacheView& c, void* ws,
+template <int D, int RG, bool SKIP = false>
+vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c, void* ws,
                      int ctas, cudaStream_t st) {
-    auto kern = attn_few_kernel<D, RG, SKIP, SHARED>;
-    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), FewCfg<D>::SMEM);
+    auto kern = attn_few_kernel<D, RG, SKIP, false>;
+    constexpr int SMEM = FewCfg<D, kFewConsumers>::SMEM;
+    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), SMEM);
     if (s != VC_OK) return s;
-    if constexpr (SHARED) return launch_pass(kern, ctas, kFewThreads, FewCfg<D>::SMEM, a.pass, st, mk, mv, a, c, ws);
-    else kern<<<ctas, kFewThreads, FewCfg<D>::SMEM, st>>>(mk, mv, a, c, ws);
+    kern<<<ctas, few_threads(kFewConsumers), SMEM, st>>>(mk, mv, a, c, ws);
     return cuda_status(cudaGetLastError());
 }
 
+template <int D, int RG>
+vc_status launch_few_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, int ctas,
+                          cudaStream_t st) {
+    auto kern = attn_few_kernel<D, RG, false, true>;
+    constexpr int SMEM = FewCfg<D, kShortConsumers>::SMEM;
+    static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs on an SM");
+    vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), SMEM);
+    if (s != VC_OK) return s;
+    return launch_after(kern, dim3(ctas), few_threads(kShortConsumers), SMEM, st, mk, mv, a, c, (void*)nullptr);
+}
+
 template <int D>
-vc_status launch_pass_d(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, void* ws,
-                        cudaStream_t st) {
+vc_status launch_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, cudaStream_t st) {
+    const int ctas = kMaxCtas * a.per_sm[a.pass - 1];
     switch (a.rt[a.pass - 1]) {
-        case 8: return launch_few<D, 1, false, true>(mk, mv, a, c, ws, kMaxCtas, st);
-        case 16: return launch_few<D, 2, false, true>(mk, mv, a, c, ws, kMaxCtas, st);
-        case 32: return launch_few<D, 4, false, true>(mk, mv, a, c, ws, kMaxCtas, st);
-        default: return launch_attn_many(mk, mv, a, c, D, a.rt[a.pass - 1], kMaxCtas, ws, st);
+        case 8: return launch_few_pass<D, 1>(mk, mv, a, c, ctas, st);
+        case 16: return launch_few_pass<D, 2>(mk, mv, a, c, ctas, st);
+        case 32: return launch_few_pass<D, 4>(mk, mv, a, c, ctas, st);
+        default: return launch_attn_many(mk, mv, a, c, D, a.rt[a.pass - 1], ctas, st);
     }
 }
 
@@ -723,43 +753,106 @@ vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void*
 //
 // Two passes with kernels as above, each over the keys that are its own: pass 1 takes the rows of a
 // group's sequences together over the prefix, which is read once for all of them, pass 2 each
-// sequence over what follows.  Both leave unscaled results in the workspace, which a third launch
-// joins.  The second pass is launched to run beside the first one: the SMs are shared out by the
-// passes' lengths, so each finds about as many free as it has parts.
+// sequence over what follows.  A small launch before them plans both, both leave unscaled results in
+// the workspace, and a last one joins those.  The second pass is launched to run beside the first
+// one: the SMs are shared out by the passes' lengths, so each finds about as many free as it has
+// parts.
 
-// A unit's time in tiles of RT rows, in hundredths of microseconds.
-static int unit_time(int RT) { return RT <= 16 ? 80 : RT == 32 ? 100 : RT == 128 ? 120 : 200; }
-
-// A pass's part of the workspace.
-static size_t shared_bytes(int RT, int d, size_t rows) { return (shared_partials_bytes(RT, d, rows) + 255) & ~(size_t)255; }
-
-size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int N, int max_q, int max_rows) {
-    const int G = Hq / c.H;
-    size_t n = 0;
-    for (int pass = 1; pass <= 2; ++pass) {
-        const int RT = pass == 1 ? tile_rows(G, N > 0 ? N : 1, T, max_rows) : tile_rows(G, B, T, max_q);
-        n += shared_bytes(RT, c.d, (size_t)T * Hq);
-    }
-    return n;
+// Rows of a sequence (or group) of q tokens, as far as the caller told.
+static int64_t hinted_rows(int G, int n, int T, int hint) {
+    return (hint > 0 ? (int64_t)hint : ((int64_t)T + n - 1) / n) * G;
 }
 
-vc_status launch_attn_shared(const SharedAttn& args, const CacheView& c, int d, int max_rows, void* ws, cudaStream_t st) {
+// Rows of a tile of each pass.  Groups of over 128 rows are cut into tiles of one size, up to 256 rows.  What follows a prefix is short as a rule: up to
+// 64 rows of a sequence go to the kernel for few of them, in two tiles if need be (60 sequences of 8 to 56 rows
+// took 155 us of 23 SMs so, 155 us of 26 in tiles of 128).
+static int shared_rows(int G, int n, int T, int hint, int pass) {
+    n = n > 0 ? n : 1;
+    const int RT = tile_rows(G, n, T, hint);
+    const int64_t rows = hinted_rows(G, n, T, hint), tiles = (rows + 255) / 256;
+    if (pass == 2) return rows > 32 && rows <= 64 ? 32 : RT;
+    return RT == 256 ? (int)(((rows + tiles - 1) / tiles + 7) & ~(int64_t)7) : RT;
+}
+
+static int per_sm_of(int RT) { return RT <= 32 ? 2 : 1; }
+
+namespace {
+struct SharedWs {
+    size_t plan, parts[2], words, sums, bytes;
+};
+}  // namespace
+
+// Where the workspace's parts begin.
+static SharedWs shared_ws(const int (&rt)[2], int d, int64_t B, int64_t N, size_t rows) {
+    auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+    SharedWs w;
+    w.plan = 0;
+    w.parts[0] = up(sizeof(PlanPart) * kMaxCtas * (per_sm_of(rt[0]) + per_sm_of(rt[1])));
+    w.parts[1] = w.parts[0] + up(shared_partials_bytes(rt[0], per_sm_of(rt[0]), d, rows));
+    w.words = w.parts[1] + up(shared_partials_bytes(rt[1], per_sm_of(rt[1]), d, rows));
+    w.sums = w.words + up(2 * rows * sizeof(uint32_t));
+    w.bytes = w.sums + up((size_t)(B + N) * sizeof(int64_t));
+    return w;
+}
+
+// Whether one pass of every sequence over all its keys, as vc_attn_paged does it, is as fast: where nothing is
+// shared; where the whole work is small (the two launches more take 6 us); and where the sequences' own
+// rows fill their tiles, since then a prefix read once for all of them is a small part of the work.  The last
+// by the time of a unit of a sequence's tiles against that of as many rows in tiles of 256.  8 heads, 21,600
+// tokens in common, shared against one pass: 8 sequences of 160 rows 127 and 161 us, 4 of 300 rows
+// 147 and 169, 8 of 400 rows 325 and 304, 3 of 600 rows 211 and 189.
+static bool one_pass(const vc_cache_shape& c, int G, int B, int T, int N, int max_q, int cols) {
+    if (N < 1 || B <= N) return true;
+    const int64_t rows = hinted_rows(G, B, T, max_q);
+    const int RT = tile_rows(G, B, T, max_q);
+    const int64_t tiles = (rows + RT - 1) / RT, units = ((int64_t)cols * c.page_size + kUnit - 1) / kUnit;
+    if (B * c.H * tiles * units <= kMaxCtas * 10) return true;
+    if (rows <= 64) return false;
+    const int64_t last = rows % 256, alone = rows / 256 * 195 + (last > 128 ? 195 : last ? 120 : 0);
+    return rows * 195 >= 256 * alone * 3 / 4;
+}
+
+size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int N, int max_q, int max_rows) {
+    const size_t one = attn_paged_workspace(c, Hq, B, T, max_q);
+    if (one_pass(c, Hq / c.H, B, T, N, max_q, 1 << 30)) return one;
+    const int G = Hq / c.H, rt[2] = {shared_rows(G, N, T, max_rows, 1), shared_rows(G, B, T, max_q, 2)};
+    const size_t two = shared_ws(rt, c.d, B, N, (size_t)T * Hq).bytes;
+    return one > two ? one : two;  // which of the two is taken depends on the table's columns too
+}
+
+// The time of a unit on an SM, in hundredths of microseconds, and what an item costs besides, in units.
+static int unit_time(int RT) { return RT <= 16 ? 45 : RT == 32 ? 185 : RT <= 128 ? 120 : 195; }
+static int item_units(int RT) { return RT <= 16 ? 3 : RT == 32 ? 1 : RT <= 128 ? 10 : kManyItemCost; }
+
+vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape, const CacheView& c, int max_rows, void* ws,
+                             cudaStream_t st) {
+    const int d = shape.d;
+    if (one_pass(shape, args.G, c.B, c.T, args.N, args.max_q, c.cols)) {
+        // (that launch is for the report alone)
+        const vc_status s = c.dev_status ? launch_shared_check(args, c, st) : VC_OK;
+        return s == VC_OK ? launch_attn_paged(args, c, d, ws, st) : s;
+    }
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, c.K8, d, c) || !make_cache_map(&mv, c.V8, d, c)) return VC_ERR_CUDA;
     SharedAttn a = args;
-    a.rt[0] = tile_rows(a.G, a.N > 0 ? a.N : 1, c.T, max_rows);
-    a.rt[1] = tile_rows(a.G, c.B, c.T, a.max_q);
+    a.rt[0] = shared_rows(a.G, a.N, c.T, max_rows, 1);
+    a.rt[1] = shared_rows(a.G, c.B, c.T, a.max_q, 2);
     for (int i = 0; i < 2; ++i) {
-        a.ic[i] = a.rt[i] <= 32 ? kItemCost : kManyItemCost;
+        a.ic[i] = item_units(a.rt[i]);
         a.unit[i] = unit_time(a.rt[i]);
+        a.per_sm[i] = per_sm_of(a.rt[i]);
     }
-    void* const at[2] = {ws, static_cast<uint8_t*>(ws) + shared_bytes(a.rt[0], d, (size_t)c.T * c.H * a.G)};
-    for (a.pass = 1; a.pass <= 2; ++a.pass) {
-        const vc_status s = d == 128 ? launch_pass_d<128>(mk, mv, a, c, at[a.pass - 1], st)
-                                     : launch_pass_d<64>(mk, mv, a, c, at[a.pass - 1], st);
-        if (s != VC_OK) return s;
-    }
-    return launch_shared_join(a, c, d, at[0], at[1], st);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    const SharedWs w = shared_ws(a.rt, d, c.B, a.N, (size_t)c.T * c.H * a.G);
+    a.plan = reinterpret_cast<PlanPart*>(base + w.plan);
+    a.parts1 = reinterpret_cast<float*>(base + w.parts[0]);
+    a.parts2 = reinterpret_cast<float*>(base + w.parts[1]);
+    a.words = reinterpret_cast<uint32_t*>(base + w.words);
+    a.sums = reinterpret_cast<int64_t*>(base + w.sums);
+    vc_status s = launch_shared_plan(a, c, st);
+    for (a.pass = 1; s == VC_OK && a.pass <= 2; ++a.pass)
+        s = d == 128 ? launch_pass<128>(mk, mv, a, c, st) : launch_pass<64>(mk, mv, a, c, st);
+    return s == VC_OK ? launch_shared_join(a, c, d, st) : s;
 }
 
 }  // namespace vc

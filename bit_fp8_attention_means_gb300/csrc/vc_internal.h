@@ -98,8 +98,14 @@ struct PagedAttn {
 struct SharedAttn : PagedAttn {  // attention over shared prefixes
     const int32_t* groups;  // [N + 1] runs of sequences
     const int32_t* prefix;  // [N]
-    // the pass of this launch; of pass 1 and 2 the rows of a tile, an item's own cost in units, a unit's relative time
-    int N, pass, rt[2], ic[2], unit[2];
+    // the pass of this launch; of pass 1 and 2 the rows of a tile, an item's own cost in units, the time of a unit on an
+    // SM, the CTAs on an SM
+    int N, pass, rt[2], ic[2], unit[2], per_sm[2];
+    // workspace: the CTAs' parts of both passes, their results, the rows' words, the planning kernel's sums
+    struct PlanPart* plan;
+    float *parts1, *parts2;
+    uint32_t* words;
+    int64_t* sums;
 };
 vc_status launch_cache_append(const uint16_t* K, const uint16_t* V, int64_t s_n, int64_t s_h, int d,
                               const CacheView& c, cudaStream_t st);
@@ -109,15 +115,18 @@ size_t attn_paged_workspace(const vc_cache_shape& c, int Hq, int B, int T, int m
 vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void* ws, cudaStream_t st);
 // over shared prefixes, `a` without what the passes need
 size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int N, int max_q, int max_rows);
-vc_status launch_attn_shared(const SharedAttn& a, const CacheView& c, int d, int max_rows, void* ws, cudaStream_t st);
-// joins the passes' results (vc_attn_shared.cu)
-vc_status launch_shared_join(const SharedAttn& a, const CacheView& c, int d, void* ws1, void* ws2, cudaStream_t st);
+vc_status launch_attn_shared(const SharedAttn& a, const vc_cache_shape& shape, const CacheView& c, int max_rows, void* ws,
+                             cudaStream_t st);
+// looks the batch and its groups over; plans the passes; joins their results (vc_attn_shared.cu)
+vc_status launch_shared_check(const SharedAttn& a, const CacheView& c, cudaStream_t st);
+vc_status launch_shared_plan(const SharedAttn& a, const CacheView& c, cudaStream_t st);
+vc_status launch_shared_join(const SharedAttn& a, const CacheView& c, int d, cudaStream_t st);
 constexpr int kManyItemCost = 7;   // see vc_attn_chunk.cu
 // its kernel for many rows, in tiles of RT = 128 or 256 (vc_attn_chunk.cu)
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, void* ws, cudaStream_t st);
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c,
-                           int d, int RT, int ctas, void* ws, cudaStream_t st);
+                           int d, int RT, int ctas, cudaStream_t st);
 
 // rotary positions (vc_rope.cu)
 struct RopeRows {

@@ -254,58 +254,32 @@ struct Part {
     int parts;
 };
 
-// Length of a pass's line; called by all NT threads of a block, the same in all of them.
-template <int NT>
-__device__ __forceinline__ int64_t line_length(const CacheView& c, const SharedAttn& a, int pass) {
-    const int RT = pass == 1 ? a.rt[0] : a.rt[1], IC = pass == 1 ? a.ic[0] : a.ic[1];
-    __shared__ int64_t sums[NT / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = seq_count<true>(c, a, pass);
-    int64_t mine = 0;
-    if ((int64_t)c.T * a.G > (int64_t)n * RT * 4) {
-        for (int b = warp; b < n; b += NT / 32) {
-            const int64_t u = seq_cost_warp<true>(a, seq_of<true>(c, a, b, pass), RT, IC, pass);
-            if (lane == 0) mine += u * c.H;
-        }
-    } else {
-        for (int b = threadIdx.x; b < n; b += NT) mine += seq_cost<true>(c, a, b, RT, IC, pass) * c.H;
-    }
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < NT / 32; ++w) total += sums[w];
-    return total;
-}
-
 // Called by all NT threads of a block; the result is the same in all of them.
 // Two passes over the sequences, NT at a time: the total, then the one that
 // holds g0.  Sequences of many tiles are added up by a warp each.
-// SHARED: the two passes run side by side, each on a share of the SMs that goes by its length and what
-// a unit costs it.
-template <int NT, bool SHARED>
-__device__ __forceinline__ Part plan_part(const CacheView& c, const AttnOf<SHARED>& a, int RT, int IC, int part, int parts) {
+template <int NT>
+__device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a, int RT, int IC, int part, int parts) {
     __shared__ int64_t warp_sum[NT / 32];
     __shared__ int64_t cost[NT];
     __shared__ Part found;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int pass = pass_of(a), seqs = seq_count<SHARED>(c, a, pass);
-    const bool by_warp = (int64_t)c.T * a.G > (int64_t)seqs * RT * 4;
+    const bool by_warp = (int64_t)c.T * a.G > (int64_t)c.B * RT * 4;
     // cost of sequence b0 + threadIdx.x
     auto costs = [&](int b0) -> int64_t {
         if (by_warp) {
-            for (int i = warp; i < NT && b0 + i < seqs; i += NT / 32) {
-                const int64_t u = seq_cost_warp<SHARED>(a, seq_of<SHARED>(c, a, b0 + i, pass), RT, IC, pass);
+            for (int i = warp; i < NT && b0 + i < c.B; i += NT / 32) {
+                const int64_t u = seq_cost_warp<false>(a, seq_info(c, b0 + i), RT, IC, 0);
                 if (lane == 0) cost[i] = u * c.H;
             }
             __syncthreads();
-            return b0 + (int)threadIdx.x < seqs ? cost[threadIdx.x] : 0;
+            return b0 + (int)threadIdx.x < c.B ? cost[threadIdx.x] : 0;
         }
-        return b0 + (int)threadIdx.x < seqs ? seq_cost<SHARED>(c, a, b0 + threadIdx.x, RT, IC, pass) * c.H : 0;
+        return b0 + (int)threadIdx.x < c.B ? seq_cost<false>(c, a, b0 + threadIdx.x, RT, IC, 0) * c.H : 0;
     };
     if (threadIdx.x == 0) found = Part{};
     const int64_t first_u = costs(0);
     int64_t mine = first_u;
-    for (int b0 = NT; b0 < seqs; b0 += NT) {
+    for (int b0 = NT; b0 < c.B; b0 += NT) {
         __syncthreads();
         mine += costs(b0);
     }
@@ -315,17 +289,6 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const AttnOf<SHARE
     int64_t total = 0;
     for (int w = 0; w < NT / 32; ++w) total += warp_sum[w];
     Part p;
-    if constexpr (SHARED) {
-        const bool first = pass == 1;
-        const int64_t mine_w = total * (first ? a.unit[0] : a.unit[1]);
-        const int64_t other_w = line_length<NT>(c, a, 3 - pass) * (first ? a.unit[1] : a.unit[0]);
-        // pass 1's share, rounded; both have one part at least where they have work
-        const int64_t w1 = first ? mine_w : other_w, w2 = first ? other_w : mine_w;
-        int p1 = w1 ? (int)((w1 * parts + (w1 + w2) / 2) / (w1 + w2)) : 0;
-        if (w1) p1 = max(p1, 1);
-        if (w2) p1 = min(p1, parts - 1);
-        parts = first ? p1 : parts - p1;
-    }
     if (total < parts) parts = (int)total;  // no empty part between two others
     p.b = 0;
     p.off = 0;
@@ -338,7 +301,7 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const AttnOf<SHARE
     p.g0 = div_small(total * part, parts);
     p.g1 = div_small(total * (part + 1), parts);
     int64_t before = 0;  // cost of the sequences of earlier rounds
-    for (int b0 = 0; b0 < seqs; b0 += NT) {
+    for (int b0 = 0; b0 < c.B; b0 += NT) {
         __syncthreads();
         const int64_t u = b0 ? costs(b0) : first_u;
         int64_t scan = u;
@@ -367,9 +330,24 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const AttnOf<SHARE
     return p;
 }
 
+// SHARED: a CTA's part as the planning kernel leaves it, with the item that g0 lies in.
+struct PlanPart {
+    int64_t g0, g1, total;
+    int parts, b, h, tile, off;  // off: g0's place in the item
+    SeqPass s;
+};
+static_assert(sizeof(PlanPart) == 64, "two sectors");
+// The part in L2: no copy that an SM may hold of earlier contents.
+__device__ __forceinline__ PlanPart load_part(const PlanPart* p) {
+    PlanPart r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<int4*>(&r)[i] = __ldcg(reinterpret_cast<const int4*>(p) + i);
+    return r;
+}
+
 // Walks the items of a CTA's part that have units in it, in order.  For whole
 // warps; all members are uniform over the warp.
-template <int IC, bool SHARED>
+template <int IC0, bool SHARED>
 struct ItemWalk {
     int64_t at, left;  // place in the line, and what is left of the part
     int b, h, tile;  // the item
@@ -377,6 +355,7 @@ struct ItemWalk {
     ItemRange r;
     int unit, end;   // units [unit, end) of 128 keys, of this item in this part
     int64_t item_end;  // the item's end in the line
+    int own;         // SHARED: an item's own cost (IC0 without)
     bool head;       // an earlier CTA has the item's first units
     bool tail;       // a later CTA has its last units
 
@@ -385,15 +364,20 @@ struct ItemWalk {
         else return b;
     }
     // Parts from this one on that have units of the item.
-    __device__ int parts_on(const Part& p, int part) const {
+    template <class P>
+    __device__ int parts_on(const P& p, int part) const {
         return tail ? (int)div_small(item_end * p.parts - 1, p.total) - part + 1 : 1;
+    }
+    __device__ int cost() const {
+        if constexpr (SHARED) return own;
+        else return IC0;
     }
     // To the first item; false where the part holds no unit at all.
     __device__ bool start(const CacheView& c, const AttnOf<SHARED>& a, int RT, const Part& p) {
         at = p.g0;
         left = p.g1 - p.g0;
         b = p.b;
-        const int pass = pass_of(a);
+        const int pass = pass_of(a), IC = IC0;
         s = seq_of<SHARED>(c, a, b, pass);
         const int64_t per_head = seq_cost_warp<SHARED>(a, s, RT, IC, pass);
         h = (int)div_small(p.off, per_head);
@@ -418,9 +402,22 @@ struct ItemWalk {
         r = item_range<SHARED>(a, s, tile, RT, pass_of(a));
         return take((int)off) || next(c, a, RT);
     }
+    __device__ bool start(const CacheView& c, const AttnOf<SHARED>& a, int RT, const PlanPart& p) {
+        at = p.g0;
+        left = p.g1 - p.g0;
+        b = p.b;
+        h = p.h;
+        tile = p.tile;
+        if constexpr (SHARED) {
+            s = p.s;
+            own = a.pass == 1 ? a.ic[0] : a.ic[1];
+        }
+        r = item_range<SHARED>(a, s, tile, RT, pass_of(a));
+        return take(p.off) || next(c, a, RT);
+    }
     // The item from place `off` of its length on; false where that holds none of its units.
     __device__ bool take(int off) {
-        const int u = r.units(), all = u + IC;
+        const int IC = cost(), u = r.units(), all = u + IC;
         const int to = left < all - off ? off + (int)left : all;
         item_end = at + all - off;
         at += to - off;
@@ -472,21 +469,15 @@ struct Partials {
 // SHARED: every row's result goes there, those of items that are not cut to a slot of the row's own
 // behind the others', and the part that an item begins in leaves a word for each of its rows.
 struct SharedPartials {
-    float* m;          // [2 * kMaxCtas * RT + rows]
+    float* m;          // [slots + rows]
     float* l;
-    float* o;          // [2 * kMaxCtas * RT + rows][D]
+    float* o;          // [slots + rows][D]
     uint32_t* word;    // [rows]
 };
 
 inline __host__ __device__ size_t partials_bytes(int RT, int D) {
     return 2 * (size_t)kMaxCtas * (32 + (size_t)RT * (D + 2) * sizeof(float));
 }
-inline __host__ __device__ size_t shared_partials_bytes(int RT, int D, size_t rows) {
-    return ((2 * (size_t)kMaxCtas * RT + rows) * (D + 2) + rows) * sizeof(float);
-}
-static_assert(sizeof(PartHeader) <= 32, "header slots");
-static_assert(kMaxCtas < 256, "parts of an item in a row's word");
-
 inline __host__ __device__ Partials partials_at(void* ws, int RT, int D) {
     Partials p;
     p.o = static_cast<float*>(ws);
@@ -496,25 +487,66 @@ inline __host__ __device__ Partials partials_at(void* ws, int RT, int D) {
     return p;
 }
 
-inline __host__ __device__ SharedPartials shared_partials_at(void* ws, int RT, int D, size_t rows) {
-    const size_t slots = 2 * (size_t)kMaxCtas * RT + rows;
+// SHARED: rows of the slots of a pass.
+inline __host__ __device__ int64_t slot_rows(int RT, int per_sm) { return 2 * (int64_t)kMaxCtas * per_sm * RT; }
+inline __host__ __device__ size_t shared_partials_bytes(int RT, int per_sm, int D, size_t rows) {
+    return (slot_rows(RT, per_sm) + rows) * (D + 2) * sizeof(float);
+}
+__device__ __forceinline__ SharedPartials shared_partials(const CacheView& c, const SharedAttn& a, int pass, int D) {
+    const size_t rows = (size_t)c.T * c.H * a.G, slots = slot_rows(pass == 1 ? a.rt[0] : a.rt[1], pass == 1 ? a.per_sm[0] : a.per_sm[1]) + rows;
     SharedPartials p;
-    p.o = static_cast<float*>(ws);
+    p.o = pass == 1 ? a.parts1 : a.parts2;
     p.m = p.o + slots * D;
     p.l = p.m + slots;
-    p.word = reinterpret_cast<uint32_t*>(p.l + slots);
+    p.word = a.words + (pass == 1 ? 0 : rows);
     return p;
 }
 template <bool SHARED>
-__device__ __forceinline__ auto partials_of(const CacheView& c, const PagedAttn& a, void* ws, int RT, int D) {
-    if constexpr (SHARED) return shared_partials_at(ws, RT, D, (size_t)c.T * c.H * a.G);
+__device__ __forceinline__ auto partials_of(const CacheView& c, const AttnOf<SHARED>& a, void* ws, int RT, int D) {
+    if constexpr (SHARED) return shared_partials(c, a, a.pass, D);
     else return partials_at(ws, RT, D);
 }
 
-// SHARED: the word of a row whose item begins in CTA i and has parts in n CTAs (n = 1: not cut).
-__device__ __forceinline__ uint32_t row_word(int cta, int parts) { return (uint32_t)cta << 8 | (uint32_t)parts; }
+// SHARED: the word of row `in` of its tile, whose item begins in CTA i and has parts in n CTAs (n = 1: not cut);
+// 0: the pass has nothing for the row.
+__device__ __forceinline__ uint32_t row_word(int in, int cta, int parts) { return (uint32_t)in << 20 | (uint32_t)cta << 10 | (uint32_t)parts; }
+static_assert(2 * kMaxCtas < 1024, "fields of a row's word");
 // A row's own place.
-__device__ __forceinline__ int64_t own_slot(int RT, int64_t row) { return 2 * (int64_t)kMaxCtas * RT + row; }
+__device__ __forceinline__ int64_t own_slot(const SharedAttn& a, int64_t row) {
+    return (a.pass == 1 ? slot_rows(a.rt[0], a.per_sm[0]) : slot_rows(a.rt[1], a.per_sm[1])) + row;
+}
+
+// Pages of runs of keys, looked up by a warp for 32 runs at a time and one such batch ahead: a table
+// entry is 0.3 to 1 us away, as long as a unit takes.  -1: a run that no row sees, -2: no page.
+struct Runs {
+    int cur, nxt, base;  // entries of the units base .. base + 32 / boxes - 1, and of as many behind
+    template <class Walk>
+    __device__ __forceinline__ int load(const CacheView& c, const Walk& w, int unit, int box_log2) const {
+        const int boxes_log2 = 7 - box_log2;
+        const int k = ((unit << boxes_log2) + (int)(threadIdx.x & 31)) << box_log2;
+        if (k >= w.end * kUnit || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
+        const int pg = __ldg(c.table + (int64_t)w.table_row() * c.s_table + (k >> c.page_log2));
+        return pg < 0 ? -2 : pg;
+    }
+    template <class Walk>
+    __device__ __forceinline__ void start(const CacheView& c, const Walk& w, int box_log2) {
+        base = w.unit;
+        cur = load(c, w, base, box_log2);
+        nxt = load(c, w, base + (32 >> (7 - box_log2)), box_log2);
+    }
+    // The entry of run `lane` of unit u (u ascending by one), -1 in lanes without a run.
+    template <class Walk>
+    __device__ __forceinline__ int at(const CacheView& c, const Walk& w, int u, int box_log2) {
+        const int boxes_log2 = 7 - box_log2, per = 32 >> boxes_log2, lane = threadIdx.x & 31;
+        if (u == base + per) {
+            base = u;
+            cur = nxt;
+            nxt = load(c, w, base + per, box_log2);
+        }
+        const int pg = __shfl_sync(0xffffffffu, cur, ((u - base) << boxes_log2) + lane);
+        return lane < (1 << boxes_log2) ? pg : -1;
+    }
+};
 
 // 1 / l for a row's sum: 0 for a row that saw nothing, NaN kept.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : __frcp_rn(l); }
@@ -590,19 +622,19 @@ __device__ __forceinline__ void store_lse(const PagedAttn& a, const CacheView& c
     if (a.lse) a.lse[(int64_t)(q0 + r / a.G) * (c.H * a.G) + h * a.G + r % a.G] = lse_of(m, l);
 }
 
-// Launches a pass of the attention over shared prefixes; the second one while the first one runs.
+// Launches `kern`, which itself waits for what it needs of the kernel before it, while that one runs.
 template <class... P, class... A>
-vc_status launch_pass(void (*kern)(P...), int ctas, int threads, int smem, int pass, cudaStream_t st, const A&... args) {
+vc_status launch_after(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
-    cfg.numAttrs = pass == 2 ? 1 : 0;
+    cfg.numAttrs = 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
 }
 

@@ -447,21 +447,6 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const CacheView c, const
     if (me == 0 && count) *count = used;
 }
 
-// Launches `kern`, which waits for the kernel before it, while that one runs.
-template <class... P, class... A>
-vc_status launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t st, A... args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, kern, args...));
-}
-
 // Blocks of 256 over the columns of a row, the rows being the grid's other side.
 unsigned col_blocks(int cols, int rows) {
     const int want = (cols + 255) / 256, room = rows >= 2048 ? 1 : 2048 / rows;
@@ -507,7 +492,7 @@ vc_status launch_pages_reserve(const CacheView& c, int d, const Pool& pool, void
     ws.off = ws.to + c.B;
     reserve_kernel<<<1, kPlan, 0, st>>>(c, pool, ws);
     if (cudaGetLastError() != cudaSuccess) return VC_ERR_CUDA;
-    return launch_after(copy_begun_kernel, dim3(c.B, c.B >= 304 ? 1 : 4), kCopy, st, c, ws, tok_log2_of(d));
+    return launch_after(copy_begun_kernel, dim3(c.B, c.B >= 304 ? 1 : 4), kCopy, 0, st, c, ws, tok_log2_of(d));
 }
 
 vc_status launch_cache_copy(const CacheView& s, const CacheView& t, int d, const int32_t* from, const int32_t* to,
@@ -527,7 +512,7 @@ vc_status launch_pages_compact(const CacheView& c, int d, const Pool& pool, int3
     ws.to = ws.from + c.pages / 2;
     compact_plan_kernel<<<1, kPlan, 0, st>>>(pool, c.pages, ws);
     if (cudaGetLastError() != cudaSuccess) return VC_ERR_CUDA;
-    return launch_after(compact_kernel, dim3(kMaxCtas * 8), kCopy, st, c, pool, ws, count, tok_log2_of(d));
+    return launch_after(compact_kernel, dim3(kMaxCtas * 8), kCopy, 0, st, c, pool, ws, count, tok_log2_of(d));
 }
 
 }  // namespace vc

@@ -400,16 +400,14 @@ def alloc_cache(pages, page_size, H, d, device):
     return c
 
 
-def _cache_parts(cache):
-    """Checks a dict of K8, sk, V8, sv (see alloc_cache): its vc_cache_shape, the four pointers, the device's index."""
-    K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
-    shape, k, t = K8.shape, K8.stride(), sk.stride()
-    if len(shape) != 4 or K8.dtype is not _U8 or V8.dtype is not _U8 or V8.shape != shape:
+@functools.lru_cache(maxsize=256)
+def _cache_shape(shape, v_shape, sk_shape, sv_shape, k, v, t, u):
+    """Checks the shapes and strides of K8, V8, sk, sv: their vc_cache_shape, which depends on these numbers alone."""
+    if len(shape) != 4 or v_shape != shape:
         raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
     pages, H, page, d = shape
-    if sk.dtype is not _F32 or sv.dtype is not _F32 or sk.shape != (pages, H, page) or sv.shape != (pages, H, page):
+    if sk_shape != (pages, H, page) or sv_shape != (pages, H, page):
         raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
-    v, u = V8.stride(), sv.stride()
     if pages < 2 or H < 2:  # a dimension of one element may have any stride: it gets a legal one
         k, v = _plain_strides(shape, k, d), _plain_strides(shape, v, d)
         t, u = _plain_strides(shape[:3], t, page), _plain_strides(shape[:3], u, page)
@@ -417,11 +415,22 @@ def _cache_parts(cache):
         raise ValueError("K8 and V8, and sk and sv, must share strides")
     if (k[3] != 1 or t[2] != 1) and min(shape) > 0:
         raise ValueError("channels and the scales' tokens must be contiguous")
+    return VcCacheShape(pages, page, H, d, k[0], k[1], k[2], t[0], t[1])
+
+
+def _cache_parts(cache):
+    """Checks a dict of K8, sk, V8, sv (see alloc_cache): its vc_cache_shape (not to be changed), the four pointers,
+    the device's index."""
+    K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
+    if K8.dtype is not _U8 or V8.dtype is not _U8:
+        raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
+    if sk.dtype is not _F32 or sv.dtype is not _F32:
+        raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
+    s = _cache_shape(K8.shape, V8.shape, sk.shape, sv.shape, K8.stride(), V8.stride(), sk.stride(), sv.stride())
     dev = K8.get_device()
     if V8.get_device() != dev or sk.get_device() != dev or sv.get_device() != dev:
         raise ValueError("the cache's tensors are on different devices")
-    return (VcCacheShape(pages, page, H, d, k[0], k[1], k[2], t[0], t[1]),
-            (K8.data_ptr(), sk.data_ptr(), V8.data_ptr(), sv.data_ptr()), dev)
+    return s, (K8.data_ptr(), sk.data_ptr(), V8.data_ptr(), sv.data_ptr()), dev
 
 
 def _plain_strides(shape, strides, unit):
@@ -431,7 +440,7 @@ def _plain_strides(shape, strides, unit):
 
 def cache_shape_of(cache) -> VcCacheShape:
     """The vc_cache_shape of a dict of K8, sk, V8, sv (see alloc_cache)."""
-    return _cache_parts(cache)[0]
+    return VcCacheShape.from_buffer_copy(_cache_parts(cache)[0])
 
 
 def _batch_of(cu, kv_len, table, T, dev) -> VcBatch:
@@ -634,17 +643,16 @@ def vc_attn_paged_shared(Q, cache, cu, kv_len, table, groups, prefix, softmax_sc
     N = prefix.numel()
     runs = _int32_vector("groups", groups, N + 1, dev), _int32_vector("prefix", prefix, N, dev)
     status = _status_ptr(dev_status, dev)
-    _need_cuda(dev)
-    _check_stream(stream, dev)
-    if _is_other(stream):
+    _check_place(stream, dev)
+    if stream is not None and _is_other(stream):
         return _on_stream(stream, vc_attn_paged_shared, Q, cache, cu, kv_len, table, groups, prefix, softmax_scale, causal,
                           max_q, max_rows, O, lse, workspace, dev_status)
     max_q, max_rows = _int32(max_q), _int32(max_rows)
     if 0 < softmax_scale < _LEAST_FP32:  # as fp32 it would be 0, the default
         softmax_scale = _LEAST_FP32
     if O is None:
-        O = torch.empty(shape, dtype=_BF16, device=dev)
         o_strides = (Hq * d, d)
+        O = _new_rows(Q, q_strides == o_strides, dev)
     else:
         o_strides = _rows("O", O, Hq, d, dev)
         if O.shape != shape:
@@ -664,6 +672,17 @@ def vc_attn_paged_shared(Q, cache, cu, kv_len, table, groups, prefix, softmax_sc
                 O.data_ptr(), *o_strides, lse.data_ptr(), workspace.data_ptr(),
                 workspace.numel() * workspace.element_size(), status), "vc_attn_paged_shared")
     return O, lse
+
+
+def _new_rows(x, contiguous, dev):
+    """A new contiguous tensor of x's shape and type (half the time of the general call where x is contiguous itself)."""
+    return torch.empty_like(x) if contiguous else torch.empty(x.shape, dtype=_BF16, device=dev)
+
+
+def _check_place(stream, dev):
+    _need_cuda(dev)
+    if stream is not None:
+        _check_stream(stream, dev)
 
 
 # ------------------------------------------------------------ rotary positions
@@ -719,7 +738,7 @@ def _rope_spec(rope, dev):
 
 def _int32_vector(name, t, n, dev):
     """Checks an int32 vector of n elements: its pointer."""
-    if t.dtype is not _I32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not _I32 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ValueError("%s must be contiguous int32 [%d]" % (name, n))
     if t.get_device() != dev:
         raise ValueError("%s is not on the other tensors' device" % name)
@@ -745,13 +764,12 @@ def vc_rope(X, rope, pos=None, cu=None, kv_len=None, inverse=0, out=None, dev_st
     B = 0 if cu is None else kv_len.numel()
     batch = (None, None) if cu is None else (_int32_vector("cu", cu, B + 1, dev), _int32_vector("kv_len", kv_len, B, dev))
     status = _status_ptr(dev_status, dev)
-    _need_cuda(dev)
-    _check_stream(stream, dev)
-    if _is_other(stream):
+    _check_place(stream, dev)
+    if stream is not None and _is_other(stream):
         return _on_stream(stream, vc_rope, X, rope, pos, cu, kv_len, inverse, out, dev_status)
     if out is None:
-        out = torch.empty((T, H, d), dtype=_BF16, device=dev)
         o_strides = (H * d, d)
+        out = _new_rows(X, strides == o_strides, dev)
     else:
         o_strides = _rows("out", out, H, d, dev)
         if out.shape[0] != T:
@@ -784,17 +802,16 @@ def vc_cache_append_rope(Q, K, V, cache, cu, kv_len, table, rope, pos=None, out=
     spec = _rope_spec(rope, dev)
     at = None if pos is None else _int32_vector("pos", pos, T, dev)
     status = _status_ptr(dev_status, dev)
-    _need_cuda(dev)
-    _check_stream(stream, dev)
-    if _is_other(stream):
+    _check_place(stream, dev)
+    if stream is not None and _is_other(stream):
         return _on_stream(stream, vc_cache_append_rope, Q, K, V, cache, cu, kv_len, table, rope, pos, out, dev_status)
     if out is not None:
         o_strides = _rows("out", out, Hq, s.d, dev)
         if out.shape[0] != T:
             raise ValueError("out must have Q's shape")
     elif Q is not None:
-        out = torch.empty((T, Hq, s.d), dtype=_BF16, device=dev)
         o_strides = (Hq * s.d, s.d)
+        out = _new_rows(Q, q_strides == o_strides, dev)
     _on_device(dev, stream, L.vc_cache_append_rope,
                (None if Q is None else Q.data_ptr(), *q_strides, Hq, K.data_ptr(), V.data_ptr(), *strides, s, K8, sk, V8, sv,
                 batch, spec, at, None if out is None else out.data_ptr(), *o_strides, status), "vc_cache_append_rope")
@@ -819,11 +836,12 @@ def _pool_of(pool, pages, dev) -> VcPool:
 
 def _table_of(name, table, dev):
     """Checks an int32 [rows, cols] table: its pointer and what the C calls take beside it (stride, rows, cols)."""
-    if table.dtype is not _I32 or table.dim() != 2:
+    shape = table.shape
+    if table.dtype is not _I32 or len(shape) != 2:
         raise ValueError("%s must be int32 [rows, cols]" % name)
     if table.get_device() != dev:
         raise ValueError("%s is not on the cache's device" % name)
-    (rows, cols), (s, one) = table.shape, table.stride()
+    (rows, cols), (s, one) = shape, table.stride()
     if one != 1 and cols > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
     return table.data_ptr(), s if rows > 1 else max(cols, 1), rows, cols
@@ -851,6 +869,13 @@ def _launch_side(stream, call):
         call()
 
 
+@functools.lru_cache(maxsize=256)
+def _reserve_bytes(page_size, B, T):
+    """vc_pages_reserve_workspace, which depends on these numbers alone."""
+    return max(lib().vc_pages_reserve_workspace(VcCacheShape(1, page_size, 1, 64, page_size * 64, page_size * 64, 64, page_size,
+                                                             page_size), B, T), 256)
+
+
 def vc_pages_reserve(cache, pool, cu, kv_len, table, T, workspace=None, dev_status=None, stream=None):
     """Pages of their own for the tokens of a call (cu, kv_len, table as that call gets them, T rows in all): entries of
     -1 in `table` get the lowest free pages of `pool` (see alloc_pool), pages that others name too are replaced by a
@@ -860,11 +885,10 @@ def vc_pages_reserve(cache, pool, cu, kv_len, table, T, workspace=None, dev_stat
     batch = _batch_of(cu, kv_len, table, T, dev)
     p = _pool_of(pool, s.pages, dev)
     status = _status_ptr(dev_status, dev)
-    _need_cuda(dev)
-    _check_stream(stream, dev)
-    if _is_other(stream):
+    _check_place(stream, dev)
+    if stream is not None and _is_other(stream):
         return _launch_side(stream, lambda: vc_pages_reserve(cache, pool, cu, kv_len, table, T, workspace, dev_status))
-    workspace = _given_workspace(workspace, L.vc_pages_reserve_workspace(s, batch.B, T), dev)
+    workspace = _given_workspace(workspace, _reserve_bytes(s.page_size, batch.B, T), dev)
     _on_device(dev, stream, L.vc_pages_reserve, (s, K8, sk, V8, sv, p, batch, workspace.data_ptr(),
                                                  workspace.numel() * workspace.element_size(), status), "vc_pages_reserve")
 
@@ -881,8 +905,7 @@ def vc_pages_fork(cache, pool, table, kv_len, parents, new_table, new_len, lens=
     args = (s, p, at, s_table, B, cols, _int32_vector("kv_len", kv_len, B, dev), _int32_vector("parents", parents, N, dev),
             None if lens is None else _int32_vector("lens", lens, N, dev), N, to, s_new, new_cols,
             _int32_vector("new_len", new_len, N, dev), _status_ptr(dev_status, dev))
-    _need_cuda(dev)
-    _check_stream(stream, dev)
+    _check_place(stream, dev)
     _on_device(dev, stream, L.vc_pages_fork, args, "vc_pages_fork")
 
 
@@ -895,8 +918,7 @@ def vc_pages_trim(cache, pool, table, kv_len, lens, dev_status=None, stream=None
     at, s_table, B, cols = _table_of("table", table, dev)
     args = (s, p, at, s_table, B, cols, _int32_vector("kv_len", kv_len, B, dev), _int32_vector("lens", lens, B, dev),
             _status_ptr(dev_status, dev))
-    _need_cuda(dev)
-    _check_stream(stream, dev)
+    _check_place(stream, dev)
     _on_device(dev, stream, L.vc_pages_trim, args, "vc_pages_trim")
 
 
@@ -908,9 +930,8 @@ def vc_pages_compact(cache, pool, table, used=None, workspace=None, dev_status=N
     p = _pool_of(pool, s.pages, dev)
     at, s_table, B, cols = _table_of("table", table, dev)
     status = _status_ptr(dev_status, dev)
-    _need_cuda(dev)
-    _check_stream(stream, dev)
-    if _is_other(stream):
+    _check_place(stream, dev)
+    if stream is not None and _is_other(stream):
         return _on_stream(stream, vc_pages_compact, cache, pool, table, used, workspace, dev_status)
     if used is None:
         used = torch.empty(1, dtype=_I32, device=dev)
@@ -933,8 +954,7 @@ def vc_cache_copy(source, target, from_pages, to_pages, dev_status=None, stream=
     N = from_pages.numel()
     args = (s, *parts, t, *to_parts, _int32_vector("from_pages", from_pages, N, dev), _int32_vector("to_pages", to_pages, N, dev), N,
             _status_ptr(dev_status, dev))
-    _need_cuda(dev)
-    _check_stream(stream, dev)
+    _check_place(stream, dev)
     _on_device(dev, stream, L.vc_cache_copy, args, "vc_cache_copy")
     return target
 
@@ -976,9 +996,8 @@ def vc_debug_attn_paged_timeout(Q, cache, cu, kv_len, table, dev_status, skip_un
     T, Hq, d = Q.shape
     strides, batch = _rows("Q", Q, Hq, s.d, dev), _batch_of(cu, kv_len, table, T, dev)
     status = _status_ptr(dev_status, dev)
-    _need_cuda(dev)
-    _check_stream(stream, dev)
-    if _is_other(stream):
+    _check_place(stream, dev)
+    if stream is not None and _is_other(stream):
         return _on_stream(stream, vc_debug_attn_paged_timeout, Q, cache, cu, kv_len, table, dev_status, skip_unit,
                           max_q)
     O = torch.empty((T, Hq, d), dtype=_BF16, device=dev)

@@ -13,12 +13,22 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
-def attend(c, cache=None, status=0, **kw):
+def tables(c, wide):
+    """The batch's arguments; wide: a table with so many columns that the work could be large, without which calls of few
+    keys take one pass over all of them."""
+    cu, kv, table = c.args(DEV)
+    if wide:
+        more = -(-1600 * 128 // (c.B * c.H * c.page)) + 1
+        table = torch.cat([table, torch.full((c.B, more), -1, dtype=torch.int32, device=DEV)], 1)
+    return cu, kv, table
+
+
+def attend(c, cache=None, status=0, wide=True, **kw):
     seen = torch.zeros(1, dtype=torch.int32, device=DEV)
     kw.setdefault("max_q", max(c.n))
     kw.setdefault("max_rows", c.most())
     groups = kw.pop("groups", c.shared_args(DEV))
-    out = vc.vc_attn_paged_shared(c.Q.to(DEV), cache or c.cache(DEV), *c.args(DEV), *groups, dev_status=seen, **kw)
+    out = vc.vc_attn_paged_shared(c.Q.to(DEV), cache or c.cache(DEV), *tables(c, wide), *groups, dev_status=seen, **kw)
     torch.cuda.synchronize()
     assert int(seen) == status
     return out
@@ -50,14 +60,14 @@ def name(k):
     return k.replace(" ", "_").replace(",", "")
 
 
-@pytest.mark.parametrize("causal", [1, 0])
+@pytest.mark.parametrize("causal,wide", [(1, True), (0, True), (1, False)])
 @pytest.mark.parametrize("case", CASES, ids=name)
-def test_attention(case, causal):
+def test_attention(case, causal, wide):
     c = Shared(seed=1, **CASES[case])
-    c.check(attend(c, causal=causal), c.cache(), causal=causal)
+    c.check(attend(c, causal=causal, wide=wide), c.cache(), causal=causal)
 
 
-@pytest.mark.parametrize("hints", [(0, 0), (1, 1), (60, 9), (9, 60), (300, 5000), (2 ** 32, 2 ** 40)], ids=str)
+@pytest.mark.parametrize("hints", [(0, 0), (1, 1), (5, 5), (10, 20), (60, 9), (9, 60), (33, 300), (65, 90), (300, 5000), (2 ** 32, 2 ** 40)], ids=str)
 def test_hints_choose_kernels_only(hints):
     """Tiles of 8 to 256 rows in both passes, whatever the batch."""
     for case in ("groups", "chunks of d 64"):
@@ -149,7 +159,7 @@ def test_without_groups():
 
 def test_rows_without_keys():
     """kv_len 0 and 0 of a prefix: O = 0, lse = -inf."""
-    c = Shared([(0, [(4, 4), (9, 1)]), (200, [(1, 1)])], H=2, G=2, seed=9)
+    c = Shared([(0, [(4, 4), (9, 1)]), (200, [(1, 1), (2, 1)])], H=2, G=2, seed=9)
     c.kv[0] = 0
     c.kv_len[0] = 0
     got = attend(c)
@@ -186,7 +196,7 @@ def test_broken_groups_are_reported_and_touch_nothing_outside():
         for max_q, max_rows in ((1, 1), (500, 500)):
             status = torch.zeros(1, dtype=torch.int32, device=DEV)
             O = torch.full((T + 2 * guard, Hq, c.d), 7.0, dtype=torch.bfloat16, device=DEV)
-            vc.vc_attn_paged_shared(c.Q.to(DEV), c.cache(DEV), *args, c.table.to(DEV), *c.shared_args(DEV), O=O[guard:-guard], max_q=max_q, max_rows=max_rows, dev_status=status)
+            vc.vc_attn_paged_shared(c.Q.to(DEV), c.cache(DEV), *args, tables(c, max_q == 1)[2], *c.shared_args(DEV), O=O[guard:-guard], max_q=max_q, max_rows=max_rows, dev_status=status)
             assert int(status) == 1 and torch.all(O[:guard] == 7.0) and torch.all(O[-guard:] == 7.0)
 
 
@@ -194,7 +204,7 @@ def test_broken_groups_are_reported_and_touch_nothing_outside():
 def test_given_outputs_and_streams(case):
     """Strided O, a workspace of the caller's with anything in it, another stream, and the C entry without lse."""
     c = Shared(seed=12, **CASES[case])
-    cache, args, groups, Q, Hq = c.cache(DEV), c.args(DEV), c.shared_args(DEV), c.Q.to(DEV), c.H * c.G
+    cache, args, groups, Q, Hq = c.cache(DEV), tables(c, True), c.shared_args(DEV), c.Q.to(DEV), c.H * c.G
     hints = dict(max_q=max(c.n), max_rows=c.most())
     want = vc.vc_attn_paged_shared(Q, cache, *args, *groups, **hints)
     c.check(want, c.cache())
@@ -243,7 +253,7 @@ def test_generation_from_forks(G, d):
     ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
     pages = 40
     cache, pool = vc.alloc_cache(pages, page, H, d, DEV), vc.alloc_pool(pages, DEV)
-    table, kv, status = torch.full((N + 1, 12), -1, dtype=torch.int32, device=DEV), torch.zeros(N + 1, dtype=torch.int32, device=DEV), ints([0])
+    table, kv, status = torch.full((N + 1, 2000), -1, dtype=torch.int32, device=DEV), torch.zeros(N + 1, dtype=torch.int32, device=DEV), ints([0])
     cu, kv[0] = ints([0, prompt]), prompt
     vc.vc_pages_reserve(cache, pool, cu, kv[:1], table[:1], prompt, dev_status=status)
     vc.vc_cache_append_rope(None, whole[0].K[:prompt].to(DEV), whole[0].V[:prompt].to(DEV), cache, cu, kv[:1], table[:1], rope)
@@ -287,7 +297,7 @@ def test_generation_from_forks(G, d):
 def test_captured_graphs_do_not_share():
     """Two graphs captured in turn, with other groups put into their buffers, replayed one after the other."""
     shapes = [dict(groups=[(200, [(9, 1)] * 4), (90, [(3, 1)] * 2)]), dict(groups=[(30, [(70, 1)]), (300, [(2, 1)] * 5)])]
-    cases = [Shared(H=2, G=4, seed=50 + i, cols=30, **kw) for i, kw in enumerate(shapes)]
+    cases = [Shared(H=2, G=4, seed=50 + i, cols=2200, **kw) for i, kw in enumerate(shapes)]
     pages = max(c.pages for c in cases)
     graphs = []
     for c in cases:
