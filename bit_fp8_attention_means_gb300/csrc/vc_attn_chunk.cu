@@ -919,7 +919,7 @@ vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const P
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, cudaStream_t st) {
     if (d == 64) return launch_many_pass<64, 32>(mk, mv, a, c, RT, ctas, st);
-    return RT == 256 ? launch_many_pass<128, 64>(mk, mv, a, c, RT, ctas, st)
+    return RT > 128 ? launch_many_pass<128, 64>(mk, mv, a, c, RT, ctas, st)
                      : launch_many_pass<128, 16>(mk, mv, a, c, RT, ctas, st);
 }
 

@@ -138,6 +138,7 @@ struct RopeRows {
     const int64_t* turns;          // [rot / 2] turns a position, as fractions of 2^64
     const int32_t* pos;            // [T], or null: the positions in the cache
     int Hq, rot, pairs;            // rows of a token in Q, turned channels, layout
+    int tokens, steps;             // most tokens of a block; rows of a group of its lanes
     float magnitude, sign;         // what cos and sin are multiplied by
 };
 vc_status launch_rope(const RopeRows& a, const CacheView& c, int d, cudaStream_t st);

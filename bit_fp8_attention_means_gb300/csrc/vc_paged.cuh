@@ -140,31 +140,6 @@ __device__ __forceinline__ int find_seq(const CacheView& c, int tok, int sub, un
     return lo;
 }
 
-// Eight fp32 values of a row that W lanes share -> eight codes; the row's scale.  The largest
-// magnitude comes from the bit patterns with the sign off, which order like the magnitudes and put
-// infinities and NaN above every number.
-template <int W>
-__device__ __forceinline__ uint2 quantize_row8(const float (&x)[8], unsigned mask, float* scale) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = W / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(mask, top, o));
-    const float amax = __uint_as_float(top);
-    if (top >= 0x7F800000u || amax < 0x1p-100f) {
-        *scale = top >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : 0.f;
-        return make_uint2(0u, 0u);
-    }
-    *scale = __fdiv_rn(amax, 448.f);
-    const float inv = __fdiv_rn(448.f, amax);
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        o[i] = cvt_e4m3x2(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv)) |
-               (cvt_e4m3x2(__fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv)) << 16);
-    return make_uint2(o[0], o[1]);
-}
-
 // ------------------------------------------------------------ work of the attention kernels
 //
 // The rows of a sequence for one key/value head are its n * G (token, query

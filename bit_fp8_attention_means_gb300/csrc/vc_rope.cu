@@ -9,11 +9,13 @@
 // sincospi.  (In fp32 a position of 10^6 would lose 20 of 24 bits of the angle; fp64 would
 // be right and slow here.)
 //
-// Memory bounds both calls: 4d bytes a row, in the cache 2d + d + 4.  A block takes
-// consecutive rows, token by token (queries, keys, values), computes the angles of its
-// tokens once for all their heads while the rows' loads are under way, and then turns, a
-// group of d/8 lanes a row.  What is written to the cache is quantized straight from fp32,
-// as in vc_cache.cu otherwise.
+// Memory bounds both calls: 4d bytes a row, in the cache 2d + d + 4; and instructions, of which a row
+// has as many as its bytes take time.  So a block takes consecutive rows, token by token (queries,
+// keys, values), and computes the angles of its tokens once for all their heads; a group of d/8 lanes
+// a row keeps them in registers from row to row; a lane holds both channels of its pairs, in either
+// layout, so that nothing is exchanged; sums and products are of two numbers at once; and the loads of
+// the next two rows are under way while one is computed.  What is written to the cache is quantized
+// straight from fp32, as in vc_cache.cu otherwise.
 #include <cuda_bf16.h>
 
 #include "vc_device.cuh"
@@ -24,7 +26,6 @@ namespace vc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 2;  // rows of a group of lanes
 
 struct Place {
     int64_t code, scale;  // of head 0; scale < 0: not in the cache
@@ -32,55 +33,103 @@ struct Place {
     int found;            // the row belongs to a sequence
 };
 
-__device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+// Eight bf16 -> the pieces' channels 0 .. 3 and 4 .. 7, two at a time.
+__device__ __forceinline__ void unpack(const uint4& v, float2 (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_bits_to_f32(w[i] & 0xFFFFu), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-template <int D, bool APPEND>
+// Largest magnitude; NaN where one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
+// Eight fp32 values of a row that W lanes share -> eight codes and the row's scale, by the steps of
+// vc_cache_append.
+template <int W>
+__device__ __forceinline__ uint2 quantize(const float2 (&x)[4], unsigned mask, float* scale) {
+    float amax = max_abs(max_abs(max_abs(x[0].x, x[0].y), max_abs(x[1].x, x[1].y)),
+                         max_abs(max_abs(x[2].x, x[2].y), max_abs(x[3].x, x[3].y)));
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1) amax = max_abs(amax, __shfl_xor_sync(mask, amax, o));
+    if (!(amax < INFINITY) || amax < 0x1p-100f) {
+        *scale = amax < 1.f ? 0.f : __int_as_float(0x7FFFFFFF);
+        return make_uint2(0u, 0u);
+    }
+    *scale = __fdiv_rn(amax, 448.f);
+    const float inv = __fdiv_rn(448.f, amax);
+    const float2 inv2 = make_float2(inv, inv);
+    float2 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(x[i], inv2);
+    return make_uint2(cvt_e4m3x2(y[0].x, y[0].y) | (cvt_e4m3x2(y[1].x, y[1].y) << 16),
+                      cvt_e4m3x2(y[2].x, y[2].y) | (cvt_e4m3x2(y[3].x, y[3].y) << 16));
+}
+
+// PAIRS: the layout of neighbouring channels.  A lane's eight channels are two pieces of four: of those that
+// turn, channels 4 l .. of the first half and as many of the second in halves, neighbours otherwise.
+template <int D, bool APPEND, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const CacheView c) {
-    constexpr int W = D / 8, GROUPS = kThreads / W, U = kRows, HALF = D / 2, TOKENS = GROUPS * U;
-    __shared__ float2 turn[TOKENS * HALF];
-    __shared__ Place place[TOKENS];
+    constexpr int W = D / 8, GROUPS = kThreads / W, HALF = D / 2;
+    extern __shared__ float4 smem[];
+    float2* turn = reinterpret_cast<float2*>(smem);                    // [tokens][4][HALF / 4]
+    Place* place = reinterpret_cast<Place*>(turn + a.tokens * HALF);   // [tokens]
     const int tid = threadIdx.x, lane = tid & 31, sub = lane & (W - 1), group = tid / W;
     const unsigned mask = ((W == 16) ? 0xFFFFu : 0xFFu) << (lane & ~(W - 1));
     if (blockIdx.x == 0 && c.cu)
         for (int b = tid; b < c.B; b += kThreads)
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
 
-    // this group's rows: token and number among the token's rows (queries, keys, values)
-    const uint32_t per = APPEND ? a.Hq + 2 * c.H : a.Hq, rows = (uint32_t)c.T * per, first = blockIdx.x * (uint32_t)TOKENS;
-    const int tok0 = (int)(first / per), tokens = (int)((min(first + TOKENS, rows) - 1) / per) - tok0 + 1;
-    uint4 x[U];
-    int tk[U], r[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t row = first + group * U + u;
-        const int tok = (int)(row / per);
-        tk[u] = row < rows ? tok - tok0 : -1;
-        r[u] = (int)(row - (uint32_t)tok * per);
-        if (tk[u] < 0) continue;
+    // rows first + group, + GROUPS and so on: token and number among the token's rows (queries, keys, values)
+    const uint32_t per = APPEND ? a.Hq + 2 * c.H : a.Hq, rows = (uint32_t)c.T * per, block_rows = (uint32_t)(GROUPS * a.steps);
+    const uint32_t first = blockIdx.x * block_rows, end = min(first + block_rows, rows);
+    const int tok0 = (int)(first / per), tokens = (int)((end - 1) / per) - tok0 + 1;
+    const int step_tok = (int)((uint32_t)GROUPS / per), step_r = (int)((uint32_t)GROUPS % per);
+    const bool turns = sub * 8 < a.rot;
+    const int p0 = PAIRS || !turns ? sub * 8 : sub * 4, p1 = PAIRS || !turns ? sub * 8 + 4 : a.rot / 2 + sub * 4;
+    int tok = (int)((first + group) / per), r = (int)(first + group - (uint32_t)tok * per);
+    auto advance = [&](int& t, int& n) {
+        t += step_tok;
+        n += step_r;
+        if (n >= (int)per) {
+            n -= (int)per;
+            ++t;
+        }
+    };
+    auto load = [&](int t, int n) -> uint4 {
         const uint16_t* src;
-        if (!APPEND || r[u] < a.Hq) src = a.Q + (int64_t)tok * a.q_sn + (int64_t)r[u] * a.q_sh;
-        else if (r[u] < a.Hq + c.H) src = a.K + (int64_t)tok * a.k_sn + (int64_t)(r[u] - a.Hq) * a.k_sh;
-        else src = a.V + (int64_t)tok * a.k_sn + (int64_t)(r[u] - a.Hq - c.H) * a.k_sh;
-        x[u] = __ldcs(reinterpret_cast<const uint4*>(src) + sub);
-    }
+        if (!APPEND || n < a.Hq) src = a.Q + (int64_t)t * a.q_sn + (int64_t)n * a.q_sh;
+        else if (n < a.Hq + c.H) src = a.K + (int64_t)t * a.k_sn + (int64_t)(n - a.Hq) * a.k_sh;
+        else src = a.V + (int64_t)t * a.k_sn + (int64_t)(n - a.Hq - c.H) * a.k_sh;
+        if (PAIRS) return __ldcs(reinterpret_cast<const uint4*>(src + p0));
+        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(src + p0)), y = __ldcs(reinterpret_cast<const uint2*>(src + p1));
+        return make_uint4(x.x, x.y, y.x, y.y);
+    };
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint32_t ahead = first + group;  // the next row to load
+    int t_ahead = tok, r_ahead = r;
+    auto next = [&]() -> uint4 {
+        const uint4 x = ahead < end ? load(t_ahead, r_ahead) : zero;
+        ahead += GROUPS;
+        advance(t_ahead, r_ahead);
+        return x;
+    };
+    uint4 x0 = next(), x1 = next();
+
     // where the tokens are
     const int pair = tid & (HALF - 1);
     const uint64_t w = pair < a.rot / 2 ? (uint64_t)__ldg(a.turns + pair) : 0;
     for (int i = group; i < tokens; i += GROUPS) {
-        const int tok = tok0 + i;
+        const int t = tok0 + i;
         Place p{0, -1, 0, 1};
         if (c.cu) {
-            const int b = find_seq<W>(c, tok, sub, mask);
+            const int b = find_seq<W>(c, t, sub, mask);
             const SeqInfo s = seq_info(c, b);
-            p.found = tok >= s.q0 && tok < s.q0 + s.n;
-            p.pos = s.L - s.n + (tok - s.q0);
+            p.found = t >= s.q0 && t < s.q0 + s.n;
+            p.pos = s.L - s.n + (t - s.q0);
             if (APPEND && p.found) {
                 const int pg = p.pos >= 0 ? page_of(c, b, p.pos) : -1;
                 if (pg >= 0) {
@@ -92,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
                 }
             }
         }
-        if (a.pos) p.pos = __ldg(a.pos + tok);
+        if (a.pos) p.pos = __ldg(a.pos + t);
         if (sub == 0) place[i] = p;
     }
     __syncthreads();
@@ -101,74 +150,105 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
             const uint64_t t = w * (uint64_t)(int64_t)place[i].pos;
             float sn, cs;
             sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn, &cs);
-            turn[i * HALF + pair] = make_float2(cs * a.magnitude, sn * a.sign);
+            // the k-th pair of each lane's side by side: no bank conflicts where a lane reads its own
+            turn[i * HALF + (pair & 3) * (HALF / 4) + (pair >> 2)] = make_float2(cs * a.magnitude, sn * a.sign);
         }
     __syncthreads();
 
-    const int half = a.rot / 2, c0 = sub * 8;
-    // halves: the lane that holds the other channels of this one's pairs
-    const int apart = half / 8, other = a.pairs || c0 >= a.rot ? lane : c0 < half ? lane + apart : lane - apart;
+    float2 cs[4], sn[4];  // of this lane's four pairs, as the products want them
+    int angles = -1;      // of this token
+    for (uint32_t row = first + group; row < end; row += GROUPS) {
+        const uint4 v = x0;
+        x0 = x1;
+        x1 = next();
+        const int tk = tok - tok0, n = r;
+        advance(tok, r);
+        if (!place[tk].found) continue;
+        const bool value = APPEND && n >= a.Hq + c.H;
+        float2 x[4];
+        unpack(v, x);
+        if (turns && !value) {
+            if (tk != angles) {
+                angles = tk;
+                const float2* t = turn + tk * HALF + sub;
+                float2 e[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const bool there = tk[u] >= 0 && place[max(tk[u], 0)].found;
-        if (!__any_sync(0xffffffffu, there)) continue;
-        const uint4 v = there ? x[u] : make_uint4(0, 0, 0, 0);
-        const uint4 o = make_uint4(__shfl_sync(0xffffffffu, v.x, other), __shfl_sync(0xffffffffu, v.y, other),
-                                   __shfl_sync(0xffffffffu, v.z, other), __shfl_sync(0xffffffffu, v.w, other));
-        float y[8];
-        unpack(v, y);
-        const bool value = APPEND && r[u] >= a.Hq + c.H;
-        const float2* t = turn + max(tk[u], 0) * HALF;
-        if (there && c0 < a.rot && !value) {
-            if (a.pairs) {
+                for (int i = 0; i < 4; ++i) e[i] = t[i * (HALF / 4)];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 e = t[c0 / 2 + i];
-                    const float y0 = y[2 * i], y1 = y[2 * i + 1];
-                    y[2 * i] = y0 * e.x - y1 * e.y;
-                    y[2 * i + 1] = y0 * e.y + y1 * e.x;
+                    if (PAIRS) {
+                        cs[i] = make_float2(e[i].x, e[i].x);
+                        sn[i] = make_float2(-e[i].y, e[i].y);
+                    } else if (i < 2) {
+                        cs[i] = make_float2(e[2 * i].x, e[2 * i + 1].x);
+                        sn[i] = make_float2(e[2 * i].y, e[2 * i + 1].y);
+                    } else {
+                        sn[i] = make_float2(-e[2 * (i - 2)].y, -e[2 * (i - 2) + 1].y);
+                    }
                 }
-            } else {
-                float z[8];
-                unpack(o, z);
-                const bool second = c0 >= half;
+            }
+            if (PAIRS) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 e = t[second ? c0 - half + i : c0 + i];
-                    y[i] = second ? z[i] * e.y + y[i] * e.x : y[i] * e.x - z[i] * e.y;
+                for (int i = 0; i < 4; ++i)
+                    x[i] = __ffma2_rn(make_float2(x[i].y, x[i].x), sn[i], __fmul2_rn(x[i], cs[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 y0 = __ffma2_rn(x[2 + i], sn[2 + i], __fmul2_rn(x[i], cs[i]));
+                    x[2 + i] = __ffma2_rn(x[2 + i], cs[i], __fmul2_rn(x[i], sn[i]));
+                    x[i] = y0;
                 }
             }
         }
-        if (!APPEND || r[u] < a.Hq) {
-            if (there) {
-                uint32_t q[4];
+        if (!APPEND || n < a.Hq) {
+            uint32_t q[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-                    q[i] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                uint16_t* dst = a.out + (int64_t)(tok0 + tk[u]) * a.o_sn + (int64_t)r[u] * a.o_sh;
-                reinterpret_cast<uint4*>(dst)[sub] = make_uint4(q[0], q[1], q[2], q[3]);
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
+                q[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
-        } else if (there && place[tk[u]].scale >= 0) {
+            uint16_t* dst = a.out + (int64_t)(tok0 + tk) * a.o_sn + (int64_t)n * a.o_sh;
+            if (PAIRS) {
+                *reinterpret_cast<uint4*>(dst + p0) = make_uint4(q[0], q[1], q[2], q[3]);
+            } else {
+                *reinterpret_cast<uint2*>(dst + p0) = make_uint2(q[0], q[1]);
+                *reinterpret_cast<uint2*>(dst + p1) = make_uint2(q[2], q[3]);
+            }
+        } else if (place[tk].scale >= 0) {
             float scale;
-            const uint2 codes = quantize_row8<W>(y, mask, &scale);
-            const int h = value ? r[u] - a.Hq - c.H : r[u] - a.Hq;
-            const int64_t at = place[tk[u]].code + (int64_t)h * c.s_head;
-            *reinterpret_cast<uint2*>((value ? c.V8 : c.K8) + at + sub * 8) = codes;
-            if (sub == 0) (value ? c.sv : c.sk)[place[tk[u]].scale + (int64_t)h * c.t_head] = scale;
+            const uint2 codes = quantize<W>(x, mask, &scale);
+            const int h = value ? n - a.Hq - c.H : n - a.Hq;
+            uint8_t* dst = (value ? c.V8 : c.K8) + place[tk].code + (int64_t)h * c.s_head;
+            if (PAIRS) {
+                *reinterpret_cast<uint2*>(dst + p0) = codes;
+            } else {
+                *reinterpret_cast<uint32_t*>(dst + p0) = codes.x;
+                *reinterpret_cast<uint32_t*>(dst + p1) = codes.y;
+            }
+            if (sub == 0) (value ? c.sv : c.sk)[place[tk].scale + (int64_t)h * c.t_head] = scale;
         }
     }
 }
 
+template <int D, bool APPEND, bool PAIRS>
+vc_status launch_layout(RopeRows a, const CacheView& c, cudaStream_t st) {
+    constexpr int GROUPS = kThreads / (D / 8), TOKEN = D / 2 * (int)sizeof(float2) + (int)sizeof(Place);
+    const uint32_t per = APPEND ? a.Hq + 2 * c.H : a.Hq, rows = (uint32_t)c.T * per;
+    // rows of a group: as many as leave four blocks an SM, two to eight
+    const uint32_t some = rows / (GROUPS * kMaxCtas * 4);
+    a.steps = some < 2 ? 2 : some > 8 ? 8 : (int)some;
+    if (per < 4) a.steps = 2;  // many tokens a block: their angles are what is shared
+    const uint32_t block_rows = GROUPS * a.steps;
+    a.tokens = (int)(per == 1 ? block_rows : (block_rows + per - 2) / per + 1);  // that so many rows can belong to
+    static_assert(GROUPS * 2 * TOKEN <= 48 * 1024 && (GROUPS * 8 / 4 + 1) * TOKEN <= 48 * 1024, "without asking for more");
+    rope_kernel<D, APPEND, PAIRS><<<(rows + block_rows - 1) / block_rows, kThreads, a.tokens * TOKEN, st>>>(a, c);
+    return cuda_status(cudaGetLastError());
+}
+
 template <bool APPEND>
 vc_status launch(const RopeRows& a, const CacheView& c, int d, cudaStream_t st) {
-    const int per_block = kThreads / (d / 8) * kRows;
-    const uint32_t rows = (uint32_t)c.T * (uint32_t)(APPEND ? a.Hq + 2 * c.H : a.Hq);
-    const unsigned grid = (rows + per_block - 1) / per_block;
-    if (d == 128) rope_kernel<128, APPEND><<<grid, kThreads, 0, st>>>(a, c);
-    else rope_kernel<64, APPEND><<<grid, kThreads, 0, st>>>(a, c);
-    return cuda_status(cudaGetLastError());
+    if (d == 128) return a.pairs ? launch_layout<128, APPEND, true>(a, c, st) : launch_layout<128, APPEND, false>(a, c, st);
+    return a.pairs ? launch_layout<64, APPEND, true>(a, c, st) : launch_layout<64, APPEND, false>(a, c, st);
 }
 
 }  // namespace
