@@ -418,7 +418,6 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const CacheView c, const
     wait_for_primary();
     const int used = ws.head[0], moved = ws.head[1];
     const int64_t me = (int64_t)blockIdx.x * kCopy + threadIdx.x, all = (int64_t)gridDim.x * kCopy;
-    copy_pages(c, c, ws.from, ws.to, moved, tok_log2);
     int32_t* table = const_cast<int32_t*>(c.table);
     for (int64_t k = me; k < (int64_t)c.B * c.cols; k += all) {
         int32_t* entry = table + k / c.cols * c.s_table + k % c.cols;
@@ -445,6 +444,7 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const CacheView c, const
         pool.free[i] = ~low & real;
     }
     if (me == 0 && count) *count = used;
+    copy_pages(c, c, ws.from, ws.to, moved, tok_log2);
 }
 
 // Blocks of 256 over the columns of a row, the rows being the grid's other side.

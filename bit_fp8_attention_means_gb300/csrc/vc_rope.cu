@@ -11,9 +11,9 @@
 //
 // Memory bounds both calls: 4d bytes a row, in the cache 2d + d + 4; and instructions, of which a row
 // has as many as its bytes take time.  So a block takes consecutive rows, token by token (queries,
-// keys, values), and computes the angles of its tokens once for all their heads; a group of d/8 lanes
-// a row keeps them in registers from row to row; a lane holds both channels of its pairs, in either
-// layout, so that nothing is exchanged; sums and products are of two numbers at once; and the loads of
+// keys, values), and computes the angles of its tokens once for all their heads; a group of
+// d/16 lanes a row keeps them in registers from row to row; a lane holds both channels of its pairs, in
+// either layout, so that nothing is exchanged; sums and products are of two numbers at once; and the loads of
 // the next two rows are under way while one is computed.  What is written to the cache is quantized
 // straight from fp32, as in vc_cache.cu otherwise.
 #include <cuda_bf16.h>
@@ -33,11 +33,20 @@ struct Place {
     int found;            // the row belongs to a sequence
 };
 
-// Eight bf16 -> the pieces' channels 0 .. 3 and 4 .. 7, two at a time.
-__device__ __forceinline__ void unpack(const uint4& v, float2 (&x)[4]) {
+// Eight bf16, two at a time.
+__device__ __forceinline__ void unpack(const uint4& v, float2* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_bits_to_f32(w[i] & 0xFFFFu), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack(const float2* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
+        w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Largest magnitude; NaN where one is.
@@ -47,38 +56,43 @@ __device__ __forceinline__ float max_abs(float a, float b) {
     return r;
 }
 
-// Eight fp32 values of a row that W lanes share -> eight codes and the row's scale, by the steps of
+// Sixteen fp32 values of a row that W lanes share -> as many codes and the row's scale, by the steps of
 // vc_cache_append.
 template <int W>
-__device__ __forceinline__ uint2 quantize(const float2 (&x)[4], unsigned mask, float* scale) {
-    float amax = max_abs(max_abs(max_abs(x[0].x, x[0].y), max_abs(x[1].x, x[1].y)),
-                         max_abs(max_abs(x[2].x, x[2].y), max_abs(x[3].x, x[3].y)));
+__device__ __forceinline__ void quantize(const float2 (&x)[8], unsigned mask, float* scale, uint2 (&codes)[2]) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max_abs(amax, max_abs(x[i].x, x[i].y));
 #pragma unroll
     for (int o = W / 2; o; o >>= 1) amax = max_abs(amax, __shfl_xor_sync(mask, amax, o));
     if (!(amax < INFINITY) || amax < 0x1p-100f) {
         *scale = amax < 1.f ? 0.f : __int_as_float(0x7FFFFFFF);
-        return make_uint2(0u, 0u);
+        codes[0] = codes[1] = make_uint2(0u, 0u);
+        return;
     }
     *scale = __fdiv_rn(amax, 448.f);
     const float inv = __fdiv_rn(448.f, amax);
     const float2 inv2 = make_float2(inv, inv);
-    float2 y[4];
+    uint32_t q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(x[i], inv2);
-    return make_uint2(cvt_e4m3x2(y[0].x, y[0].y) | (cvt_e4m3x2(y[1].x, y[1].y) << 16),
-                      cvt_e4m3x2(y[2].x, y[2].y) | (cvt_e4m3x2(y[3].x, y[3].y) << 16));
+    for (int i = 0; i < 4; ++i) {
+        const float2 y = __fmul2_rn(x[2 * i], inv2), z = __fmul2_rn(x[2 * i + 1], inv2);
+        q[i] = cvt_e4m3x2(y.x, y.y) | (cvt_e4m3x2(z.x, z.y) << 16);
+    }
+    codes[0] = make_uint2(q[0], q[1]);
+    codes[1] = make_uint2(q[2], q[3]);
 }
 
-// PAIRS: the layout of neighbouring channels.  A lane's eight channels are two pieces of four: of those that
-// turn, channels 4 l .. of the first half and as many of the second in halves, neighbours otherwise.
+// PAIRS: the layout of neighbouring channels.  A lane's sixteen channels are two pieces of eight: of those that
+// turn, channels 8 l .. of the first half and as many of the second in halves, neighbours otherwise.
 template <int D, bool APPEND, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const CacheView c) {
-    constexpr int W = D / 8, GROUPS = kThreads / W, HALF = D / 2;
+    constexpr int W = D / 16, GROUPS = kThreads / W, HALF = D / 2;
     extern __shared__ float4 smem[];
-    float2* turn = reinterpret_cast<float2*>(smem);                    // [tokens][4][HALF / 4]
+    float2* turn = reinterpret_cast<float2*>(smem);                    // [tokens][8][HALF / 8]
     Place* place = reinterpret_cast<Place*>(turn + a.tokens * HALF);   // [tokens]
     const int tid = threadIdx.x, lane = tid & 31, sub = lane & (W - 1), group = tid / W;
-    const unsigned mask = ((W == 16) ? 0xFFFFu : 0xFFu) << (lane & ~(W - 1));
+    const unsigned mask = ((1u << W) - 1u) << (lane & ~(W - 1));
     if (blockIdx.x == 0 && c.cu)
         for (int b = tid; b < c.B; b += kThreads)
             if (!seq_valid(c, b)) flag_invalid(c.dev_status);
@@ -88,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
     const uint32_t first = blockIdx.x * block_rows, end = min(first + block_rows, rows);
     const int tok0 = (int)(first / per), tokens = (int)((end - 1) / per) - tok0 + 1;
     const int step_tok = (int)((uint32_t)GROUPS / per), step_r = (int)((uint32_t)GROUPS % per);
-    const bool turns = sub * 8 < a.rot;
-    const int p0 = PAIRS || !turns ? sub * 8 : sub * 4, p1 = PAIRS || !turns ? sub * 8 + 4 : a.rot / 2 + sub * 4;
+    const bool turns = sub * 16 < a.rot;
+    const int p0 = PAIRS || !turns ? sub * 16 : sub * 8, p1 = PAIRS || !turns ? sub * 16 + 8 : a.rot / 2 + sub * 8;
     int tok = (int)((first + group) / per), r = (int)(first + group - (uint32_t)tok * per);
     auto advance = [&](int& t, int& n) {
         t += step_tok;
@@ -99,34 +113,35 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
             ++t;
         }
     };
-    auto load = [&](int t, int n) -> uint4 {
+    struct Row {
+        uint4 lo, hi;
+    };
+    auto load = [&](int t, int n) -> Row {
         const uint16_t* src;
         if (!APPEND || n < a.Hq) src = a.Q + (int64_t)t * a.q_sn + (int64_t)n * a.q_sh;
         else if (n < a.Hq + c.H) src = a.K + (int64_t)t * a.k_sn + (int64_t)(n - a.Hq) * a.k_sh;
         else src = a.V + (int64_t)t * a.k_sn + (int64_t)(n - a.Hq - c.H) * a.k_sh;
-        if (PAIRS) return __ldcs(reinterpret_cast<const uint4*>(src + p0));
-        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(src + p0)), y = __ldcs(reinterpret_cast<const uint2*>(src + p1));
-        return make_uint4(x.x, x.y, y.x, y.y);
+        return Row{__ldcs(reinterpret_cast<const uint4*>(src + p0)), __ldcs(reinterpret_cast<const uint4*>(src + p1))};
     };
-    const uint4 zero = make_uint4(0, 0, 0, 0);
     uint32_t ahead = first + group;  // the next row to load
     int t_ahead = tok, r_ahead = r;
-    auto next = [&]() -> uint4 {
-        const uint4 x = ahead < end ? load(t_ahead, r_ahead) : zero;
+    auto next = [&]() -> Row {
+        Row x{};
+        if (ahead < end) x = load(t_ahead, r_ahead);
         ahead += GROUPS;
         advance(t_ahead, r_ahead);
         return x;
     };
-    uint4 x0 = next(), x1 = next();
+    Row x0 = next(), x1 = next();
 
     // where the tokens are
     const int pair = tid & (HALF - 1);
     const uint64_t w = pair < a.rot / 2 ? (uint64_t)__ldg(a.turns + pair) : 0;
-    for (int i = group; i < tokens; i += GROUPS) {
+    for (int i = tid >> 5; i < tokens; i += kThreads / 32) {
         const int t = tok0 + i;
         Place p{0, -1, 0, 1};
         if (c.cu) {
-            const int b = find_seq<W>(c, t, sub, mask);
+            const int b = find_seq<32>(c, t, lane, 0xffffffffu);
             const SeqInfo s = seq_info(c, b);
             p.found = t >= s.q0 && t < s.q0 + s.n;
             p.pos = s.L - s.n + (t - s.q0);
@@ -136,13 +151,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
                     const int in = p.pos & ((1 << c.page_log2) - 1);
                     p.code = (int64_t)pg * c.s_page + (int64_t)in * c.s_tok;
                     p.scale = (int64_t)pg * c.t_page + in;
-                } else if (sub == 0) {
+                } else if (lane == 0) {
                     flag_invalid(c.dev_status);
                 }
             }
         }
         if (a.pos) p.pos = __ldg(a.pos + t);
-        if (sub == 0) place[i] = p;
+        if (lane == 0) place[i] = p;
     }
     __syncthreads();
     if (pair < a.rot / 2)
@@ -151,80 +166,64 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
             float sn, cs;
             sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn, &cs);
             // the k-th pair of each lane's side by side: no bank conflicts where a lane reads its own
-            turn[i * HALF + (pair & 3) * (HALF / 4) + (pair >> 2)] = make_float2(cs * a.magnitude, sn * a.sign);
+            turn[i * HALF + (pair & 7) * (HALF / 8) + (pair >> 3)] = make_float2(cs * a.magnitude, sn * a.sign);
         }
     __syncthreads();
 
-    float2 cs[4], sn[4];  // of this lane's four pairs, as the products want them
-    int angles = -1;      // of this token
+    float2 e[8];      // (c, s) of this lane's eight pairs in pairs; c and s of two of them each in halves
+    int angles = -1;  // of this token
     for (uint32_t row = first + group; row < end; row += GROUPS) {
-        const uint4 v = x0;
+        const Row v = x0;
         x0 = x1;
         x1 = next();
         const int tk = tok - tok0, n = r;
         advance(tok, r);
         if (!place[tk].found) continue;
         const bool value = APPEND && n >= a.Hq + c.H;
-        float2 x[4];
-        unpack(v, x);
+        float2 x[8];
+        unpack(v.lo, x);
+        unpack(v.hi, x + 4);
         if (turns && !value) {
             if (tk != angles) {
                 angles = tk;
                 const float2* t = turn + tk * HALF + sub;
-                float2 e[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] = t[i * (HALF / 4)];
+                for (int i = 0; i < 8; ++i) e[i] = t[i * (HALF / 8)];
+                if (!PAIRS)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (PAIRS) {
-                        cs[i] = make_float2(e[i].x, e[i].x);
-                        sn[i] = make_float2(-e[i].y, e[i].y);
-                    } else if (i < 2) {
-                        cs[i] = make_float2(e[2 * i].x, e[2 * i + 1].x);
-                        sn[i] = make_float2(e[2 * i].y, e[2 * i + 1].y);
-                    } else {
-                        sn[i] = make_float2(-e[2 * (i - 2)].y, -e[2 * (i - 2) + 1].y);
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 c2 = make_float2(e[i].x, e[i + 1].x);
+                        e[i + 1] = make_float2(e[i].y, e[i + 1].y);
+                        e[i] = c2;
                     }
-                }
             }
             if (PAIRS) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = __ffma2_rn(make_float2(x[i].y, x[i].x), sn[i], __fmul2_rn(x[i], cs[i]));
+                for (int i = 0; i < 8; ++i)
+                    x[i] = __ffma2_rn(make_float2(x[i].y, x[i].x), make_float2(-e[i].y, e[i].y),
+                                      __fmul2_rn(x[i], make_float2(e[i].x, e[i].x)));
             } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 y0 = __ffma2_rn(x[2 + i], sn[2 + i], __fmul2_rn(x[i], cs[i]));
-                    x[2 + i] = __ffma2_rn(x[2 + i], cs[i], __fmul2_rn(x[i], sn[i]));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 c2 = e[2 * i], s2 = e[2 * i + 1];
+                    const float2 y0 = __ffma2_rn(make_float2(-x[4 + i].x, -x[4 + i].y), s2, __fmul2_rn(x[i], c2));
+                    x[4 + i] = __ffma2_rn(x[4 + i], c2, __fmul2_rn(x[i], s2));
                     x[i] = y0;
                 }
             }
         }
         if (!APPEND || n < a.Hq) {
-            uint32_t q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x[i].x, x[i].y);
-                q[i] = *reinterpret_cast<const uint32_t*>(&b);
-            }
             uint16_t* dst = a.out + (int64_t)(tok0 + tk) * a.o_sn + (int64_t)n * a.o_sh;
-            if (PAIRS) {
-                *reinterpret_cast<uint4*>(dst + p0) = make_uint4(q[0], q[1], q[2], q[3]);
-            } else {
-                *reinterpret_cast<uint2*>(dst + p0) = make_uint2(q[0], q[1]);
-                *reinterpret_cast<uint2*>(dst + p1) = make_uint2(q[2], q[3]);
-            }
+            *reinterpret_cast<uint4*>(dst + p0) = pack(x);
+            *reinterpret_cast<uint4*>(dst + p1) = pack(x + 4);
         } else if (place[tk].scale >= 0) {
             float scale;
-            const uint2 codes = quantize<W>(x, mask, &scale);
+            uint2 codes[2];
+            quantize<W>(x, mask, &scale, codes);
             const int h = value ? n - a.Hq - c.H : n - a.Hq;
             uint8_t* dst = (value ? c.V8 : c.K8) + place[tk].code + (int64_t)h * c.s_head;
-            if (PAIRS) {
-                *reinterpret_cast<uint2*>(dst + p0) = codes;
-            } else {
-                *reinterpret_cast<uint32_t*>(dst + p0) = codes.x;
-                *reinterpret_cast<uint32_t*>(dst + p1) = codes.y;
-            }
+            *reinterpret_cast<uint2*>(dst + p0) = codes[0];
+            *reinterpret_cast<uint2*>(dst + p1) = codes[1];
             if (sub == 0) (value ? c.sv : c.sk)[place[tk].scale + (int64_t)h * c.t_head] = scale;
         }
     }
@@ -232,12 +231,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeRows a, const 
 
 template <int D, bool APPEND, bool PAIRS>
 vc_status launch_layout(RopeRows a, const CacheView& c, cudaStream_t st) {
-    constexpr int GROUPS = kThreads / (D / 8), TOKEN = D / 2 * (int)sizeof(float2) + (int)sizeof(Place);
+    constexpr int GROUPS = kThreads / (D / 16), TOKEN = D / 2 * (int)sizeof(float2) + (int)sizeof(Place);
     const uint32_t per = APPEND ? a.Hq + 2 * c.H : a.Hq, rows = (uint32_t)c.T * per;
-    // rows of a group: as many as leave four blocks an SM, two to eight
+    // rows of a group: as many as leave four blocks an SM, one to eight
     const uint32_t some = rows / (GROUPS * kMaxCtas * 4);
-    a.steps = some < 2 ? 2 : some > 8 ? 8 : (int)some;
-    if (per < 4) a.steps = 2;  // many tokens a block: their angles are what is shared
+    a.steps = some < 1 ? 1 : some > 8 ? 8 : (int)some;
+    if (per < 4 && a.steps > 2) a.steps = 2;  // many tokens a block: their angles fill the shared memory
     const uint32_t block_rows = GROUPS * a.steps;
     a.tokens = (int)(per == 1 ? block_rows : (block_rows + per - 2) / per + 1);  // that so many rows can belong to
     static_assert(GROUPS * 2 * TOKEN <= 48 * 1024 && (GROUPS * 8 / 4 + 1) * TOKEN <= 48 * 1024, "without asking for more");
