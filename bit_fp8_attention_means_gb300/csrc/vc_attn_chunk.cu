@@ -67,7 +67,7 @@ constexpr int kRegsSoftmax = 152, kRegsConv = 104, kRegsOther = 104;
 
 // What an item costs besides its units, in units: its queries (5 us), the first scores and the
 // last rows, with both pipelines empty, against 2 us a unit.
-constexpr int kItemCost = kManyItemCost;
+constexpr int kItemCost = 7;
 // The value scale, as -log2, up to which M follows s + log2 sv: below those of the cache that are not 0
 // (2^-109), and so that the P of 64 keys whose values are all zero sum up to less than 2^118.
 constexpr float kLeastLog2 = 110.f;
@@ -237,7 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int pg = __ldg(c.table + (int64_t)w.table_row() * c.s_table + (k >> c.page_log2));
                     return pg < 0 ? -2 : pg;
                 };
-                int ahead = entry(w.unit);
+                int ahead = -1;
+                Runs runs;
+                if constexpr (SHARED) runs.start(c, w, box_log2);
+                else ahead = entry(w.unit);
                 // the item's queries on their way to L2 while the last item's units are under way
                 for (int i = lane; i < rows; i += 32) {
                     const int r = r0 + i, tok = r / a.G;
@@ -247,9 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (D == 128) prefetch_l2(src + 64);
                 }
                 for (int u = w.unit; u < w.end; ++u, ++it) {
-                    const int key0 = u * kUnit;
+                    const int key0 = w.key0(u);
                     int pg = ahead;
-                    ahead = entry(u + 1);
+                    if constexpr (SHARED) pg = runs.at(c, w, u, box_log2);
+                    else ahead = entry(u + 1);
                     const bool missing = pg == -2 || pg >= c.pages;
                     if (missing) {
                         flag_invalid(c.dev_status);

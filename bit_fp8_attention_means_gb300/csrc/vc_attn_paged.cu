@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(few_threads(SHARED ? kShortConsumers : kFewCon
                     if (D == 128) prefetch_l2(src + 64);
                 }
             for (int u = w.unit; u < w.end; ++u, ++it) {
-                const int st = it % NS, key0 = u * kUnit;
+                const int st = it % NS, key0 = w.key0(u);
                 const bool skip = SKIP && it == a.skip_unit && role < 2;
                 int pg = ahead;
                 if constexpr (SHARED) pg = runs.at(c, w, u, box_log2);
@@ -771,7 +771,7 @@ static int shared_rows(int G, int n, int T, int hint, int pass) {
     const int RT = tile_rows(G, n, T, hint);
     const int64_t rows = hinted_rows(G, n, T, hint), tiles = (rows + 255) / 256;
     if (pass == 2) return rows > 32 && rows <= 64 ? 32 : RT;
-    return RT == 256 ? (int)(((rows + tiles - 1) / tiles + 7) & ~(int64_t)7) : RT;
+    return RT == 256 ? (int)(((rows + tiles - 1) / tiles + 7) & ~(int64_t)7) : RT == 32 ? 128 : RT;
 }
 
 static int per_sm_of(int RT) { return RT <= 32 ? 2 : 1; }
@@ -820,9 +820,9 @@ size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int 
     return one > two ? one : two;  // which of the two is taken depends on the table's columns too
 }
 
-// The time of a unit on an SM, in hundredths of microseconds, and what an item costs besides, in units.
-static int unit_time(int RT) { return RT <= 16 ? 45 : RT == 32 ? 185 : RT <= 128 ? 120 : 195; }
-static int item_units(int RT) { return RT <= 16 ? 3 : RT == 32 ? 1 : RT <= 128 ? 10 : kManyItemCost; }
+// The time of a unit in a CTA, in hundredths of microseconds, and what an item costs besides, in units.
+static int unit_time(int RT) { return RT <= 8 ? 90 : RT == 16 ? 150 : RT == 32 ? 400 : RT <= 128 ? 120 : 195; }
+static int item_units(int RT) { return RT <= 16 ? 3 : RT == 32 ? 1 : RT <= 128 ? 10 : 6; }
 
 vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape, const CacheView& c, int max_rows, void* ws,
                              cudaStream_t st) {
@@ -835,6 +835,7 @@ vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape
     CUtensorMap mk, mv;
     if (!make_cache_map(&mk, c.K8, d, c) || !make_cache_map(&mv, c.V8, d, c)) return VC_ERR_CUDA;
     SharedAttn a = args;
+    a.run = shape.page_size < kUnit ? shape.page_size : kUnit;
     a.rt[0] = shared_rows(a.G, a.N, c.T, max_rows, 1);
     a.rt[1] = shared_rows(a.G, c.B, c.T, a.max_q, 2);
     for (int i = 0; i < 2; ++i) {

@@ -12,71 +12,102 @@ namespace {
 constexpr int kPlan = 1024;
 constexpr int kThreads = 128;
 
-// Inclusive sum over the block of one number a thread; the total for all of them.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* total) {
-    __shared__ int64_t sums[kPlan / 32];
+// Inclusive sums over the block of two numbers a thread; the totals for all of them.
+__device__ __forceinline__ void block_sums(int64_t (&v)[2], int64_t (&total)[2]) {
+    __shared__ int64_t sums[2][kPlan / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
-    }
-    __syncthreads();  // the last call's sums have been read
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    int64_t s = sums[lane];
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
+        for (int i = 0; i < 2; ++i) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v[i], o);
+            if (lane >= o) v[i] += u;
+        }
+    __syncthreads();  // the last call's sums have been read
+    if (lane == 31) sums[0][warp] = v[0], sums[1][warp] = v[1];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int64_t s = sums[i][lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        total[i] = __shfl_sync(0xffffffffu, s, 31);
+        const int64_t before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+        v[i] += warp ? before : 0;
     }
-    *total = __shfl_sync(0xffffffffu, s, 31);
-    const int64_t before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
-    return (warp ? before : 0) + v;
 }
 
 // shared_plan_kernel: the first block gives every CTA of both passes its part of the pass's line
 // (vc_paged.cuh), with the item that it begins in; all blocks clear the rows' words.  The passes
-// share the SMs by their lengths and what a unit costs each, so that both end together.  (Planned by
-// every CTA for itself, those without a part held the joining up by 4 us at the end.)
+// share the SMs so that both end together.  (Planned by every CTA for itself, those without a part held the
+// joining up by 4 us at the end.)
 __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const SharedAttn a, const CacheView c) {
     __shared__ int64_t cost[kPlan];
+    __shared__ unsigned long long found[3];  // items of the passes, the best share
     const int tid = threadIdx.x, lane = tid & 31;
     launch_dependents();
     const int64_t words = 2 * (int64_t)c.T * c.H * a.G;
     for (int64_t i = (int64_t)blockIdx.x * kPlan + tid; i < words; i += (int64_t)gridDim.x * kPlan) a.words[i] = 0u;
     if (blockIdx.x) return;
-    int64_t total[2];
+    if (tid < 3) found[tid] = tid == 2 ? ~0ull : 0ull;
+    int64_t total[2] = {0, 0};
+    unsigned long long tiles[2] = {0, 0};
+    for (int b0 = 0; b0 < max(a.N, c.B); b0 += kPlan) {
+        int64_t u[2], all[2];
 #pragma unroll
-    for (int pass = 1; pass <= 2; ++pass) {
-        const int seqs = seq_count<true>(c, a, pass), RT = a.rt[pass - 1], IC = a.ic[pass - 1];
-        int64_t* sums = a.sums + (pass == 1 ? 0 : a.N);
-        int64_t before = 0;
-        for (int b0 = 0; b0 < seqs; b0 += kPlan) {
-            int64_t u = 0, all;
+        for (int i = 0; i < 2; ++i) {
+            const int pass = i + 1, seqs = seq_count<true>(c, a, pass), RT = a.rt[i], IC = a.ic[i], b = b0 + tid;
+            u[i] = 0;
+            if (b0 >= seqs) continue;
             if ((int64_t)c.T * a.G > (int64_t)seqs * RT * 4) {  // many tiles: a warp a sequence
                 __syncthreads();
-                for (int i = tid >> 5; i < kPlan && b0 + i < seqs; i += kPlan / 32) {
-                    const int64_t x = seq_cost_warp<true>(a, seq_of<true>(c, a, b0 + i, pass), RT, IC, pass);
-                    if (lane == 0) cost[i] = x * c.H;
+                for (int k = tid >> 5; k < kPlan && b0 + k < seqs; k += kPlan / 32) {
+                    const int64_t x = seq_cost_warp<true>(a, seq_of<true>(c, a, b0 + k, pass), RT, IC, pass);
+                    if (lane == 0) cost[k] = x * c.H;
                 }
                 __syncthreads();
-                if (b0 + tid < seqs) u = cost[tid];
-            } else if (b0 + tid < seqs) {
-                u = seq_cost<true>(c, a, b0 + tid, RT, IC, pass) * c.H;
+                if (b < seqs) u[i] = cost[tid];
+            } else if (b < seqs) {
+                u[i] = seq_cost<true>(c, a, b, RT, IC, pass) * c.H;
             }
-            const int64_t end = before + block_sum(u, &all);
-            if (b0 + tid < seqs) sums[b0 + tid] = end;
-            before += all;
+            if (u[i]) tiles[i] += (unsigned long long)seq_tiles(a, seq_of<true>(c, a, b, pass), RT) * c.H;
         }
-        total[pass - 1] = before;
+        block_sums(u, all);
+        if (b0 + tid < a.N) a.sums[b0 + tid] = total[0] + u[0];
+        if (b0 + tid < c.B) a.sums[a.N + b0 + tid] = total[1] + u[1];
+        total[0] += all[0];
+        total[1] += all[1];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tiles[i] += __shfl_xor_sync(0xffffffffu, tiles[i], o);
+        if (lane == 0 && tiles[i]) atomicAdd(&found[i], tiles[i]);
     }
     __syncthreads();
-    // pass 1's share of the SMs, rounded; both have one at least where they have work
-    const int64_t w1 = total[0] * a.unit[0], w2 = total[1] * a.unit[1];
-    int sms = w1 ? (int)((w1 * kMaxCtas + (w1 + w2) / 2) / (w1 + w2)) : 0;
-    if (w1) sms = max(sms, 1);
-    if (w2) sms = min(sms, kMaxCtas - 1);
+    // pass 1's share of the SMs: the one with which the later of the two ends first.  A part's time is that of its
+    // units and of beginning and ending its items, of which it has one at least.
+    int sms = total[1] ? 0 : kMaxCtas;
+    if (total[0] && total[1]) {
+        if (tid < 160) {  // five warps
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float parts = (float)((i ? kMaxCtas - 1 - tid : tid + 1) * a.per_sm[i]), n = (float)found[i];
+                const float units = (float)(total[i] - (int64_t)found[i] * a.ic[i]);
+                t = fmaxf(t, (float)a.unit[i] * (units / parts + (float)a.ic[i] * fmaxf(n / parts, 1.f)));
+            }
+            unsigned long long x = tid < kMaxCtas - 1 ? (unsigned long long)__float_as_uint(t) << 32 | (unsigned)(tid + 1) : ~0ull;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0) atomicMin(&found[2], x);
+        }
+        __syncthreads();
+        sms = (int)(found[2] & 0xFFFFFFFFu);
+    }
 #pragma unroll
     for (int pass = 1; pass <= 2; ++pass) {
         const int seqs = seq_count<true>(c, a, pass), RT = a.rt[pass - 1], IC = a.ic[pass - 1], per_sm = a.per_sm[pass - 1];

@@ -98,8 +98,9 @@ struct PagedAttn {
 struct SharedAttn : PagedAttn {  // attention over shared prefixes
     const int32_t* groups;  // [N + 1] runs of sequences
     const int32_t* prefix;  // [N]
-    // the pass of this launch; of pass 1 and 2 the rows of a tile, an item's own cost in units, the time of a unit on an
-    // SM, the CTAs on an SM
+    int run;                // keys of a run in one page: min(page_size, 128)
+    // the pass of this launch; of pass 1 and 2 the rows of a tile, an item's own cost in units, the time of a unit in a
+    // CTA, the CTAs on an SM
     int N, pass, rt[2], ic[2], unit[2], per_sm[2];
     // workspace: the CTAs' parts of both passes, their results, the rows' words, the planning kernel's sums
     struct PlanPart* plan;
@@ -121,7 +122,6 @@ vc_status launch_attn_shared(const SharedAttn& a, const vc_cache_shape& shape, c
 vc_status launch_shared_check(const SharedAttn& a, const CacheView& c, cudaStream_t st);
 vc_status launch_shared_plan(const SharedAttn& a, const CacheView& c, cudaStream_t st);
 vc_status launch_shared_join(const SharedAttn& a, const CacheView& c, int d, cudaStream_t st);
-constexpr int kManyItemCost = 7;   // see vc_attn_chunk.cu
 // its kernel for many rows, in tiles of RT = 128 or 256 (vc_attn_chunk.cu)
 vc_status launch_attn_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAttn& a, const CacheView& c,
                            int d, int RT, int ctas, void* ws, cudaStream_t st);

@@ -162,6 +162,15 @@ struct ItemRange {
     __device__ int first() const { return lo / kUnit; }
     __device__ int units() const { return hi < lo ? 0 : hi / kUnit - lo / kUnit + 1; }
 };
+// SHARED: units count from the first key's run of keys in one page on, so that what follows a prefix
+// does not begin with the rest of a unit.
+struct PassRange : ItemRange {
+    int origin;
+    __device__ int first() const { return 0; }
+    __device__ int units() const { return hi < lo ? 0 : (hi - origin) / kUnit + 1; }
+};
+template <bool SHARED>
+using RangeOf = std::conditional_t<SHARED, PassRange, ItemRange>;
 
 // The pass of this launch; 0: the only one.
 __device__ __forceinline__ constexpr int pass_of(const PagedAttn&) { return 0; }
@@ -174,13 +183,18 @@ __device__ __forceinline__ int row_first(const PagedAttn& a, int last) {
 }
 
 template <bool SHARED>
-__device__ __forceinline__ ItemRange item_range(const AttnOf<SHARED>& a, const SeqOf<SHARED>& s, int tile, int RT, int pass) {
+__device__ __forceinline__ RangeOf<SHARED> item_range(const AttnOf<SHARED>& a, const SeqOf<SHARED>& s, int tile, int RT, int pass) {
     const int r0 = tile * RT, r1 = min(r0 + RT, s.n * a.G) - 1;
     const int h0 = row_last(a, s, r0 / a.G, pass), h1 = row_last(a, s, r1 / a.G, pass);
-    ItemRange r;
-    r.lo = SHARED ? first_of<SHARED>(s) : row_first(a, h0);
+    RangeOf<SHARED> r;
+    if constexpr (SHARED) {
+        r.lo = r.lo_all = s.lo;
+        r.origin = s.lo & ~(a.run - 1);
+    } else {
+        r.lo = row_first(a, h0);
+        r.lo_all = row_first(a, h1);
+    }
     r.hi = h1;
-    r.lo_all = SHARED ? first_of<SHARED>(s) : row_first(a, h1);
     r.hi_all = h0;
     return r;
 }
@@ -327,13 +341,18 @@ struct ItemWalk {
     int64_t at, left;  // place in the line, and what is left of the part
     int b, h, tile;  // the item
     SeqOf<SHARED> s;
-    ItemRange r;
+    RangeOf<SHARED> r;
     int unit, end;   // units [unit, end) of 128 keys, of this item in this part
     int64_t item_end;  // the item's end in the line
     int own;         // SHARED: an item's own cost (IC0 without)
     bool head;       // an earlier CTA has the item's first units
     bool tail;       // a later CTA has its last units
 
+    // First key of unit u.
+    __device__ int key0(int u) const {
+        if constexpr (SHARED) return r.origin + u * kUnit;
+        else return u * kUnit;
+    }
     __device__ int table_row() const {
         if constexpr (SHARED) return s.row;
         else return b;
@@ -497,9 +516,8 @@ struct Runs {
     int cur, nxt, base;  // entries of the units base .. base + 32 / boxes - 1, and of as many behind
     template <class Walk>
     __device__ __forceinline__ int load(const CacheView& c, const Walk& w, int unit, int box_log2) const {
-        const int boxes_log2 = 7 - box_log2;
-        const int k = ((unit << boxes_log2) + (int)(threadIdx.x & 31)) << box_log2;
-        if (k >= w.end * kUnit || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
+        const int k = w.key0(unit) + ((int)(threadIdx.x & 31) << box_log2);
+        if (k >= w.key0(w.end) || k > w.r.hi || k + (1 << box_log2) <= w.r.lo) return -1;
         const int pg = __ldg(c.table + (int64_t)w.table_row() * c.s_table + (k >> c.page_log2));
         return pg < 0 ? -2 : pg;
     }

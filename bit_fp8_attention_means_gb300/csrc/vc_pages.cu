@@ -15,6 +15,8 @@
 // names beyond theirs.  Finding the last of them needs no table: each subtracts one from the
 // page's count; where none is left, all of them offer their place in the order to the same
 // word, and the largest has it.
+#include <climits>
+
 #include "vc_device.cuh"
 #include "vc_internal.h"
 #include "vc_paged.cuh"
@@ -65,6 +67,36 @@ __device__ __forceinline__ uint32_t free_word(const Pool& pool, int pages, int i
     if (i >= words) return 0u;
     const uint32_t w = __ldcg(pool.free + i);
     return i == words - 1 && (pages & 31) ? w & ((1u << (pages & 31)) - 1u) : w;
+}
+
+// Words of the free bits that a thread of the planning block takes at a time: neighbours, few of a small
+// pool, so that more threads have some.
+constexpr int kWords = 8;
+__device__ __forceinline__ int words_of(int pages) { return min(kWords, (pages / 32 + kPlan) / kPlan); }
+
+// The pages of the bits of words i .. i + per - 1 to list[at] and on, below `limit`; put(p, at) for each.  A
+// warp takes its lanes' words one after the other, a bit a lane (a thread alone has up to 256 stores to make).
+template <class Put>
+__device__ __forceinline__ void expand(const uint32_t (&word)[kWords], int per, int i, int at, int limit, int32_t* list, Put put) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+        if (k >= per) break;
+        if (!__any_sync(0xffffffffu, word[k] != 0u && at < limit)) {
+            at += __popc(word[k]);
+            continue;
+        }
+        for (int src = 0; src < 32; ++src) {
+            const uint32_t w = __shfl_sync(0xffffffffu, word[k], src);
+            const int first = __shfl_sync(0xffffffffu, at, src), base = __shfl_sync(0xffffffffu, i + k, src) * 32;
+            const int to = first + __popc(w & ((1u << lane) - 1u));
+            if ((w >> lane & 1u) && to < limit) {
+                list[to] = base + lane;
+                put(base + lane, to);
+            }
+        }
+        at += __popc(word[k]);
+    }
 }
 
 // ------------------------------------------------------------ forking and giving back
@@ -205,21 +237,20 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const CacheView c, const
     block_scan(need, &all);
     need = all;
     // the lowest free pages
-    constexpr int WORDS = 8;  // of a thread at a time
+    const int per = words_of(c.pages);
     int found = 0;
-    for (int i0 = 0; found < need && i0 * 32 < c.pages; i0 += kPlan * WORDS) {
-        uint32_t word[WORDS];
+    for (int i0 = 0; found < need && i0 * 32 < c.pages; i0 += kPlan * per) {
+        const int i = i0 + tid * per;
+        uint32_t word[kWords];
         int mine = 0;
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) {
-            word[k] = free_word(pool, c.pages, i0 + tid * WORDS + k);
+        for (int k = 0; k < kWords; ++k) {
+            word[k] = k < per ? free_word(pool, c.pages, i + k) : 0u;
             mine += __popc(word[k]);
         }
-        int some, at = found + block_scan(mine, &some);
-#pragma unroll
-        for (int k = 0; k < WORDS; ++k)
-            for (uint32_t bits = word[k]; bits && at < need; bits &= bits - 1)
-                ws.fresh[at++] = (i0 + tid * WORDS + k) * 32 + __ffs(bits) - 1;
+        int some;
+        const int at = found + block_scan(mine, &some);
+        expand(word, per, i, at, need, ws.fresh, [](int, int) {});
         found += some;
     }
     __syncthreads();
@@ -368,42 +399,33 @@ __global__ void __launch_bounds__(kCopy) copy_begun_kernel(const CacheView c, co
 // place in the lists, believed only if the list names p there.
 
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool pool, int pages, const CompactWs ws) {
-    constexpr int WORDS = 8;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, per = words_of(pages);
     launch_dependents();
     int sum = 0, all;
     for (int i = tid; i * 32 < pages; i += kPlan) sum += __popc(free_word(pool, pages, i));
     block_scan(sum, &all);
     const int used = pages - all;
     int holes = 0, moved = 0;
-    for (int i0 = 0; i0 * 32 < pages; i0 += kPlan * WORDS) {
-        uint32_t hole[WORDS], move[WORDS];
+    for (int i0 = 0; i0 * 32 < pages; i0 += kPlan * per) {
+        const int i = i0 + tid * per;
+        uint32_t hole[kWords], move[kWords];
         int nh = 0, nm = 0;
 #pragma unroll
-        for (int k = 0; k < WORDS; ++k) {
-            const int i = i0 + tid * WORDS + k, base = i * 32;
-            const uint32_t w = free_word(pool, pages, i);
+        for (int k = 0; k < kWords; ++k) {
+            const int base = (i + k) * 32;
+            const uint32_t w = k < per ? free_word(pool, pages, i + k) : 0u;
             // bits of pages below `used`, and of pages there are
             const uint32_t low = base + 32 <= used ? ~0u : base >= used ? 0u : (1u << (used - base)) - 1u;
-            const uint32_t real = base + 32 <= pages ? ~0u : base >= pages ? 0u : (1u << (pages - base)) - 1u;
+            const uint32_t real = k >= per ? 0u : base + 32 <= pages ? ~0u : base >= pages ? 0u : (1u << (pages - base)) - 1u;
             hole[k] = w & low;
             move[k] = ~w & ~low & real;
             nh += __popc(hole[k]);
             nm += __popc(move[k]);
         }
         int some_h, some_m;
-        int h = holes + block_scan(nh, &some_h);
-        int m = moved + block_scan(nm, &some_m);
-#pragma unroll
-        for (int k = 0; k < WORDS; ++k) {
-            const int base = (i0 + tid * WORDS + k) * 32;
-            for (uint32_t bits = hole[k]; bits; bits &= bits - 1) ws.to[h++] = base + __ffs(bits) - 1;
-            for (uint32_t bits = move[k]; bits; bits &= bits - 1) {
-                const int p = base + __ffs(bits) - 1;
-                ws.number[p] = m;
-                ws.from[m++] = p;
-            }
-        }
+        const int h = holes + block_scan(nh, &some_h), m = moved + block_scan(nm, &some_m);
+        expand(hole, per, i, h, INT_MAX, ws.to, [](int, int) {});
+        expand(move, per, i, m, INT_MAX, ws.from, [&](int p, int at) { ws.number[p] = at; });
         holes += some_h;
         moved += some_m;
     }
@@ -455,11 +477,12 @@ unsigned col_blocks(int cols, int rows) {
 
 int tok_log2_of(int d) { return d == 128 ? 3 : 2; }  // 16-byte pieces of a token's codes
 
-// Eight blocks of 256 threads an SM, fewer where there is less to copy.
+// Blocks of 256 threads, many an SM so that none ends late (of 4,000 pages of 135 KB: 8 an SM 182 us, 32 166 us),
+// fewer where there is less to copy.
 unsigned copy_blocks(const CacheView& c, int d, int64_t pages) {
     const int64_t codes = (int64_t)c.H << (c.page_log2 + tok_log2_of(d)), scales = (int64_t)c.H << (c.page_log2 - 2);
     const int64_t tiles = pages * 2 * ((codes + kTile - 1) / kTile + (scales + kTile - 1) / kTile);
-    return (unsigned)(tiles < kMaxCtas * 8 ? tiles : kMaxCtas * 8);
+    return (unsigned)(tiles < kMaxCtas * 32 ? tiles : kMaxCtas * 32);
 }
 
 }  // namespace
@@ -512,7 +535,7 @@ vc_status launch_pages_compact(const CacheView& c, int d, const Pool& pool, int3
     ws.to = ws.from + c.pages / 2;
     compact_plan_kernel<<<1, kPlan, 0, st>>>(pool, c.pages, ws);
     if (cudaGetLastError() != cudaSuccess) return VC_ERR_CUDA;
-    return launch_after(compact_kernel, dim3(kMaxCtas * 8), kCopy, 0, st, c, pool, ws, count, tok_log2_of(d));
+    return launch_after(compact_kernel, dim3(kMaxCtas * 16), kCopy, 0, st, c, pool, ws, count, tok_log2_of(d));
 }
 
 }  // namespace vc

@@ -401,18 +401,15 @@ def alloc_cache(pages, page_size, H, d, device):
 
 
 @functools.lru_cache(maxsize=256)
-def _cache_shape(shape, v_shape, sk_shape, sv_shape, k, v, t, u):
-    """Checks the shapes and strides of K8, V8, sk, sv: their vc_cache_shape, which depends on these numbers alone."""
-    if len(shape) != 4 or v_shape != shape:
+def _cache_shape(shape, sk_shape, k, t):
+    """The vc_cache_shape of K8 (and V8) and sk (and sv) of these shapes and strides, which depends on them alone."""
+    if len(shape) != 4:
         raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
     pages, H, page, d = shape
-    if sk_shape != (pages, H, page) or sv_shape != (pages, H, page):
+    if sk_shape != (pages, H, page):
         raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
     if pages < 2 or H < 2:  # a dimension of one element may have any stride: it gets a legal one
-        k, v = _plain_strides(shape, k, d), _plain_strides(shape, v, d)
-        t, u = _plain_strides(shape[:3], t, page), _plain_strides(shape[:3], u, page)
-    if v != k or u != t:
-        raise ValueError("K8 and V8, and sk and sv, must share strides")
+        k, t = _plain_strides(shape, k, d), _plain_strides(shape[:3], t, page)
     if (k[3] != 1 or t[2] != 1) and min(shape) > 0:
         raise ValueError("channels and the scales' tokens must be contiguous")
     return VcCacheShape(pages, page, H, d, k[0], k[1], k[2], t[0], t[1])
@@ -422,11 +419,18 @@ def _cache_parts(cache):
     """Checks a dict of K8, sk, V8, sv (see alloc_cache): its vc_cache_shape (not to be changed), the four pointers,
     the device's index."""
     K8, V8, sk, sv = cache["K8"], cache["V8"], cache["sk"], cache["sv"]
-    if K8.dtype is not _U8 or V8.dtype is not _U8:
+    if K8.dtype is not _U8 or V8.dtype is not _U8 or V8.shape != K8.shape:
         raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
-    if sk.dtype is not _F32 or sv.dtype is not _F32:
+    if sk.dtype is not _F32 or sv.dtype is not _F32 or sv.shape != sk.shape:
         raise ValueError("sk and sv must be fp32 [pages, H, page_size]")
-    s = _cache_shape(K8.shape, V8.shape, sk.shape, sv.shape, K8.stride(), V8.stride(), sk.stride(), sv.stride())
+    shape, scales, k, t = K8.shape, sk.shape, K8.stride(), sk.stride()
+    s = _cache_shape(shape, scales, k, t)
+    v, u = V8.stride(), sv.stride()
+    if v != k or u != t:  # they may differ where a dimension has one element
+        page, d = shape[2:]
+        if _plain_strides(shape, v, d) != _plain_strides(shape, k, d) or \
+                _plain_strides(scales, u, page) != _plain_strides(scales, t, page):
+            raise ValueError("K8 and V8, and sk and sv, must share strides")
     dev = K8.get_device()
     if V8.get_device() != dev or sk.get_device() != dev or sv.get_device() != dev:
         raise ValueError("the cache's tensors are on different devices")
@@ -485,10 +489,12 @@ def _on_device(dev, stream, fn, args, where):
     if here != dev:
         torch.cuda.set_device(dev)
     try:
-        _check(fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream), where)
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     finally:
         if here != dev:
             torch.cuda.set_device(here)
+    if code:
+        raise VcError(code, where)
 
 
 def _check_stream(stream, dev):
@@ -738,7 +744,7 @@ def _rope_spec(rope, dev):
 
 def _int32_vector(name, t, n, dev):
     """Checks an int32 vector of n elements: its pointer."""
-    if t.dtype is not _I32 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
+    if t.dtype is not _I32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous int32 [%d]" % (name, n))
     if t.get_device() != dev:
         raise ValueError("%s is not on the other tensors' device" % name)
