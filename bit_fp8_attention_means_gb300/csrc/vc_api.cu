@@ -456,7 +456,9 @@ vc_status vc_pages_fork(vc_cache_shape cache, vc_pool pool, const int32_t* table
     if ((st = check_table(cache, new_table, s_new, N, new_cols)) != VC_OK) return st;
     if (!kv_len || !parents || !new_len || !aligned4(kv_len) || !aligned4(parents) || !aligned4(lens) || !aligned4(new_len))
         return VC_ERR_INVALID_ARG;
-    if (overlap(table, (B - 1) * s_table + cols, new_table, (N - 1) * s_new + new_cols) || overlap(kv_len, B, new_len, N))
+    const int64_t new_size = (N - 1) * s_new + new_cols;
+    if (overlap(table, (B - 1) * s_table + cols, new_table, new_size) || overlap(kv_len, B, new_len, N) ||
+        overlap(parents, N, new_len, N) || overlap(parents, N, new_table, new_size))
         return VC_ERR_INVALID_ARG;
     ForkArgs f;
     f.table_in = table;

@@ -795,26 +795,30 @@ static SharedWs shared_ws(const int (&rt)[2], int d, int64_t B, int64_t N, size_
     return w;
 }
 
-// Whether one pass of every sequence over all its keys, as vc_attn_paged does it, is as fast: where nothing is
-// shared; where the whole work is small (the two launches more take 6 us); and where the sequences' own
-// rows fill their tiles, since then a prefix read once for all of them is a small part of the work.  The last
-// by the time of a unit of a sequence's tiles against that of as many rows in tiles of 256.  8 heads, 21,600
-// tokens in common, shared against one pass: 8 sequences of 160 rows 127 and 161 us, 4 of 300 rows
-// 147 and 169, 8 of 400 rows 325 and 304, 3 of 600 rows 211 and 189.
-static bool one_pass(const vc_cache_shape& c, int G, int B, int T, int N, int max_q, int cols) {
-    if (N < 1 || B <= N) return true;
+// Whether two passes can be faster than one of every sequence over all its keys, as vc_attn_paged does it: not
+// where nothing is shared, nor where the sequences' own rows fill their tiles, since then a prefix read once
+// for all of them is a small part of the work.  That goes by the time of a unit of a sequence's tiles against that
+// of as many rows in tiles of 256.  8 heads, 21,600 tokens in common, two passes against one: 8 sequences of 160
+// rows 132 and 164 us, 4 of 300 rows 132 and 167, 8 of 400 rows 308 and 303, 3 of 600 rows 192 and 187.
+static bool worth_sharing(int G, int B, int T, int N, int max_q) {
+    if (N < 1 || B <= N) return false;
     const int64_t rows = hinted_rows(G, B, T, max_q);
-    const int RT = tile_rows(G, B, T, max_q);
-    const int64_t tiles = (rows + RT - 1) / RT, units = ((int64_t)cols * c.page_size + kUnit - 1) / kUnit;
-    if (B * c.H * tiles * units <= kMaxCtas * 10) return true;
-    if (rows <= 64) return false;
+    if (rows <= 64) return true;
     const int64_t last = rows % 256, alone = rows / 256 * 195 + (last > 128 ? 195 : last ? 120 : 0);
-    return rows * 195 >= 256 * alone * 3 / 4;
+    return rows * 195 < 256 * alone * 3 / 4;
+}
+
+// Whether the whole work is so small that two launches more, 6 us, are not won back: 4 sequences of 730 keys took
+// 18.6 us in two passes and 14.5 in one.
+static bool small_work(const vc_cache_shape& c, int G, int B, int T, int max_q, int cols) {
+    const int RT = tile_rows(G, B, T, max_q);
+    const double tiles = (double)((hinted_rows(G, B, T, max_q) + RT - 1) / RT), units = ((double)cols * c.page_size + kUnit - 1) / kUnit;
+    return (double)B * c.H * tiles * units <= kMaxCtas * 10.0;
 }
 
 size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int N, int max_q, int max_rows) {
     const size_t one = attn_paged_workspace(c, Hq, B, T, max_q);
-    if (one_pass(c, Hq / c.H, B, T, N, max_q, 1 << 30)) return one;
+    if (!worth_sharing(Hq / c.H, B, T, N, max_q)) return one;
     const int G = Hq / c.H, rt[2] = {shared_rows(G, N, T, max_rows, 1), shared_rows(G, B, T, max_q, 2)};
     const size_t two = shared_ws(rt, c.d, B, N, (size_t)T * Hq).bytes;
     return one > two ? one : two;  // which of the two is taken depends on the table's columns too
@@ -827,7 +831,7 @@ static int item_units(int RT) { return RT <= 16 ? 3 : RT == 32 ? 1 : RT <= 128 ?
 vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape, const CacheView& c, int max_rows, void* ws,
                              cudaStream_t st) {
     const int d = shape.d;
-    if (one_pass(shape, args.G, c.B, c.T, args.N, args.max_q, c.cols)) {
+    if (!worth_sharing(args.G, c.B, c.T, args.N, args.max_q) || small_work(shape, args.G, c.B, c.T, args.max_q, c.cols)) {
         // (that launch is for the report alone)
         const vc_status s = c.dev_status ? launch_shared_check(args, c, st) : VC_OK;
         return s == VC_OK ? launch_attn_paged(args, c, d, ws, st) : s;

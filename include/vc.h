@@ -504,7 +504,8 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
  *   N = 0    no groups (the pointers may be NULL).
  *   max_rows the most tokens of this call in a group, as far as the caller knows it (0: unknown); a
  *            hint as max_q.
- * That sequences of a group hold the same tokens is not checked: the first one's are taken.  groups
+ * That sequences of a group hold the same tokens is not checked: each row may see its own sequence's or
+ * the first one's (calls that gain nothing from sharing run as vc_attn_paged does).  groups
  * and prefix that break their rules are clamped and reported as cu and kv_len are; nothing is read
  * outside the caller's buffers, but rows of such a group or sequence are unspecified.
  *   workspace  >= vc_attn_paged_shared_workspace(...) bytes, 256-byte aligned.
@@ -620,7 +621,8 @@ vc_status vc_pages_reserve(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t
  * given back.  Parents may come several times.
  *   table    int32 [B, cols], row stride s_table (>= cols); kv_len int32 [B]; parents, lens int32 [N].
  *   new_table  int32 [N, new_cols], row stride s_new; new_len int32 [N].  The memory from the first
- *            to the last row of the two tables must not overlap, nor kv_len and new_len.
+ *            to the last row of the two tables must not overlap, nor new_len with kv_len, nor parents with
+ *            what is written.
  * A parent outside -1 .. B - 1, a length below 0 or beyond either table's columns gives an empty
  * row, an entry that names no page -1; both are reported.  N = 0 does nothing.
  * Errors: VC_ERR_INVALID_ARG (null or misaligned pointers, B < 1, N < 0, cols or strides out of

@@ -116,7 +116,8 @@ def test_fork_and_trim_refusals(L):
         assert call(cols=1 << 26, s=1 << 26) == 2
     assert trim(lens=None) == 1
     for kw in (dict(parents=None), dict(new=None), dict(new=TWO), dict(N=-1), dict(s_new=3), dict(new_cols=0), dict(new_len=None), dict(new_len=FAKE), dict(new=FAKE),
-               dict(new=ctypes.c_void_p(0x10000 + 4 * 11)), dict(new=ctypes.c_void_p(0x10000 - 4 * 7)), dict(new_len=ctypes.c_void_p(0x10000 - 4))):
+               dict(new=ctypes.c_void_p(0x10000 + 4 * 11)), dict(new=ctypes.c_void_p(0x10000 - 4 * 7)), dict(new_len=ctypes.c_void_p(0x10000 - 4)),
+               dict(parents=apart), dict(parents=ctypes.c_void_p(0x20004))):
         assert fork(**kw) == 1, kw
     assert fork(new_cols=1 << 26, s_new=1 << 26) == 2 and fork(N=0, new=None) == 0
 
