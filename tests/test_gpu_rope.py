@@ -63,6 +63,18 @@ def test_rope(layout, d, rot, T, H):
         check(vc.vc_rope(X, rope, pos=pos.to(DEV), inverse=inverse), X, pos.tolist(), rope, inverse)
 
 
+@pytest.mark.parametrize("T,H,d,rot,layout", [(3001, 40, 128, 96, "halves"), (5003, 24, 64, 64, "pairs"), (60001, 1, 128, 32, "pairs"), (30011, 3, 64, 16, "halves"),
+                                              (20011, 7, 128, 64, "halves")])
+def test_many_rows(T, H, d, rot, layout):
+    """Several rows a group of lanes, tokens that end anywhere among them."""
+    rope = vc.make_rope(rot, layout=layout, device=DEV)
+    X, pos = rows(T, H, d, 30), some_positions(T, 31)
+    check(vc.vc_rope(X, rope, pos=pos.to(DEV)), X, pos.tolist(), rope)
+    in_place = X.clone()
+    vc.vc_rope(in_place, rope, pos=pos.to(DEV), out=in_place, inverse=1)
+    check(in_place, X, pos.tolist(), rope, 1)
+
+
 @pytest.mark.parametrize("kw", [dict(scaling="positions", factor=4.0), dict(scaling="base", factor=8.0, base=500000.0),
                                 dict(scaling="ramp", factor=16.0), dict(scaling="ramp", factor=2.0, magnitude=0.75, original=8192)], ids=str)
 def test_scaled_contexts(kw):
@@ -168,7 +180,8 @@ def test_no_rows():
 # ---------------------------------------------------------------- with the cache
 
 APPEND_CASES = [dict(n=[1], kv=[1], H=1, d=64), dict(n=[1] * 5, kv=[1, 17, 128, 5000, 16], H=8, G=4), dict(n=[0, 5, 0, 40, 0], kv=[0, 9, 33, 40, 7], H=3, G=2, d=64, page=32),
-                dict(n=[300], kv=[500], H=5, page=128), dict(n=[3] * 70, kv=[50] * 70, H=2, d=64, tail=5), dict(n=[16, 256], kv=[16, 256], H=1, G=16, page=256)]
+                dict(n=[300], kv=[500], H=5, page=128), dict(n=[3] * 70, kv=[50] * 70, H=2, d=64, tail=5), dict(n=[16, 256], kv=[16, 256], H=1, G=16, page=256),
+                dict(n=[1500, 0, 703], kv=[1600, 9, 703], H=8, G=5, page=64), dict(n=[9000], kv=[9001], H=2, G=3, d=64, page=128, tail=3)]
 
 
 @pytest.mark.parametrize("case", APPEND_CASES, ids=lambda c: "B%d_H%d" % (len(c["n"]), c["H"]))

@@ -202,7 +202,7 @@ def test_broken_groups_are_reported_and_touch_nothing_outside():
 
 @pytest.mark.parametrize("case", ["two", "groups", "many rows"], ids=name)
 def test_given_outputs_and_streams(case):
-    """Strided O, a workspace of the caller's with anything in it, another stream, and the C entry without lse."""
+    """Strided Q and O, a workspace of the caller's with anything in it, another stream, and the C entry without lse."""
     c = Shared(seed=12, **CASES[case])
     cache, args, groups, Q, Hq = c.cache(DEV), tables(c, True), c.shared_args(DEV), c.Q.to(DEV), c.H * c.G
     hints = dict(max_q=max(c.n), max_rows=c.most())
@@ -210,6 +210,9 @@ def test_given_outputs_and_streams(case):
     c.check(want, c.cache())
     big = torch.full((c.T, Hq + 1, c.d + 8), 3.0, dtype=torch.bfloat16, device=DEV)
     size = vc.attn_paged_shared_workspace_bytes(cache, Hq, c.B, c.T, len(c.prefix), **hints)
+    wide_q = torch.full((c.T, Hq, 2, c.d), math.nan, dtype=torch.bfloat16, device=DEV)
+    wide_q[:, :, 1] = Q
+    assert same_bits(vc.vc_attn_paged_shared(wide_q[:, :, 1], cache, *args, *groups, **hints)[0], want[0])
     for fill in (0, 255, 170):
         ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
         vc.vc_attn_paged_shared(Q, cache, *args, *groups, O=big[:, :Hq, :c.d], workspace=ws, **hints)
