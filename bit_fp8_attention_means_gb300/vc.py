@@ -836,6 +836,21 @@ def alloc_pool(pages, device):
     return dict(refs=torch.zeros(pages, dtype=_I32, device=device), free=bits)
 
 
+@functools.lru_cache(maxsize=256)
+def _pages_shape(shape):
+    """A vc_cache_shape for calls that look at the pages' number and size alone, for K8 of this shape."""
+    if len(shape) != 4:
+        raise ValueError("K8 and V8 must be uint8 [pages, H, page_size, d]")
+    pages, H, page, d = shape
+    return VcCacheShape(pages, page, H, d, H * page * d, page * d, d, H * page, page)
+
+
+def _pages_of(cache):
+    """The pages of a cache: what _pages_shape says, the device's index."""
+    K8 = cache["K8"]
+    return _pages_shape(K8.shape), K8.get_device()
+
+
 def _pool_of(pool, pages, dev) -> VcPool:
     return VcPool(_int32_vector("refs", pool["refs"], pages, dev), _int32_vector("free", pool["free"], -(-pages // 32), dev))
 
@@ -904,7 +919,7 @@ def vc_pages_fork(cache, pool, table, kv_len, parents, new_table, new_len, lens=
     lens[i] tokens (all of them without lens) of sequence parents[i] of `table`; parents[i] = -1: an empty one.
     Nothing is copied before vc_pages_reserve.  What the rows held is not given back: vc_pages_trim does that."""
     L = lib()
-    s, _, dev = _cache_parts(cache)
+    s, dev = _pages_of(cache)
     p = _pool_of(pool, s.pages, dev)
     at, s_table, B, cols = _table_of("table", table, dev)
     to, s_new, N, new_cols = _table_of("new_table", new_table, dev)
@@ -919,7 +934,7 @@ def vc_pages_trim(cache, pool, table, kv_len, lens, dev_status=None, stream=None
     """Each sequence keeps the pages of its first lens[b] tokens (int32 [B]; 0 ends it, a negative one leaves it
     alone): its other entries of `table` become -1, kv_len at most lens."""
     L = lib()
-    s, _, dev = _cache_parts(cache)
+    s, dev = _pages_of(cache)
     p = _pool_of(pool, s.pages, dev)
     at, s_table, B, cols = _table_of("table", table, dev)
     args = (s, p, at, s_table, B, cols, _int32_vector("kv_len", kv_len, B, dev), _int32_vector("lens", lens, B, dev),
