@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(256) fork_kernel(const ForkArgs f, const Pool 
         int p = -1;
         if (col < held) {
             p = named(f.table_in[(int64_t)parent * f.s_in + col], f.pages);
+            if (p >= 0 && (__ldg(pool.free + (p >> 5)) >> (p & 31) & 1u)) p = -1;  // counted for nobody: others may get it
             if (p >= 0) atomicAdd(pool.refs + p, 1);
             else flag_invalid(f.dev_status);
         }
@@ -204,10 +205,11 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const CacheView c, const
     for (int w = tid; w < W; w += kPlan) {
         const int b = sequence(w);
         const SeqInfo s = seq_info(c, b);
-        const int e = table[(int64_t)b * c.s_table + first_col(s, c.page_log2) + w - off[b]], p = named(e, c.pages);
-        if (strange(e, c.pages)) flag_invalid(c.dev_status);
+        const int e = table[(int64_t)b * c.s_table + first_col(s, c.page_log2) + w - off[b]];
+        int p = named(e, c.pages);
         const int names = p < 0 ? 0 : __ldcg(pool.refs + p);
-        if (p >= 0 && names < 1) flag_invalid(c.dev_status);
+        if (names < 1) p = -1;  // counted for nobody: others may get it
+        if (e != -1 && p < 0) flag_invalid(c.dev_status);
         const int cls = p < 0 ? kMissing : names > 1 ? kShared : kOwn;
         shared |= cls == kShared;
         need += cls == kMissing;

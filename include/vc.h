@@ -602,7 +602,8 @@ typedef struct {
  * into no page of others (it finds a page that is not there, which it reports); calling again
  * with enough free pages makes up for it, and vc_pages_trim frees such a page like any other.
  *   Nothing at all is done for a batch that breaks its rules (reported).  kv_len[b] < n_b counts
- * the positions from 0 on.
+ * the positions from 0 on.  An entry there that names no page, or a free one, is reported and gets a
+ * new page.
  *   workspace  >= vc_pages_reserve_workspace(cache, B, T) bytes, 256-byte aligned.
  * Errors as vc_cache_append (without K and V), VC_ERR_INVALID_ARG for a null or misaligned pool,
  * VC_ERR_UNSUPPORTED for pages > 2^30 or H * page_size * d >= 2^31, VC_ERR_WORKSPACE.
@@ -624,7 +625,7 @@ vc_status vc_pages_reserve(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t
  *            to the last row of the two tables must not overlap, nor new_len with kv_len, nor parents with
  *            what is written.
  * A parent outside -1 .. B - 1, a length below 0 or beyond either table's columns gives an empty
- * row, an entry that names no page -1; both are reported.  N = 0 does nothing.
+ * row, an entry that names no page, or a free one, -1; all are reported.  N = 0 does nothing.
  * Errors: VC_ERR_INVALID_ARG (null or misaligned pointers, B < 1, N < 0, cols or strides out of
  * range, overlap), VC_ERR_UNSUPPORTED as vc_pages_reserve and vc_cache_append; VC_ERR_CUDA.
  */

@@ -214,6 +214,32 @@ def test_broken_batches_and_pools_are_reported():
         assert int(dev.status) == 1 and int(dev.kv[3]) == 0 and dev.table[3].eq(-1).all() and int(dev.kv[4]) == (1 if lens else 40)
 
 
+def test_free_pages_that_a_table_names_get_no_second_owner():
+    """An entry that names a free page: a fork leaves it out, reserving replaces it; both report it."""
+    m = grown(seed=7)
+    free = max(p for p in range(m.pages) if not m.refs[p])
+    for entry in (free, -2 - free):
+        dev = Device(m)
+        dev.table[1, 1] = entry
+        vc.vc_pages_fork(dev.cache, dev.pool, dev.table[:3], dev.kv[:3], ints([1]), dev.table[3:4], dev.kv[3:4], dev_status=dev.status)
+        assert int(dev.status) == 1 and int(dev.kv[3]) == 40
+        assert dev.table[3].tolist() == [m.table[1][0], -1, m.table[1][2]] + [-1] * 5
+        m2 = grown(seed=7)
+        m2.refs[m.table[1][0]] += 1
+        m2.refs[m.table[1][2]] += 1
+        assert dev.pool["refs"].tolist() == m2.refs and dev.pool["free"].tolist() == m2.bits()
+
+        m2 = grown(seed=7)
+        dev = Device(m)
+        n = [0, 20, 0, 0, 0, 0]                                  # positions 20 .. 39: columns 1 and 2
+        dev.table[1, 1] = entry
+        dev.reserve(n)
+        m2.refs[m2.table[1][1]] = 1                              # its own page before, still counted
+        lowest = min(p for p in range(m.pages) if not m.refs[p])
+        m2.table[1][1], m2.refs[lowest] = lowest, 1
+        dev.same(m2, 1)
+
+
 def test_fork_into_fewer_columns():
     m = grown(seed=5)
     dev = Device(m)
