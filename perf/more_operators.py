@@ -27,31 +27,31 @@ FRAME = 3600   # one latent frame of 45 x 80 tokens
 def listed():
     return [
         # serving: the queries of one new token of each sequence, all channels
-        dict(name="rotate one token each", op="rotate", T=100, H=32, d=128, rot=128, layout="halves", scaling="none", base=10000.0, factor=1.0, far=8192, inverse=False),
+        dict(name="rotate, one token each", op="rotate", T=100, H=32, d=128, rot=128, layout="halves", scaling="none", base=10000.0, factor=1.0, far=8192, inverse=False),
         # the way back through the rotation of a long prompt's keys: half of the channels, neighbouring pairs, a context stretched eight times
-        dict(name="rotate back a long prompt", op="rotate", T=20011, H=40, d=128, rot=64, layout="pairs", scaling="ramp", base=500000.0, factor=8.0, far=262144, inverse=True),
+        dict(name="rotate back, a long prompt", op="rotate", T=20011, H=40, d=128, rot=64, layout="pairs", scaling="ramp", base=500000.0, factor=8.0, far=262144, inverse=True),
         # serving: a new token of each sequence on its way into the cache, grouped heads
-        dict(name="rotate and append a token", op="append", B=100, n_lo=1, n_hi=1, kv_lo=1, kv_hi=8192, H=8, G=4, d=128, page=16, rot=128, layout="halves", scaling="none",
+        dict(name="rotate and append, a token", op="append", B=100, n_lo=1, n_hi=1, kv_lo=1, kv_hi=8192, H=8, G=4, d=128, page=16, rot=128, layout="halves", scaling="none",
              base=10000.0, factor=1.0, lens=21),
         # prompts of different lengths, one of them empty, far into a stretched context
-        dict(name="rotate and append prompts", op="append", B=7, n_lo=0, n_hi=6007, kv_lo=6007, kv_hi=131072, H=8, G=5, d=128, page=64, rot=96, layout="halves",
+        dict(name="rotate and append, prompts", op="append", B=7, n_lo=0, n_hi=6007, kv_lo=6007, kv_hi=131072, H=8, G=5, d=128, page=64, rot=96, layout="halves",
              scaling="ramp", base=1000000.0, factor=4.0, lens=22),
         # 64 continuations of a prompt begin: the old ones' pages are given back, the prompt is forked, and each gets a page of its own for its first token
-        dict(name="pages a prompt forked", op="fork", B=1, N=64, kv_lo=8183, kv_hi=8183, n=1, H=8, d=128, page=64, used=0.3, pages=4096, lens=23),
+        dict(name="pages, a prompt forked", op="fork", B=1, N=64, kv_lo=8183, kv_hi=8183, n=1, H=8, d=128, page=64, used=0.3, pages=4096, lens=23),
         # drafts of 512 sequences are taken back to what was accepted, and pages reserved for the next ones
-        dict(name="pages drafts", op="drafts", B=512, N=0, kv_lo=100, kv_hi=4000, n=8, H=1, d=64, page=16, used=0.7, pages=190001, lens=24),
+        dict(name="pages, drafts", op="drafts", B=512, N=0, kv_lo=100, kv_hi=4000, n=8, H=1, d=64, page=16, used=0.7, pages=190001, lens=24),
         # half of a pool's pages moved together after many sequences have ended
-        dict(name="pages moved together", op="compact", B=40, N=0, kv_lo=2000, kv_hi=16000, n=0, H=8, d=128, page=64, used=0.5, pages=12000, lens=25),
+        dict(name="pages, moved together", op="compact", B=40, N=0, kv_lo=2000, kv_hi=16000, n=0, H=8, d=128, page=64, used=0.5, pages=12000, lens=25),
         # one sequence's pages to another pool
-        dict(name="pages to another pool", op="copy", B=1, N=0, kv_lo=20000, kv_hi=20000, n=0, H=4, d=64, page=32, used=0.5, pages=1500, lens=26),
+        dict(name="pages, to another pool", op="copy", B=1, N=0, kv_lo=20000, kv_hi=20000, n=0, H=4, d=64, page=32, used=0.5, pages=1500, lens=26),
         # the smallest: four continuations of a short prompt
-        dict(name="shared a short prompt", op="shared", B=4, N=1, p_lo=700, p_hi=700, s_lo=1, s_hi=60, n_lo=1, n_hi=1, H=2, G=2, d=64, page=16, causal=True, lens=27),
+        dict(name="shared, a short prompt", op="shared", B=4, N=1, p_lo=700, p_hi=700, s_lo=1, s_hi=60, n_lo=1, n_hi=1, H=2, G=2, d=64, page=16, causal=True, lens=27),
         # 100 continuations of a prompt of 8,000 tokens, one token each
-        dict(name="shared one token each", op="shared", B=100, N=1, p_lo=8000, p_hi=8000, s_lo=1, s_hi=900, n_lo=1, n_hi=1, H=8, G=4, d=128, page=16, causal=True, lens=28),
+        dict(name="shared, one token each", op="shared", B=100, N=1, p_lo=8000, p_hi=8000, s_lo=1, s_hi=900, n_lo=1, n_hi=1, H=8, G=4, d=128, page=16, causal=True, lens=28),
         # several prompts with continuations, a few drafted tokens each
-        dict(name="shared prompts with drafts", op="shared", B=60, N=5, p_lo=300, p_hi=30000, s_lo=7, s_hi=700, n_lo=1, n_hi=7, H=4, G=8, d=128, page=64, causal=True, lens=29),
+        dict(name="shared, prompts with drafts", op="shared", B=60, N=5, p_lo=300, p_hi=30000, s_lo=7, s_hi=700, n_lo=1, n_hi=7, H=4, G=8, d=128, page=64, causal=True, lens=29),
         # two versions of the next latent frame over six frames that they have in common, 40 heads
-        dict(name="shared frames of a clip", op="shared", B=2, N=1, p_lo=6 * FRAME, p_hi=6 * FRAME, s_lo=FRAME, s_hi=FRAME, n_lo=FRAME, n_hi=FRAME, H=40, G=1, d=128, page=128,
+        dict(name="shared, frames of a clip", op="shared", B=2, N=1, p_lo=6 * FRAME, p_hi=6 * FRAME, s_lo=FRAME, s_hi=FRAME, n_lo=FRAME, n_hi=FRAME, H=40, G=1, d=128, page=128,
              causal=False, lens=30),
     ]
 
