@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(kCopy) copy_begun_kernel(const CacheView c, co
 // ------------------------------------------------------------ moving together
 //
 // With U pages in use, the used ones from number U on go to the free ones below, in
-// ascending order on both sides (as many by definition).  ws.number[p] is a moved page's
-// place in the lists, believed only if the list names p there.
+// ascending order on both sides (as many by definition).  ws.number[p] is the place of a moved
+// page, or of a free one that is moved into, in its list, believed only if the list names p
+// there.
 
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool pool, int pages, const CompactWs ws) {
     const int tid = threadIdx.x, per = words_of(pages);
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Pool pool, in
         }
         int some_h, some_m;
         const int h = holes + block_scan(nh, &some_h), m = moved + block_scan(nm, &some_m);
-        expand(hole, per, i, h, INT_MAX, ws.to, [](int, int) {});
+        expand(hole, per, i, h, INT_MAX, ws.to, [&](int p, int at) { ws.number[p] = at; });
         expand(move, per, i, m, INT_MAX, ws.from, [&](int p, int at) { ws.number[p] = at; });
         holes += some_h;
         moved += some_m;
@@ -446,16 +447,18 @@ __global__ void __launch_bounds__(kCopy) compact_kernel(const CacheView c, const
     for (int64_t k = me; k < (int64_t)c.B * c.cols; k += all) {
         int32_t* entry = table + k / c.cols * c.s_table + k % c.cols;
         const int e = *entry, p = named(e, c.pages);
-        if (p < used) {
+        if (p < 0) {
             if (strange(e, c.pages)) flag_invalid(c.dev_status);
             continue;
         }
         const int m = ws.number[p];
-        if (m < 0 || m >= moved || ws.from[m] != p) {  // named here and counted nowhere
+        const bool listed = m >= 0 && m < moved && (p < used ? ws.to : ws.from)[m] == p;
+        if (listed != (p >= used)) {  // named here and counted nowhere; one moved into has an owner from now on
             flag_invalid(c.dev_status);
+            if (listed) *entry = -1;
             continue;
         }
-        *entry = e < -1 ? -2 - ws.to[m] : ws.to[m];
+        if (listed) *entry = e < -1 ? -2 - ws.to[m] : ws.to[m];
     }
     for (int64_t k = me; k < moved; k += all) {
         pool.refs[ws.to[k]] = pool.refs[ws.from[k]];

@@ -647,8 +647,8 @@ vc_status vc_pages_trim(vc_cache_shape cache, vc_pool pool, int32_t* table, int6
  * Moves the pages in use together: with U of them, those of numbers from U on go to the free
  * numbers below U, in ascending order on both sides, with their codes, scales and counts, and the
  * entries of `table` follow; pages U .. pages - 1 are free then, and U is written to *used (nullable,
- * device int32).  `table` must hold all entries that name pages of the pool: one that names a page
- * which nobody is counted for stays and is reported.
+ * device int32).  `table` must hold all entries that name pages of the pool.  One that names a page
+ * which nobody is counted for is reported; it stays, or becomes -1 where another page moves there.
  *   workspace  >= vc_pages_compact_workspace(cache) bytes, 256-byte aligned.
  * Errors as vc_pages_reserve.
  */
