@@ -47,7 +47,8 @@ __device__ __forceinline__ bool seq_valid(const CacheView& c, int b) {
 
 // Attention over shared prefixes (SHARED kernels) takes two passes over the same rows.  Pass 1:
 // "sequence" g is group g, its rows those of all its sequences, its keys the prefix, found through
-// the first sequence's row of the table.  Pass 2: sequence b, keys from its group's prefix on.
+// the table's row of the first that has tokens in the call (others may have ended, and hold no pages).
+// Pass 2: sequence b, keys from its group's prefix on.
 
 // Of the N groups, the one that sequence b belongs to; -1: none.
 __device__ __forceinline__ int group_of(const SharedAttn& a, int b) {
@@ -68,11 +69,18 @@ __device__ __forceinline__ int prefix_of(const CacheView& c, const SharedAttn& a
 __device__ __forceinline__ SeqPass group_info(const CacheView& c, const SharedAttn& a, int g) {
     SeqPass s;
     const int b0 = min(max(__ldg(a.groups + g), 0), c.B), b1 = min(max(__ldg(a.groups + g + 1), b0), c.B);
-    s.q0 = min(max(__ldg(c.cu + b0), 0), c.T);
+    const int q0 = __ldg(c.cu + b0);
+    s.q0 = min(max(q0, 0), c.T);
     s.n = min(max(__ldg(c.cu + b1), s.q0), c.T) - s.q0;
     s.L = prefix_of(c, a, g);
     s.lo = 0;
-    s.row = min(b0, c.B - 1);
+    int lo = b0, hi = b1;  // the last b with cu[b] <= q0: the first with tokens, as a rule b0
+    while (hi - lo > 1) {
+        const int mid = lo == b0 ? b0 + 1 : (lo + hi) >> 1;
+        if (__ldg(c.cu + mid) <= q0) lo = mid;
+        else hi = mid;
+    }
+    s.row = min(lo, c.B - 1);
     return s;
 }
 

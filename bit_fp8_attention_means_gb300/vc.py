@@ -635,7 +635,8 @@ def vc_attn_paged_shared(Q, cache, cu, kv_len, table, groups, prefix, softmax_sc
     N runs of sequences, prefix int32 [N] how many tokens a run's sequences have in common, in the same pages but for
     the page that the prefix ends in.  Each prefix is read once for all rows of its run.  Returns (O, lse).
 
-    A prefix holds none of the call's tokens; 0 and runs of one sequence are fine, as are sequences of no run.
+    A prefix holds none of the call's tokens; 0 and runs of one sequence are fine, as are sequences of no run, and
+    sequences without tokens in the call, which may have ended.
     max_q: the longest chunk among the sequences, max_rows: the most tokens of this call in one run, if known (they
     choose kernels, nothing else)."""
     L = lib()

@@ -497,17 +497,18 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
  * limits of accuracy and the errors are vc_attn_paged's.
  *   groups   int32 [N+1], non-decreasing, 0 <= groups[0], groups[N] <= B: group g is the sequences
  *            groups[g] .. groups[g+1] - 1.  Sequences before groups[0] and from groups[N] on are in none.
- *   prefix   int32 [N]: the first prefix[g] tokens of all sequences of group g are the same, found
- *            through the table row of its first sequence (which needs them there even where it has no
- *            token of this call).  They hold none of this call's tokens: prefix[g] <= max(kv_len[b] -
- *            n_b, 0) where n_b > 0.  Any length, 0 too; a page that a prefix ends in may differ behind its end.
+ *   prefix   int32 [N]: the first prefix[g] tokens of all sequences of group g that have tokens in this
+ *            call (n_b > 0) are the same; those without may have ended.  They hold none of this call's
+ *            tokens: prefix[g] <= max(kv_len[b] - n_b, 0) where n_b > 0.  Any length, 0 too; a page that
+ *            a prefix ends in may differ behind its end.
  *   N = 0    no groups (the pointers may be NULL).
  *   max_rows the most tokens of this call in a group, as far as the caller knows it (0: unknown); a
  *            hint as max_q.
  * That sequences of a group hold the same tokens is not checked: each row may see its own sequence's or
- * the first one's (calls that gain nothing from sharing run as vc_attn_paged does).  groups
- * and prefix that break their rules are clamped and reported as cu and kv_len are; nothing is read
- * outside the caller's buffers, but rows of such a group or sequence are unspecified.
+ * those of the group's first one with tokens in the call (calls that gain nothing from sharing run as
+ * vc_attn_paged does).  groups and prefix that break their rules are clamped and reported as cu and
+ * kv_len are; nothing is read outside the caller's buffers, but rows of such a group or sequence are
+ * unspecified.
  *   workspace  >= vc_attn_paged_shared_workspace(...) bytes, 256-byte aligned.
  */
 size_t vc_attn_paged_shared_workspace(vc_cache_shape cache, int Hq, int B, int T, int N, int max_q, int max_rows);
