@@ -37,6 +37,17 @@ __device__ __forceinline__ int named(int e, int pages) {
 
 __device__ __forceinline__ bool strange(int e, int pages) { return e != -1 && named(e, pages) < 0; }
 
+// Too few free pages: over an invalid argument, not over a timeout.
+__device__ __forceinline__ void flag_pages(int32_t* dev_status) {
+    if (!dev_status) return;
+    int* word = reinterpret_cast<int*>(dev_status);
+    for (int seen = *word; seen != (int)VC_ERR_TIMEOUT && seen < (int)VC_ERR_PAGES;) {
+        const int was = atomicCAS(word, seen, (int)VC_ERR_PAGES);
+        if (was == seen) break;
+        seen = was;
+    }
+}
+
 // Exclusive sum over the block of one number a thread; the total for all of them.
 __device__ __forceinline__ int block_scan(int v, int* total) {
     __shared__ int sums[kPlan / 32];
@@ -258,7 +269,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const CacheView c, const
     __syncthreads();
     if (found < need) {
         // the counts as they were, and pages that would have to be copied marked: held, not to be written
-        if (tid == 0 && c.dev_status) atomicMax(reinterpret_cast<int*>(c.dev_status), (int)VC_ERR_PAGES);
+        if (tid == 0) flag_pages(c.dev_status);
         for (int w = tid; w < W; w += kPlan)
             if (ws.cls[w] == kKeep) pool.refs[ws.page[w]] = 0;
         __syncthreads();

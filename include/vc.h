@@ -33,6 +33,9 @@
  *     VC_ERR_TIMEOUT to *dev_status (an int32 in device memory, nullable;
  *     the caller zeroes it beforehand and reads it after synchronising); the
  *     kernel then releases what it holds and returns instead of hanging.
+ *     The call's outputs are unspecified then.  Calls may share a status
+ *     word: the gravest of what they report stays, a timeout above too few
+ *     pages (VC_ERR_PAGES) above what breaks a batch's rules (VC_ERR_INVALID_ARG).
  *   - Token blocks are 128 tokens; nblk = ceil(N/128), Npad = 128*nblk.
  *   - NaN or Inf inputs are outside the contract.
  */
