@@ -418,9 +418,17 @@ static vc_status check_table(const vc_cache_shape& c, const int32_t* table, int6
     return VC_OK;
 }
 
-static bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uint64_t)m * 4 && y < x + (uint64_t)n * 4;
+// Memory of a call: what its blocks read must not be what other blocks write.
+struct Words {
+    const int32_t* at;
+    int64_t n;
+};
+static Words table_words(const int32_t* table, int64_t s_table, int rows, int cols) {
+    return Words{table, (rows - 1) * s_table + cols};  // from the first to the last row
+}
+static bool overlap(const Words& a, const Words& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && x < y + (uint64_t)b.n * 4 && y < x + (uint64_t)a.n * 4;
 }
 
 size_t vc_pages_reserve_workspace(vc_cache_shape cache, int B, int T) {
@@ -440,6 +448,8 @@ vc_status vc_pages_reserve(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t
     CacheView v;
     if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
     if (!workspace_ok(workspace, workspace_bytes, pages_reserve_workspace(v.B, v.T, v.page_log2))) return VC_ERR_WORKSPACE;
+    const Words rows = table_words(batch.table, batch.s_table, v.B, v.cols);
+    if (overlap(rows, Words{v.cu, v.B + 1}) || overlap(rows, Words{v.kv_len, v.B})) return VC_ERR_INVALID_ARG;
     return launch_pages_reserve(v, cache.d, p, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -456,10 +466,12 @@ vc_status vc_pages_fork(vc_cache_shape cache, vc_pool pool, const int32_t* table
     if ((st = check_table(cache, new_table, s_new, N, new_cols)) != VC_OK) return st;
     if (!kv_len || !parents || !new_len || !aligned4(kv_len) || !aligned4(parents) || !aligned4(lens) || !aligned4(new_len))
         return VC_ERR_INVALID_ARG;
-    const int64_t new_size = (N - 1) * s_new + new_cols;
-    if (overlap(table, (B - 1) * s_table + cols, new_table, new_size) || overlap(kv_len, B, new_len, N) ||
-        overlap(parents, N, new_len, N) || overlap(parents, N, new_table, new_size))
-        return VC_ERR_INVALID_ARG;
+    const Words rows = table_words(new_table, s_new, N, new_cols), lengths{new_len, N};
+    if (overlap(rows, lengths)) return VC_ERR_INVALID_ARG;
+    for (const Words& in : {table_words(table, s_table, B, cols), Words{kv_len, B}, Words{parents, N}})
+        if (overlap(in, rows) || overlap(in, lengths)) return VC_ERR_INVALID_ARG;
+    // (lens may be new_len: len_i read in its place gives len_i again)
+    if (overlap(Words{lens, N}, rows) || (overlap(Words{lens, N}, lengths) && lens != new_len)) return VC_ERR_INVALID_ARG;
     ForkArgs f;
     f.table_in = table;
     f.kv_in = kv_len;
@@ -486,6 +498,8 @@ vc_status vc_pages_trim(vc_cache_shape cache, vc_pool pool, int32_t* table, int6
     if ((st = check_pool(cache, pool, &p)) != VC_OK) return st;
     if ((st = check_table(cache, table, s_table, B, cols)) != VC_OK) return st;
     if (!kv_len || !lens || !aligned4(kv_len) || !aligned4(lens)) return VC_ERR_INVALID_ARG;
+    const Words rows = table_words(table, s_table, B, cols), lengths{kv_len, B}, keep{lens, B};
+    if (overlap(rows, lengths) || overlap(rows, keep) || (overlap(lengths, keep) && lens != kv_len)) return VC_ERR_INVALID_ARG;
     TrimArgs t;
     t.table = table;
     t.kv_len = kv_len;
@@ -515,6 +529,7 @@ vc_status vc_pages_compact(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t
     CacheView v;
     if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
     if (!workspace_ok(workspace, workspace_bytes, pages_compact_workspace(cache.pages))) return VC_ERR_WORKSPACE;
+    if (overlap(table_words(table, s_table, B, cols), Words{used, 1})) return VC_ERR_INVALID_ARG;
     return launch_pages_compact(v, cache.d, p, used, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -609,7 +609,8 @@ typedef struct {
  * the positions from 0 on.  An entry there that names no page, or a free one, is reported and gets a
  * new page.
  *   workspace  >= vc_pages_reserve_workspace(cache, B, T) bytes, 256-byte aligned.
- * Errors as vc_cache_append (without K and V), VC_ERR_INVALID_ARG for a null or misaligned pool,
+ * Errors as vc_cache_append (without K and V), VC_ERR_INVALID_ARG for a null or misaligned pool or cu or
+ * kv_len within the table (from its first to its last row),
  * VC_ERR_UNSUPPORTED for pages > 2^30 or H * page_size * d >= 2^31, VC_ERR_WORKSPACE.
  */
 size_t vc_pages_reserve_workspace(vc_cache_shape cache, int B, int T);
@@ -625,9 +626,9 @@ vc_status vc_pages_reserve(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t
  * makes an empty row.  What the rows of new_table and new_len held before is overwritten, not
  * given back.  Parents may come several times.
  *   table    int32 [B, cols], row stride s_table (>= cols); kv_len int32 [B]; parents, lens int32 [N].
- *   new_table  int32 [N, new_cols], row stride s_new; new_len int32 [N].  The memory from the first
- *            to the last row of the two tables must not overlap, nor new_len with kv_len, nor parents with
- *            what is written.
+ *   new_table  int32 [N, new_cols], row stride s_new; new_len int32 [N].  What is read and what is
+ *            written must not overlap, nor the two outputs (of a table, the memory from its first to its
+ *            last row counts), but for lens, which may be new_len itself.
  * A parent outside -1 .. B - 1, a length below 0 or beyond either table's columns gives an empty
  * row, an entry that names no page, or a free one, -1; all are reported.  N = 0 does nothing.
  * Errors: VC_ERR_INVALID_ARG (null or misaligned pointers, B < 1, N < 0, cols or strides out of
@@ -642,7 +643,8 @@ vc_status vc_pages_fork(vc_cache_shape cache, vc_pool pool, const int32_t* table
  * first lens[b] tokens; its other entries become -1, and pages that nobody names any more are
  * free.  kv_len[b] becomes lens[b] where it was more.  lens[b] = 0 ends the sequence, a negative
  * one leaves it alone.  An entry that names a page which nobody is counted for, or none, is
- * reported.  Errors as vc_pages_fork.
+ * reported.  lens must not overlap the table, nor kv_len unless it is kv_len itself, nor kv_len the table.
+ * Errors as vc_pages_fork.
  */
 vc_status vc_pages_trim(vc_cache_shape cache, vc_pool pool, int32_t* table, int64_t s_table, int B, int cols,
                         int32_t* kv_len, const int32_t* lens, int32_t* dev_status, vc_stream_t stream);
@@ -654,7 +656,7 @@ vc_status vc_pages_trim(vc_cache_shape cache, vc_pool pool, int32_t* table, int6
  * device int32).  `table` must hold all entries that name pages of the pool.  One that names a page
  * which nobody is counted for is reported; it stays, or becomes -1 where another page moves there.
  *   workspace  >= vc_pages_compact_workspace(cache) bytes, 256-byte aligned.
- * Errors as vc_pages_reserve.
+ * Errors as vc_pages_reserve; `used` must not lie in the table.
  */
 size_t vc_pages_compact_workspace(vc_cache_shape cache);
 vc_status vc_pages_compact(vc_cache_shape cache, uint8_t* K8, float* sk, uint8_t* V8, float* sv, vc_pool pool,
