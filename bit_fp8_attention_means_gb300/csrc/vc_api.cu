@@ -321,6 +321,43 @@ static vc_status check_rope(const vc_rope_spec& r, int d) {
     return VC_OK;
 }
 
+// Rows (token, head) of d channels of bf16.
+struct RowsAt {
+    const void* at;
+    int64_t s_n, s_h;
+    int T, H, d;
+};
+// Whether a row of `a` and one of `b` (as many tokens) share memory.  Exact where both have the same strides, as
+// heads of one tensor do; with others, known only where both begin at the same place or lie apart.
+static bool rows_meet(RowsAt a, RowsAt b) {
+    if (a.T == 1) a.s_n = b.s_n;  // one token or head: any stride
+    if (a.H == 1) a.s_h = b.s_h;
+    if (b.H == 1) b.s_h = a.s_h;
+    const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at)) / 2;
+    auto size = [](const RowsAt& r) { return (r.T - 1) * r.s_n + (r.H - 1) * r.s_h + r.d; };
+    if (off >= size(a) || -off >= size(b)) return false;
+    if (a.s_n != b.s_n || a.s_h != b.s_h) return off == 0;
+    // some t in -(T-1) .. T-1 and h in -(a.H-1) .. b.H-1 with |off + t s_n + h s_h| < d: the shorter range step by
+    // step, of the other one the number nearest to it
+    struct Range {
+        int64_t lo, hi, step;
+    } t{1 - (int64_t)a.T, (int64_t)a.T - 1, a.s_n}, h{1 - (int64_t)a.H, (int64_t)b.H - 1, a.s_h};
+    const Range &some = t.hi - t.lo < h.hi - h.lo ? t : h, &other = &some == &t ? h : t;
+    for (int64_t i = some.lo; i <= some.hi; ++i) {
+        const int64_t at = off + i * some.step, near = -at / other.step;
+        for (int64_t n = near - 1; n <= near + 1; ++n) {
+            const int64_t k = n < other.lo ? other.lo : n > other.hi ? other.hi : n, x = at + k * other.step;
+            if (x < a.d && -x < a.d) return true;
+        }
+    }
+    return false;
+}
+// Whether rows may be turned into `out`: in place, or apart from what is read.
+static bool place_ok(const RowsAt& x, const RowsAt& out) {
+    const bool same = x.at == out.at && (x.T == 1 || x.s_n == out.s_n) && (x.H == 1 || x.s_h == out.s_h);
+    return same || !rows_meet(x, out);
+}
+
 static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 static vc_status rope_rows(const vc_rope_spec& r, const int32_t* pos, int inverse, RopeRows* a) {
@@ -346,6 +383,7 @@ vc_status vc_rope(const void* X, int64_t s_n, int64_t s_h, int T, int H, int d, 
     if (T == 0) return VC_OK;
     if (!X || !out || !aligned16(X) || !aligned16(out) || (!cu) != (!kv_len) || (!pos && !cu) || (cu && B < 1))
         return VC_ERR_INVALID_ARG;
+    if (!place_ok(RowsAt{X, s_n, s_h, T, H, d}, RowsAt{out, o_sn, o_sh, T, H, d})) return VC_ERR_INVALID_ARG;
     RopeRows a;
     if ((st = rope_rows(rope, pos, inverse, &a)) != VC_OK) return st;
     a.Q = static_cast<const uint16_t*>(X);
@@ -383,6 +421,12 @@ vc_status vc_cache_append_rope(const void* Q, int64_t q_sn, int64_t q_sh, int Hq
     if ((st = rope_rows(rope, pos, 0, &a)) != VC_OK) return st;
     CacheView v;
     if ((st = cache_view(cache, K8, sk, V8, sv, batch, dev_status, &v)) != VC_OK) return st;
+    if (Hq) {
+        const RowsAt o{Q_out, o_sn, o_sh, batch.T, Hq, cache.d};
+        if (!place_ok(RowsAt{Q, q_sn, q_sh, batch.T, Hq, cache.d}, o) || rows_meet(RowsAt{K, s_n, s_h, batch.T, cache.H, cache.d}, o) ||
+            rows_meet(RowsAt{V, s_n, s_h, batch.T, cache.H, cache.d}, o))
+            return VC_ERR_INVALID_ARG;
+    }
     a.Q = static_cast<const uint16_t*>(Q);
     a.K = static_cast<const uint16_t*>(K);
     a.V = static_cast<const uint16_t*>(V);

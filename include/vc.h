@@ -547,11 +547,12 @@ typedef struct {
  *   inverse  1: s = -m sin a, the transposed map: with m = 1 it takes vc_rope back, and the gradient
  *            of a loss in X is vc_rope with inverse = 1 of its gradient in `out`.
  *   out      bf16 [T, H, d], strides o_sn, o_sh as X's, 16-byte aligned: X itself with X's strides,
- *            or not overlapping it.
+ *            or sharing no row's memory with it (refused as far as the host can tell: for the same
+ *            strides, as heads of one tensor have, or the same first row).
  * A row that is not finite gives what the formula gives.  T = 0 does nothing.
  * Errors, before any launch: VC_ERR_INVALID_ARG (a null or misaligned pointer, a stride or size out
  * of the ranges above, inverse not in {0, 1}, rot, layout or magnitude out of theirs, neither pos
- * nor cu and kv_len, B < 1 with cu), VC_ERR_UNSUPPORTED (d not 64 or 128, T * H >= 2^31);
+ * nor cu and kv_len, B < 1 with cu, an overlapping `out`), VC_ERR_UNSUPPORTED (d not 64 or 128, T * H >= 2^31);
  * VC_ERR_CUDA if a launch fails.  cu or kv_len that break their rules are clamped and reported
  * through *dev_status as for the cache.
  */
@@ -565,6 +566,7 @@ vc_status vc_rope(const void* X, int64_t s_n, int64_t s_h, int T, int H, int d, 
  * turned fp32 values, not rounded to bf16 in between; values and their scales are as
  * vc_cache_append writes them, bit for bit.
  *   Q, Q_out bf16 [T, Hq, d] as X and out of vc_rope; Hq = 0: no queries (the pointers may be NULL).
+ *            Q_out shares no memory with K and V either.
  *   pos      int32 [T], or NULL: the tokens' positions in the cache, kv_len[b] - n_b + i.
  * Where a token is written does not depend on pos.  A key row whose turned values are not all
  * finite numbers is written as zeros with a NaN scale, as vc_cache_append does with such rows.

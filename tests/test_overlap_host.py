@@ -68,3 +68,47 @@ def test_reserve_and_compact(L):
     for bad in (dict(cu=11), dict(cu=-3), dict(kv=11), dict(kv=-2), dict(kv=4)):
         assert reserve(**bad) == 1, bad
     assert [compact(x) for x in (None, at(12), at(-1))] == [PAST] * 3 and [compact(x) for x in (at(0), at(11))] == [1, 1]
+
+
+def rows_of(at, s_n, s_h, T, H, d):
+    return [range(a, a + d) for a in (at + t * s_n + h * s_h for t in range(T) for h in range(H))]
+
+
+def meet(a, b):
+    return any(x.start < y.stop and y.start < x.stop for x in a for y in b)
+
+
+def test_rows_turned_into_others_place(L):
+    """vc_rope and vc_cache_append_rope into rows that hold what is still to be read: against every pair of rows.
+    Offsets of heads of 64 channels, in units of 8 elements."""
+    rope = vc.VcRopeSpec(0x10000, 64, 0, 1.0)
+    base, d, seen = 0x400000, 64, set()
+
+    def element(x):
+        return ctypes.c_void_p(base + 16 * x)
+
+    def turn(x, s, out, o, T, H):
+        return L.vc_rope(element(x), 8 * s[0], 8 * s[1], T, H, d, rope, at(0), None, None, 0, 0, element(out), 8 * o[0], 8 * o[1], None, None)
+
+    for T, H, s in ((3, 2, (48, 8)), (3, 2, (8, 24)), (1, 3, (16, 8)), (4, 1, (24, 8)), (2, 3, (25, 9)), (5, 2, (16, 40))):
+        x = rows_of(0, *s, T, H, 8)
+        for out in range(-120, 121):
+            want = 1 if out and meet(x, rows_of(out, *s, T, H, 8)) else PAST
+            seen.add((out == 0, want))
+            assert turn(0, s, out, s, T, H) == want, (T, H, s, out)
+    assert seen == {(True, PAST), (False, 1), (False, PAST)}
+    # a dimension of one row or head has any stride; X itself with other strides is not X itself
+    assert turn(0, (48, 8), 0, (99, 8), 1, 3) == turn(0, (48, 8), 0, (48, 77), 3, 1) == PAST
+    assert turn(0, (48, 8), 0, (56, 8), 3, 3) == turn(0, (48, 8), 0, (48, 16), 3, 3) == 1
+    # queries, keys and values as heads of one tensor: in place, into a part of it, and into what keys or values hold
+    code = [ctypes.c_void_p(0x200000)] * 4
+
+    def append(out, Hq=3, q=0, k=24, v=40, o=(64, 8)):
+        b = batch(T=3)
+        return L.vc_cache_append_rope(element(q), 512, 64, Hq, element(k), element(v), 512, 64, cache(d=64, s_page=2048, s_head=1024, s_tok=64), *code, b, rope, None,
+                                      element(out), 8 * o[0], 8 * o[1], None, None)
+    q, k, v = (rows_of(x, 64, 8, 3, H, 8) for x, H in ((0, 3), (24, 2), (40, 2)))
+    for out in range(-200, 201):
+        o = rows_of(out, 64, 8, 3, 3, 8)
+        assert append(out) == (1 if meet(o, k) or meet(o, v) or (out and meet(o, q)) else PAST), out
+    assert append(500, o=(24, 8)) == PAST and append(0, o=(24, 8)) == append(24, Hq=1, o=(8, 8)) == 1
