@@ -328,12 +328,12 @@ __device__ __forceinline__ Part plan_part(const CacheView& c, const PagedAttn& a
 }
 
 // SHARED: a CTA's part as the planning kernel leaves it, with the item that g0 lies in.
-struct PlanPart {
+struct alignas(16) PlanPart {  // read and written 16 bytes at a time
     int64_t g0, g1, total;
     int parts, b, h, tile, off;  // off: g0's place in the item
     SeqPass s;
 };
-static_assert(sizeof(PlanPart) == 64, "two sectors");
+static_assert(sizeof(PlanPart) == 64 && alignof(PlanPart) == 16, "two sectors, in four pieces");
 // The part in L2: no copy that an SM may hold of earlier contents.
 __device__ __forceinline__ PlanPart load_part(const PlanPart* p) {
     PlanPart r;
