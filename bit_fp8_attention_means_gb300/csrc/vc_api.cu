@@ -677,11 +677,12 @@ size_t vc_attn_paged_shared_workspace(vc_cache_shape cache, int Hq, int B, int T
     return attn_shared_workspace(cache, Hq, B, T, N, max_q, max_rows);
 }
 
-vc_status vc_attn_paged_shared(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
-                               const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv, vc_batch batch,
-                               const int32_t* groups, const int32_t* prefix, int N, float softmax_scale, int causal,
-                               int max_q, int max_rows, void* O, int64_t o_sn, int64_t o_sh, float* lse,
-                               void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+static vc_status attn_shared_call(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, const vc_cache_shape& cache,
+                                  const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                                  const vc_batch& batch, const int32_t* groups, const int32_t* prefix, int N,
+                                  float softmax_scale, int causal, int max_q, int max_rows, void* O, int64_t o_sn,
+                                  int64_t o_sh, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                  vc_stream_t stream, int skip_pass, int skip_unit) {
     SharedAttn a{};
     CacheView v;
     bool nothing = false;
@@ -695,8 +696,28 @@ vc_status vc_attn_paged_shared(const void* Q, int64_t q_sn, int64_t q_sh, int Hq
     a.groups = groups;
     a.prefix = prefix;
     a.N = N;
-    a.skip_unit = -1;
-    return launch_attn_shared(a, cache, v, max_rows, workspace, reinterpret_cast<cudaStream_t>(stream));
+    a.skip_unit = skip_unit;
+    return launch_attn_shared(a, cache, v, max_rows, skip_pass, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+vc_status vc_attn_paged_shared(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
+                               const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv, vc_batch batch,
+                               const int32_t* groups, const int32_t* prefix, int N, float softmax_scale, int causal,
+                               int max_q, int max_rows, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                               void* workspace, size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream) {
+    return attn_shared_call(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, groups, prefix, N, softmax_scale, causal,
+                            max_q, max_rows, O, o_sn, o_sh, lse, workspace, workspace_bytes, dev_status, stream, 0, -1);
+}
+
+vc_status vc_debug_attn_paged_shared_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
+                                             const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                                             vc_batch batch, const int32_t* groups, const int32_t* prefix, int N,
+                                             int max_q, int max_rows, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                             vc_stream_t stream, int skip_pass, int skip_unit) {
+    if (!dev_status || skip_pass < 1 || skip_pass > 2 || skip_unit < 0) return VC_ERR_INVALID_ARG;
+    return attn_shared_call(Q, q_sn, q_sh, Hq, cache, K8, sk, V8, sv, batch, groups, prefix, N, 0.f, 1, max_q, max_rows,
+                            O, o_sn, o_sh, lse, workspace, workspace_bytes, dev_status, stream, skip_pass, skip_unit);
 }
 
 vc_status vc_debug_attn_paged_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,

@@ -882,7 +882,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (SHARED) wait_for_primary();  // the second pass's end is the first one's too
+    if constexpr (SHARED) {
+        if (threadIdx.x == 0 && *abort_flag) *a.gave_up = 1;
+        wait_for_primary();  // the second pass's end is the first one's too
+    }
 }
 
 template <int D, int kChunk, bool SKIP>
@@ -902,13 +905,20 @@ vc_status launch_many(const CUtensorMap& mk, const CUtensorMap& mv, const PagedA
                            : launch_many_as<D, kChunk, true>(mk, mv, a, c, RT, ctas, ws, st);
 }
 
-template <int D, int kChunk>
-vc_status launch_many_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, int RT,
-                           int ctas, cudaStream_t st) {
-    auto kern = attn_many_kernel<D, kChunk, false, true>;
+template <int D, int kChunk, bool SKIP>
+vc_status launch_many_pass_as(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, int RT,
+                              int ctas, cudaStream_t st) {
+    auto kern = attn_many_kernel<D, kChunk, SKIP, true>;
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), ManyCfg<D>::SMEM);
     if (s != VC_OK) return s;
     return launch_after(kern, dim3(ctas), kThreads, ManyCfg<D>::SMEM, st, mk, mv, a, c, RT, (void*)nullptr);
+}
+
+template <int D, int kChunk>
+vc_status launch_many_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, int RT,
+                           int ctas, cudaStream_t st) {
+    return a.skip_unit < 0 ? launch_many_pass_as<D, kChunk, false>(mk, mv, a, c, RT, ctas, st)
+                           : launch_many_pass_as<D, kChunk, true>(mk, mv, a, c, RT, ctas, st);
 }
 
 }  // namespace

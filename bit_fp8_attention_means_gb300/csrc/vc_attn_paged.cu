@@ -539,7 +539,10 @@ __global__ void __launch_bounds__(few_threads(SHARED ? kShortConsumers : kFewCon
         }
     }
     __syncthreads();
-    if (SHARED) wait_for_primary();  // the second pass's end is the first one's too
+    if constexpr (SHARED) {
+        if (threadIdx.x == 0 && *abort_flag) *a.gave_up = 1;
+        wait_for_primary();  // the second pass's end is the first one's too
+    }
 }
 
 // ------------------------------------------------------------ joining
@@ -688,10 +691,10 @@ vc_status launch_few(const CUtensorMap& mk, const CUtensorMap& mv, const PagedAt
     return cuda_status(cudaGetLastError());
 }
 
-template <int D, int RG>
+template <int D, int RG, bool SKIP = false>
 vc_status launch_few_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, int ctas,
                           cudaStream_t st) {
-    auto kern = attn_few_kernel<D, RG, false, true>;
+    auto kern = attn_few_kernel<D, RG, SKIP, true>;
     constexpr int SMEM = FewCfg<D, kShortConsumers>::SMEM;
     static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs on an SM");
     vc_status s = ensure_smem_attr(reinterpret_cast<const void*>(kern), SMEM);
@@ -703,7 +706,9 @@ template <int D>
 vc_status launch_pass(const CUtensorMap& mk, const CUtensorMap& mv, const SharedAttn& a, const CacheView& c, cudaStream_t st) {
     const int ctas = kMaxCtas * a.per_sm[a.pass - 1];
     switch (a.rt[a.pass - 1]) {
-        case 8: return launch_few_pass<D, 1>(mk, mv, a, c, ctas, st);
+        case 8:
+            return a.skip_unit < 0 ? launch_few_pass<D, 1>(mk, mv, a, c, ctas, st)
+                                   : launch_few_pass<D, 1, true>(mk, mv, a, c, ctas, st);
         case 16: return launch_few_pass<D, 2>(mk, mv, a, c, ctas, st);
         case 32: return launch_few_pass<D, 4>(mk, mv, a, c, ctas, st);
         default: return launch_attn_many(mk, mv, a, c, D, a.rt[a.pass - 1], ctas, st);
@@ -778,7 +783,7 @@ static int per_sm_of(int RT) { return RT <= 32 ? 2 : 1; }
 
 namespace {
 struct SharedWs {
-    size_t plan, parts[2], words, sums, bytes;
+    size_t plan, parts[2], words, sums, gave_up, bytes;
 };
 }  // namespace
 
@@ -791,7 +796,8 @@ static SharedWs shared_ws(const int (&rt)[2], int d, int64_t B, int64_t N, size_
     w.parts[1] = w.parts[0] + up(shared_partials_bytes(rt[0], per_sm_of(rt[0]), d, rows));
     w.words = w.parts[1] + up(shared_partials_bytes(rt[1], per_sm_of(rt[1]), d, rows));
     w.sums = w.words + up(2 * rows * sizeof(uint32_t));
-    w.bytes = w.sums + up((size_t)(B + N) * sizeof(int64_t));
+    w.gave_up = w.sums + (size_t)(B + N) * sizeof(int64_t);
+    w.bytes = up(w.gave_up + sizeof(int32_t));
     return w;
 }
 
@@ -828,10 +834,11 @@ size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int 
 static int unit_time(int RT) { return RT <= 8 ? 90 : RT == 16 ? 150 : RT == 32 ? 400 : RT <= 128 ? 120 : 195; }
 static int item_units(int RT) { return RT <= 16 ? 3 : RT == 32 ? 1 : RT <= 128 ? 10 : 6; }
 
-vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape, const CacheView& c, int max_rows, void* ws,
-                             cudaStream_t st) {
+vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape, const CacheView& c, int max_rows, int skip_pass,
+                             void* ws, cudaStream_t st) {
     const int d = shape.d;
     if (!worth_sharing(args.G, c.B, c.T, args.N, args.max_q) || small_work(shape, args.G, c.B, c.T, args.max_q, c.cols)) {
+        if (skip_pass) return VC_ERR_INVALID_ARG;
         // (that launch is for the report alone)
         const vc_status s = c.dev_status ? launch_shared_check(args, c, st) : VC_OK;
         return s == VC_OK ? launch_attn_paged(args, c, d, ws, st) : s;
@@ -842,6 +849,7 @@ vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape
     a.run = shape.page_size < kUnit ? shape.page_size : kUnit;
     a.rt[0] = shared_rows(a.G, a.N, c.T, max_rows, 1);
     a.rt[1] = shared_rows(a.G, c.B, c.T, a.max_q, 2);
+    if (skip_pass && a.rt[skip_pass - 1] <= 32) a.rt[skip_pass - 1] = 8;  // of the kernel for few rows, one instance with the hook
     for (int i = 0; i < 2; ++i) {
         a.ic[i] = item_units(a.rt[i]);
         a.unit[i] = unit_time(a.rt[i]);
@@ -854,9 +862,12 @@ vc_status launch_attn_shared(const SharedAttn& args, const vc_cache_shape& shape
     a.parts2 = reinterpret_cast<float*>(base + w.parts[1]);
     a.words = reinterpret_cast<uint32_t*>(base + w.words);
     a.sums = reinterpret_cast<int64_t*>(base + w.sums);
+    a.gave_up = reinterpret_cast<int32_t*>(base + w.gave_up);
     vc_status s = launch_shared_plan(a, c, st);
-    for (a.pass = 1; s == VC_OK && a.pass <= 2; ++a.pass)
+    for (a.pass = 1; s == VC_OK && a.pass <= 2; ++a.pass) {
+        a.skip_unit = a.pass == skip_pass ? args.skip_unit : -1;
         s = d == 128 ? launch_pass<128>(mk, mv, a, c, st) : launch_pass<64>(mk, mv, a, c, st);
+    }
     return s == VC_OK ? launch_shared_join(a, c, d, st) : s;
 }
 

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kPlan) shared_plan_kernel(const SharedAttn a, 
     const int64_t words = 2 * (int64_t)c.T * c.H * a.G;
     for (int64_t i = (int64_t)blockIdx.x * kPlan + tid; i < words; i += (int64_t)gridDim.x * kPlan) a.words[i] = 0u;
     if (blockIdx.x) return;
+    if (tid == 0) *a.gave_up = 0;
     if (tid < 3) found[tid] = tid == 2 ? ~0ull : 0ull;
     int64_t total[2] = {0, 0};
     unsigned long long tiles[2] = {0, 0};
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(kThreads) shared_check_kernel(const SharedAttn
 //   O = sum_k w_k A_k / sum_k w_k l_k,   lse = ln 2 (m + log2 sum_k w_k l_k).
 // A row's word in each pass says in which CTA its item begins and how many have parts of it, so
 // that one launch joins everything, in key order.  A warp takes a row: the parts' maxima and sums a
-// lane each, then their accumulators, D/32 channels a lane.
+// lane each, then their accumulators, D/32 channels a lane.  Where a pass gave up waiting, rows have no
+// word, or slots of an earlier call: all of the call's become NaN.
 template <int D>
 __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedAttn a, const CacheView c) {
     constexpr int E = D / 32;
@@ -177,6 +179,7 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedAttn 
     const int tok = (int)(row / Hq), hq = (int)(row - (int64_t)tok * Hq), h = hq / a.G, j = hq - h * a.G;
     const SharedPartials p1 = shared_partials(c, a, 1, D), p2 = shared_partials(c, a, 2, D);
     const uint32_t w1 = __ldcg(p1.word + row), w2 = __ldcg(p2.word + row);
+    const bool lost = __ldcg(a.gave_up) != 0;
     if (!(w1 | w2)) {
         // no keys, or no sequence
         const SeqInfo s = seq_info(c, find_seq<32>(c, tok, lane, 0xffffffffu));
@@ -233,6 +236,7 @@ __global__ void __launch_bounds__(kThreads) shared_join_kernel(const SharedAttn 
             }
         }
     }
+    if (lost) l = __int_as_float(0x7FFFFFFF);
     store_row(a, tok, h, j, lane * E, acc, inverse_sum(l));
     if (lane == 0) store_lse(a, c, tok, h, j, m, l);
 }

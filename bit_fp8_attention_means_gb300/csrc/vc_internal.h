@@ -107,6 +107,7 @@ struct SharedAttn : PagedAttn {  // attention over shared prefixes
     float *parts1, *parts2;
     uint32_t* words;
     int64_t* sums;
+    int32_t* gave_up;  // not 0: a wait of a pass ran out
 };
 vc_status launch_cache_append(const uint16_t* K, const uint16_t* V, int64_t s_n, int64_t s_h, int d,
                               const CacheView& c, cudaStream_t st);
@@ -116,8 +117,9 @@ size_t attn_paged_workspace(const vc_cache_shape& c, int Hq, int B, int T, int m
 vc_status launch_attn_paged(const PagedAttn& a, const CacheView& c, int d, void* ws, cudaStream_t st);
 // over shared prefixes, `a` without what the passes need
 size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int N, int max_q, int max_rows);
-vc_status launch_attn_shared(const SharedAttn& a, const vc_cache_shape& shape, const CacheView& c, int max_rows, void* ws,
-                             cudaStream_t st);
+// skip_pass: the pass that a.skip_unit (the test hook) is for, refused where the call takes one pass; 0: none
+vc_status launch_attn_shared(const SharedAttn& a, const vc_cache_shape& shape, const CacheView& c, int max_rows, int skip_pass,
+                             void* ws, cudaStream_t st);
 // looks the batch and its groups over; plans the passes; joins their results (vc_attn_shared.cu)
 vc_status launch_shared_check(const SharedAttn& a, const CacheView& c, cudaStream_t st);
 vc_status launch_shared_plan(const SharedAttn& a, const CacheView& c, cudaStream_t st);

@@ -133,6 +133,9 @@ def lib():
         L.vc_attn_paged_shared.restype = i32
         L.vc_attn_paged_shared.argtypes = [_vp, i64, i64, i32, VcCacheShape, _vp, _vp, _vp, _vp, VcBatch, _vp, _vp, i32,
                                            ctypes.c_float, i32, i32, i32, _vp, i64, i64, _vp, _vp, ctypes.c_size_t, _vp, _vp]
+        L.vc_debug_attn_paged_shared_timeout.restype = i32
+        L.vc_debug_attn_paged_shared_timeout.argtypes = [_vp, i64, i64, i32, VcCacheShape, _vp, _vp, _vp, _vp, VcBatch, _vp, _vp, i32,
+                                                         i32, i32, _vp, i64, i64, _vp, _vp, ctypes.c_size_t, _vp, _vp, i32, i32]
         L.vc_debug_attn_paged_timeout.restype = ctypes.c_int
         L.vc_debug_attn_paged_timeout.argtypes = [_vp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, VcCacheShape, _vp,
                                                   _vp, _vp, _vp, VcBatch, ctypes.c_int, _vp, ctypes.c_int64,
@@ -1028,3 +1031,23 @@ def vc_debug_attn_paged_timeout(Q, cache, cu, kv_len, table, dev_status, skip_un
                (Q.data_ptr(), *strides, Hq, s, K8, sk, V8, sv, batch, max_q, O.data_ptr(), Hq * d, d, ws.data_ptr(),
                 ws.numel(), status), "vc_debug_attn_paged_timeout")
     return O
+
+
+def vc_debug_attn_paged_shared_timeout(Q, cache, cu, kv_len, table, groups, prefix, dev_status, skip_pass, skip_unit, max_q=0,
+                                       max_rows=0, workspace=None):
+    """vc_attn_paged_shared whose pass `skip_pass` leaves out the keys of each CTA's unit `skip_unit`: as
+    vc_debug_attn_paged_timeout.  Returns (O, lse): NaN in the rows of all sequences if a wait ran out."""
+    L = lib()
+    s, (K8, sk, V8, sv), dev = _cache_parts(cache)
+    T, Hq, d = Q.shape
+    strides, batch = _rows("Q", Q, Hq, s.d, dev), _batch_of(cu, kv_len, table, T, dev)
+    N = prefix.numel()
+    runs = _int32_vector("groups", groups, N + 1, dev), _int32_vector("prefix", prefix, N, dev)
+    status = _status_ptr(dev_status, dev)
+    _need_cuda(dev)
+    O, lse = torch.empty((T, Hq, d), dtype=_BF16, device=dev), torch.empty((T, Hq), dtype=_F32, device=dev)
+    workspace = _given_workspace(workspace, L.vc_attn_paged_shared_workspace(s, Hq, batch.B, T, N, max_q, max_rows), dev)
+    _on_device(dev, None, lambda *args: L.vc_debug_attn_paged_shared_timeout(*args, skip_pass, skip_unit),
+               (Q.data_ptr(), *strides, Hq, s, K8, sk, V8, sv, batch, *runs, N, max_q, max_rows, O.data_ptr(), Hq * d, d,
+                lse.data_ptr(), workspace.data_ptr(), workspace.numel(), status), "vc_debug_attn_paged_shared_timeout")
+    return O, lse

@@ -741,6 +741,19 @@ vc_status vc_debug_attn_paged_timeout(const void* Q, int64_t q_sn, int64_t q_sh,
                                       vc_batch batch, int max_q, void* O, int64_t o_sn, int64_t o_sh, void* workspace,
                                       size_t workspace_bytes, int32_t* dev_status, vc_stream_t stream, int skip_unit);
 
+/*
+ * The same for vc_attn_paged_shared: of pass `skip_pass` (1: prefixes, 2: what follows them), every CTA's
+ * unit `skip_unit` is left out, and that pass's waits give up after about a quarter of a second.  If one
+ * did, O and lse are NaN in the rows of all sequences.  VC_ERR_INVALID_ARG where the call would run as
+ * vc_attn_paged does.
+ */
+vc_status vc_debug_attn_paged_shared_timeout(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_cache_shape cache,
+                                             const uint8_t* K8, const float* sk, const uint8_t* V8, const float* sv,
+                                             vc_batch batch, const int32_t* groups, const int32_t* prefix, int N,
+                                             int max_q, int max_rows, void* O, int64_t o_sn, int64_t o_sh, float* lse,
+                                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                             vc_stream_t stream, int skip_pass, int skip_unit);
+
 #ifdef __cplusplus
 }
 #endif
