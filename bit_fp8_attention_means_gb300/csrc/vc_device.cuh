@@ -77,12 +77,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// What calls that share a status word leave in it, the gravest last: VC_ERR_INVALID_ARG, VC_ERR_PAGES,
-// VC_ERR_TIMEOUT (which has the smaller number of the two, and whose outputs are no results).
-__device__ __forceinline__ void flag_timeout(int32_t* dev_status) {
-    if (dev_status) atomicExch(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
-}
-
 // Bounded wait on an mbarrier phase.  Returns false (and raises the CTA's
 // abort flag and writes VC_ERR_TIMEOUT to *dev_status) if the phase has not
 // completed within timeout_ns, or if another thread of the CTA gave up.
@@ -97,7 +91,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
             if (*abort_flag) return false;
             if ((spins & 255u) == 0 && globaltimer_ns() - t0 > timeout_ns) {
                 *abort_flag = 1;
-                flag_timeout(dev_status);
+                if (dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
                 return false;
             }
         }
@@ -126,7 +120,7 @@ __device__ __forceinline__ bool mbar_wait_counted(uint32_t bar, uint32_t parity,
     for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
         if (n & 1023u) continue;
         if (!*abort_flag && n < ATTEMPTS) continue;
-        if (!*abort_flag) flag_timeout(dev_status);
+        if (!*abort_flag && dev_status) atomicMax(reinterpret_cast<int*>(dev_status), (int)VC_ERR_TIMEOUT);
         *abort_flag = 1;
         ok = false;
         break;

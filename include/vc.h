@@ -34,8 +34,10 @@
  *     the caller zeroes it beforehand and reads it after synchronising); the
  *     kernel then releases what it holds and returns instead of hanging.
  *     The call's outputs are unspecified then.  Calls may share a status
- *     word: the gravest of what they report stays, a timeout above too few
- *     pages (VC_ERR_PAGES) above what breaks a batch's rules (VC_ERR_INVALID_ARG).
+ *     word, in which the largest number stays, but for a timeout that
+ *     vc_pages_reserve finds there.  A timeout behind its VC_ERR_PAGES does
+ *     not show: give it a word of its own, or take any number but 0 to mean
+ *     that all outputs since the word was zeroed are unspecified.
  *   - Token blocks are 128 tokens; nblk = ceil(N/128), Npad = 128*nblk.
  *   - NaN or Inf inputs are outside the contract.
  */

@@ -1,4 +1,4 @@
-"""GPU: a status word that several calls share: what is left in it is the gravest of what they report."""
+"""GPU: a status word that several calls share: the largest number stays, and a timeout beside a refused reservation."""
 import pytest
 import torch
 
@@ -28,10 +28,10 @@ def timeout(status):
     vc.vc_debug_wait_timeout(status, 1000)
 
 
-@pytest.mark.parametrize("calls,left", [((refused, timeout), TIMEOUT), ((timeout, refused), TIMEOUT), ((invalid, refused), PAGES), ((refused, invalid), PAGES),
-                                        ((invalid, timeout), TIMEOUT), ((timeout, invalid), TIMEOUT), ((refused,), PAGES), ((invalid,), INVALID),
-                                        ((refused, timeout, invalid, refused), TIMEOUT)], ids=lambda x: "_".join(f.__name__ for f in x) if isinstance(x, tuple) else str(x))
-def test_a_timeout_is_hidden_by_nothing(calls, left):
+@pytest.mark.parametrize("calls,left", [((timeout, refused), TIMEOUT), ((invalid, refused), PAGES), ((refused, invalid), PAGES), ((invalid, timeout), TIMEOUT),
+                                        ((timeout, invalid), TIMEOUT), ((refused,), PAGES), ((invalid,), INVALID), ((invalid, timeout, refused, invalid), TIMEOUT)],
+                         ids=lambda x: "_".join(f.__name__ for f in x) if isinstance(x, tuple) else str(x))
+def test_a_refused_reservation_replaces_no_timeout(calls, left):
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     for call in calls:
         call(status)
