@@ -589,6 +589,12 @@ vc_status vc_cache_append_rope(const void* Q, int64_t q_sn, int64_t q_sh, int Hq
  * there.  A new pool has refs = 0 and all pages' bits set, and tables of -1.
  * The page calls keep both up to date; the state that they leave depends on
  * what was called, not on the order of anything inside a call.
+ *
+ * A pool belongs to one vc_cache_shape, whose data the calls that move any copy.
+ * The layers of a model share a table and a pool where their heads lie side by
+ * side in the same pages: the page calls get the cache of all layers' heads
+ * (H times the layers), append and attention get a layer's part of it, from
+ * K8 + layer * H * s_head (sk + layer * H * t_head) on, with the same strides.
  */
 typedef struct {
     int32_t* refs;        /* int32 [pages]: entries that name the page */
