@@ -805,7 +805,12 @@ static SharedWs shared_ws(const int (&rt)[2], int d, int64_t B, int64_t N, size_
 // where nothing is shared, nor where the sequences' own rows fill their tiles, since then a prefix read once
 // for all of them is a small part of the work.  That goes by the time of a unit of a sequence's tiles against that
 // of as many rows in tiles of 256.  8 heads, 21,600 tokens in common, two passes against one: 8 sequences of 160
-// rows 132 and 164 us, 4 of 300 rows 132 and 167, 8 of 400 rows 308 and 303, 3 of 600 rows 192 and 187.
+// rows 129 and 166 us, 4 of 300 rows 132 and 164, 8 of 400 rows 297 and 305, 3 of 600 rows 198 and 185; with d = 64
+// 119 and 155, 119 and 153, 272 and 292, 174 and 172 (the 195 and 120 are those of d = 128).
+// The rule knows no lengths, so prefixes that are short beside what follows cost their passes: 4,000 tokens of
+// their own behind 0, 128 and 1,000 in common, 60 sequences of 32 rows 118, 123 and 136 us against 104, 105 and 122
+// in one pass (d = 64: 84, 88 and 115 against 76, 77 and 89), 8 of 160 rows behind 0 63 and 61; 100 of 4 rows gain
+// or lose nothing (150, 154, 157 and 150, 152, 171; d = 64 89, 92, 94 and 113, 116, 136).
 static bool worth_sharing(int G, int B, int T, int N, int max_q) {
     if (N < 1 || B <= N) return false;
     const int64_t rows = hinted_rows(G, B, T, max_q);
@@ -815,7 +820,7 @@ static bool worth_sharing(int G, int B, int T, int N, int max_q) {
 }
 
 // Whether the whole work is so small that two launches more, 6 us, are not won back: 4 sequences of 730 keys took
-// 18.6 us in two passes and 14.5 in one.
+// 19.0 us in two passes and 14.4 in one (d = 64: 17.9 and 11.8).
 static bool small_work(const vc_cache_shape& c, int G, int B, int T, int max_q, int cols) {
     const int RT = tile_rows(G, B, T, max_q);
     const double tiles = (double)((hinted_rows(G, B, T, max_q) + RT - 1) / RT), units = ((double)cols * c.page_size + kUnit - 1) / kUnit;
@@ -830,7 +835,8 @@ size_t attn_shared_workspace(const vc_cache_shape& c, int Hq, int B, int T, int 
     return one > two ? one : two;  // which of the two is taken depends on the table's columns too
 }
 
-// The time of a unit in a CTA, in hundredths of microseconds, and what an item costs besides, in units.
+// The time of a unit in a CTA, in hundredths of microseconds, and what an item costs besides, in units: measured
+// with d = 128.  The shares of the SMs with d = 64 go by the same numbers, though its units are shorter.
 static int unit_time(int RT) { return RT <= 8 ? 90 : RT == 16 ? 150 : RT == 32 ? 400 : RT <= 128 ? 120 : 195; }
 static int item_units(int RT) { return RT <= 16 ? 3 : RT == 32 ? 1 : RT <= 128 ? 10 : 6; }
 
