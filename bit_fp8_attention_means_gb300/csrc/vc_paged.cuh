@@ -116,13 +116,14 @@ __device__ __forceinline__ bool seq_valid_in(const CacheView& c, const AttnOf<SH
         const int g = group_of(a, b);
         if (g < 0) return true;
         const int prefix = __ldg(a.prefix + g), n = __ldg(c.cu + b + 1) - __ldg(c.cu + b);
-        return prefix >= 0 && (n == 0 || prefix <= max(__ldg(c.kv_len + b) - n, 0));
+        return n == 0 || (prefix >= 0 && prefix <= max(__ldg(c.kv_len + b) - n, 0));
     }
     return true;
 }
+// (A prefix is held against its sequences; that of a group without tokens in the call is not looked at.)
 __device__ __forceinline__ bool group_valid(const CacheView& c, const SharedAttn& a, int g) {
     const int b0 = __ldg(a.groups + g), b1 = __ldg(a.groups + g + 1);
-    return b0 >= 0 && b1 >= b0 && b1 <= c.B && __ldg(a.prefix + g) <= (c.cols << c.page_log2);
+    return b0 >= 0 && b1 >= b0 && b1 <= c.B;
 }
 
 // Page of position p (0 <= p < cols * page_size), or -1 where it is not there.

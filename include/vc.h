@@ -504,8 +504,8 @@ vc_status vc_attn_paged(const void* Q, int64_t q_sn, int64_t q_sh, int Hq, vc_ca
  *            groups[g] .. groups[g+1] - 1.  Sequences before groups[0] and from groups[N] on are in none.
  *   prefix   int32 [N]: the first prefix[g] tokens of all sequences of group g that have tokens in this
  *            call (n_b > 0) are the same; those without may have ended.  They hold none of this call's
- *            tokens: prefix[g] <= max(kv_len[b] - n_b, 0) where n_b > 0.  Any length, 0 too; a page that
- *            a prefix ends in may differ behind its end.
+ *            tokens: 0 <= prefix[g] <= max(kv_len[b] - n_b, 0) where n_b > 0 (in a group without tokens it
+ *            may be any number).  A page that a prefix ends in may differ behind its end.
  *   N = 0    no groups (the pointers may be NULL).
  *   max_rows the most tokens of this call in a group, as far as the caller knows it (0: unknown); a
  *            hint as max_q.

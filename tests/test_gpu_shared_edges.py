@@ -42,6 +42,16 @@ def test_sequences_of_a_group_that_have_ended(case, wide):
         c.check(attend(c, wide=wide, max_q=hints[0], max_rows=hints[1]), c.cache())
 
 
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("prefix", [0, 5000, 2 ** 31 - 1, -1, -2 ** 31])
+def test_groups_without_tokens_have_any_prefix(prefix, wide):
+    """Groups without sequences, and such whose sequences all ended: their prefix is not looked at, and nothing is
+    reported."""
+    c = ended(dict(groups=[(200, [(9, 1), (3, 2)]), (0, []), (0, [(1, 0), (2, 0)]), (90, [(5, 5)]), (0, [])], H=2, G=2), [2, 3])
+    c.prefix = [c.prefix[0], prefix, prefix, c.prefix[3], prefix]
+    c.check(attend(c, wide=wide), c.cache())
+
+
 LOST = {  # groups, hints that choose the tiles of both passes
     "few_few": (dict(groups=[(5000, [(300, 1)] * 12)], H=8, G=1, d=64, page=64), 1, 8),
     "many_few": (dict(groups=[(5000, [(600, 2)] * 20)], H=8, G=4, page=16, tail=3), 2, 64),
